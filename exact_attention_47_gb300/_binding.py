@@ -19,6 +19,7 @@ ATTN_OK = 0
 ATTN_DEV_TIMEOUT = 0x1
 ATTN_DEV_BAD_BLOCK = 0x2
 ATTN_DEV_BAD_SEQLEN = 0x4
+ATTN_DEV_BAD_SEQID = 0x8
 BLOCK_SIZE = 16
 
 # C entry points and their signatures (mirrors include/attn47.h)
@@ -42,6 +43,15 @@ _SIGS = {
     "ssd_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "ssd_chunked_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P,
                              ctypes.c_size_t, _P]),
+    "rope_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "rope_bwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "rope_append_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "kv4_record_bytes": (ctypes.c_size_t, [_I, _I]),
+    "rope_append_paged_kv4": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "kv4_read_paged": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "attn_decode_paged_kv4_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "attn_decode_paged_kv4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
+                                   ctypes.c_size_t, _P]),
     "attn_get_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint)]),
     "attn_set_wait_timeout_ns": (None, [ctypes.c_ulonglong]),
     "attn_set_decode_max_ctas": (None, [_I]),
@@ -52,6 +62,23 @@ _SIGS = {
     "attn_last_error": (ctypes.c_char_p, []),
     "attn_abi_version": (_I, []),
 }
+
+
+
+class _Heads(ctypes.Structure):
+    """attn_heads_t of include/attn47.h."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("heads", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    """attn_rope_t of include/attn47.h."""
+
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("axes", ctypes.c_int), ("stride_axis", ctypes.c_int64),
+                ("stride_batch", ctypes.c_int64), ("pair_axis", ctypes.c_char_p)]
+
 
 _lib = None
 
@@ -110,8 +137,8 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _need_cuda(name, t, dtype, device=None):
-    """`t` is a contiguous CUDA tensor of `dtype` (any dtype if None) on
+def _need_cuda(name, t, dtype, device=None, contiguous=True):
+    """`t` is a (contiguous) CUDA tensor of `dtype` (any dtype if None) on
     `device` (if given)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -121,7 +148,7 @@ def _need_cuda(name, t, dtype, device=None):
         raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
@@ -400,6 +427,268 @@ def ssd_chunked_fwd(x, dt, A, B, C, chunk=256, h0=None, y=None, h_final=None, wo
           _ptr(h_final), batch, L, H, G, P, N, chunk, _ptr(workspace),
           workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
     return y, h_final
+
+
+def _heads(name, t, device, dim):
+    """attn_heads_t of a bf16 tensor [B, H, N, d] (``dim`` 4) or [T, H, d]
+    (``dim`` 3), any strides but a contiguous last dimension."""
+    _need_cuda(name, t, torch.bfloat16, device, contiguous=False)
+    if t.dim() != dim:
+        raise ValueError("%s must be %s" % (name, "[B, H, N, d]" if dim == 4 else "[T, H, d]"))
+    stride = t.stride()
+    if stride[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    if dim == 4:
+        return _Heads(t.data_ptr(), _step(t, 0), _step(t, 2), _step(t, 1), t.shape[1])
+    return _Heads(t.data_ptr(), 0, _step(t, 0), _step(t, 1), t.shape[1])
+
+
+def _step(t, i):
+    """The stride of dimension `i` (0 where it has one entry, whose stride
+    means nothing)."""
+    return t.stride(i) if t.shape[i] > 1 else 0
+
+
+def _rope(inv_freq, positions, lead, pair_axis, interleaved, device):
+    """attn_rope_t.  ``lead`` is the shape that a position axis may have: (N,)
+    or (B, N); ``positions`` is that, or with ``pair_axis`` [axes, ...that]."""
+    _need_cuda("inv_freq", inv_freq, torch.float32, device)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    r = _Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, None, 1, 0, 0, None)
+    if pair_axis is not None:
+        if len(pair_axis) != inv_freq.shape[0]:
+            raise ValueError("pair_axis has %d entries, inv_freq %d" % (len(pair_axis), inv_freq.shape[0]))
+        r.pair_axis = bytes(pair_axis)
+    if positions is None:
+        if pair_axis is not None:
+            raise ValueError("pair_axis needs positions with axes")
+        return r
+    _need_cuda("the rotation's positions", positions, torch.int32, device, contiguous=False)
+    shape = tuple(positions.shape)
+    if pair_axis is not None:
+        if not shape:
+            raise ValueError("with pair_axis, positions must be [axes, ...]")
+        r.axes, shape = shape[0], shape[1:]
+        r.stride_axis = _step(positions, 0)
+    if shape != lead and shape != lead[-1:]:
+        raise ValueError("positions of an axis must have shape %s, got %s"
+                         % (" or ".join(map(str, sorted({lead, lead[-1:]}))), shape))
+    if len(shape) == 2:
+        r.stride_batch = _step(positions, positions.dim() - 2)
+    if positions.shape[-1] > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions must have a contiguous last dimension")
+    r.positions = positions.data_ptr()
+    return r
+
+
+def _ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out, stream):
+    hq = _heads("q", q, None, 4)
+    dev = q.device
+    B, _, N, d = q.shape
+    hk = None
+    if k is not None:
+        hk = _heads("k", k, dev, 4)
+        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+            raise ValueError("k must be [B, Hk, N, d] matching q")
+    rope = _rope(inv_freq, positions, (B, N), pair_axis, interleaved, dev)
+    outs, ho = [], []
+    for name, x, out in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if x is None:
+            if out is not None:
+                raise ValueError("%s without its input" % name)
+            outs.append(None)
+            ho.append(None)
+            continue
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        ho.append(_heads(name, out, dev, 4))
+        _need_shape(name, out, x.shape)
+        outs.append(out)
+    _call(func, dev, _ref(hq), _ref(hk), _ref(ho[0]), _ref(ho[1]), _ref(rope), B, N, d, _stream_handle(stream, dev))
+    return tuple(outs)
+
+
+def rope_fwd(q, k, positions, inv_freq, pair_axis=None, interleaved=False, q_out=None, k_out=None,
+             stream=None):
+    """Rotary positions on queries and keys.  q [B,Hq,N,d], k [B,Hk,N,d] (or
+    None) bf16 with any strides but a contiguous last dimension, so a
+    projection output [B,N,H*d] goes in as ``.view(B,N,H,d).transpose(1,2)``;
+    inv_freq [rot/2] fp32; positions int32 [N] or [B,N], or, with ``pair_axis``
+    (rot/2 axis numbers, e.g. 0 time, 1 height, 2 width), [axes,N] or
+    [axes,B,N].
+
+    Returns (q_out, k_out) bf16: new contiguous [B,H,N,d] tensors, as
+    ``attn_fwd`` takes them, unless given (any strides; the inputs themselves
+    for a rotation in place).
+    """
+    return _rope_apply("rope_fwd", q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out, stream)
+
+
+def rope_bwd(dq_out, dk_out, positions, inv_freq, pair_axis=None, interleaved=False, dq=None, dk=None,
+             stream=None):
+    """Gradients of rope_fwd: from those of its outputs (dq_out [B,Hq,N,d],
+    dk_out or None) to those of its inputs.  The other arguments are
+    rope_fwd's.  Returns (dq, dk), new contiguous tensors unless given."""
+    return _rope_apply("rope_bwd", dq_out, dk_out, positions, inv_freq, pair_axis, interleaved, dq, dk, stream)
+
+
+def _token_map(block_table, seq_ids, positions, T, device):
+    """Checks shared by the calls that address cached tokens one by one."""
+    for name, t in (("block_table", block_table), ("seq_ids", seq_ids), ("positions", positions)):
+        _need_cuda(name, t, torch.int32, device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_seqs, max_blocks]")
+    _need_shape("seq_ids", seq_ids, (T,))
+    _need_shape("positions", positions, (T,))
+
+
+def _append_args(q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved,
+                 q_out):
+    hk = _heads("k", k, None, 3)
+    dev = k.device
+    hv = _heads("v", v, dev, 3)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape [T, Hkv, d]")
+    T, _, d = k.shape
+    _token_map(block_table, seq_ids, positions, T, dev)
+    hq = ho = None
+    if q is not None:
+        hq = _heads("q", q, dev, 3)
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, d] matching k")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        ho = _heads("q_out", q_out, dev, 3)
+        _need_shape("q_out", q_out, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope = None
+    if inv_freq is not None:
+        rope = _rope(inv_freq, rope_positions, (T,), pair_axis, interleaved, dev)
+    elif rope_positions is not None or pair_axis is not None:
+        raise ValueError("rope_positions and pair_axis need inv_freq")
+    return dev, T, d, hq, hk, hv, ho, rope, q_out
+
+
+def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions, inv_freq=None,
+                      rope_positions=None, pair_axis=None, interleaved=False, q_out=None, stream=None):
+    """A step's new tokens into the paged cache: queries rotated, keys rotated
+    and stored, values stored, in one kernel.  q [T,Hq,d] (or None), k and v
+    [T,Hkv,d] bf16, any strides but a contiguous last dimension; caches
+    [num_blocks,Hkv,16,d] bf16 (updated in place); block_table
+    [num_seqs,max_blocks], seq_ids [T] (negative: a padding row, nothing is
+    done for it) and positions [T] int32: row t takes position positions[t] of
+    sequence seq_ids[t].  inv_freq [rot/2] fp32 (None: no rotation);
+    rope_positions [T], or with ``pair_axis`` [axes,T], where the rotation's
+    positions are not the cache's.
+
+    Returns q_out [T,Hq,d] (new unless given; its padding rows are left as
+    they were), or None without q.
+    """
+    dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
+        q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need_cuda(name, t, torch.bfloat16, dev)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("caches must be [num_blocks,Hkv,block_size,d]")
+    nb, Hkv, bs, dc = k_cache.shape
+    if Hkv != k.shape[1] or dc != d:
+        raise ValueError("caches must have k's heads and head dim")
+    _call("rope_append_paged", dev, _ref(hq), _ref(hk), _ref(hv), _ref(ho), _ref(rope), _ptr(k_cache), _ptr(v_cache),
+          _ptr(block_table), _ptr(seq_ids), _ptr(positions), T, block_table.shape[0], d, bs, block_table.shape[1], nb,
+          _stream_handle(stream, dev))
+    return q_out
+
+
+def kv4_record_bytes(d, group):
+    """Bytes of one (block, KV head) record of a 4-bit cache."""
+    n = int(load_library().kv4_record_bytes(int(d), int(group)))
+    if n == 0:
+        raise ValueError("a 4-bit cache has d 64 or 128 and groups of 32 or 64, got d %d, group %d" % (d, group))
+    return n
+
+
+def _need_kv4(kv_cache, d, group, device):
+    _need_cuda("kv_cache", kv_cache, torch.uint8, device)
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != kv4_record_bytes(d, group):
+        raise ValueError("kv_cache must be [num_blocks, Hkv, %d] for d %d and group %d, got %s"
+                         % (kv4_record_bytes(d, group), d, group, tuple(kv_cache.shape)))
+
+
+def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, group, inv_freq=None,
+                          rope_positions=None, pair_axis=None, interleaved=False, q_out=None, stream=None):
+    """rope_append_paged into a 4-bit cache: kv_cache
+    [num_blocks,Hkv,kv4_record_bytes(d, group)] uint8 (updated in place), 4-bit
+    codes with a bf16 (min, scale) per ``group`` (32 or 64) consecutive
+    elements of a key or value.  Returns q_out (or None without q)."""
+    dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
+        q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
+    _need_kv4(kv_cache, d, group, dev)
+    nb, Hkv, _ = kv_cache.shape
+    if Hkv != k.shape[1]:
+        raise ValueError("kv_cache must have k's heads")
+    _call("rope_append_paged_kv4", dev, _ref(hq), _ref(hk), _ref(hv), _ref(ho), _ref(rope), _ptr(kv_cache), group,
+          _ptr(block_table), _ptr(seq_ids), _ptr(positions), T, block_table.shape[0], d, BLOCK_SIZE,
+          block_table.shape[1], nb, _stream_handle(stream, dev))
+    return q_out
+
+
+def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, v=None, stream=None):
+    """The values that cached tokens of a 4-bit cache stand for: row t is
+    position positions[t] of sequence seq_ids[t] ([T] int32; negative
+    sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16."""
+    if not isinstance(seq_ids, torch.Tensor) or seq_ids.dim() != 1:
+        raise ValueError("seq_ids must be a [T] tensor")
+    _need_kv4(kv_cache, d, group, None)
+    dev, T = kv_cache.device, seq_ids.shape[0]
+    _token_map(block_table, seq_ids, positions, T, dev)
+    nb, Hkv, _ = kv_cache.shape
+    k = _output("k", k, (T, Hkv, d), torch.bfloat16, dev)
+    v = _output("v", v, (T, Hkv, d), torch.bfloat16, dev)
+    _call("kv4_read_paged", dev, _ptr(kv_cache), group, _ptr(block_table), _ptr(seq_ids), _ptr(positions), _ptr(k),
+          _ptr(v), T, block_table.shape[0], Hkv, d, BLOCK_SIZE, block_table.shape[1], nb, _stream_handle(stream, dev))
+    return k, v
+
+
+def attn_decode_paged_kv4_workspace_size(num_seqs, Hq, Hkv, d):
+    return int(load_library().attn_decode_paged_kv4_workspace_size(num_seqs, Hq, Hkv, d))
+
+
+def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None, o=None, lse=None,
+                          workspace=None, return_lse=True, stream=None):
+    """attn_decode_paged over a 4-bit cache.  q [S,Hq,d] bf16; kv_cache
+    [num_blocks,Hkv,kv4_record_bytes(d, group)] uint8; block_table
+    [S,max_blocks] int32; seq_lens [S] int32 (all on the GPU).
+
+    Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32 or None).
+    """
+    _need_cuda("q", q, torch.bfloat16)
+    dev = q.device
+    if q.dim() != 3:
+        raise ValueError("q must be [S,Hq,d]")
+    S, Hq, d = q.shape
+    _need_kv4(kv_cache, d, group, dev)
+    nb, Hkv, _ = kv_cache.shape
+    _need_cuda("block_table", block_table, torch.int32, dev)
+    _need_cuda("seq_lens", seq_lens, torch.int32, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must be [S, max_blocks]")
+    _need_shape("seq_lens", seq_lens, (S,))
+    o = _output("o", o, (S, Hq, d), torch.bfloat16, dev)
+    if lse is not None or return_lse:
+        lse = _output("lse", lse, (S, Hq), torch.float32, dev)
+    if scale is None:
+        scale = d ** -0.5
+    workspace = _workspace("workspace", workspace, attn_decode_paged_kv4_workspace_size(S, Hq, Hkv, d), dev)
+    _call("attn_decode_paged_kv4", dev, _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), S, Hq, Hkv, d,
+          group, BLOCK_SIZE, block_table.shape[1], nb, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+    return o, lse
 
 
 def device_status(stream=None):

@@ -12,13 +12,17 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "attn47.h"
+#include "decode_kv4_sm103.h"
 #include "decode_sm103.h"
 #include "bwd_sm103.h"
 #include "fusion_sm103.h"
 #include "gemm_sm103.h"
 #include "fwd_sm103.h"
+#include "kv4.cuh"
+#include "rope_sm103.h"
 #include "ssd_sm103.h"
 #include "ptx.cuh"
 
@@ -314,6 +318,274 @@ attn_status_t decode_launch(const DeviceInfo& dev, const void* q, const void* k_
   a.timeout_ns = g_timeout_ns;
   a.stream = static_cast<cudaStream_t>(stream);
   return launch_result(attn47::launch_decode_sm103(a), "attn_decode_paged");
+}
+
+// ------------------------------------------------------ rows given by strides
+// Elements from the first to one past the last of a view.
+long long heads_extent(const attn_heads_t& h, int B, int N, int d) {
+  return (B - 1) * h.stride_batch + (N - 1) * h.stride_token + (h.heads - 1) * h.stride_head + d;
+}
+
+attn_status_t check_heads(const attn_heads_t* h, const char* name, int B, int N, int d, bool output) {
+  if (h == nullptr || h->data == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s must be non-null", name);
+  if (h->heads < 1) return fail(ATTN_ERR_INVALID_ARG, "%s must have heads >= 1", name);
+  if (!aligned16(h->data)) return fail(ATTN_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  struct {
+    long long stride, n;
+  } dim[3] = {{h->stride_batch, B}, {h->stride_token, N}, {h->stride_head, h->heads}};
+  for (const auto& x : dim) {
+    if (x.stride < 0 || x.stride % 8 != 0)
+      return fail(ATTN_ERR_INVALID_ARG, "%s: strides must be non-negative multiples of 8 elements", name);
+    if (x.n > 1 && x.stride > (1LL << 46) / x.n) return fail(ATTN_ERR_INVALID_ARG, "%s: stride too large", name);
+  }
+  if (output) {
+    // No two rows may share an element: taken from the smallest stride up,
+    // each stride spans all that lies inside it.
+    for (int i = 0; i < 3; ++i)
+      for (int j = i + 1; j < 3; ++j)
+        if (dim[j].stride < dim[i].stride) std::swap(dim[i], dim[j]);
+    long long inner = d;
+    for (const auto& x : dim) {
+      if (x.n == 1) continue;
+      if (x.stride < inner) return fail(ATTN_ERR_INVALID_ARG, "%s: rows overlap each other", name);
+      inner += (x.n - 1) * x.stride;
+    }
+  }
+  return ATTN_OK;
+}
+
+bool heads_identical(const attn_heads_t& a, const attn_heads_t& b, int B, int N) {
+  return a.data == b.data && a.heads == b.heads && (B == 1 || a.stride_batch == b.stride_batch) &&
+         (N == 1 || a.stride_token == b.stride_token) && (a.heads == 1 || a.stride_head == b.stride_head);
+}
+
+// Whether two views certainly share no element: their address ranges are
+// apart, or both repeat with the same token stride and lie beside each other
+// within it (parts of one merged projection output).
+bool heads_disjoint(const attn_heads_t& a, const attn_heads_t& b, int B, int N, int d) {
+  if (!overlap(a.data, static_cast<size_t>(heads_extent(a, B, N, d)) * 2, b.data,
+               static_cast<size_t>(heads_extent(b, B, N, d)) * 2))
+    return true;
+  const long long st = a.stride_token;
+  if (N > 1 || B > 1) {
+    if (st <= 0 || st != b.stride_token) return false;
+    if (B > 1 && (a.stride_batch % st != 0 || b.stride_batch % st != 0)) return false;
+  } else {
+    return false;
+  }
+  const long long ea = heads_extent(a, 1, 1, d), eb = heads_extent(b, 1, 1, d);
+  const long long bytes = static_cast<long long>(reinterpret_cast<uintptr_t>(b.data)) -
+                          static_cast<long long>(reinterpret_cast<uintptr_t>(a.data));
+  if (bytes % 2 != 0) return false;
+  const long long off = ((bytes / 2) % st + st) % st;
+  return off >= ea && off + eb <= st;
+}
+
+attn_status_t check_apart(const attn_heads_t* out, const char* out_name, const attn_heads_t* in,
+                          const char* in_name, bool may_be_same, int B, int N, int d) {
+  if (out == nullptr || in == nullptr) return ATTN_OK;
+  if (may_be_same && heads_identical(*out, *in, B, N)) return ATTN_OK;
+  if (!heads_disjoint(*out, *in, B, N, d))
+    return fail(ATTN_ERR_INVALID_ARG, "%s overlaps %s", out_name, in_name);
+  return ATTN_OK;
+}
+
+attn47::HeadRows head_rows(const attn_heads_t* h) {
+  attn47::HeadRows r;
+  if (h != nullptr) {
+    r.data = h->data;
+    r.batch = h->stride_batch;
+    r.token = h->stride_token;
+    r.head = h->stride_head;
+    r.heads = h->heads;
+  }
+  return r;
+}
+
+// Host-side checks of a rotation and its form for the kernels.
+attn_status_t check_rope(const attn_rope_t* r, int B, int d, bool needs_positions, attn47::RopeSpec* out) {
+  *out = attn47::RopeSpec();
+  if (r == nullptr) return ATTN_OK;              // no rotation
+  if (r->rot < 16 || r->rot > d || r->rot % 16 != 0)
+    return fail(ATTN_ERR_UNSUPPORTED, "rot %d not supported (a multiple of 16, 16 .. %d)", r->rot, d);
+  if (r->axes < 1 || r->axes > 4) return fail(ATTN_ERR_UNSUPPORTED, "axes %d not supported (1 .. 4)", r->axes);
+  if (!r->inv_freq || (reinterpret_cast<uintptr_t>(r->inv_freq) & 3u))
+    return fail(ATTN_ERR_INVALID_ARG, "inv_freq must be non-null and 4-byte aligned");
+  if (r->positions == nullptr && (needs_positions || r->axes != 1))
+    return fail(ATTN_ERR_INVALID_ARG, "the rotation's positions must be non-null");
+  if (reinterpret_cast<uintptr_t>(r->positions) & 3u)
+    return fail(ATTN_ERR_INVALID_ARG, "the rotation's positions must be 4-byte aligned");
+  if (r->stride_axis < 0 || r->stride_batch < 0 || r->stride_axis > (1LL << 40) ||
+      (B > 1 && r->stride_batch > (1LL << 46) / B))
+    return fail(ATTN_ERR_INVALID_ARG, "position strides must be non-negative and not too large");
+  out->inv_freq = r->inv_freq;
+  out->rot = r->rot;
+  out->axes = r->axes;
+  out->interleaved = r->interleaved != 0;
+  out->positions = r->positions;
+  out->axis_stride = r->stride_axis;
+  out->batch_stride = r->stride_batch;
+  if (r->pair_axis != nullptr) {
+    for (int i = 0; i < r->rot / 2; ++i) {
+      if (r->pair_axis[i] >= r->axes)
+        return fail(ATTN_ERR_INVALID_ARG, "pair_axis[%d] = %d is not below axes (%d)", i, r->pair_axis[i], r->axes);
+      out->pair_axis[i / 16] |= static_cast<uint32_t>(r->pair_axis[i]) << (2 * (i % 16));
+    }
+  }
+  return ATTN_OK;
+}
+
+size_t rope_position_bytes(const attn_rope_t* r, int B, int N) {
+  return static_cast<size_t>((r->axes - 1) * r->stride_axis + (B - 1) * r->stride_batch + N) * 4;
+}
+
+attn_status_t rope_apply(const char* what, const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* q_out,
+                         const attn_heads_t* k_out, const attn_rope_t* rope, int B, int N, int d, bool inverse,
+                         void* stream) {
+  if (B < 0 || N < 0) return fail(ATTN_ERR_INVALID_ARG, "sizes must satisfy B >= 0, N >= 0");
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (rope == nullptr) return fail(ATTN_ERR_INVALID_ARG, "rope must be non-null");
+  const bool empty = B == 0 || N == 0;
+  attn47::RopeLaunch a;
+  attn_status_t st = check_rope(rope, B, d, !empty, &a.spec);
+  if (st != ATTN_OK) return st;
+  if (empty) {
+    g_last_error[0] = '\0';
+    return ATTN_OK;
+  }
+  if ((st = check_heads(q, "q", B, N, d, false)) != ATTN_OK) return st;
+  if ((st = check_heads(q_out, "q_out", B, N, d, true)) != ATTN_OK) return st;
+  if (q->heads != q_out->heads) return fail(ATTN_ERR_INVALID_ARG, "q and q_out have different heads");
+  if ((k == nullptr) != (k_out == nullptr))
+    return fail(ATTN_ERR_INVALID_ARG, "k and k_out must both be given or both be NULL");
+  if (k != nullptr) {
+    if ((st = check_heads(k, "k", B, N, d, false)) != ATTN_OK) return st;
+    if ((st = check_heads(k_out, "k_out", B, N, d, true)) != ATTN_OK) return st;
+    if (k->heads != k_out->heads) return fail(ATTN_ERR_INVALID_ARG, "k and k_out have different heads");
+  }
+  if ((st = check_apart(q_out, "q_out", q, "q", true, B, N, d)) != ATTN_OK) return st;
+  if ((st = check_apart(q_out, "q_out", k, "k", false, B, N, d)) != ATTN_OK) return st;
+  if ((st = check_apart(k_out, "k_out", k, "k", true, B, N, d)) != ATTN_OK) return st;
+  if ((st = check_apart(k_out, "k_out", q, "q", false, B, N, d)) != ATTN_OK) return st;
+  if ((st = check_apart(k_out, "k_out", q_out, "q_out", false, B, N, d)) != ATTN_OK) return st;
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != ATTN_OK) return st;
+  auto bytes = [&](const attn_heads_t* h) { return h ? static_cast<size_t>(heads_extent(*h, B, N, d)) * 2 : 0; };
+  if ((st = check_bufs(*dev, {{q->data, bytes(q), "q"}, {q_out->data, bytes(q_out), "q_out"},
+                              {k ? k->data : nullptr, bytes(k), "k"},
+                              {k_out ? k_out->data : nullptr, bytes(k_out), "k_out"},
+                              {rope->inv_freq, static_cast<size_t>(rope->rot / 2) * 4, "inv_freq"},
+                              {rope->positions, rope_position_bytes(rope, B, N), "positions"}})) != ATTN_OK)
+    return st;
+  a.spec.inverse = inverse;
+  a.q = head_rows(q);
+  a.k = head_rows(k);
+  a.q_out = head_rows(q_out);
+  a.k_out = head_rows(k_out);
+  a.B = B;
+  a.N = N;
+  a.d = d;
+  a.sms = dev->sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(attn47::launch_rope_sm103(a), what);
+}
+
+// Both appends: kv_cache == nullptr and group == 0 for the bf16 cache.
+attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                          const attn_heads_t* q_out, const attn_rope_t* rope, void* k_cache, void* v_cache,
+                          void* kv_cache, int group, const int32_t* block_table, const int32_t* seq_ids,
+                          const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                          int max_blocks_per_seq, int num_blocks, void* stream) {
+  const bool kv4 = group != 0;
+  if (T < 0 || num_seqs < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
+    return fail(ATTN_ERR_INVALID_ARG, "sizes must satisfy T >= 0, num_seqs, max_blocks_per_seq, num_blocks >= 1");
+  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  attn47::RopeAppendLaunch a;
+  attn_status_t st = check_rope(rope, 1, d, false, &a.spec);
+  if (st != ATTN_OK) return st;
+  if (T == 0) {
+    g_last_error[0] = '\0';
+    return ATTN_OK;
+  }
+  if ((st = check_heads(k, "k", 1, T, d, false)) != ATTN_OK) return st;
+  if ((st = check_heads(v, "v", 1, T, d, false)) != ATTN_OK) return st;
+  if (k->heads != v->heads) return fail(ATTN_ERR_INVALID_ARG, "k and v have different heads");
+  if ((q == nullptr) != (q_out == nullptr))
+    return fail(ATTN_ERR_INVALID_ARG, "q and q_out must both be given or both be NULL");
+  if (q != nullptr) {
+    if ((st = check_heads(q, "q", 1, T, d, false)) != ATTN_OK) return st;
+    if ((st = check_heads(q_out, "q_out", 1, T, d, true)) != ATTN_OK) return st;
+    if (q->heads != q_out->heads) return fail(ATTN_ERR_INVALID_ARG, "q and q_out have different heads");
+  }
+  if (!block_table || !seq_ids || !positions)
+    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_ids and positions must be non-null");
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_ids and positions must be 4-byte aligned");
+  const int Hkv = k->heads;
+  if (kv4 ? (!kv_cache || !aligned16(kv_cache)) : (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)))
+    return fail(ATTN_ERR_INVALID_ARG, "the cache must be non-null and 16-byte aligned");
+  const size_t cache = static_cast<size_t>(num_blocks) * Hkv *
+                       (kv4 ? attn47::kv4_record_bytes_of(d, group) : static_cast<size_t>(16) * d * 2);
+  if ((st = check_apart(q_out, "q_out", q, "q", true, 1, T, d)) != ATTN_OK) return st;
+  if ((st = check_apart(q_out, "q_out", k, "k", false, 1, T, d)) != ATTN_OK) return st;
+  if ((st = check_apart(q_out, "q_out", v, "v", false, 1, T, d)) != ATTN_OK) return st;
+  if (!kv4 && overlap(k_cache, cache, v_cache, cache))
+    return fail(ATTN_ERR_INVALID_ARG, "k_cache overlaps v_cache");
+  const struct {
+    const attn_heads_t* h;
+    const char* name;
+  } rows[] = {{q, "q"}, {k, "k"}, {v, "v"}, {q_out, "q_out"}};
+  for (const auto& x : rows) {
+    if (x.h == nullptr) continue;
+    const size_t n = static_cast<size_t>(heads_extent(*x.h, 1, T, d)) * 2;
+    if (kv4 ? overlap(kv_cache, cache, x.h->data, n)
+            : overlap(k_cache, cache, x.h->data, n) || overlap(v_cache, cache, x.h->data, n))
+      return fail(ATTN_ERR_INVALID_ARG, "%s overlaps the cache", x.name);
+  }
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != ATTN_OK) return st;
+  auto bytes = [&](const attn_heads_t* h) { return h ? static_cast<size_t>(heads_extent(*h, 1, T, d)) * 2 : 0; };
+  const size_t ints = static_cast<size_t>(T) * 4;
+  if ((st = check_bufs(*dev, {{q ? q->data : nullptr, bytes(q), "q"}, {k->data, bytes(k), "k"},
+                              {v->data, bytes(v), "v"}, {q_out ? q_out->data : nullptr, bytes(q_out), "q_out"},
+                              {k_cache, kv4 ? 0 : cache, "k_cache"}, {v_cache, kv4 ? 0 : cache, "v_cache"},
+                              {kv_cache, kv4 ? cache : 0, "kv_cache"},
+                              {block_table, static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, "block_table"},
+                              {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"},
+                              {rope ? rope->inv_freq : nullptr, rope ? static_cast<size_t>(rope->rot / 2) * 4 : 0,
+                               "inv_freq"},
+                              {rope ? rope->positions : nullptr, rope ? rope_position_bytes(rope, 1, T) : 0,
+                               "the rotation's positions"}})) != ATTN_OK)
+    return st;
+  a.q = head_rows(q);
+  a.k = head_rows(k);
+  a.v = head_rows(v);
+  a.q_out = head_rows(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.kv_cache = kv_cache;
+  a.group = group;
+  a.block_table = block_table;
+  a.seq_ids = seq_ids;
+  a.positions = positions;
+  a.T = T;
+  a.num_seqs = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.d = d;
+  a.sms = dev->sms;
+  a.status = dev->status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(attn47::launch_rope_append_sm103(a), what);
+}
+
+attn_status_t check_group(int group) {
+  if (group != 32 && group != 64) return fail(ATTN_ERR_UNSUPPORTED, "group %d not supported (32 or 64)", group);
+  return ATTN_OK;
 }
 
 __global__ void selftest_wait_kernel(unsigned int* status, unsigned long long timeout_ns) {
@@ -882,6 +1154,175 @@ attn_status_t ssd_chunked_fwd(const void* x, const float* dt, const float* A, co
   a.timeout_ns = g_timeout_ns;
   a.stream = static_cast<cudaStream_t>(stream);
   return launch_result(attn47::launch_ssd_sm103(a), "ssd_chunked_fwd");
+}
+
+attn_status_t rope_fwd(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* q_out,
+                       const attn_heads_t* k_out, const attn_rope_t* rope, int B, int N, int d, void* stream) {
+  return rope_apply("rope_fwd", q, k, q_out, k_out, rope, B, N, d, false, stream);
+}
+
+attn_status_t rope_bwd(const attn_heads_t* dq_out, const attn_heads_t* dk_out, const attn_heads_t* dq,
+                       const attn_heads_t* dk, const attn_rope_t* rope, int B, int N, int d, void* stream) {
+  return rope_apply("rope_bwd", dq_out, dk_out, dq, dk, rope, B, N, d, true, stream);
+}
+
+attn_status_t rope_append_paged(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                                const attn_heads_t* q_out, const attn_rope_t* rope, void* k_cache,
+                                void* v_cache, const int32_t* block_table, const int32_t* seq_ids,
+                                const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                                int max_blocks_per_seq, int num_blocks, void* stream) {
+  return rope_append("rope_append_paged", q, k, v, q_out, rope, k_cache, v_cache, nullptr, 0, block_table, seq_ids,
+                     positions, T, num_seqs, d, block_size, max_blocks_per_seq, num_blocks, stream);
+}
+
+size_t kv4_record_bytes(int d, int group) {
+  if ((d != 64 && d != 128) || (group != 32 && group != 64)) return 0;
+  return attn47::kv4_record_bytes_of(d, group);
+}
+
+attn_status_t rope_append_paged_kv4(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                                    const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
+                                    int group, const int32_t* block_table, const int32_t* seq_ids,
+                                    const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                                    int max_blocks_per_seq, int num_blocks, void* stream) {
+  const attn_status_t st = check_group(group);
+  if (st != ATTN_OK) return st;
+  return rope_append("rope_append_paged_kv4", q, k, v, q_out, rope, nullptr, nullptr, kv_cache, group, block_table,
+                     seq_ids, positions, T, num_seqs, d, block_size, max_blocks_per_seq, num_blocks, stream);
+}
+
+attn_status_t kv4_read_paged(const void* kv_cache, int group, const int32_t* block_table,
+                             const int32_t* seq_ids, const int32_t* positions, void* k, void* v, int T,
+                             int num_seqs, int Hkv, int d, int block_size, int max_blocks_per_seq,
+                             int num_blocks, void* stream) {
+  attn_status_t st = check_group(group);
+  if (st != ATTN_OK) return st;
+  if (T < 0 || num_seqs < 1 || Hkv < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
+    return fail(ATTN_ERR_INVALID_ARG, "sizes must satisfy T >= 0, num_seqs, Hkv, max_blocks_per_seq, num_blocks >= 1");
+  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  if (T == 0) {
+    g_last_error[0] = '\0';
+    return ATTN_OK;
+  }
+  if (!kv_cache || !block_table || !seq_ids || !positions || !k || !v)
+    return fail(ATTN_ERR_INVALID_ARG, "kv_cache, block_table, seq_ids, positions, k and v must be non-null");
+  if (!aligned16(kv_cache) || !aligned16(k) || !aligned16(v))
+    return fail(ATTN_ERR_INVALID_ARG, "kv_cache, k and v must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_ids and positions must be 4-byte aligned");
+  const size_t cache = static_cast<size_t>(num_blocks) * Hkv * attn47::kv4_record_bytes_of(d, group);
+  const size_t out = static_cast<size_t>(T) * Hkv * d * 2;
+  if (overlap(k, out, v, out) || overlap(k, out, kv_cache, cache) || overlap(v, out, kv_cache, cache))
+    return fail(ATTN_ERR_INVALID_ARG, "k, v and kv_cache must not overlap");
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != ATTN_OK) return st;
+  const size_t ints = static_cast<size_t>(T) * 4;
+  if ((st = check_bufs(*dev, {{kv_cache, cache, "kv_cache"},
+                              {block_table, static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, "block_table"},
+                              {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"}, {k, out, "k"},
+                              {v, out, "v"}})) != ATTN_OK)
+    return st;
+  attn47::Kv4ReadLaunch a;
+  a.kv_cache = kv_cache;
+  a.block_table = block_table;
+  a.seq_ids = seq_ids;
+  a.positions = positions;
+  a.k = k;
+  a.v = v;
+  a.T = T;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.group = group;
+  a.num_seqs = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.sms = dev->sms;
+  a.status = dev->status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(attn47::launch_kv4_read_sm103(a), "kv4_read_paged");
+}
+
+size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d) {
+  if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
+  return attn47::decode_kv4_workspace_bytes(Hq, Hkv, d);
+}
+
+attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const int32_t* block_table,
+                                    const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int d,
+                                    int group, int block_size, int max_blocks_per_seq, int num_blocks,
+                                    float scale, void* o, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  attn_status_t st = check_group(group);
+  if (st != ATTN_OK) return st;
+  if (num_seqs < 0 || Hq < 1 || Hkv < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
+    return fail(ATTN_ERR_INVALID_ARG,
+                "sizes must satisfy num_seqs >= 0, Hq, Hkv, max_blocks_per_seq, num_blocks >= 1");
+  if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq (%d) is not a multiple of Hkv (%d)", Hq, Hkv);
+  if (!finite_positive(scale)) return fail(ATTN_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (Hq / Hkv > 16) return fail(ATTN_ERR_UNSUPPORTED, "Hq/Hkv = %d > 16 not supported", Hq / Hkv);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  if (static_cast<long long>(num_seqs) * Hq >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "num_seqs * Hq too large");
+  if (num_seqs == 0) {
+    g_last_error[0] = '\0';
+    return ATTN_OK;
+  }
+  if (!q || !kv_cache || !block_table || !seq_lens || !o || !workspace)
+    return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, block_table, seq_lens, o and workspace must be non-null");
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o) || !aligned16(workspace))
+    return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, o and workspace must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
+  const size_t need = attn47::decode_kv4_workspace_bytes(Hq, Hkv, d);
+  if (workspace_bytes < need)
+    return fail(ATTN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  const size_t qb = static_cast<size_t>(num_seqs) * Hq * d * 2;
+  const size_t cache = static_cast<size_t>(num_blocks) * Hkv * attn47::kv4_record_bytes_of(d, group);
+  const size_t table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, lens = static_cast<size_t>(num_seqs) * 4;
+  const size_t lb = static_cast<size_t>(num_seqs) * Hq * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } others[] = {{q, qb}, {kv_cache, cache}, {block_table, table}, {seq_lens, lens}, {o, qb}, {lse, lse ? lb : 0}};
+  for (const auto& x : others)
+    if (x.n && overlap(workspace, need, x.p, x.n))
+      return fail(ATTN_ERR_INVALID_ARG, "workspace overlaps an input or output of the decode");
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != ATTN_OK) return st;
+  if ((st = check_bufs(*dev, {{workspace, need, "workspace"}, {q, qb, "q"}, {kv_cache, cache, "kv_cache"},
+                              {block_table, table, "block_table"}, {seq_lens, lens, "seq_lens"}, {o, qb, "o"},
+                              {lse, lb, "lse"}})) != ATTN_OK)
+    return st;
+  attn47::DecKv4Launch a;
+  a.q = q;
+  a.kv_cache = kv_cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.num_seqs = num_seqs;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.group = group;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.sms = dev->sms;
+  a.epoch = next_decode_epoch();
+  a.scale = scale;
+  a.status = dev->status;
+  a.timeout_ns = g_timeout_ns;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(attn47::launch_decode_kv4_sm103(a), "attn_decode_paged_kv4");
 }
 
 attn_status_t attn_get_device_status(void* stream, unsigned int* flags_out) {

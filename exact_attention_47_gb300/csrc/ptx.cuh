@@ -14,6 +14,7 @@ namespace attn47 {
 constexpr unsigned int kDevTimeout = 0x1u;
 constexpr unsigned int kDevBadBlock = 0x2u;
 constexpr unsigned int kDevBadSeqLen = 0x4u;
+constexpr unsigned int kDevBadSeqId = 0x8u;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -345,6 +346,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
       : "memory");
 }
+// The same copy with an L2 cache policy.
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
 // Contiguous global -> L2 prefetch (no destination; 16-byte aligned, size a
 // multiple of 16).
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
@@ -590,6 +600,50 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same with fp16 operands.
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit cells over the warp: lane l holds
+// cells (l / 4, 2 (l % 4)) and the one after it, before and after.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// ---------------------------------------- arrival of the parts of a split run
+// Counts one part of a run that is split over CTAs (one lane).  The counter
+// holds a call's tag (never 0) in its high half and the parts arrived in its
+// low half; a value with another tag (a previous call, or memory never
+// written by this library) counts as zero arrivals.  Returns whether this was
+// the last part; the last part resets the counter to zero for the next call
+// (a replayed graph reuses its tag).  The first guess of the counter's value
+// is what the usual order of arrivals gives: part 0 is the last segment of
+// its CTA and arrives after the others.
+__device__ __forceinline__ bool count_arrival(unsigned long long* slot, unsigned int epoch, int part, int nparts,
+                                              unsigned int* status) {
+  const unsigned long long tag = static_cast<unsigned long long>(epoch) << 32;
+  unsigned long long cur = part == 0 ? tag | static_cast<unsigned int>(nparts - 1) : 0ull;
+  for (int i = 0; i < 2 * nparts + 2; ++i) {
+    const unsigned long long base = (cur >> 32) == epoch ? cur : tag;
+    const unsigned long long next = base + 1;
+    const unsigned long long prev = atomicCAS(slot, cur, next);
+    if (prev == cur) {
+      const bool last = static_cast<int>(next & 0xffffffffu) >= nparts;
+      if (last) atomicExch(slot, 0ull);
+      return last;
+    }
+    cur = prev;
+  }
+  atomicOr(status, kDevTimeout);   // more arrivals than parts: cannot happen
+  return false;
 }
 
 }  // namespace attn47

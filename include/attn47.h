@@ -54,6 +54,16 @@
  *                     (per-chunk cumulative decay, fwd_pass_state, chunk
  *                     outputs)
  *
+ * and what lies between the projections and the attention:
+ *
+ *  rope_fwd, rope_bwd rotary positions on queries and keys, with one to four
+ *                     position axes, and their gradients
+ *  rope_append_paged  new tokens' queries rotated, their keys rotated and
+ *                     stored with their values in the paged cache
+ *  rope_append_paged_kv4, kv4_read_paged, attn_decode_paged_kv4
+ *                     the same append into a cache held in 4 bits, the
+ *                     read-back of its rows, and the decode over it
+ *
  * Conventions shared by every call
  *  - Pointers are DEVICE pointers of the current CUDA device unless stated.
  *    The caller owns every buffer and the stream; the library allocates no
@@ -105,7 +115,11 @@ typedef enum attn_status {
 #define ATTN_DEV_BAD_SEQLEN 0x4u /* a seq_lens entry was < 0 or > max_blocks_per_seq*block_size
                                     (decode), or a ctx_lens entry was < 0 or
                                     > max_blocks_per_seq*block_size - N (chunked prefill);
-                                    it was clamped into range, outputs of that sequence invalid */
+                                    it was clamped into range, outputs of that sequence invalid;
+                                    or a token's cache position was outside its table (rope_append_*,
+                                    kv4_read_paged): nothing was written for that token */
+#define ATTN_DEV_BAD_SEQID 0x8u  /* a token's seq_ids entry was >= num_seqs (rope_append_*,
+                                    kv4_read_paged): nothing was written for that token */
 
 /*
  * attn_fwd — exact attention forward (prefill).
@@ -393,6 +407,188 @@ attn_status_t ssd_chunked_fwd(const void* x, const float* dt, const float* A, co
                               const void* C, const float* h0, void* y, float* h_final, int batch,
                               int L, int H, int G, int P, int N, int chunk, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of d bf16 values, d contiguous: head h of token n of batch b starts
+ * `b stride_batch + n stride_token + h stride_head` elements after `data`.
+ * Strides are non-negative multiples of 8, data 16-byte aligned.  A view of a
+ * merged projection output (token-major) and the contiguous [B, H, N, d] of
+ * attn_fwd are both of this form.
+ */
+typedef struct attn_heads {
+  void* data;
+  int64_t stride_batch, stride_token, stride_head;
+  int heads;
+} attn_heads_t;
+
+/*
+ * A rotation by positions.  Pair p of a head's first `rot` elements turns by
+ * the angle positions[axis of p] * inv_freq[p]:
+ *   (x, y) -> (x cos a - y sin a, y cos a + x sin a),
+ * where pair p is elements (p, p + rot/2), or (2p, 2p + 1) if `interleaved`;
+ * elements from rot on pass through.  The angle is exact for the fp32
+ * frequency given, at any 31-bit position: it is reduced to a turn in 64-bit
+ * fixed point (error under 2^-32 turns for |inv_freq| <= 1, growing with
+ * |inv_freq| above); the rest is fp32, rounded once to bf16.  A non-finite
+ * frequency gives NaN.
+ *
+ *  inv_freq   [rot/2] fp32 (device)
+ *  rot        a multiple of 16, 16 .. d
+ *  positions  int32 (device): token n of batch b has position
+ *             positions[a stride_axis + b stride_batch + n] on axis a (any
+ *             value, negative ones too; stride_batch 0 shares them)
+ *  axes       1 .. 4, e.g. 3 for time, height and width
+ *  pair_axis  HOST array of rot/2 bytes, the axis of each pair; NULL: axis 0
+ */
+typedef struct attn_rope {
+  const float* inv_freq;
+  int rot, interleaved;
+  const int32_t* positions;
+  int axes;
+  int64_t stride_axis, stride_batch;
+  const uint8_t* pair_axis;
+} attn_rope_t;
+
+/*
+ * rope_fwd — rotary positions on queries and keys, from one layout to another.
+ *
+ *  q, k           [B, heads, N, d] by their strides; k may be NULL (queries
+ *                 only).  Inputs may be broadcast (stride 0).
+ *  q_out, k_out   the same shapes (written).  Each is its input (in place) or
+ *                 shares no element with any other view of the call.
+ *  d must be 64 or 128.  B == 0 or N == 0: ATTN_OK, nothing launched.  One
+ *  kernel, deterministic.
+ */
+attn_status_t rope_fwd(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* q_out,
+                       const attn_heads_t* k_out, const attn_rope_t* rope, int B, int N, int d,
+                       void* stream);
+
+/*
+ * rope_bwd — gradients of rope_fwd: dq and dk (written) are the gradients
+ * with respect to its inputs, dq_out and dk_out (read) those with respect to
+ * its outputs.  The same arguments and rules; the rotation by the negative
+ * angle.
+ */
+attn_status_t rope_bwd(const attn_heads_t* dq_out, const attn_heads_t* dk_out, const attn_heads_t* dq,
+                       const attn_heads_t* dk, const attn_rope_t* rope, int B, int N, int d, void* stream);
+
+/*
+ * rope_append_paged — a step's new tokens on their way into the paged cache,
+ * in one kernel: their queries rotated, their keys rotated and stored, their
+ * values stored.  Row t of the batch belongs to sequence seq_ids[t] and takes
+ * its logical position positions[t]: slot positions[t] % 16 of physical block
+ * block_table[seq_ids[t]][positions[t] / 16].  Any mix of sequences and any
+ * number of tokens of each, in any order (a decode step: one of each; a
+ * prefill: many; both in one batch).  Rows with seq_ids[t] < 0 are padding:
+ * nothing is read or written for them.  Other slots of the blocks touched
+ * keep what they hold.  Two rows of one call with the same sequence and
+ * position leave either one's values.
+ *
+ *  q          [T, Hq, d] by strides (stride_batch unused), or NULL
+ *  k, v       [T, Hkv, d] by strides
+ *  q_out      [T, Hq, d] by strides (written): q itself or memory of its own;
+ *             NULL with q
+ *  rope       the rotation, or NULL for none (q is then copied).  Its positions
+ *             may be NULL: the cache positions; else token t of batch 0
+ *  k_cache,
+ *  v_cache    [num_blocks, Hkv, 16, d] bf16 (written at the new slots)
+ *  block_table [num_seqs, max_blocks_per_seq] int32, seq_ids and positions
+ *             [T] int32 (device)
+ *  block_size must be 16; d 64 or 128.  T == 0: ATTN_OK, nothing launched.
+ *  A position outside the table sets ATTN_DEV_BAD_SEQLEN, a sequence >=
+ *  num_seqs ATTN_DEV_BAD_SEQID, a table entry outside the pool
+ *  ATTN_DEV_BAD_BLOCK; nothing is written for that row.
+ */
+attn_status_t rope_append_paged(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                                const attn_heads_t* q_out, const attn_rope_t* rope, void* k_cache,
+                                void* v_cache, const int32_t* block_table, const int32_t* seq_ids,
+                                const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                                int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
+ * kv4_record_bytes — bytes of one (block, KV head) record of a 4-bit cache:
+ * 16 d for the codes of its 16 keys and values, 128 d/group for their
+ * parameters.  0 unless d is 64 or 128 and group 32 or 64.
+ *
+ * A 4-bit cache is [num_blocks, Hkv, kv4_record_bytes(d, group)] bytes.  Each
+ * group of `group` consecutive elements of a key or value has
+ *   min = bf16(lowest), scale = bf16((highest - min) / 15),
+ *   code = (x - min) / scale to the nearest whole number (half to even), 0 .. 15
+ * in fp32, and stands for code * scale + min.  So |x - value| <= scale / 2
+ * but for the roundings of min and scale (2^-9 of each).  A group whose range
+ * is not finite gets NaN parameters and stands for NaN; a scale under 2^-126
+ * becomes 0 (every value of the group is min).  Record layout, in bytes:
+ *   K codes [16][d/2], V codes [16][d/2], K parameters [16][d/group][4],
+ *   V parameters [16][d/group][4]
+ * with parameters (min, scale) as two bf16, and codes as 4-bit cells, the low
+ * half of a byte first: element e = 32 w + 8 i + 2 c + h of a key is cell
+ * 8 ((d/32) c + w) + i + 4 h of its row, element e = r + 8 (8 w + n) of a
+ * value cell 8 ((d/64) r + w) + n.  A cache written by other means needs
+ * scales >= 0.
+ */
+size_t kv4_record_bytes(int d, int group);
+
+/*
+ * rope_append_paged_kv4 — rope_append_paged into a 4-bit cache: the rotated
+ * keys and the values are quantised from fp32 (not through bf16).
+ *
+ *  kv_cache   [num_blocks, Hkv, kv4_record_bytes(d, group)] bytes, 16-byte
+ *             aligned (the new slots' codes and parameters are written)
+ *  group      32 or 64
+ *  The other arguments, rules and device flags are those of rope_append_paged.
+ */
+attn_status_t rope_append_paged_kv4(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                                    const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
+                                    int group, const int32_t* block_table, const int32_t* seq_ids,
+                                    const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                                    int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
+ * kv4_read_paged — the values that cached tokens of a 4-bit cache stand for:
+ * row t is the token at logical position positions[t] of sequence seq_ids[t]
+ * (for a chunk that attends to what the cache holds, or to move a prefix to a
+ * bf16 cache).
+ *
+ *  k, v       [T, Hkv, d] bf16, contiguous, 16-byte aligned (written)
+ *  The other arguments, rules and device flags are those of
+ *  rope_append_paged_kv4; rows with seq_ids[t] < 0 are left as they were.
+ */
+attn_status_t kv4_read_paged(const void* kv_cache, int group, const int32_t* block_table,
+                             const int32_t* seq_ids, const int32_t* positions, void* k, void* v, int T,
+                             int num_seqs, int Hkv, int d, int block_size, int max_blocks_per_seq,
+                             int num_blocks, void* stream);
+
+/*
+ * attn_decode_paged_kv4_workspace_size — bytes of device workspace that
+ * attn_decode_paged_kv4 needs: partial results of the query heads of a KV head
+ * and an arrival counter for each of at most 256 CTAs.  It does not depend on
+ * the sequences, but for 0 for an empty problem.
+ */
+size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d);
+
+/*
+ * attn_decode_paged_kv4 — attn_decode_paged over a 4-bit cache: one query
+ * token per sequence, softmax(scale * q . k) v over the values that the
+ * cached codes stand for (fp32 accumulation; the softmax numerators are
+ * rounded to 11 bits, q, codes and parameters enter exactly).
+ *
+ *  kv_cache   [num_blocks, Hkv, kv4_record_bytes(d, group)] bytes, 16-byte
+ *             aligned; slots past seq_lens[b] are never used, whatever they
+ *             hold
+ *  group      32 or 64
+ *  workspace  >= attn_decode_paged_kv4_workspace_size(...) bytes, 16-byte
+ *             aligned; contents on entry are ignored
+ *  q, block_table, seq_lens, o, lse, scale, sizes, empty sequences and device
+ *  flags as for attn_decode_paged (Hq / Hkv <= 16).  One kernel; the parts of
+ *  a split (sequence, KV head) are merged in a fixed order, so the result is
+ *  deterministic for a given device.  Calls that share a workspace must not
+ *  overlap on the GPU.
+ */
+attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const int32_t* block_table,
+                                    const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int d,
+                                    int group, int block_size, int max_blocks_per_seq, int num_blocks,
+                                    float scale, void* o, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /*
  * attn_get_device_status — synchronises `stream`, copies the current

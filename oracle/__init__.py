@@ -20,8 +20,9 @@ routine and invariants the mathematics fixes: the forward and decode by
 ``tests/test_oracle_pins.py``, the backward by
 ``tests/test_oracle_backward_pins.py``, the chunked prefill over a paged
 cache by ``tests/test_oracle_paged_prefill_pins.py``, the fusions by
-``tests/test_oracle_fusion_pins.py``, the SSD by ``tests/test_oracle_ssd_pins.py``.  No function is
-"parity unpinned".
+``tests/test_oracle_fusion_pins.py``, the SSD by ``tests/test_oracle_ssd_pins.py``, the rotary positions and the
+4-bit cache (plain definitions, no page describes them) by ``tests/test_oracle_rope_kv4_pins.py``.  No
+function is "parity unpinned".
 """
 
 from .definitions import (  # noqa: F401
@@ -37,6 +38,16 @@ from .definitions import (  # noqa: F401
     split_partials,
 )
 from .fusions import add_rmsnorm, round_bf16, swiglu, swiglu_projection  # noqa: F401
+from .kv4 import (  # noqa: F401
+    decode_paged_kv4,
+    kv4_cell,
+    kv4_quantise,
+    kv4_record_bytes,
+    kv4_store,
+    kv4_unpack,
+    kv4_values,
+)
+from .rope import rope_rotate  # noqa: F401
 from .ssd import (  # noqa: F401
     ssd_chunk_cumsum,
     ssd_chunk_output,

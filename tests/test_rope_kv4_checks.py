@@ -1,0 +1,262 @@
+"""Refusals of the rotary-position and 4-bit-cache calls (CPU): the C entry
+points on the host before any device is touched, and the binding before the
+library."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import exact_attention_47_gb300 as attn
+from exact_attention_47_gb300 import _binding
+from exact_attention_47_gb300._binding import _Heads, _Rope
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 5
+BF, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(attn.library_path()):
+        import __graft_entry__
+        __graft_entry__.build()
+    return attn.load_library()
+
+
+def test_declared_and_exported(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "attn47.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b((?:rope|kv4)_[a-z_0-9]+|attn_decode_paged_kv4[a-z_]*)\s*\(", text))
+    assert names == {"rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "kv4_record_bytes",
+                     "kv4_read_paged", "attn_decode_paged_kv4", "attn_decode_paged_kv4_workspace_size"}
+    for n in names:
+        assert hasattr(lib, n) and n in _binding._SIGS
+
+
+def heads(at, H=2, N=16, d=64, batch=None, token=None, head=None):
+    token = H * d if token is None else token
+    return _Heads(at, N * token if batch is None else batch, token, d if head is None else head, H)
+
+
+def rope(rot=64, axes=1, pos=0x9000000, inv=0x8000000, axis=None, stride_axis=16):
+    return _Rope(inv, rot, 0, pos, axes, stride_axis, 0, axis)
+
+
+def ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+Q, K, QO, KO = 0x1000000, 0x2000000, 0x3000000, 0x4000000
+
+
+def fwd(lib, q=None, k=0, qo=None, ko=0, r=None, B=1, N=16, d=64, func="rope_fwd"):
+    q = heads(Q) if q is None else q
+    k = heads(K) if k == 0 else k
+    qo = heads(QO) if qo is None else qo
+    ko = heads(KO) if ko == 0 else ko
+    r = rope() if r is None else r
+    return getattr(lib, func)(ref(q), ref(k), ref(qo), ref(ko), ref(r), B, N, d, None)
+
+
+@pytest.mark.parametrize("func", ["rope_fwd", "rope_bwd"])
+def test_rope_refusals(lib, func):
+    def call(**kw):
+        return fwd(lib, func=func, **kw)
+
+    assert call(d=96) == UNSUPPORTED
+    assert call(B=-1) == INVALID
+    assert call(r=rope(rot=24)) == UNSUPPORTED and call(r=rope(rot=0)) == UNSUPPORTED
+    assert call(r=rope(rot=80)) == UNSUPPORTED                       # beyond d
+    assert call(r=rope(axes=5)) == UNSUPPORTED and call(r=rope(axes=0)) == UNSUPPORTED
+    assert call(r=rope(axes=2, axis=bytes([0] * 31 + [2]))) == INVALID
+    assert call(r=rope(pos=None)) == INVALID and call(r=rope(inv=None)) == INVALID
+    assert call(r=rope(stride_axis=-1)) == INVALID
+    assert call(q=heads(Q + 8)) == INVALID                           # misaligned
+    assert call(q=heads(Q, token=100)) == INVALID                    # stride not a multiple of 8
+    assert call(q=heads(Q, token=-128)) == INVALID
+    assert call(q=heads(Q, H=3), qo=heads(QO, H=2)) == INVALID
+    assert call(qo=heads(QO, token=64)) == INVALID                   # output rows overlap
+    assert "overlap" in lib.attn_last_error().decode()
+    assert call(qo=heads(QO, token=0)) == INVALID
+    assert call(ko=None) == INVALID                                  # k without k_out
+    assert call(qo=heads(Q, token=256)) == INVALID                   # over its input with other strides
+    assert call(qo=heads(Q + 128)) == INVALID                        # shifted over its input
+    assert call(qo=heads(K)) == INVALID                              # over k
+    assert call(ko=heads(QO)) == INVALID                             # over q_out
+    assert call(B=0) == OK and call(N=0) == OK
+
+
+def test_merged_parts_are_told_apart(lib):
+    """q and k inside one merged buffer, rotated in place: not refused for
+    overlapping (the call then fails on the missing device, not on arguments)."""
+    q, k = heads(Q, token=512), heads(Q + 2 * 128, token=512)
+    assert fwd(lib, q=q, k=k, qo=q, ko=k) not in (INVALID, UNSUPPORTED, OK)
+    k2 = heads(Q + 2 * 64, token=512)                                # starts inside q's rows
+    assert fwd(lib, q=q, k=k2, qo=q, ko=k2) == INVALID
+
+
+KC, VC, TAB, IDS, POS = (ctypes.c_void_p(0x20000000 + i * 0x1000000) for i in range(5))
+
+
+def append(lib, q=0, k=None, v=None, qo=0, r=0, kc=KC, vc=VC, T=8, S=2, d=64, bs=16, mb=4, nb=8, ids=IDS, group=None):
+    q = heads(Q, N=T) if q == 0 else q
+    k = heads(K, N=T) if k is None else k
+    v = heads(K + 0x100000, N=T) if v is None else v
+    qo = heads(QO, N=T) if qo == 0 else qo
+    r = rope() if r == 0 else r
+    if group is not None:
+        return lib.rope_append_paged_kv4(ref(q), ref(k), ref(v), ref(qo), ref(r), kc, group, TAB, ids, POS, T, S, d, bs,
+                                         mb, nb, None)
+    return lib.rope_append_paged(ref(q), ref(k), ref(v), ref(qo), ref(r), kc, vc, TAB, ids, POS, T, S, d, bs, mb, nb,
+                                 None)
+
+
+@pytest.mark.parametrize("group", [None, 32, 64])
+def test_append_refusals(lib, group):
+    def call(**kw):
+        return append(lib, group=group, **kw)
+
+    assert call(bs=8) == UNSUPPORTED and call(d=80) == UNSUPPORTED
+    assert call(T=-1) == INVALID and call(S=0) == INVALID and call(mb=0) == INVALID and call(nb=0) == INVALID
+    assert call(mb=1 << 27) == UNSUPPORTED
+    assert call(v=heads(K + 0x100000, H=3)) == INVALID
+    assert call(qo=None) == INVALID
+    assert call(kc=None) == INVALID and call(kc=ctypes.c_void_p(0x20000008)) == INVALID
+    assert call(ids=None) == INVALID and call(ids=ctypes.c_void_p(0x20000002)) == INVALID
+    assert call(qo=heads(K)) == INVALID                              # q_out over k
+    assert call(kc=ctypes.c_void_p(K)) == INVALID                    # cache over k
+    assert call(r=rope(rot=40)) == UNSUPPORTED
+    assert call(r=rope(axes=3, pos=None, axis=bytes(32))) == INVALID
+    if group is None:
+        assert call(vc=KC) == INVALID
+    assert call(T=0) == OK
+
+
+def test_group_is_checked(lib):
+    assert append(lib, group=16) == UNSUPPORTED and append(lib, group=128) == UNSUPPORTED
+    assert lib.kv4_record_bytes(128, 16) == 0 and lib.kv4_record_bytes(96, 32) == 0
+    for d in (64, 128):
+        for g in (32, 64):
+            assert lib.kv4_record_bytes(d, g) == 16 * d + 128 * (d // g)
+
+
+def read(lib, kv=KC, k=0x5000000, v=0x6000000, T=8, S=2, Hkv=2, d=64, group=32, bs=16, mb=4, nb=8):
+    return lib.kv4_read_paged(kv, group, TAB, IDS, POS, k, v, T, S, Hkv, d, bs, mb, nb, None)
+
+
+def test_read_refusals(lib):
+    assert read(lib, group=48) == UNSUPPORTED and read(lib, d=32) == UNSUPPORTED and read(lib, bs=32) == UNSUPPORTED
+    assert read(lib, T=-1) == INVALID and read(lib, Hkv=0) == INVALID
+    assert read(lib, k=None) == INVALID and read(lib, v=0x6000004) == INVALID
+    assert read(lib, v=0x5000010) == INVALID                         # k and v overlap
+    assert read(lib, k=0x20000000) == INVALID                        # over the cache
+    assert read(lib, T=0) == OK
+
+
+def decode(lib, S=2, Hq=12, Hkv=2, d=128, group=32, bs=16, mb=4, nb=8, scale=0.1, ws=0x7000000, ws_bytes=None,
+           o=0x5000000):
+    need = lib.attn_decode_paged_kv4_workspace_size(S, Hq, Hkv, d)
+    return lib.attn_decode_paged_kv4(Q, KC, TAB, IDS, S, Hq, Hkv, d, group, bs, mb, nb, scale, o, None, ws,
+                                     need if ws_bytes is None else ws_bytes, None)
+
+
+def test_decode_refusals(lib):
+    assert decode(lib, group=128) == UNSUPPORTED and decode(lib, d=80) == UNSUPPORTED and decode(lib, bs=8) == UNSUPPORTED
+    assert decode(lib, Hq=34) == UNSUPPORTED and decode(lib, mb=1 << 27) == UNSUPPORTED
+    assert decode(lib, Hq=13) == INVALID and decode(lib, S=-1) == INVALID and decode(lib, nb=0) == INVALID
+    assert decode(lib, scale=0.0) == INVALID and decode(lib, scale=float("inf")) == INVALID
+    assert decode(lib, o=None) == INVALID and decode(lib, ws=None) == INVALID and decode(lib, ws=0x7000008) == INVALID
+    assert decode(lib, ws_bytes=64) == WORKSPACE
+    assert decode(lib, o=0x7000000) == INVALID and "overlaps" in lib.attn_last_error().decode()
+    assert decode(lib, S=0) == OK
+    size = lib.attn_decode_paged_kv4_workspace_size
+    assert size(5, 12, 2, 128) == size(500, 12, 2, 128) == 256 * 8 + 512 * 6 * 130 * 4
+    assert size(0, 12, 2, 128) == 0
+
+
+# ------------------------------------------------------------------ binding
+class _OnCuda0(torch.Tensor):
+    """A CPU tensor that claims to be on cuda:0 (it never reaches the library)."""
+
+    @property
+    def is_cuda(self):
+        return True
+
+    @property
+    def device(self):
+        return torch.device("cuda", 0)
+
+
+def dev(shape, dtype):
+    return torch.Tensor._make_subclass(_OnCuda0, torch.zeros(shape, dtype=dtype))
+
+
+@pytest.fixture
+def no_library_calls(monkeypatch, lib):
+    def refuse(func, device, *args):
+        raise AssertionError("%s reached the library with bad arguments" % func)
+
+    monkeypatch.setattr(_binding, "_call", refuse)
+
+
+def test_binding_refuses_rope(no_library_calls):
+    q, k, f, pos = dev((2, 4, 8, 64), BF), dev((2, 2, 8, 64), BF), dev((32,), F32), dev((8,), I32)
+    out = dict(q_out=dev((2, 4, 8, 64), BF), k_out=dev((2, 2, 8, 64), BF))
+    for bad, match in [
+        (dict(q=dev((2, 4, 8, 64), F32)), "q must be torch.bfloat16"),
+        (dict(q=torch.zeros((2, 4, 8, 64), dtype=BF)), "q must be a CUDA tensor"),
+        (dict(q=dev((4, 8, 64), BF)), r"q must be \[B, H, N, d\]"),
+        (dict(k=dev((2, 2, 9, 64), BF)), "k must be"),
+        (dict(q=dev((2, 4, 8, 128), BF)[..., ::2]), "contiguous last dimension"),
+        (dict(positions=dev((9,), I32)), "positions of an axis"),
+        (dict(positions=dev((8,), torch.int64)), "positions must be torch.int32"),
+        (dict(positions=dev((3, 9), I32), pair_axis=[0] * 32), "positions of an axis"),
+        (dict(pair_axis=[0] * 31, positions=dev((3, 8), I32)), "pair_axis has 31"),
+        (dict(inv_freq=dev((32,), BF)), "inv_freq must be torch.float32"),
+        (dict(q_out=dev((2, 4, 8, 128), BF)), "q_out must have shape"),
+        (dict(k=None), "k_out without its input"),
+    ]:
+        args = dict(dict(q=q, k=k, positions=pos, inv_freq=f), **out, **{})
+        args.update(bad)
+        with pytest.raises(ValueError, match=match):
+            attn.rope_fwd(**args)
+    with pytest.raises(ValueError):
+        attn.rope_fwd(q, k, dev((3, 8), I32), f, pair_axis=[300] * 32, **out)
+
+
+def test_binding_refuses_append_read_decode(no_library_calls):
+    T, S, Hq, Hkv, d = 6, 2, 4, 2, 64
+    rec = attn.kv4_record_bytes(d, 32)
+    base = dict(q=dev((T, Hq, d), BF), k=dev((T, Hkv, d), BF), v=dev((T, Hkv, d), BF), block_table=dev((S, 4), I32),
+                seq_ids=dev((T,), I32), positions=dev((T,), I32), inv_freq=dev((32,), F32), q_out=dev((T, Hq, d), BF))
+    bf = dict(k_cache=dev((9, Hkv, 16, d), BF), v_cache=dev((9, Hkv, 16, d), BF))
+    k4 = dict(kv_cache=dev((9, Hkv, rec), U8), group=32)
+    shared = [(dict(v=dev((T, Hkv + 1, d), BF)), "same shape"), (dict(seq_ids=dev((T + 1,), I32)), "seq_ids must have"),
+              (dict(positions=dev((T,), torch.int64)), "positions must be torch.int32"),
+              (dict(block_table=dev((S,), I32)), "block_table must be"), (dict(q=None), "q_out without q"),
+              (dict(inv_freq=None, rope_positions=dev((T,), I32)), "need inv_freq"),
+              (dict(pair_axis=[0] * 32), "needs positions"), (dict(q=dev((T, Hq, 128), BF)), "q must be")]
+    for func, own, more in (
+            (attn.rope_append_paged, bf, [(dict(v_cache=dev((8, Hkv, 16, d), BF)), "caches"),
+                                          (dict(k_cache=dev((9, 1, 16, d), BF), v_cache=dev((9, 1, 16, d), BF)), "k's heads")]),
+            (attn.rope_append_paged_kv4, k4, [(dict(kv_cache=dev((9, Hkv, rec + 16), U8)), "kv_cache must be"),
+                                              (dict(kv_cache=dev((9, Hkv, rec), torch.int8)), "kv_cache must be torch.uint8"),
+                                              (dict(kv_cache=dev((9, 3, rec), U8)), "k's heads"), (dict(group=16), "groups of 32 or 64")])):
+        for bad, match in shared + more:
+            with pytest.raises(ValueError, match=match):
+                func(**dict(base, **own, **{}) | bad)
+    r = dict(kv_cache=k4["kv_cache"], block_table=base["block_table"], seq_ids=base["seq_ids"],
+             positions=base["positions"], d=d, group=32, k=dev((T, Hkv, d), BF), v=dev((T, Hkv, d), BF))
+    for bad, match in [(dict(d=128), "kv_cache must be"), (dict(k=dev((T, Hkv, 128), BF)), "k must have shape"),
+                       (dict(seq_ids=dev((T, 1), I32)), "seq_ids must be")]:
+        with pytest.raises(ValueError, match=match):
+            attn.kv4_read_paged(**(r | bad))
+    need = attn.attn_decode_paged_kv4_workspace_size(S, Hq, Hkv, d)
+    c = dict(q=dev((S, Hq, d), BF), kv_cache=k4["kv_cache"], block_table=base["block_table"], seq_lens=dev((S,), I32),
+             group=32, o=dev((S, Hq, d), BF), lse=dev((S, Hq), F32), workspace=dev((need,), U8))
+    for bad, match in [(dict(group=64), "kv_cache must be"), (dict(seq_lens=dev((3,), I32)), "seq_lens must have"),
+                       (dict(workspace=dev((need - 16,), U8)), "workspace has"), (dict(o=dev((S, Hq, 128), BF)), "o must have")]:
+        with pytest.raises(ValueError, match=match):
+            attn.attn_decode_paged_kv4(**(c | bad))

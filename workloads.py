@@ -239,3 +239,41 @@ def ssd_inputs(batch, L, H, P, N, G, seed):
     dt = torch.exp(lo + (hi - lo) * torch.rand((batch, L, H), generator=gen, dtype=torch.float32))
     A = -torch.exp(math.log(16.0) * torch.rand((H,), generator=gen, dtype=torch.float32))
     return dict(x=x, dt=dt, A=A, B=B, C=C)
+
+
+def rope_inv_freq(rot, base=10000.0):
+    """base^(-2p/rot) for the rot/2 pairs, rounded to fp32."""
+    p = torch.arange(rot // 2, dtype=torch.float64)
+    return (base ** (-2.0 * p / rot)).to(torch.float32)
+
+
+def token_map(ctx_lens, new_lens, seed=0, padding=0, spare_blocks=0):
+    """Cache positions of new tokens: sequence b holds ctx_lens[b] tokens and
+    brings new_lens[b].  Returns CPU tensors block_table [S, max_blocks] int32
+    (a random permutation of the pool, padded with -1), seq_ids and positions
+    [T + padding] int32 (padding rows have sequence -1), and the pool size."""
+    gen = torch.Generator().manual_seed(int(seed))
+    nblk = [(c + n + BLOCK_SIZE - 1) // BLOCK_SIZE for c, n in zip(ctx_lens, new_lens)]
+    num_blocks = max(1, sum(nblk) + spare_blocks)
+    perm = torch.randperm(num_blocks, generator=gen).to(torch.int32)
+    table = torch.full((len(nblk), max(nblk + [1])), -1, dtype=torch.int32)
+    off = 0
+    for b, n in enumerate(nblk):
+        table[b, :n] = perm[off:off + n]
+        off += n
+    ids = [b for b, n in enumerate(new_lens) for _ in range(n)] + [-1] * padding
+    pos = [c + i for c, n in zip(ctx_lens, new_lens) for i in range(n)] + [0] * padding
+    return table, torch.tensor(ids, dtype=torch.int32), torch.tensor(pos, dtype=torch.int32), num_blocks
+
+
+def kv4_cache(num_blocks, Hkv, record_bytes, d, group, seed, scale=0.3, spread=0.4):
+    """A 4-bit cache of random codes whose parameters look like those of
+    normalised activations: scale ~ `scale` exp(`spread` N(0,1)), min near
+    -7.5 scales.  uint8 [num_blocks, Hkv, record_bytes] (CPU)."""
+    gen = torch.Generator().manual_seed(int(seed))
+    rec = torch.randint(0, 256, (num_blocks, Hkv, record_bytes), generator=gen, dtype=torch.uint8)
+    n = 2 * BLOCK_SIZE * (d // group)
+    s = (scale * torch.exp(spread * _randn(gen, (num_blocks, Hkv, n)))).to(torch.bfloat16)
+    low = (-7.5 * s.float() * (1 + 0.15 * _randn(gen, (num_blocks, Hkv, n)))).to(torch.bfloat16)
+    rec[..., 2 * BLOCK_SIZE * (d // 2):] = torch.stack([low, s], -1).reshape(num_blocks, Hkv, 2 * n).view(torch.uint8)
+    return rec
