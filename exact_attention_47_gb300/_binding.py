@@ -10,6 +10,7 @@ built, every call raises ``RuntimeError``.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -65,19 +66,11 @@ _SIGS = {
 
 
 
-class _Heads(ctypes.Structure):
-    """attn_heads_t of include/attn47.h."""
-
-    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_token", ctypes.c_int64),
-                ("stride_head", ctypes.c_int64), ("heads", ctypes.c_int)]
-
-
-class _Rope(ctypes.Structure):
-    """attn_rope_t of include/attn47.h."""
-
-    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
-                ("positions", ctypes.c_void_p), ("axes", ctypes.c_int), ("stride_axis", ctypes.c_int64),
-                ("stride_batch", ctypes.c_int64), ("pair_axis", ctypes.c_char_p)]
+# attn_heads_t and attn_rope_t of include/attn47.h, packed as bytes (their
+# address goes to the library): a ctypes structure costs several times as much
+# to fill, and a decode step's small calls are bound by the host.
+_HEADS = struct.Struct("Pqqqi")
+_ROPE = struct.Struct("PiiPiqqP")
 
 
 _lib = None
@@ -127,14 +120,16 @@ def _stream_handle(stream, device=None):
     """The raw cudaStream_t of `stream` (default: torch's current stream of
     `device`); a stream of another device is refused."""
     if stream is None:
+        if device is not None and device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)   # no Stream object made
         stream = torch.cuda.current_stream(device)
     elif device is not None and stream.device != device:
         raise ValueError("stream is on %s but the tensors are on %s" % (stream.device, device))
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _need_cuda(name, t, dtype, device=None, contiguous=True):
@@ -142,6 +137,9 @@ def _need_cuda(name, t, dtype, device=None, contiguous=True):
     `device` (if given)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if (t.is_cuda and (dtype is None or t.dtype is dtype) and (device is None or t.device == device)
+            and (not contiguous or t.is_contiguous())):
+        return
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if device is not None and t.device != device:
@@ -153,7 +151,7 @@ def _need_cuda(name, t, dtype, device=None, contiguous=True):
 
 
 def _need_shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -180,10 +178,14 @@ def _workspace(name, t, need, device):
 
 def _call(func, device, *args):
     """Call C entry point `func` with `device` current and raise on error."""
-    lib = load_library()
-    with torch.cuda.device(device):
-        st = getattr(lib, func)(*args)
-    _check(func, st)
+    fn = getattr(load_library(), func)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != ATTN_OK:
+        _check(func, st)
 
 
 def attn_fwd(q, k, v, causal=True, scale=None, o=None, lse=None, return_lse=True, stream=None):
@@ -433,57 +435,52 @@ def _heads(name, t, device, dim):
     """attn_heads_t of a bf16 tensor [B, H, N, d] (``dim`` 4) or [T, H, d]
     (``dim`` 3), any strides but a contiguous last dimension."""
     _need_cuda(name, t, torch.bfloat16, device, contiguous=False)
-    if t.dim() != dim:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dim:
         raise ValueError("%s must be %s" % (name, "[B, H, N, d]" if dim == 4 else "[T, H, d]"))
-    stride = t.stride()
-    if stride[-1] != 1 and t.shape[-1] > 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s must have a contiguous last dimension" % name)
+    # The stride of a dimension with one entry means nothing.
     if dim == 4:
-        return _Heads(t.data_ptr(), _step(t, 0), _step(t, 2), _step(t, 1), t.shape[1])
-    return _Heads(t.data_ptr(), 0, _step(t, 0), _step(t, 1), t.shape[1])
-
-
-def _step(t, i):
-    """The stride of dimension `i` (0 where it has one entry, whose stride
-    means nothing)."""
-    return t.stride(i) if t.shape[i] > 1 else 0
+        return _HEADS.pack(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[2] if shape[2] > 1 else 0,
+                           stride[1] if shape[1] > 1 else 0, shape[1])
+    return _HEADS.pack(t.data_ptr(), 0, stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0, shape[1])
 
 
 def _rope(inv_freq, positions, lead, pair_axis, interleaved, device):
-    """attn_rope_t.  ``lead`` is the shape that a position axis may have: (N,)
-    or (B, N); ``positions`` is that, or with ``pair_axis`` [axes, ...that]."""
+    """attn_rope_t and what has to live as long as it.  ``lead`` is the shape
+    that a position axis may have: (N,) or (B, N); ``positions`` is that, or
+    with ``pair_axis`` [axes, ...that]."""
     _need_cuda("inv_freq", inv_freq, torch.float32, device)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot / 2]")
-    r = _Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, None, 1, 0, 0, None)
+    pairs = inv_freq.shape[0]
+    at, axes, stride_axis, stride_batch, table, table_at = 0, 1, 0, 0, None, 0
     if pair_axis is not None:
-        if len(pair_axis) != inv_freq.shape[0]:
-            raise ValueError("pair_axis has %d entries, inv_freq %d" % (len(pair_axis), inv_freq.shape[0]))
-        r.pair_axis = bytes(pair_axis)
-    if positions is None:
-        if pair_axis is not None:
+        if len(pair_axis) != pairs:
+            raise ValueError("pair_axis has %d entries, inv_freq %d" % (len(pair_axis), pairs))
+        if positions is None:
             raise ValueError("pair_axis needs positions with axes")
-        return r
-    _need_cuda("the rotation's positions", positions, torch.int32, device, contiguous=False)
-    shape = tuple(positions.shape)
-    if pair_axis is not None:
-        if not shape:
-            raise ValueError("with pair_axis, positions must be [axes, ...]")
-        r.axes, shape = shape[0], shape[1:]
-        r.stride_axis = _step(positions, 0)
-    if shape != lead and shape != lead[-1:]:
-        raise ValueError("positions of an axis must have shape %s, got %s"
-                         % (" or ".join(map(str, sorted({lead, lead[-1:]}))), shape))
-    if len(shape) == 2:
-        r.stride_batch = _step(positions, positions.dim() - 2)
-    if positions.shape[-1] > 1 and positions.stride(-1) != 1:
-        raise ValueError("positions must have a contiguous last dimension")
-    r.positions = positions.data_ptr()
-    return r
-
-
-def _ref(x):
-    return ctypes.byref(x) if x is not None else None
+        table = ctypes.c_char_p(bytes(pair_axis))
+        table_at = ctypes.cast(table, ctypes.c_void_p).value
+    if positions is not None:
+        _need_cuda("the rotation's positions", positions, torch.int32, device, contiguous=False)
+        shape, stride = tuple(positions.shape), positions.stride()
+        if pair_axis is not None:
+            if not shape:
+                raise ValueError("with pair_axis, positions must be [axes, ...]")
+            axes, stride_axis = shape[0], stride[0] if shape[0] > 1 else 0
+            shape, stride = shape[1:], stride[1:]
+        if shape != lead and shape != lead[-1:]:
+            raise ValueError("positions of an axis must have shape %s, got %s"
+                             % (" or ".join(map(str, sorted({lead, lead[-1:]}))), shape))
+        if len(shape) == 2 and shape[0] > 1:
+            stride_batch = stride[0]
+        if shape[-1] > 1 and stride[-1] != 1:
+            raise ValueError("positions must have a contiguous last dimension")
+        at = positions.data_ptr()
+    return _ROPE.pack(inv_freq.data_ptr(), 2 * pairs, 1 if interleaved else 0, at, axes, stride_axis, stride_batch,
+                      table_at), table
 
 
 def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out, stream):
@@ -495,7 +492,7 @@ def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, 
         hk = _heads("k", k, dev, 4)
         if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
             raise ValueError("k must be [B, Hk, N, d] matching q")
-    rope = _rope(inv_freq, positions, (B, N), pair_axis, interleaved, dev)
+    rope, keep = _rope(inv_freq, positions, (B, N), pair_axis, interleaved, dev)
     outs, ho = [], []
     for name, x, out in (("q_out", q, q_out), ("k_out", k, k_out)):
         if x is None:
@@ -509,7 +506,8 @@ def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, 
         ho.append(_heads(name, out, dev, 4))
         _need_shape(name, out, x.shape)
         outs.append(out)
-    _call(func, dev, _ref(hq), _ref(hk), _ref(ho[0]), _ref(ho[1]), _ref(rope), B, N, d, _stream_handle(stream, dev))
+    _call(func, dev, hq, hk, ho[0], ho[1], rope, B, N, d, _stream_handle(stream, dev))
+    del keep                                       # the library has read the axis table by now
     return tuple(outs)
 
 
@@ -567,7 +565,7 @@ def _append_args(q, k, v, block_table, seq_ids, positions, inv_freq, rope_positi
         _need_shape("q_out", q_out, q.shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rope = None
+    rope = (None, None)
     if inv_freq is not None:
         rope = _rope(inv_freq, rope_positions, (T,), pair_axis, interleaved, dev)
     elif rope_positions is not None or pair_axis is not None:
@@ -599,7 +597,7 @@ def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions
     nb, Hkv, bs, dc = k_cache.shape
     if Hkv != k.shape[1] or dc != d:
         raise ValueError("caches must have k's heads and head dim")
-    _call("rope_append_paged", dev, _ref(hq), _ref(hk), _ref(hv), _ref(ho), _ref(rope), _ptr(k_cache), _ptr(v_cache),
+    _call("rope_append_paged", dev, hq, hk, hv, ho, rope[0], _ptr(k_cache), _ptr(v_cache),
           _ptr(block_table), _ptr(seq_ids), _ptr(positions), T, block_table.shape[0], d, bs, block_table.shape[1], nb,
           _stream_handle(stream, dev))
     return q_out
@@ -632,7 +630,7 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
     nb, Hkv, _ = kv_cache.shape
     if Hkv != k.shape[1]:
         raise ValueError("kv_cache must have k's heads")
-    _call("rope_append_paged_kv4", dev, _ref(hq), _ref(hk), _ref(hv), _ref(ho), _ref(rope), _ptr(kv_cache), group,
+    _call("rope_append_paged_kv4", dev, hq, hk, hv, ho, rope[0], _ptr(kv_cache), group,
           _ptr(block_table), _ptr(seq_ids), _ptr(positions), T, block_table.shape[0], d, BLOCK_SIZE,
           block_table.shape[1], nb, _stream_handle(stream, dev))
     return q_out

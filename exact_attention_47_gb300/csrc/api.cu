@@ -85,6 +85,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 EncodeTiledFn g_encode = nullptr;
 using AddressRangeFn = CUresult (*)(CUdeviceptr*, size_t*, CUdeviceptr);
 AddressRangeFn g_address_range = nullptr;
+using PointerAttributesFn = CUresult (*)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
+PointerAttributesFn g_pointer_attributes = nullptr;
 
 // Current device, checked once: compute capability 10.3, status word address.
 attn_status_t current_device(DeviceInfo** out) {
@@ -130,6 +132,15 @@ attn_status_t current_device(DeviceInfo** out) {
       else
         cudaGetLastError();   // optional: without it only the memory type is checked
     }
+    if (g_pointer_attributes == nullptr) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      e = cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 12000, cudaEnableDefault, &q);
+      if (e == cudaSuccess && q == cudaDriverEntryPointSuccess && fn != nullptr)
+        g_pointer_attributes = reinterpret_cast<PointerAttributesFn>(fn);
+      else
+        cudaGetLastError();   // optional: without it every check takes the longer way
+    }
     d.usable = true;
     d.checked = true;
   }
@@ -159,9 +170,30 @@ struct Buf {
 // TMA or to a kernel would be accessed as if it were device memory, and an
 // undersized buffer would be overrun; both are refused here, before any
 // launch, with ATTN_ERR_INVALID_ARG.
+//
+// One driver query answers for an ordinary buffer; whatever it does not
+// clear goes through the separate queries, which name what is wrong.  (A
+// decode step's small calls are bound by the host, and these checks were over
+// half of their time in the library.)
+bool buf_clears(const DeviceInfo& d, const Buf& b) {
+  if (g_pointer_attributes == nullptr) return false;
+  unsigned int type = 0, managed = 0;
+  int ordinal = -1;
+  CUdeviceptr base = 0;
+  size_t size = 0;
+  CUpointer_attribute attrs[5] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED,
+                                  CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
+                                  CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+  void* out[5] = {&type, &managed, &ordinal, &base, &size};
+  const uintptr_t p = reinterpret_cast<uintptr_t>(b.p);
+  if (g_pointer_attributes(5, attrs, out, static_cast<CUdeviceptr>(p)) != CUDA_SUCCESS) return false;
+  return type == CU_MEMORYTYPE_DEVICE && managed == 0 && ordinal == d.index && size != 0 && p >= base &&
+         p - base <= size && b.bytes <= size - (p - base);
+}
+
 attn_status_t check_bufs(const DeviceInfo& d, std::initializer_list<Buf> bufs) {
   for (const Buf& b : bufs) {
-    if (b.p == nullptr || b.bytes == 0) continue;
+    if (b.p == nullptr || b.bytes == 0 || buf_clears(d, b)) continue;
     cudaPointerAttributes attr;
     const cudaError_t e = cudaPointerGetAttributes(&attr, b.p);
     if (e != cudaSuccess) {
@@ -320,6 +352,10 @@ attn_status_t decode_launch(const DeviceInfo& dev, const void* q, const void* k_
   return launch_result(attn47::launch_decode_sm103(a), "attn_decode_paged");
 }
 
+// Most token rows of one launch of the kernels that take a warp per row (they
+// count in 32 bits).
+constexpr long long kMaxTokens = 0x7f000000LL;
+
 // ------------------------------------------------------ rows given by strides
 // Elements from the first to one past the last of a view.
 long long heads_extent(const attn_heads_t& h, int B, int N, int d) {
@@ -463,6 +499,8 @@ attn_status_t rope_apply(const char* what, const attn_heads_t* q, const attn_hea
     if ((st = check_heads(k_out, "k_out", B, N, d, true)) != ATTN_OK) return st;
     if (k->heads != k_out->heads) return fail(ATTN_ERR_INVALID_ARG, "k and k_out have different heads");
   }
+  if (static_cast<long long>(B) * N >= kMaxTokens)
+    return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
   if ((st = check_apart(q_out, "q_out", q, "q", true, B, N, d)) != ATTN_OK) return st;
   if ((st = check_apart(q_out, "q_out", k, "k", false, B, N, d)) != ATTN_OK) return st;
   if ((st = check_apart(k_out, "k_out", k, "k", true, B, N, d)) != ATTN_OK) return st;
@@ -503,6 +541,7 @@ attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_he
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
   if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
     return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  if (T >= kMaxTokens) return fail(ATTN_ERR_UNSUPPORTED, "T too large");
   attn47::RopeAppendLaunch a;
   attn_status_t st = check_rope(rope, 1, d, false, &a.spec);
   if (st != ATTN_OK) return st;
@@ -1203,6 +1242,7 @@ attn_status_t kv4_read_paged(const void* kv_cache, int group, const int32_t* blo
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
   if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
     return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  if (T >= kMaxTokens) return fail(ATTN_ERR_UNSUPPORTED, "T too large");
   if (T == 0) {
     g_last_error[0] = '\0';
     return ATTN_OK;
@@ -1268,8 +1308,10 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
   if (Hq / Hkv > 16) return fail(ATTN_ERR_UNSUPPORTED, "Hq/Hkv = %d > 16 not supported", Hq / Hkv);
   if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
     return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
-  if (static_cast<long long>(num_seqs) * Hq >= 0x7fffffffLL)
-    return fail(ATTN_ERR_UNSUPPORTED, "num_seqs * Hq too large");
+  // The split counts blocks (and a few more units per run) in 32 bits.
+  if (static_cast<long long>(num_seqs) * Hq >= 0x7fffffffLL ||
+      static_cast<__int128>(num_seqs) * Hkv * (static_cast<long long>(max_blocks_per_seq) + 64) >= 0x7fffffff)
+    return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
   if (num_seqs == 0) {
     g_last_error[0] = '\0';
     return ATTN_OK;

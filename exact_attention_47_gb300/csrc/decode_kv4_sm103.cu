@@ -12,10 +12,9 @@
 // two that loses nothing:
 //   q    scaled per head so its largest element is in [2^14, 2^15): every
 //        bf16 element within 2^-24 of it stays exact;
-//   p scale  times ne, a power of two that follows the largest V scale met so
-//        far (as the running maximum follows the scores) and puts it just
-//        under 2^7; p <= 2^8, so weights stay under 2^15 and are rounded to
-//        11 bits.
+//   p scale  the stabiliser of a head's softmax is its running maximum plus
+//        the exponent of the largest V scale met so far (less 7), so weights
+//        stay under 2^15; they are rounded to 11 bits.
 // The min terms of the scores are one more MMA (bf16, exact: sum(q_g) is split
 // into three bf16 parts); those of the output are summed in fp32.
 //
@@ -43,6 +42,10 @@
 namespace attn47 {
 namespace {
 
+#ifndef KV4_WARPS
+#define KV4_WARPS 8
+#define KV4_STAGES 4
+#endif
 constexpr int kBS = kKv4Slots;
 // CTAs a launch may have (one per SM); the workspace has room for this many.
 constexpr int kMaxCtas = 256;
@@ -50,7 +53,9 @@ constexpr int kRunCost = 4;
 // Lazy stabilisers (see attn_decode_paged): the running maximum moves only
 // when a score exceeds it by more than kTau (log2 units).
 constexpr float kTau = 8.f;
-constexpr int kSeqCache = 2048;
+// Entries of the plan's prefix sums (one per sequence up to this many, then
+// one per several).
+constexpr int kPlan = 1024;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // NT: column tiles of 8 query heads (1 or 2).
@@ -59,17 +64,18 @@ struct DecKv4Cfg {
   using Rec = Kv4Layout<D, G>;
   // 12 warps with 168 registers each, or 8 with 255 when two column tiles
   // double the accumulators.
-  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kWarps = NT == 1 ? KV4_WARPS : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? (NT == 1 ? KV4_STAGES : 4) : 8;   // a power of two
   static constexpr int kRows = NT * 8;                       // head rows of a piece
   static constexpr int kPitch = D + 4;                       // floats; conflict-free stores
   static constexpr int kPiece = kRows * kPitch * 4;
   static constexpr int kRing = kStages * Rec::kBytes;        // per warp
   static constexpr int kOffFirst = kWarps * kRing;           // first pieces, one per warp
   static constexpr int kOffMl = kOffFirst + kWarps * kPiece; // (max, sum): [warp][2][kRows]
-  static constexpr int kOffCache = kOffMl + kWarps * 2 * kRows * 8;
-  static constexpr int kOffShared = kOffCache + kSeqCache * 4;
+  static constexpr int kOffPlan = kOffMl + kWarps * 2 * kRows * 8;
+  static constexpr int kOffSrc = kOffPlan + (3 * kPlan + 4) * 4;        // record addresses: [warp][2 batches of 32]
+  static constexpr int kOffShared = kOffSrc + kWarps * 64 * 8;
   static constexpr int kSmem = kOffShared + 2048 + 128;      // + alignment slack
   static_assert(kRing >= kPiece, "a warp's last piece reuses its ring");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -78,17 +84,15 @@ struct DecKv4Cfg {
 struct WarpMeta {
   int f_valid, l_valid, l_start;   // l_start: the last piece holds its run's block 0
   int fb, fg, lb, lg;              // runs of the two pieces
-  int active;
-  long long fcost, lcost;          // cost positions where those runs start
 };
 
 struct DecKv4Shared {
-  uint64_t full[12][8];
-  WarpMeta meta[12];
-  long long total;                 // cost of all runs
-  long long part_sum[12];
-  int bad;
-  int last;
+  uint64_t full[16][8];
+  uint64_t ready[16];              // a warp's first piece is there for the warp before it
+  WarpMeta meta[16];
+  int2 scan[16];
+  int part_cta0[2], part_n[2];     // parts of this CTA (see below): their run's first CTA and part count (0: none)
+  int last[2];
   int abort;
 };
 static_assert(sizeof(DecKv4Shared) <= 2048, "shared control block");
@@ -114,66 +118,55 @@ __device__ __forceinline__ int kv4_seq_len(const DecKv4Params& p, int b) {
   const int L = p.seq_lens[b];
   return L < 0 ? 0 : min(L, p.max_blocks * kBS);
 }
-__device__ __forceinline__ int kv4_seq_blocks(const DecKv4Params& p, const int* cache, int b) {
-  return b < kSeqCache ? cache[b] : (kv4_seq_len(p, b) + kBS - 1) / kBS;
-}
 
-// Block position in the flat order of runs.
-struct RunPos {
-  int b, g, blk, nblk;
-  long long cost;                  // cost position where the run starts
+// Work in cost units: every run (sequence, KV head) is kRunCost units followed
+// by one per block, runs in order of (sequence, head).  cost[e] and runs[e]
+// are the units and the runs before entry e, an entry being `per` sequences;
+// blocks[e] the blocks of a head of sequence e (per == 1).
+struct Plan {
+  const int* cost;
+  const int* runs;
+  const int* blocks;
+  int entries, per, total;
+  __device__ __forceinline__ int seq_blocks(const DecKv4Params& p, int b) const {
+    return per == 1 ? blocks[b] : (kv4_seq_len(p, b) + kBS - 1) / kBS;
+  }
 };
 
-// The position of cost unit x (its run, and the first block at or after it),
-// and the blocks before it.  One warp; all lanes get the result.
-__device__ __forceinline__ void locate(const DecKv4Params& p, const int* cache, long long x, long long total,
-                                       int lane, RunPos& at, long long& flat) {
-  at.b = -1;
-  flat = 0;
-  long long cost = 0;
-  if (x >= total) x = -1;          // the end: only the block count is wanted
-  for (int base = 0; base < p.num_seqs; base += 32) {
-    const int b = base + lane;
-    const int blocks = b < p.num_seqs ? kv4_seq_blocks(p, cache, b) : 0;
-    const long long f = static_cast<long long>(blocks) * p.Hkv;
-    const long long c = blocks > 0 ? f + static_cast<long long>(kRunCost) * p.Hkv : 0;
-    long long ci = c, fi = f;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long cy = __shfl_up_sync(0xffffffffu, ci, o);
-      const long long fy = __shfl_up_sync(0xffffffffu, fi, o);
-      if (lane >= o) {
-        ci += cy;
-        fi += fy;
-      }
-    }
-    const bool here = x >= 0 && c > 0 && cost + ci - c <= x && x < cost + ci;
-    const unsigned hit = __ballot_sync(0xffffffffu, here);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      at.b = base + src;
-      at.nblk = __shfl_sync(0xffffffffu, blocks, src);
-      const long long start = cost + __shfl_sync(0xffffffffu, ci - c, src);
-      const long long rel = x - start;
-      const int per = at.nblk + kRunCost;
-      at.g = static_cast<int>(rel / per);
-      at.blk = max(0, static_cast<int>(rel - static_cast<long long>(at.g) * per) - kRunCost);
-      at.cost = start + static_cast<long long>(at.g) * per;
-      flat += __shfl_sync(0xffffffffu, fi - f, src) + static_cast<long long>(at.g) * at.nblk + at.blk;
-      return;
-    }
-    cost += __shfl_sync(0xffffffffu, ci, 31);
-    flat += __shfl_sync(0xffffffffu, fi, 31);
+struct RunPos {
+  int b, g, blk, nblk;
+  int cost;                        // cost position where the run starts
+};
+
+// The run of cost unit x < total and the first block at or after it; returns
+// the blocks before that one.  (One thread.)
+__device__ __forceinline__ int locate(const DecKv4Params& p, const Plan& plan, int x, RunPos& at) {
+  int e = 0;                                     // last entry that starts at or before x
+  for (int step = 1 << (31 - __clz(plan.entries)); step > 0; step >>= 1)
+    if (e + step < plan.entries && plan.cost[e + step] <= x) e += step;
+  int start = plan.cost[e], runs = plan.runs[e];
+  at.b = e * plan.per;
+  at.nblk = plan.seq_blocks(p, at.b);
+  for (int i = 1; i < plan.per; ++i) {           // several sequences to the entry: pass those before x
+    const int c = at.nblk > 0 ? (at.nblk + kRunCost) * p.Hkv : 0;
+    if (start + c > x) break;
+    start += c;
+    if (c > 0) runs += p.Hkv;
+    at.nblk = plan.seq_blocks(p, ++at.b);
   }
+  const int cost = at.nblk + kRunCost;
+  at.g = (x - start) / cost;
+  at.cost = start + at.g * cost;
+  at.blk = max(0, x - at.cost - kRunCost);
+  return at.cost - (runs + at.g) * kRunCost + at.blk;
 }
 
 // Walk over the runs of a warp's share.
 struct Walk {
   RunPos at;
-  long long left;                  // blocks of the share not yet passed
-  const int* cache;
-  __device__ int count() const { return static_cast<int>(min(left, static_cast<long long>(at.nblk - at.blk))); }
-  __device__ void next_run(const DecKv4Params& p, int passed) {
+  int left;                        // blocks of the share not yet passed
+  __device__ __forceinline__ int count() const { return min(left, at.nblk - at.blk); }
+  __device__ __forceinline__ void next_run(const DecKv4Params& p, const Plan& plan, int passed) {
     left -= passed;
     at.blk = 0;
     at.cost += at.nblk + kRunCost;
@@ -181,11 +174,11 @@ struct Walk {
       at.g = 0;
       do {
         ++at.b;
-        at.nblk = (left > 0 && at.b < p.num_seqs) ? kv4_seq_blocks(p, cache, at.b) : 1;
+        at.nblk = (left > 0 && at.b < p.num_seqs) ? plan.seq_blocks(p, at.b) : 1;
       } while (left > 0 && at.nblk == 0);
     }
   }
-  __device__ void skip(const DecKv4Params& p, int k) {
+  __device__ __forceinline__ void skip(const DecKv4Params& p, const Plan& plan, int k) {
     while (k > 0 && left > 0) {
       const int c = count();
       if (k < c) {
@@ -193,12 +186,63 @@ struct Walk {
         left -= k;
         k = 0;
       } else {
-        next_run(p, c);
+        next_run(p, plan, c);
         k -= c;
       }
     }
   }
 };
+
+// Arrivals at a run that is split over CTAs.  The counter holds a call's tag
+// (never 0) in its high half and the arrivals in its low half.  Whatever it
+// held, every CTA that has a part first sees to it that it carries this
+// call's tag (only the first one there changes it), and adds its arrival much
+// later; the last one leaves it at zero.  So the arrival itself is one add:
+// with the tag settled on arrival, by compare and swap, the CTAs of a long run,
+// which finish together, held each other up for 6 us.
+__device__ __forceinline__ void ready_counter(unsigned long long* slot, unsigned int epoch) {
+  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(slot);
+  while ((cur >> 32) != epoch) {                 // each failed swap is another CTA's success
+    const unsigned long long prev = atomicCAS(slot, cur, static_cast<unsigned long long>(epoch) << 32);
+    if (prev == cur) break;
+    cur = prev;
+  }
+}
+__device__ __forceinline__ bool count_ready(unsigned long long* slot, int nparts) {
+  // Release and acquire: with a CTA barrier before and behind, the CTA's
+  // stores are visible to whoever counts later, and its loads see theirs.
+  unsigned long long before;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(before) : "l"(slot), "l"(1ull) : "memory");
+  const bool last = static_cast<int>(before & 0xffffffffu) + 1 >= nparts;
+  if (last) atomicExch(slot, 0ull);
+  return last;
+}
+
+// Loads of pieces, from shared memory or from what other CTAs have written
+// (never through L1).
+__device__ __forceinline__ float2 ld_shared_or_l2(const float2* p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_or_l2(const float4* p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Bounded wait of a whole warp; the loop that polls is kept out of line, so
+// that the usual case costs one test and one vote.
+__device__ __noinline__ bool wait_warp_slow(uint32_t bar, uint32_t parity, const WaitCtl w) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return wait_warp_slow(bar, parity, w);
+}
 
 // fp16 operand registers of two of a word's four pairs: nibbles (0, 4) and
 // (1, 5) of x, or (2, 6) and (3, 7) of x >> 8, as code 2^-24 and code 2^-20.
@@ -212,18 +256,41 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float word_scale(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float word_min(uint32_t w) { return __uint_as_float(w << 16); }
 
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&r)[N]) {
+// N words from shared memory at address + OFFSET.
+template <int N, int OFFSET>
+__device__ __forceinline__ void load_words(uint32_t address, uint32_t (&r)[N]) {
   static_assert(N == 1 || N == 2 || N == 4, "");
   if constexpr (N == 4)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4+%5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(address), "n"(OFFSET));
   else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(r[0]), "=r"(r[1]) : "r"(address), "n"(OFFSET));
   else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(r[0]) : "r"(address), "n"(OFFSET));
 }
+
+// Where a lane's data lies in every record, as shared addresses for a record
+// at `ring`.
+template <int D, int G>
+struct LaneData {
+  uint32_t k, par, par_min, v0, v1;
+  int slot;
+  // MMA row 2c + i (i < 2) and 8 + 2c + (i - 2) hold slot 4c + (i ^ (c & 1)):
+  // a lane's four V slots are neighbours, and the exchange of pairs in odd
+  // quads spreads its V loads over all banks.  So row r is `slot` and row
+  // r + 8 is slot + 2.
+  __device__ __forceinline__ LaneData(uint32_t ring, int lane) {
+    using Rec = Kv4Layout<D, G>;
+    const int r = lane >> 2, c = lane & 3;
+    slot = 4 * (r >> 1) + ((r & 1) ^ ((r >> 1) & 1));
+    k = ring + slot * Rec::kRow + c * (D / 8);
+    par = ring + slot * Rec::kParRow;
+    par_min = par + (c % (D / G)) * 4;
+    v0 = ring + (4 * c + (c & 1)) * Rec::kRow + r * (D / 16);
+    v1 = ring + (4 * c + 1 - (c & 1)) * Rec::kRow + r * (D / 16);
+  }
+};
 
 // Queries of one (sequence, KV head) as B operands, and what undoes their
 // scaling.
@@ -234,22 +301,35 @@ struct QueryFrag {
   float back[NT][2];               // score factor of heads 2 (lane % 4), + 1
 };
 
+// The query rows as they are: element pairs 16 s + 2 c and 16 s + 8 + 2 c of
+// head lane / 4 of a tile (c = lane % 4).
+template <int D, int NT>
+struct QueryRaw {
+  uint32_t w[NT][D / 16][2];
+  __device__ __forceinline__ void load(const DecKv4Params& p, int b, int g, int lane) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int head = nt * 8 + (lane >> 2);
+      const bool live = head < p.group;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.q + (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * p.group + (live ? head : 0)) * D) + (lane & 3);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        w[nt][s][0] = live ? src[8 * s] : 0u;
+        w[nt][s][1] = live ? src[8 * s + 4] : 0u;
+      }
+    }
+  }
+};
+
 template <int D, int G, int NT>
-__device__ __forceinline__ void load_queries(const DecKv4Params& p, int b, int g, int lane, QueryFrag<D, G, NT>& f) {
+__device__ __forceinline__ void make_queries(const DecKv4Params& p, const QueryRaw<D, NT>& all, int lane,
+                                             QueryFrag<D, G, NT>& f) {
   constexpr int kGroups = D / G;
   const int c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int head = nt * 8 + (lane >> 2);
-    const bool live = head < p.group;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        p.q + (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(g) * p.group + (live ? head : 0)) * D) + c;
-    uint32_t raw[D / 16][2];
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      raw[s][0] = live ? src[8 * s] : 0u;
-      raw[s][1] = live ? src[8 * s + 4] : 0u;
-    }
+    const uint32_t (&raw)[D / 16][2] = all.w[nt];
     uint32_t mx = 0;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
@@ -293,14 +373,15 @@ __device__ __forceinline__ void load_queries(const DecKv4Params& p, int b, int g
   }
 }
 
-// Running state of one run: O^T tiles, the min terms, maxima and sums.
+// Running state of one run: O^T tiles, the min terms, stabilisers and sums,
+// all in units of 2^stab per head.
 template <int D, int G, int NT>
 struct RunState {
-  float o[NT][D / 16][4];          // rows r and r + 8 (the latter times 16), heads 2c, 2c + 1
+  float o[NT][D / 16][4];          // rows r and r + 8 (the latter times 16), heads 2c, 2c + 1; times 2^-24
   float mins[NT][D / G][2];        // sum of p min over this lane's tokens
-  float m[NT][2], l[NT][2];
+  float stab[NT][2], l[NT][2];
+  float limit[NT][2];              // raw score from which the stabiliser has to move
   uint32_t cap;                    // largest parameter word the weights have room for
-  float ne;                        // power of two on the weights
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -309,11 +390,56 @@ struct RunState {
       for (int i = 0; i < D / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / G; ++i) mins[nt][i][0] = mins[nt][i][1] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      // (A block without tokens may come first: its weights are then
+      // ex2(-inf + 1e30) = 0.)
+      stab[nt][0] = stab[nt][1] = -1e30f;
+      limit[nt][0] = limit[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
     cap = 0;
-    ne = 1.f;
+  }
+
+  // The power of two (log2) that the weights carry for V scales up to `cap`:
+  // scales of exponent field E are below 2^(E - 126), and 2^(133 - E) brings
+  // them under 2^7.  (At most 2^40, which keeps the min terms finite: values
+  // all under 2^-50 lose bits.)
+  static __device__ __forceinline__ float room(uint32_t cap_) {
+    const int E = static_cast<int>(cap_ >> 23);
+    return static_cast<float>(min(133 - E, 40));
+  }
+
+  // Moves the stabilisers for raw scores up to s (and V parameter words up to
+  // `big`); rare, and the same for the whole warp.
+  __device__ __forceinline__ void move(const float (&s)[NT][2], const float (&back)[NT][2], uint32_t big) {
+    big = __reduce_max_sync(0xffffffffu, big);
+    const float before = room(cap);
+    if (big > cap) cap = ((min((big >> 23) & 0xffu, 254u) + 1) << 23) - 1;
+    const float now = room(cap);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float mx = s[nt][h] * back[nt][h];
+#pragma unroll
+        for (int o_ = 4; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o_));
+        const float top = stab[nt][h] + before;  // the running maximum
+        const float to = (mx > top + kTau ? mx : top) - now;
+        f[h] = to == stab[nt][h] ? 1.f : ex2(stab[nt][h] - to);
+        stab[nt][h] = to;
+        limit[nt][h] = (to + now + kTau) / back[nt][h];
+        l[nt][h] *= f[h];
+#pragma unroll
+        for (int g = 0; g < D / G; ++g) mins[nt][g][h] *= f[h];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        o[nt][i][0] *= f[0];
+        o[nt][i][1] *= f[1];
+        o[nt][i][2] *= f[0];
+        o[nt][i][3] *= f[1];
+      }
+    }
   }
 
   // Sums over the token rows of the warp, and O in units of V.
@@ -329,190 +455,170 @@ struct RunState {
           for (int i = 0; i < D / G; ++i) mins[nt][i][h] += __shfl_xor_sync(0xffffffffu, mins[nt][i][h], o_);
         }
       }
-      const float inv = 1.f / ne;                // exact: a power of two
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          o[nt][i][h] = fmaf(o[nt][i][h] * 0x1p24f, inv, mins[nt][16 * i / G][h]);
-          o[nt][i][2 + h] = fmaf(o[nt][i][2 + h] * 0x1p20f, inv, mins[nt][16 * i / G][h]);
+          o[nt][i][h] = fmaf(o[nt][i][h], 0x1p24f, mins[nt][16 * i / G][h]);
+          o[nt][i][2 + h] = fmaf(o[nt][i][2 + h], 0x1p20f, mins[nt][16 * i / G][h]);
         }
       }
     }
   }
 };
 
-// One block: 16 slots, of which the first `valid` hold tokens.
+// Two blocks of one run: 16 slots each, of which the first valid[i] (16 or
+// more: all) hold tokens; their records rec[i] bytes into the ring.  Two at a
+// time, because one block is a chain of dependent steps and a scheduler has
+// only three warps to fill its gaps with.
 template <int D, int G, int NT>
-__device__ __forceinline__ void take_block(uint32_t rec, int valid, int lane, const QueryFrag<D, G, NT>& q,
-                                           RunState<D, G, NT>& st) {
+__device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint32_t (&rec)[2], const int (&valid)[2],
+                                            const QueryFrag<D, G, NT>& q, RunState<D, G, NT>& st) {
   using Rec = Kv4Layout<D, G>;
   constexpr int kGroups = D / G, kKW = D / 32, kVW = D / 64;
-  const int r = lane >> 2, c = lane & 3;
-  // MMA row 2c + i (i < 2) and 8 + 2c + (i - 2) hold slot 4c + (i ^ (c & 1)):
-  // a lane's four V slots are neighbours, and the exchange of pairs in odd
-  // quads spreads its V loads over all banks.
-  const int slot = 4 * (r >> 1) + ((r & 1) ^ ((r >> 1) & 1));   // row r; row r + 8 is slot + 2
-
-  uint32_t ka[kKW], kb[kKW], kpa[kGroups], kpb[kGroups];
-  lds_words<kKW>(rec + slot * Rec::kRow + c * (D / 8), ka);
-  lds_words<kKW>(rec + (slot + 2) * Rec::kRow + c * (D / 8), kb);
-  lds_words<kGroups>(rec + Rec::kOffParK + slot * Rec::kParRow, kpa);
-  lds_words<kGroups>(rec + Rec::kOffParK + (slot + 2) * Rec::kParRow, kpb);
-  uint32_t vw[4][kVW], vpa[kGroups], vpb[kGroups];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    lds_words<kVW>(rec + Rec::kOffV + (4 * c + (i ^ (c & 1))) * Rec::kRow + r * (D / 16), vw[i]);
-  lds_words<kGroups>(rec + Rec::kOffParV + slot * Rec::kParRow, vpa);
-  lds_words<kGroups>(rec + Rec::kOffParV + (slot + 2) * Rec::kParRow, vpb);
 
   // --- S^T: rows = slots, columns = heads
-  float s[NT][4];
-  {
-    uint32_t mw = kpa[0], mw8 = kpb[0];          // this lane's group: lane % 4
+  float s[2][NT][4];
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
-      if (c == i) {
-        mw = kpa[i];
-        mw8 = kpb[i];
+  for (int n = 0; n < 2; ++n) {
+    // The min terms: lane c of a quad brings group c (the others of its group
+    // count meet zero operands).
+    uint32_t lo[1], lo8[1];
+    load_words<1, Rec::kOffParK>(at.par_min + rec[n], lo);
+    load_words<1, Rec::kOffParK + 2 * Rec::kParRow>(at.par_min + rec[n], lo8);
+    lo[0] = __byte_perm(lo[0], 0, 0x1010);
+    lo8[0] = __byte_perm(lo8[0], 0, 0x1010);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mma_16816_bf16_first(s[n][nt], lo[0], lo8[0], lo[0], lo8[0], q.sums[nt][0], q.sums[nt][1]);
+  }
+  {
+    uint32_t ka[2][kKW], kb[2][kKW], kpa[2][kGroups], kpb[2][kGroups];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      load_words<kKW, 0>(at.k + rec[n], ka[n]);
+      load_words<kKW, 2 * Rec::kRow>(at.k + rec[n], kb[n]);
+      load_words<kGroups, Rec::kOffParK>(at.par + rec[n], kpa[n]);
+      load_words<kGroups, Rec::kOffParK + 2 * Rec::kParRow>(at.par + rec[n], kpb[n]);
+    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float acc[2][NT][4];
+#pragma unroll
+      for (int ws = 0; ws < G / 32; ++ws) {
+        const int w = g * (G / 32) + ws;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t xa = ka[n][w], xb = kb[n][w], ya = xa >> 8, yb = xb >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (ws == 0)
+              mma_16816_f16_first(acc[n][nt], codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb), q.b[nt][2 * w][0],
+                                  q.b[nt][2 * w][1]);
+            else
+              mma_16816_f16(acc[n][nt], codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb), q.b[nt][2 * w][0],
+                            q.b[nt][2 * w][1]);
+            mma_16816_f16(acc[n][nt], codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb), q.b[nt][2 * w + 1][0],
+                          q.b[nt][2 * w + 1][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float sa = word_scale(kpa[n][g]), sb = word_scale(kpb[n][g]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s[n][nt][0] = fmaf(sa, acc[n][nt][0], s[n][nt][0]);
+          s[n][nt][1] = fmaf(sa, acc[n][nt][1], s[n][nt][1]);
+          s[n][nt][2] = fmaf(sb, acc[n][nt][2], s[n][nt][2]);
+          s[n][nt][3] = fmaf(sb, acc[n][nt][3], s[n][nt][3]);
+        }
       }
     }
-    const uint32_t lo = __byte_perm(mw, 0, 0x1010), lo8 = __byte_perm(mw8, 0, 0x1010);
-    const uint32_t a[4] = {lo, lo8, lo, lo8};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      mma_16816(s[nt], a, q.sums[nt][0], q.sums[nt][1]);
-    }
   }
+
+  uint32_t vpa[2][kGroups], vpb[2][kGroups];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    float acc[NT][4];
+  for (int n = 0; n < 2; ++n) {
+    load_words<kGroups, Rec::kOffParV>(at.par + rec[n], vpa[n]);
+    load_words<kGroups, Rec::kOffParV + 2 * Rec::kParRow>(at.par + rec[n], vpb[n]);
+  }
+  if (min(valid[0], valid[1]) < kBS) {
+    // Slots past the end may hold anything: no score, no parameters.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-    for (int ws = 0; ws < G / 32; ++ws) {
-      const int w = g * (G / 32) + ws;
-      const uint32_t xa = ka[w], xb = kb[w], ya = xa >> 8, yb = xb >> 8;
+    for (int n = 0; n < 2; ++n) {
+      const bool dead = at.slot >= valid[n], dead8 = at.slot + 2 >= valid[n];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_16816_f16(acc[nt], codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb), q.b[nt][2 * w][0],
-                      q.b[nt][2 * w][1]);
-        mma_16816_f16(acc[nt], codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb), q.b[nt][2 * w + 1][0],
-                      q.b[nt][2 * w + 1][1]);
+        if (dead) s[n][nt][0] = s[n][nt][1] = -INFINITY;
+        if (dead8) s[n][nt][2] = s[n][nt][3] = -INFINITY;
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if (dead) vpa[n][g] = 0;
+        if (dead8) vpb[n][g] = 0;
       }
     }
-    const float sa = word_scale(kpa[g]), sb = word_scale(kpb[g]);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      s[nt][0] = fmaf(sa, acc[nt][0], s[nt][0]);
-      s[nt][1] = fmaf(sa, acc[nt][1], s[nt][1]);
-      s[nt][2] = fmaf(sb, acc[nt][2], s[nt][2]);
-      s[nt][3] = fmaf(sb, acc[nt][3], s[nt][3]);
-    }
   }
+
+  uint32_t big = 0;
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) big = max(big, max(vpa[n][g], vpb[n][g]));
+  bool move = big > st.cap;
+  float top[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[nt][e] *= q.back[nt][e & 1];
-
-  if (valid < kBS) {
-    // Slots past the end may hold anything: no score, no parameters.
-    const bool dead = slot >= valid, dead8 = slot + 2 >= valid;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (dead) s[nt][0] = s[nt][1] = -INFINITY;
-      if (dead8) s[nt][2] = s[nt][3] = -INFINITY;
+    for (int h = 0; h < 2; ++h) {
+      top[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+      move |= top[nt][h] > st.limit[nt][h];
     }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (dead) vpa[g] = 0;
-      if (dead8) vpb[g] = 0;
-    }
-  }
-
-  // --- stabilisers: rare, and the same for the whole warp
-  uint32_t big = max(vpa[0], vpb[0]);
-#pragma unroll
-  for (int g = 1; g < kGroups; ++g) big = max(big, max(vpa[g], vpb[g]));
-  bool move = big > st.cap;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    move |= fmaxf(s[nt][0], s[nt][2]) > st.m[nt][0] + kTau;
-    move |= fmaxf(s[nt][1], s[nt][3]) > st.m[nt][1] + kTau;
-  }
-  if (__any_sync(0xffffffffu, move)) {
-    big = __reduce_max_sync(0xffffffffu, big);
-    float turn = 1.f;
-    if (big > st.cap) {
-      // Scales of this exponent are below 2^(E - 126): 2^(133 - E) brings
-      // them under 2^7 (at most 2^100, so that p ne stays finite; scales
-      // under 2^-93 then lose bits).
-      const uint32_t E = min((big >> 23) & 0xffu, 254u);
-      const float ne = __uint_as_float(min(260u - E, 227u) << 23);
-      turn = st.cap ? ne / st.ne : 0.f;
-      st.ne = ne;
-      st.cap = ((E + 1) << 23) - 1;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = fmaxf(s[nt][h], s[nt][2 + h]);
-#pragma unroll
-        for (int o_ = 4; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o_));
-        const bool up = mx > st.m[nt][h] + kTau;
-        const float mn = up ? mx : st.m[nt][h];
-        f[h] = up ? ex2(st.m[nt][h] - mn) : 1.f;
-        st.m[nt][h] = mn;
-        st.l[nt][h] *= f[h];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) st.mins[nt][g][h] *= f[h];
-      }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        st.o[nt][i][0] *= f[0] * turn;
-        st.o[nt][i][1] *= f[1] * turn;
-        st.o[nt][i][2] *= f[0] * turn;
-        st.o[nt][i][3] *= f[1] * turn;
-      }
-    }
-  }
+  if (__any_sync(0xffffffffu, move)) st.move(top, q.back, big);
 
   // --- weights and O^T: rows = elements of V, columns = heads
-  uint32_t pw[NT][kGroups][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float p0 = ex2(s[nt][0] - st.m[nt][0]), p1 = ex2(s[nt][1] - st.m[nt][1]);
-    const float p2 = ex2(s[nt][2] - st.m[nt][0]), p3 = ex2(s[nt][3] - st.m[nt][1]);
-    st.l[nt][0] += p0 + p2;
-    st.l[nt][1] += p1 + p3;
-    const float n0 = p0 * st.ne, n1 = p1 * st.ne, n2 = p2 * st.ne, n3 = p3 * st.ne;
+  for (int n = 0; n < 2; ++n) {
+    uint32_t pw[NT][kGroups][2];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float sa = word_scale(vpa[g]), sb = word_scale(vpb[g]);
-      const float ma = word_min(vpa[g]), mb = word_min(vpb[g]);
-      st.mins[nt][g][0] = fmaf(p0, ma, fmaf(p2, mb, st.mins[nt][g][0]));
-      st.mins[nt][g][1] = fmaf(p1, ma, fmaf(p3, mb, st.mins[nt][g][1]));
-      pw[nt][g][0] = movmatrix_trans(pack_f16x2(n0 * sa, n1 * sa));
-      pw[nt][g][1] = movmatrix_trans(pack_f16x2(n2 * sb, n3 * sb));
+    for (int nt = 0; nt < NT; ++nt) {
+      const float p0 = ex2(fmaf(s[n][nt][0], q.back[nt][0], -st.stab[nt][0]));
+      const float p1 = ex2(fmaf(s[n][nt][1], q.back[nt][1], -st.stab[nt][1]));
+      const float p2 = ex2(fmaf(s[n][nt][2], q.back[nt][0], -st.stab[nt][0]));
+      const float p3 = ex2(fmaf(s[n][nt][3], q.back[nt][1], -st.stab[nt][1]));
+      st.l[nt][0] += p0 + p2;
+      st.l[nt][1] += p1 + p3;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float sa = word_scale(vpa[n][g]), sb = word_scale(vpb[n][g]);
+        const float ma = word_min(vpa[n][g]), mb = word_min(vpb[n][g]);
+        st.mins[nt][g][0] = fmaf(p0, ma, fmaf(p2, mb, st.mins[nt][g][0]));
+        st.mins[nt][g][1] = fmaf(p1, ma, fmaf(p3, mb, st.mins[nt][g][1]));
+        pw[nt][g][0] = movmatrix_trans(pack_f16x2(p0 * sa, p1 * sa));
+        pw[nt][g][1] = movmatrix_trans(pack_f16x2(p2 * sb, p3 * sb));
+      }
     }
-  }
+    uint32_t vw[4][kVW];
+    load_words<kVW, Rec::kOffV>(at.v0 + rec[n], vw[0]);
+    load_words<kVW, Rec::kOffV>(at.v1 + rec[n], vw[1]);
+    load_words<kVW, Rec::kOffV + 2 * Rec::kRow>(at.v0 + rec[n], vw[2]);
+    load_words<kVW, Rec::kOffV + 2 * Rec::kRow>(at.v1 + rec[n], vw[3]);
 #pragma unroll
-  for (int w = 0; w < kVW; ++w) {
+    for (int w = 0; w < kVW; ++w) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t sel = hf ? 0x7632u : 0x5410u;
-      const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel), y = __byte_perm(vw[2][w], vw[3][w], sel);
-      const uint32_t x8 = x >> 8, y8 = y >> 8;
-      const int i = 4 * w + 2 * hf;              // tiles i and i + 1 of 16 elements
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t sel = hf ? 0x7632u : 0x5410u;
+        const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel), y = __byte_perm(vw[2][w], vw[3][w], sel);
+        const uint32_t x8 = x >> 8, y8 = y >> 8;
+        const int i = 4 * w + 2 * hf;            // tiles i and i + 1 of 16 elements
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma_16816_f16(st.o[nt][i], codes_lo(x), codes_hi(x), codes_lo(y), codes_hi(y), pw[nt][16 * i / G][0],
-                      pw[nt][16 * i / G][1]);
-        mma_16816_f16(st.o[nt][i + 1], codes_lo(x8), codes_hi(x8), codes_lo(y8), codes_hi(y8),
-                      pw[nt][16 * (i + 1) / G][0], pw[nt][16 * (i + 1) / G][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816_f16(st.o[nt][i], codes_lo(x), codes_hi(x), codes_lo(y), codes_hi(y), pw[nt][16 * i / G][0],
+                        pw[nt][16 * i / G][1]);
+          mma_16816_f16(st.o[nt][i + 1], codes_lo(x8), codes_hi(x8), codes_lo(y8), codes_hi(y8),
+                        pw[nt][16 * (i + 1) / G][0], pw[nt][16 * (i + 1) / G][1]);
+        }
       }
     }
   }
@@ -527,140 +633,268 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
   DecKv4Shared* sh = reinterpret_cast<DecKv4Shared*>(smem + Cfg::kOffShared);
-  int* cache = reinterpret_cast<int*>(smem + Cfg::kOffCache);
+  int* cost = reinterpret_cast<int*>(smem + Cfg::kOffPlan);             // [kPlan + 1]
+  int* runs = cost + kPlan + 2;                                         // [kPlan + 1]
+  int* seq_blocks = runs + kPlan + 2;                                   // [kPlan]
   float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffMl);           // [warp][2][kRows]
   auto first_piece = [&](int w) { return reinterpret_cast<float*>(smem + Cfg::kOffFirst + w * Cfg::kPiece); };
   auto last_piece = [&](int w) { return reinterpret_cast<float*>(smem + w * Cfg::kRing); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    sh->bad = 0;
-    sh->last = 0;
+    sh->part_n[0] = sh->part_n[1] = 0;
     sh->abort = 0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) mbar_init(smem_addr(&sh->full[w][s]), 1);
-    fence_mbar_init();
+  }
+  if (lane < kStages) mbar_init(smem_addr(&sh->full[warp][lane]), 1);
+  if (lane == kStages) mbar_init(smem_addr(&sh->ready[warp]), 1);
+  fence_mbar_init();
+  if (tid == 0) {
+    // What the plan and the first loads will read, into L2 while the work
+    // before this kernel drains (hints only: nothing is read here).
+    auto prefetch_share = [&](const void* base, size_t bytes) {
+      const uintptr_t lo = (reinterpret_cast<uintptr_t>(base) + 15) & ~static_cast<uintptr_t>(15);
+      const uintptr_t hi = (reinterpret_cast<uintptr_t>(base) + bytes) & ~static_cast<uintptr_t>(15);
+      if (hi <= lo) return;
+      const size_t share = ((hi - lo) / gridDim.x + 16) & ~static_cast<size_t>(15);
+      const uintptr_t at = lo + share * blockIdx.x;
+      if (at < hi) bulk_prefetch_l2(reinterpret_cast<const void*>(at), static_cast<uint32_t>(min(share, static_cast<size_t>(hi - at))));
+    };
+    prefetch_share(p.seq_lens, static_cast<size_t>(p.num_seqs) * 4);
+    prefetch_share(p.block_table, static_cast<size_t>(p.num_seqs) * p.max_blocks * 4);
+    prefetch_share(p.q, static_cast<size_t>(p.num_seqs) * p.Hq * D * 2);
   }
   pdl_wait_primary();
 
   // ------------------------------------------------------------------ plan
+  Plan plan;
+  plan.cost = cost;
+  plan.runs = runs;
+  plan.blocks = seq_blocks;
+  plan.per = (p.num_seqs + kPlan - 1) / kPlan;
+  plan.entries = (p.num_seqs + plan.per - 1) / plan.per;
   {
-    long long sum = 0;
+    // Thread t sums entries [t E, (t + 1) E); warp scan, then the warps' sums.
+    constexpr int E = (kPlan + kThreads - 1) / kThreads;
+    const int each = (plan.entries + kThreads - 1) / kThreads;          // <= E
+    int ec[E], er[E], c = 0, r = 0;
     bool bad = false;
-    for (int b = tid; b < p.num_seqs; b += kThreads) {
-      const int L = p.seq_lens[b];
-      bad |= L < 0 || L > p.max_blocks * kBS;
-      const int blocks = ((L < 0 ? 0 : min(L, p.max_blocks * kBS)) + kBS - 1) / kBS;
-      if (b < kSeqCache) cache[b] = blocks;
-      if (blocks > 0) sum += static_cast<long long>(blocks + kRunCost) * p.Hkv;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      ec[i] = c;
+      er[i] = r;
+      const int e = tid * each + i;
+      if (i >= each || e >= plan.entries) continue;
+      for (int b = e * plan.per; b < min(p.num_seqs, (e + 1) * plan.per); ++b) {
+        const int L = p.seq_lens[b];
+        bad |= L < 0 || L > p.max_blocks * kBS;
+        const int blocks = ((L < 0 ? 0 : min(L, p.max_blocks * kBS)) + kBS - 1) / kBS;
+        if (plan.per == 1) seq_blocks[b] = blocks;
+        if (blocks > 0) {
+          c += (blocks + kRunCost) * p.Hkv;
+          r += p.Hkv;
+        }
+      }
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kDevBadSeqLen);
+    int cs = c, rs = r;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int cy = __shfl_up_sync(0xffffffffu, cs, o), ry = __shfl_up_sync(0xffffffffu, rs, o);
+      if (lane >= o) {
+        cs += cy;
+        rs += ry;
+      }
+    }
+    if (lane == 31) sh->scan[warp] = make_int2(cs, rs);
+    __syncthreads();
+    int c0 = cs - c, r0 = rs - r, total = 0, total_runs = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int2 v = sh->scan[w];
+      if (w < warp) {
+        c0 += v.x;
+        r0 += v.y;
+      }
+      total += v.x;
+      total_runs += v.y;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sh->part_sum[warp] = sum;
-    if (bad && blockIdx.x == 0) atomicOr(p.status, kDevBadSeqLen);
+    for (int i = 0; i < E; ++i) {
+      const int e = tid * each + i;
+      if (i >= each || e >= plan.entries) continue;
+      cost[e] = c0 + ec[i];
+      runs[e] = r0 + er[i];
+    }
+    if (tid == 0) {
+      cost[plan.entries] = total;
+      runs[plan.entries] = total_runs;
+    }
+    plan.total = total;
   }
   __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sh->part_sum[w];
   // Every share but the last of all holds at least one block (a share longer
   // than a run's start cost cannot lie inside it).
-  const long long shares = static_cast<long long>(gridDim.x) * kWarps;
-  const long long chunk = max(static_cast<long long>(kRunCost + 1), (total + shares - 1) / shares);
+  const int shares = static_cast<int>(gridDim.x) * kWarps;
+  const int chunk = max(kRunCost + 1, (plan.total - 1) / shares + 1);
   const long long mine = (static_cast<long long>(blockIdx.x) * kWarps + warp) * chunk;
 
   const WaitCtl wc{&sh->abort, p.status, p.timeout_ns};
   WarpMeta meta = {};
-  RunPos begin, end;
-  long long flat0 = 0, flat1 = 0;
-  begin.b = -1;
-  if (mine < total) {
-    locate(p, cache, mine, total, lane, begin, flat0);
-    locate(p, cache, mine + chunk, total, lane, end, flat1);
+  int blocks = 0;
+  Walk w;
+  RunPos end;
+  {
+    // Lane 0 finds where this warp's share begins, the other lanes where it
+    // ends.
+    RunPos at;
+    at.b = at.g = at.blk = at.nblk = at.cost = 0;
+    const long long x = mine + (lane > 0 ? chunk : 0);
+    const int flat = x < plan.total ? locate(p, plan, static_cast<int>(x), at)
+                                    : plan.total - runs[plan.entries] * kRunCost;
+    const int from = __shfl_sync(0xffffffffu, flat, 0);
+    blocks = __shfl_sync(0xffffffffu, flat, 1) - from;
+    auto give = [&](int v, int& begin, int& finish) {
+      begin = __shfl_sync(0xffffffffu, v, 0);
+      finish = __shfl_sync(0xffffffffu, v, 1);
+    };
+    give(at.b, w.at.b, end.b);
+    give(at.g, w.at.g, end.g);
+    give(at.blk, w.at.blk, end.blk);
+    give(at.nblk, w.at.nblk, end.nblk);
+    give(at.cost, w.at.cost, end.cost);
   }
-  const long long blocks = begin.b >= 0 ? flat1 - flat0 : 0;
 
   if (blocks > 0) {
-    meta.active = 1;
-    const uint32_t ring = smem_addr(smem + warp * Cfg::kRing);
-    Walk w;
-    w.at = begin;
+    uint8_t* ring = smem + warp * Cfg::kRing;
     w.left = blocks;
-    w.cache = cache;
-    // Lane j translates block j of every batch of 32, two batches ahead.
+    // The first run's queries are on their way while the table is read.
+    QueryRaw<D, NT> raw;
+    raw.load(p, w.at.b, w.at.g, lane);
+    // Lane j looks up block j of every batch of 32, two batches ahead, and
+    // leaves its record's address for the issuing lane (0: not in the pool).
+    // Returns the batch's mask of blocks that have a record.
     Walk ahead = w;
-    ahead.skip(p, lane);
-    auto fetch = [&](int& ph, int& g) {
-      ph = -1;
-      g = 0;
+    ahead.skip(p, plan, lane);
+    const uint8_t** src = reinterpret_cast<const uint8_t**>(smem + Cfg::kOffSrc) + warp * 64;
+    auto fetch = [&](int batch) {
+      const uint8_t* rec = nullptr;
       if (ahead.left > 0) {
-        g = ahead.at.g;
-        ph = p.block_table[static_cast<size_t>(ahead.at.b) * p.max_blocks + ahead.at.blk];
-      }
-      ahead.skip(p, 32);
-    };
-    int ph0, g0, ph1, g1;
-    fetch(ph0, g0);
-    fetch(ph1, g1);
-    const uint64_t policy = l2_policy_evict_first();
-    unsigned present = 0;            // bit s: stage s holds a record (its table entry was in the pool)
-    long long issued = 0;
-    int stage_in = 0;
-    auto issue = [&]() {
-      const int src = static_cast<int>(issued & 31);
-      bool ok = false;
-      if (lane == src) {
-        ok = static_cast<unsigned>(ph0) < static_cast<unsigned>(p.num_blocks);
-        const uint32_t bar = smem_addr(&sh->full[warp][stage_in]);
-        if (ok) {
-          mbar_arrive_expect_tx(bar, Rec::kBytes);
-          bulk_load_hint(ring + stage_in * Rec::kBytes,
-                         p.kv_cache + (static_cast<size_t>(ph0) * p.Hkv + g0) * Rec::kBytes, Rec::kBytes, bar, policy);
-        } else {
+        const int ph = p.block_table[static_cast<size_t>(ahead.at.b) * p.max_blocks + ahead.at.blk];
+        if (static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks))
+          rec = p.kv_cache + (static_cast<size_t>(ph) * p.Hkv + ahead.at.g) * Rec::kBytes;
+        else
           atomicOr(p.status, kDevBadBlock);      // outside the pool: that block is skipped
-          mbar_arrive(bar);
-        }
       }
-      const bool got = __any_sync(0xffffffffu, ok);
-      present = (present & ~(1u << stage_in)) | (got ? 1u << stage_in : 0u);
-      stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
-      if ((++issued & 31) == 0) {
-        ph0 = ph1;
-        g0 = g1;
-        fetch(ph1, g1);
-      }
+      ahead.skip(p, plan, 32);
+      src[(batch & 1) * 32 + lane] = rec;
+      return __ballot_sync(0xffffffffu, rec != nullptr);
     };
-    for (int s = 0; s < kStages && issued < blocks; ++s) issue();
+    const uint64_t policy = l2_policy_evict_first();
+    unsigned present = fetch(0);
+    const uint32_t ring_at = smem_addr(ring), bars = smem_addr(&sh->full[warp][0]);
+    // Block i of the share goes to stage i % kStages; blocks [0, taken +
+    // kStages) are issued.  (One lane.)
+    auto issue = [&](int i) {
+      const uint8_t* from = src[i & 63];
+      const uint32_t bar = bars + (i % kStages) * 8;
+      mbar_arrive_expect_tx(bar, from != nullptr ? Rec::kBytes : 0);
+      if (from != nullptr) bulk_load_hint(ring_at + (i % kStages) * Rec::kBytes, from, Rec::kBytes, bar, policy);
+    };
+    if (lane < min(blocks, kStages)) issue(lane);
+    unsigned next_present = blocks > 32 ? fetch(1) : 0u;
+    __syncwarp();
+    const LaneData<D, G> at(ring_at, lane);
+
+    // Runs that this CTA holds a part of: one that began before it and ends in
+    // it (kind 0), one that goes on behind it (kind 1).  Their counters are
+    // made ready now, long before they are counted on.
+    if (lane == 0) {
+      const long long cta_chunk = static_cast<long long>(chunk) * kWarps;
+      auto take_part = [&](int kind, const RunPos& run) {
+        const int first = run.cost + kRunCost;   // cost position of its block 0
+        const int cta0 = static_cast<int>(first / cta_chunk), cta1 = static_cast<int>((first + run.nblk - 1) / cta_chunk);
+        sh->part_cta0[kind] = cta0;
+        sh->part_n[kind] = cta1 - cta0 + 1;
+        ready_counter(p.arrive + cta0, p.epoch);
+      };
+      if (warp == 0 && w.at.blk > 0 && w.at.cost + kRunCost + w.at.nblk <= mine + cta_chunk) take_part(0, w.at);
+      if (warp == kWarps - 1 && end.blk > 0) take_part(1, end);
+    }
 
     QueryFrag<D, G, NT> q;
     RunState<D, G, NT> st;
-    int stage = 0;
-    uint32_t phase = 0;
+    int taken = 0;
     bool fail = false;
     while (w.left > 0 && !fail) {
       const int cnt = w.count();
-      const int L = kv4_seq_len(p, w.at.b);
-      load_queries<D, G, NT>(p, w.at.b, w.at.g, lane, q);
+      int valid = kv4_seq_len(p, w.at.b) - w.at.blk * kBS;      // tokens from this block on
+      if (taken > 0) raw.load(p, w.at.b, w.at.g, lane);
+      make_queries<D, G, NT>(p, raw, lane, q);
       st.reset();
-      for (int i = 0; i < cnt; ++i) {
-        if (!mbar_wait_warp(smem_addr(&sh->full[warp][stage]), phase, wc)) {
+      for (const int end = taken + cnt; taken < end;) {
+        const int stage = taken % kStages, stage1 = (taken + 1) % kStages;
+        const bool two = taken + 1 < end;
+        if (!wait_warp(bars + stage * 8, (taken / kStages) & 1, wc) ||
+            (two && !wait_warp(bars + stage1 * 8, ((taken + 1) / kStages) & 1, wc))) {
           fail = true;
           break;
         }
-        if ((present >> stage) & 1u)
-          take_block<D, G, NT>(ring + stage * Rec::kBytes, min(kBS, L - (w.at.blk + i) * kBS), lane, q, st);
-        __syncwarp();                            // every lane has read the stage
-        if (issued < blocks) issue();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+        // Without a second block the first one's record stands in, with no
+        // slot of it alive.
+        const uint32_t rec0 = static_cast<uint32_t>(stage * Rec::kBytes);
+        const uint32_t rec[2] = {rec0, two ? static_cast<uint32_t>(stage1 * Rec::kBytes) : rec0};
+        const int alive[2] = {(present >> (taken & 31)) & 1u ? valid : 0,
+                              two && ((taken & 31) == 31 ? next_present & 1u : (present >> ((taken + 1) & 31)) & 1u)
+                                  ? valid - kBS : 0};
+        take_blocks<D, G, NT>(at, rec, alive, q, st);
+        __syncwarp();                            // every lane has read the stages
+        const int n = two ? 2 : 1;
+        if (lane < n && taken + lane + kStages < blocks) issue(taken + lane + kStages);
+        valid -= n * kBS;
+        if (((taken + n) ^ taken) & 32) {        // (the issuer is less than a batch ahead)
+          present = next_present;
+          next_present = ((taken + n) & ~31) + 32 < blocks ? fetch(((taken + n) >> 5) + 1) : 0u;
+          __syncwarp();
         }
+        taken += n;
       }
       if (fail) break;
       st.finish();
       const bool has_start = w.at.blk == 0, has_end = w.at.blk + cnt == w.at.nblk;
       const int c = lane & 3, r = lane >> 2;
-      if (has_start && has_end) {
+      bool whole = has_start && has_end;
+      // A run that lies in two neighbouring warps' shares is finished by the
+      // one that holds its start, from the piece that the other one, to which
+      // it was the first thing to do, has left: with runs about as long as
+      // shares that is most of them, and at the CTA's end they would queue.
+      const int run0 = w.at.cost + kRunCost, run1 = run0 + w.at.nblk;
+      const bool to_previous = has_end && !has_start && warp > 0 && run0 >= mine - chunk;
+      if (has_start && !has_end && warp + 1 < kWarps && run1 <= mine + 2 * chunk) {
+        if (!wait_warp(smem_addr(&sh->ready[warp + 1]), 0, wc)) {
+          fail = true;
+          break;
+        }
+        const float* src = first_piece(warp + 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 v = ml[(warp + 1) * 2 * kRows + nt * 8 + 2 * c + h];
+            const float to = fmaxf(st.stab[nt][h], v.x);
+            const float f0 = ex2(st.stab[nt][h] - to), f1 = ex2(v.x - to);
+            st.stab[nt][h] = to;
+            st.l[nt][h] = st.l[nt][h] * f0 + v.y * f1;
+            const float* row = src + (nt * 8 + 2 * c + h) * Cfg::kPitch + r;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              st.o[nt][i][h] = st.o[nt][i][h] * f0 + row[16 * i] * f1;
+              st.o[nt][i][2 + h] = st.o[nt][i][2 + h] * f0 + row[16 * i + 8] * f1;
+            }
+          }
+        }
+        whole = true;
+      }
+      if (whole) {
         const size_t h0 = static_cast<size_t>(w.at.b) * p.Hq + static_cast<size_t>(w.at.g) * p.group;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -681,7 +915,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
             for (int h = 0; h < 2; ++h) {
               const int hd = nt * 8 + 2 * c + h;
               if (hd < p.group)
-                p.lse[h0 + hd] = st.l[nt][h] == 0.f ? -INFINITY : (st.m[nt][h] + __log2f(st.l[nt][h])) * kLn2;
+                p.lse[h0 + hd] = st.l[nt][h] == 0.f ? -INFINITY : (st.stab[nt][h] + __log2f(st.l[nt][h])) * kLn2;
             }
           }
         }
@@ -701,36 +935,38 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
               row[16 * i + 8] = st.o[nt][i][2 + h];
             }
             if (r == 0)
-              ml[(warp * 2 + (f ? 0 : 1)) * kRows + nt * 8 + 2 * c + h] = make_float2(st.m[nt][h], st.l[nt][h]);
+              ml[(warp * 2 + (f ? 0 : 1)) * kRows + nt * 8 + 2 * c + h] = make_float2(st.stab[nt][h], st.l[nt][h]);
           }
         }
-        if (f) {
+        if (to_previous) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh->ready[warp]));
+        } else if (f) {
           meta.f_valid = 1;
           meta.fb = w.at.b;
           meta.fg = w.at.g;
-          meta.fcost = w.at.cost;
         } else {
           meta.l_valid = 1;
           meta.l_start = has_start;
           meta.lb = w.at.b;
           meta.lg = w.at.g;
-          meta.lcost = w.at.cost;
         }
       }
-      w.next_run(p, cnt);
+      w.next_run(p, plan, cnt);
     }
     if (fail) {
       // Copies in flight must land before the CTA may exit.
       for (int s = 0; s < kStages; ++s) {
-        const long long fills = issued / kStages + (s < issued % kStages ? 1 : 0);
-        if (fills > 0) mbar_wait_warp_drain(smem_addr(&sh->full[warp][s]), static_cast<uint32_t>((fills - 1) & 1), wc);
+        const int issued = min(blocks, taken + kStages);
+        const int fills = issued / kStages + (s < issued % kStages ? 1 : 0);
+        if (fills > 0) mbar_wait_warp_drain(bars + s * 8, static_cast<uint32_t>((fills - 1) & 1), wc);
       }
     }
   }
   if (lane == 0) sh->meta[warp] = meta;
   // Sequences without tokens: O = 0, LSE = -inf.
-  for (long long b = static_cast<long long>(blockIdx.x) * kWarps + warp; b < p.num_seqs; b += shares) {
-    if (kv4_seq_blocks(p, cache, static_cast<int>(b)) != 0) continue;
+  for (int b = static_cast<int>(blockIdx.x) * kWarps + warp; b < p.num_seqs; b += shares) {
+    if (plan.seq_blocks(p, b) != 0) continue;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(b) * p.Hq * D);
     for (int i = lane; i < p.Hq * D / 2; i += 32) dst[i] = 0u;
     if (p.lse != nullptr)
@@ -738,47 +974,126 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
   }
   __syncthreads();
   pdl_launch_dependents();
-  if (sh->abort) return;
+  const bool parts_here[2] = {sh->part_n[0] > 0, sh->part_n[1] > 0};
+  auto arrive = [&]() {                          // warps 0 and 1, one lane: one arrival per part
+    if (lane == 0 && warp < 2 && parts_here[warp])
+      sh->last[warp] = count_ready(p.arrive + sh->part_cta0[warp], sh->part_n[warp]);
+  };
+  if (sh->abort) {
+    arrive();                                    // so that the counters are left at zero
+    return;
+  }
 
   // ------------------------------------------------- pieces of split runs
-  // Pieces of one run lie in consecutive warps: last pieces, then one first
-  // piece where the run ends.  A run that starts before this CTA or goes on
-  // behind it becomes one part per CTA.
-  const long long cta_chunk = chunk * kWarps;
-  for (int wi = 0; wi < kWarps; ++wi) {
-    const WarpMeta& mt = sh->meta[wi];
-    const bool tail = mt.l_valid && (wi == kWarps - 1 || !sh->meta[wi + 1].active);
-    for (int kind = 0; kind < 2; ++kind) {       // 0: a run that ends in warp wi; 1: the CTA's last run, going on
-      if (kind == 0 ? !mt.f_valid : !tail) continue;
-      int lo = wi;                               // first warp of the chain
-      bool started = kind == 1 && mt.l_start;
-      while (!started && lo > 0) {
-        --lo;
-        started = sh->meta[lo].l_start != 0;
+  // The pieces of a run lie in consecutive warps: last pieces, from the warp
+  // that holds its start (or the CTA's first), up to the first piece of the
+  // warp where it ends.  They are merged here; of a run that starts before
+  // this CTA (kind 0) or goes on behind it (kind 1) that leaves one part,
+  // which is published, and the CTA that arrives last at the run merges its
+  // parts.  Both merges are the same loop, over jobs: the code is then fetched
+  // once (cold, it took longer than its work).
+  unsigned ends, starts;
+  {
+    const bool in = lane < kWarps;
+    const WarpMeta& mt = sh->meta[in ? lane : 0];
+    ends = __ballot_sync(0xffffffffu, in && mt.f_valid);
+    starts = __ballot_sync(0xffffffffu, in && mt.l_valid && mt.l_start);
+  }
+  constexpr int W = D / 4;                       // lanes of a head's row, four columns each
+  const int sub = lane / W, col = (lane % W) * 4;
+  constexpr unsigned kGoesOn = 1u << 31;
+  unsigned todo = ends | (parts_here[1] ? kGoesOn : 0u);
+  for (bool parts = false;; parts = true) {
+    for (; todo != 0; todo &= todo - 1) {
+      const int bit = __ffs(todo) - 1;
+      const int kind = bit == 31 ? 1 : 0;
+      const int wi = kind ? kWarps - 1 : bit;
+      const WarpMeta& mt = sh->meta[wi];
+      const size_t h0 = static_cast<size_t>(kind ? mt.lb : mt.fb) * p.Hq + static_cast<size_t>(kind ? mt.lg : mt.fg) * p.group;
+      // Piece x < n - 1 lies x steps from the first, piece n - 1 by itself.
+      const float *o0, *o1;
+      const float2 *m0, *m1;
+      int n, o_step, m_step, pitch;
+      bool whole = true;
+      if (!parts) {
+        const unsigned before = starts & (kind ? (2u << wi) - 1 : (1u << wi) - 1);
+        const int lo = before ? 31 - __clz(before) : 0;
+        whole = kind == 0 && before != 0;
+        n = wi - lo + 1;
+        o0 = last_piece(lo);
+        o_step = Cfg::kRing / 4;
+        o1 = kind ? last_piece(wi) : first_piece(wi);
+        m0 = ml + (lo * 2 + 1) * kRows;
+        m_step = 2 * kRows;
+        m1 = ml + (wi * 2 + kind) * kRows;
+        pitch = Cfg::kPitch;
+      } else {
+        // Part x is in CTA cta0 + x's slot 1, the run's end in slot 0.
+        const int cta0 = sh->part_cta0[kind];
+        n = sh->part_n[kind];
+        const size_t s0 = (2 * static_cast<size_t>(cta0) + 1) * p.group, s1 = 2 * static_cast<size_t>(cta0 + n - 1) * p.group;
+        o0 = p.ws_o + s0 * D;
+        o1 = p.ws_o + s1 * D;
+        o_step = 2 * p.group * D;
+        m0 = reinterpret_cast<const float2*>(p.ws_ml) + s0;
+        m1 = reinterpret_cast<const float2*>(p.ws_ml) + s1;
+        m_step = 2 * p.group;
+        pitch = D;
       }
-      const int rb = kind == 0 ? mt.fb : mt.lb, rg = kind == 0 ? mt.fg : mt.lg;
-      const long long rcost = (kind == 0 ? mt.fcost : mt.lcost) + kRunCost;
-      const bool whole = kind == 0 && started;
-      const size_t h0 = static_cast<size_t>(rb) * p.Hq + static_cast<size_t>(rg) * p.group;
-      const int ws_slot = 2 * static_cast<int>(blockIdx.x) + kind;
-      auto piece_of = [&](int w) { return kind == 0 && w == wi ? first_piece(w) : last_piece(w); };
-      auto ml_of = [&](int w) { return ml + (w * 2 + (kind == 0 && w == wi ? 0 : 1)) * kRows; };
-      for (int item = tid; item < p.group * (D / 4); item += kThreads) {
-        const int h = item / (D / 4), col = (item % (D / 4)) * 4;
-        float M = -INFINITY;
-        for (int w2 = lo; w2 <= wi; ++w2) M = fmaxf(M, ml_of(w2)[h].x);
+      for (int hb = warp * (32 / W); hb < p.group; hb += kWarps * (32 / W)) {
+        const bool live = hb + sub < p.group;
+        const int h = live ? hb + sub : hb;
+        float M = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        for (int w2 = lo; w2 <= wi; ++w2) {
-          const float2 v = ml_of(w2)[h];
-          const float wt = v.x == -INFINITY ? (v.y == 0.f ? 0.f : v.y) : ex2(v.x - M);
-          const float4 x = *reinterpret_cast<const float4*>(piece_of(w2) + h * Cfg::kPitch + col);
-          l += wt * v.y;
-          acc.x += wt * x.x;
-          acc.y += wt * x.y;
-          acc.z += wt * x.z;
-          acc.w += wt * x.w;
+        // 16 pieces at a time: their rows and their (stabiliser, sum) pairs are
+        // all asked for before any is used (a part published by another CTA
+        // takes over a microsecond to come), lane x of a row weighs piece x.
+        for (int x0 = 0; x0 < n; x0 += 16) {
+          const int m = min(16, n - x0);         // the same for all lanes
+          float4 y[16];
+#pragma unroll
+          for (int q4 = 0; q4 < 16; q4 += 4) {
+            if (q4 >= m) break;
+#pragma unroll
+            for (int i = q4; i < q4 + 4; ++i) {
+              y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (i < m)
+                y[i] = ld_shared_or_l2(reinterpret_cast<const float4*>(
+                    (x0 + i == n - 1 ? o1 : o0 + static_cast<size_t>(x0 + i) * o_step) + h * pitch + col));
+            }
+          }
+          const int x = x0 + lane % 16;
+          float2 v = make_float2(-INFINITY, 0.f);
+          if (x < n) v = ld_shared_or_l2(x == n - 1 ? m1 + h : m0 + x * m_step + h);
+          float mx = v.x;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx = fmaxf(M, mx);
+          const float turn = ex2(M - mx);
+          const float wt = x < n ? ex2(v.x - mx) : 0.f;
+          float sum = wt * v.y;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          l = l * turn + sum;
+          M = mx;
+          acc.x *= turn;
+          acc.y *= turn;
+          acc.z *= turn;
+          acc.w *= turn;
+#pragma unroll
+          for (int q4 = 0; q4 < 16; q4 += 4) {
+            if (q4 >= m) break;
+#pragma unroll
+            for (int i = q4; i < q4 + 4; ++i) {
+              const float w_i = __shfl_sync(0xffffffffu, wt, sub * W + i);
+              acc.x += w_i * y[i].x;
+              acc.y += w_i * y[i].y;
+              acc.z += w_i * y[i].z;
+              acc.w += w_i * y[i].w;
+            }
+          }
         }
+        if (!live) continue;
         if (whole) {
           const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
           uint2 pk;
@@ -787,54 +1102,18 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
           *reinterpret_cast<uint2*>(p.o + (h0 + h) * D + col) = pk;
           if (col == 0 && p.lse != nullptr) p.lse[h0 + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
         } else {
-          *reinterpret_cast<float4*>(p.ws_o + (static_cast<size_t>(ws_slot) * p.group + h) * D + col) = acc;
-          if (col == 0)
-            *reinterpret_cast<float2*>(p.ws_ml + (static_cast<size_t>(ws_slot) * p.group + h) * 2) = make_float2(M, l);
+          const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + kind) * p.group + h;
+          *reinterpret_cast<float4*>(p.ws_o + slot * D + col) = acc;
+          if (col == 0) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(M, l);
         }
       }
-      if (whole) continue;
-      const int per_run = kv4_seq_blocks(p, cache, rb);
-      const int cta0 = static_cast<int>(rcost / cta_chunk);
-      const int cta1 = static_cast<int>((rcost + per_run - 1) / cta_chunk);
-      const int nparts = cta1 - cta0 + 1;
-      // Publish: every thread's part visible to the GPU, then one arrival.
-      __threadfence();
-      __syncthreads();
-      if (tid == 0)
-        sh->last = count_arrival(p.arrive + cta0, p.epoch, static_cast<int>(blockIdx.x) - cta0, nparts, p.status);
-      __syncthreads();
-      const bool last = sh->last != 0;
-      if (last) {
-        __threadfence();
-        // Part x is in CTA x's slot 1, the run's end in slot 0.
-        auto slot_of = [&](int x) { return static_cast<size_t>(2 * x + (x == cta1 ? 0 : 1)) * p.group; };
-        for (int item = tid; item < p.group * (D / 4); item += kThreads) {
-          const int h = item / (D / 4), col = (item % (D / 4)) * 4;
-          float M = -INFINITY;
-          for (int x = cta0; x <= cta1; ++x)
-            M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(x) + h).x);
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float l = 0.f;
-          for (int x = cta0; x <= cta1; ++x) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(x) + h);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (slot_of(x) + h) * D + col));
-            const float wt = v.x == -INFINITY ? (v.y == 0.f ? 0.f : v.y) : ex2(v.x - M);
-            l += wt * v.y;
-            acc.x += wt * y.x;
-            acc.y += wt * y.y;
-            acc.z += wt * y.z;
-            acc.w += wt * y.w;
-          }
-          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-          uint2 pk;
-          pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-          pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2*>(p.o + (h0 + h) * D + col) = pk;
-          if (col == 0 && p.lse != nullptr) p.lse[h0 + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
-        }
-      }
-      __syncthreads();                           // sh->last is free again
     }
+    if (parts || !(parts_here[0] || parts_here[1])) break;   // the same for the whole CTA
+    __syncthreads();
+    arrive();
+    __syncthreads();
+    // The run that ended here and began before this CTA is the first that ended.
+    todo = (parts_here[0] && sh->last[0] ? ends & (0u - ends) : 0u) | (parts_here[1] && sh->last[1] ? kGoesOn : 0u);
   }
 }
 

@@ -11,11 +11,25 @@ import torch
 
 import exact_attention_47_gb300 as attn
 from exact_attention_47_gb300 import _binding
-from exact_attention_47_gb300._binding import _Heads, _Rope
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 5
 BF, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+class _Heads(ctypes.Structure):
+    """attn_heads_t"""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("heads", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    """attn_rope_t"""
+
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("axes", ctypes.c_int), ("stride_axis", ctypes.c_int64),
+                ("stride_batch", ctypes.c_int64), ("pair_axis", ctypes.c_char_p)]
 
 
 @pytest.fixture(scope="module")
@@ -33,6 +47,17 @@ def test_declared_and_exported(lib):
                      "kv4_read_paged", "attn_decode_paged_kv4", "attn_decode_paged_kv4_workspace_size"}
     for n in names:
         assert hasattr(lib, n) and n in _binding._SIGS
+
+
+def test_packed_structures_match_the_header():
+    """The binding packs the two structures as bytes: the same size (but for
+    the tail padding) and fields as the C ones."""
+    h = _Heads.from_buffer_copy(_binding._HEADS.pack(0x10, 1, 2, 3, 4) + bytes(4))
+    assert (h.data, h.stride_batch, h.stride_token, h.stride_head, h.heads) == (0x10, 1, 2, 3, 4)
+    assert _binding._ROPE.size == ctypes.sizeof(_Rope)
+    r = _Rope.from_buffer_copy(_binding._ROPE.pack(0x20, 64, 1, 0x30, 3, 5, 6, 0))
+    assert (r.inv_freq, r.rot, r.interleaved, r.positions, r.axes) == (0x20, 64, 1, 0x30, 3)
+    assert (r.stride_axis, r.stride_batch, r.pair_axis) == (5, 6, None)
 
 
 def heads(at, H=2, N=16, d=64, batch=None, token=None, head=None):
