@@ -9,6 +9,7 @@ built, every call raises ``RuntimeError``.
 """
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -503,8 +504,11 @@ def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, 
             continue
         if out is None:
             out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
-        ho.append(_heads(name, out, dev, 4))
-        _need_shape(name, out, x.shape)
+            H = x.shape[1]
+            ho.append(_HEADS.pack(out.data_ptr(), H * N * d, d, N * d, H))
+        else:
+            ho.append(_heads(name, out, dev, 4))
+            _need_shape(name, out, x.shape)
         outs.append(out)
     _call(func, dev, hq, hk, ho[0], ho[1], rope, B, N, d, _stream_handle(stream, dev))
     del keep                                       # the library has read the axis table by now
@@ -603,6 +607,7 @@ def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions
     return q_out
 
 
+@functools.lru_cache(maxsize=None)
 def kv4_record_bytes(d, group):
     """Bytes of one (block, KV head) record of a 4-bit cache."""
     n = int(load_library().kv4_record_bytes(int(d), int(group)))
@@ -612,10 +617,13 @@ def kv4_record_bytes(d, group):
 
 
 def _need_kv4(kv_cache, d, group, device):
+    """(num_blocks, Hkv) of a 4-bit cache."""
     _need_cuda("kv_cache", kv_cache, torch.uint8, device)
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != kv4_record_bytes(d, group):
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[2] != kv4_record_bytes(d, group):
         raise ValueError("kv_cache must be [num_blocks, Hkv, %d] for d %d and group %d, got %s"
-                         % (kv4_record_bytes(d, group), d, group, tuple(kv_cache.shape)))
+                         % (kv4_record_bytes(d, group), d, group, tuple(shape)))
+    return shape[0], shape[1]
 
 
 def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, group, inv_freq=None,
@@ -626,8 +634,7 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
     elements of a key or value.  Returns q_out (or None without q)."""
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
-    _need_kv4(kv_cache, d, group, dev)
-    nb, Hkv, _ = kv_cache.shape
+    nb, Hkv = _need_kv4(kv_cache, d, group, dev)
     if Hkv != k.shape[1]:
         raise ValueError("kv_cache must have k's heads")
     _call("rope_append_paged_kv4", dev, hq, hk, hv, ho, rope[0], _ptr(kv_cache), group,
@@ -642,10 +649,9 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
     sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16."""
     if not isinstance(seq_ids, torch.Tensor) or seq_ids.dim() != 1:
         raise ValueError("seq_ids must be a [T] tensor")
-    _need_kv4(kv_cache, d, group, None)
+    nb, Hkv = _need_kv4(kv_cache, d, group, None)
     dev, T = kv_cache.device, seq_ids.shape[0]
     _token_map(block_table, seq_ids, positions, T, dev)
-    nb, Hkv, _ = kv_cache.shape
     k = _output("k", k, (T, Hkv, d), torch.bfloat16, dev)
     v = _output("v", v, (T, Hkv, d), torch.bfloat16, dev)
     _call("kv4_read_paged", dev, _ptr(kv_cache), group, _ptr(block_table), _ptr(seq_ids), _ptr(positions), _ptr(k),
@@ -653,6 +659,7 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_decode_paged_kv4_workspace_size(num_seqs, Hq, Hkv, d):
     return int(load_library().attn_decode_paged_kv4_workspace_size(num_seqs, Hq, Hkv, d))
 
@@ -670,11 +677,11 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
     if q.dim() != 3:
         raise ValueError("q must be [S,Hq,d]")
     S, Hq, d = q.shape
-    _need_kv4(kv_cache, d, group, dev)
-    nb, Hkv, _ = kv_cache.shape
+    nb, Hkv = _need_kv4(kv_cache, d, group, dev)
     _need_cuda("block_table", block_table, torch.int32, dev)
     _need_cuda("seq_lens", seq_lens, torch.int32, dev)
-    if block_table.dim() != 2 or block_table.shape[0] != S:
+    table_shape = block_table.shape
+    if len(table_shape) != 2 or table_shape[0] != S:
         raise ValueError("block_table must be [S, max_blocks]")
     _need_shape("seq_lens", seq_lens, (S,))
     o = _output("o", o, (S, Hq, d), torch.bfloat16, dev)
@@ -684,7 +691,7 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
         scale = d ** -0.5
     workspace = _workspace("workspace", workspace, attn_decode_paged_kv4_workspace_size(S, Hq, Hkv, d), dev)
     _call("attn_decode_paged_kv4", dev, _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), S, Hq, Hkv, d,
-          group, BLOCK_SIZE, block_table.shape[1], nb, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+          group, BLOCK_SIZE, table_shape[1], nb, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
     return o, lse
 

@@ -1359,7 +1359,9 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
   a.max_blocks = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.sms = dev->sms;
+  a.device = dev->index;
   a.epoch = next_decode_epoch();
+  a.early_plan = g_decode_early_plan.load() > 0 ? 1 : 0;
   a.scale = scale;
   a.status = dev->status;
   a.timeout_ns = g_timeout_ns;

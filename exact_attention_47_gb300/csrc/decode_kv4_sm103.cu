@@ -32,6 +32,8 @@
 // holds whole is written by it; pieces of a run go to shared memory, are merged
 // per CTA, and if the run reaches into other CTAs the merged part is published
 // and the CTA that arrives last merges the parts.
+#include <atomic>
+
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -42,10 +44,6 @@
 namespace attn47 {
 namespace {
 
-#ifndef KV4_WARPS
-#define KV4_WARPS 8
-#define KV4_STAGES 4
-#endif
 constexpr int kBS = kKv4Slots;
 // CTAs a launch may have (one per SM); the workspace has room for this many.
 constexpr int kMaxCtas = 256;
@@ -63,10 +61,12 @@ template <int D, int G, int NT>
 struct DecKv4Cfg {
   using Rec = Kv4Layout<D, G>;
   // 12 warps with 168 registers each, or 8 with 255 when two column tiles
-  // double the accumulators.
-  static constexpr int kWarps = NT == 1 ? KV4_WARPS : 8;
+  // double the accumulators.  (With one tile, per block of a long context: 12
+  // warps stream 6.1 TB/s, 8 warps 5.6, 16 warps spill; 10, uneven over the
+  // four schedulers, lose to 8.)
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = D == 128 ? (NT == 1 ? KV4_STAGES : 4) : 8;   // a power of two
+  static constexpr int kStages = D == 128 ? 4 : 8;           // a power of two
   static constexpr int kRows = NT * 8;                       // head rows of a piece
   static constexpr int kPitch = D + 4;                       // floats; conflict-free stores
   static constexpr int kPiece = kRows * kPitch * 4;
@@ -109,6 +109,7 @@ struct DecKv4Params {
   unsigned long long* arrive;      // [kMaxCtas]
   int num_seqs, Hq, Hkv, group, max_blocks, num_blocks;
   unsigned int epoch;
+  int early_plan;                  // plan before waiting for the preceding kernel
   float scale_log2;
   unsigned int* status;
   unsigned long long timeout_ns;
@@ -543,6 +544,14 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
     load_words<kGroups, Rec::kOffParV>(at.par + rec[n], vpa[n]);
     load_words<kGroups, Rec::kOffParV + 2 * Rec::kParRow>(at.par + rec[n], vpb[n]);
   }
+  uint32_t vw[2][4][kVW];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    load_words<kVW, Rec::kOffV>(at.v0 + rec[n], vw[n][0]);
+    load_words<kVW, Rec::kOffV>(at.v1 + rec[n], vw[n][1]);
+    load_words<kVW, Rec::kOffV + 2 * Rec::kRow>(at.v0 + rec[n], vw[n][2]);
+    load_words<kVW, Rec::kOffV + 2 * Rec::kRow>(at.v1 + rec[n], vw[n][3]);
+  }
   if (min(valid[0], valid[1]) < kBS) {
     // Slots past the end may hold anything: no score, no parameters.
 #pragma unroll
@@ -599,17 +608,12 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
         pw[nt][g][1] = movmatrix_trans(pack_f16x2(p2 * sb, p3 * sb));
       }
     }
-    uint32_t vw[4][kVW];
-    load_words<kVW, Rec::kOffV>(at.v0 + rec[n], vw[0]);
-    load_words<kVW, Rec::kOffV>(at.v1 + rec[n], vw[1]);
-    load_words<kVW, Rec::kOffV + 2 * Rec::kRow>(at.v0 + rec[n], vw[2]);
-    load_words<kVW, Rec::kOffV + 2 * Rec::kRow>(at.v1 + rec[n], vw[3]);
 #pragma unroll
     for (int w = 0; w < kVW; ++w) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint32_t sel = hf ? 0x7632u : 0x5410u;
-        const uint32_t x = __byte_perm(vw[0][w], vw[1][w], sel), y = __byte_perm(vw[2][w], vw[3][w], sel);
+        const uint32_t x = __byte_perm(vw[n][0][w], vw[n][1][w], sel), y = __byte_perm(vw[n][2][w], vw[n][3][w], sel);
         const uint32_t x8 = x >> 8, y8 = y >> 8;
         const int i = 4 * w + 2 * hf;            // tiles i and i + 1 of 16 elements
 #pragma unroll
@@ -663,7 +667,10 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     prefetch_share(p.block_table, static_cast<size_t>(p.num_seqs) * p.max_blocks * 4);
     prefetch_share(p.q, static_cast<size_t>(p.num_seqs) * p.Hq * D * 2);
   }
-  pdl_wait_primary();
+  // With the early plan, seq_lens and the block table are read before the
+  // preceding kernel has finished; the queries, the cache and everything that
+  // is written come after the wait further down.
+  if (!p.early_plan) pdl_wait_primary();
 
   // ------------------------------------------------------------------ plan
   Plan plan;
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     w.left = blocks;
     // The first run's queries are on their way while the table is read.
     QueryRaw<D, NT> raw;
-    raw.load(p, w.at.b, w.at.g, lane);
+    if (!p.early_plan) raw.load(p, w.at.b, w.at.g, lane);
     // Lane j looks up block j of every batch of 32, two batches ahead, and
     // leaves its record's address for the issuing lane (0: not in the pool).
     // Returns the batch's mask of blocks that have a record.
@@ -791,6 +798,10 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     };
     const uint64_t policy = l2_policy_evict_first();
     unsigned present = fetch(0);
+    if (p.early_plan) {
+      pdl_wait_primary();
+      raw.load(p, w.at.b, w.at.g, lane);
+    }
     const uint32_t ring_at = smem_addr(ring), bars = smem_addr(&sh->full[warp][0]);
     // Block i of the share goes to stage i % kStages; blocks [0, taken +
     // kStages) are issued.  (One lane.)
@@ -963,6 +974,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       }
     }
   }
+  if (p.early_plan) pdl_wait_primary();          // (warps without work)
   if (lane == 0) sh->meta[warp] = meta;
   // Sequences without tokens: O = 0, LSE = -inf.
   for (int b = static_cast<int>(blockIdx.x) * kWarps + warp; b < p.num_seqs; b += shares) {
@@ -1121,8 +1133,15 @@ template <int D, int G, int NT>
 cudaError_t launch_t(const DecKv4Launch& a) {
   using Cfg = DecKv4Cfg<D, G, NT>;
   auto kern = attn_decode_kv4_kernel<D, G, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-  if (e != cudaSuccess) return e;
+  // The attribute belongs to the device's copy of the kernel: set once for each
+  // (the host's time bounds a small decode).
+  static std::atomic<unsigned long long> allowed{0};
+  const unsigned long long bit = 1ull << a.device;
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_release);
+  }
   DecKv4Params p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.kv_cache = static_cast<const uint8_t*>(a.kv_cache);
@@ -1140,6 +1159,7 @@ cudaError_t launch_t(const DecKv4Launch& a) {
   p.ws_o = reinterpret_cast<float*>(p.arrive + kMaxCtas);
   p.ws_ml = p.ws_o + static_cast<size_t>(2) * kMaxCtas * p.group * D;
   p.epoch = a.epoch;
+  p.early_plan = a.early_plan;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;

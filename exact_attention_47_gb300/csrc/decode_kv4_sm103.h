@@ -15,8 +15,9 @@ struct DecKv4Launch {
   float* lse;                  // [S, Hq] fp32 or nullptr
   void* workspace;
   int num_seqs, Hq, Hkv, d, group, max_blocks, num_blocks;
-  int sms;
+  int sms, device;
   unsigned int epoch;          // tag of this call's arrival counters (never 0)
+  int early_plan;              // >= 1: see attn_set_decode_early_plan
   float scale;
   unsigned int* status;
   unsigned long long timeout_ns;

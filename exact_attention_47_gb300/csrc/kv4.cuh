@@ -45,33 +45,48 @@ struct Kv4Layout {
   static_assert(kBytes % 128 == 0, "records are copied whole, 16-byte aligned");
 };
 
-// One step of a transposition of 4-bit cells over lanes: with lane bit `s`
-// and cell blocks of `s` cells, swaps the off-diagonal blocks.
-template <int S>
-__device__ __forceinline__ uint32_t nibble_swap(uint32_t x, int lane) {
-  constexpr uint32_t lo = S == 4 ? 0x0000ffffu : S == 2 ? 0x00ff00ffu : 0x0f0f0f0fu;
-  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, S);
-  return (lane & S) ? (x & ~lo) | ((y >> (4 * S)) & lo) : (x & lo) | ((y & lo) << (4 * S));
-}
-
-// K rows: lane j of the D/8 lanes of a row holds elements 8 j .. 8 j + 7 with
-// element 2 c + h in nibble c + 4 h; afterwards it holds the row's word
-// (D/32) (j % 4) + j / 4.  The steps are their own inverse.
-__device__ __forceinline__ uint32_t kv4_k_transpose(uint32_t x, int lane) {
-  x = nibble_swap<2>(x, lane);
-  return nibble_swap<1>(x, lane);
-}
+// Rows between lanes and memory.  A row is held by D/16 lanes, 16 neighbouring
+// elements each, as two words of eight 4-bit cells (the 8-element pieces 2 j
+// and 2 j + 1 of lane j).  In memory, cell p of a word belongs to piece p of a
+// block of pieces, so packing a row is a transposition of cells over pieces:
+// piece bit by piece bit the off-diagonal blocks change places, bit 0 between
+// the lane's two words, the others between lanes, where blocks of 8 and 16
+// bits move with one byte permutation whose selector depends on the lane.
+struct CellTranspose {
+  uint32_t sel8, sel16;
+  __device__ __forceinline__ explicit CellTranspose(int lane) {
+    sel8 = (lane & 1) ? 0x3715u : 0x6240u;
+    sel16 = (lane & 2) ? 0x3276u : 0x5410u;
+  }
+  __device__ __forceinline__ void bit0(uint32_t (&x)[2]) const {
+    const uint32_t a = x[0], b = x[1];
+    x[0] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+    x[1] = (b & 0xf0f0f0f0u) | ((a >> 4) & 0x0f0f0f0fu);
+  }
+  __device__ __forceinline__ uint32_t bit1(uint32_t x) const {
+    return __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 1), sel8);
+  }
+  __device__ __forceinline__ uint32_t bit2(uint32_t x) const {
+    return __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 2), sel16);
+  }
+  // Keys: cell c + 4 h of a piece's word is its element 2 c + h; afterwards
+  // piece j's word is the row's word kv4_k_word(j).  Its own inverse.
+  __device__ __forceinline__ void key(uint32_t (&x)[2]) const {
+    bit0(x);
+    x[0] = bit1(x[0]);
+    x[1] = bit1(x[1]);
+  }
+  // Values: cell e is element e; afterwards piece j's word is the row's word
+  // kv4_v_word(j).  Its own inverse.
+  __device__ __forceinline__ void value(uint32_t (&x)[2]) const {
+    bit0(x);
+    x[0] = bit2(bit1(x[0]));
+    x[1] = bit2(bit1(x[1]));
+  }
+};
 template <int D>
-__device__ __forceinline__ int kv4_k_word(int j) { return (D / 32) * (j & 3) + (j >> 2); }
-
-// V rows: lane j holds elements 8 j .. 8 j + 7 in nibbles 0 .. 7; afterwards
-// the row's word (D/64) (j % 8) + j / 8.  The steps are their own inverse.
-__device__ __forceinline__ uint32_t kv4_v_transpose(uint32_t x, int lane) {
-  x = nibble_swap<4>(x, lane);
-  x = nibble_swap<2>(x, lane);
-  return nibble_swap<1>(x, lane);
-}
+__device__ __forceinline__ int kv4_k_word(int piece) { return (D / 32) * (piece & 3) + (piece >> 2); }
 template <int D>
-__device__ __forceinline__ int kv4_v_word(int j) { return (D / 64) * (j & 7) + (j >> 3); }
+__device__ __forceinline__ int kv4_v_word(int piece) { return (D / 64) * (piece & 7) + (piece >> 3); }
 
 }  // namespace attn47

@@ -13,9 +13,8 @@
 // with |f_p| above that).
 //
 // All of it is data movement with a little arithmetic: a row (one head of
-// one token) is held by d/8 lanes, one 16-byte piece each, so a warp moves
-// 512 bytes a step and keeps several loads in flight; the partner elements of
-// a half-split pair come from another lane by shuffle.  A warp takes one
+// one token) is held by d/16 lanes, both members of eight pairs each, so a
+// warp moves 1 KB a step and keeps several loads in flight.  A warp takes one
 // token's rows (all of them when there are many tokens, a slice when there are
 // few), so the angles of a token are formed once for all its heads, each by one
 // lane of the warp.
@@ -32,6 +31,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlots = kKv4Slots;
 enum Mode { kRotate, kAppend, kAppendKv4 };
+// Resident CTAs per SM (the register budget follows), and so the size of the
+// persistent grids: one CTA more than fits would be a second wave.
+constexpr int ctas_per_sm(int mode) { return mode == kAppendKv4 ? 3 : 4; }
+constexpr int kReadCtas = 6;
 
 struct RowPtr {
   const __nv_bfloat16* data;
@@ -104,6 +107,7 @@ __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
   return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                     pack_bf16x2(y[6], y[7]));
 }
+// NaN-propagating extremes, of two and (sm_100+) of three.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -114,23 +118,41 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
-// 4-bit codes of this lane's 8 elements and the parameter word of their
-// group (the G/8 lanes of a group agree on it).  low = bf16(min), scale =
-// bf16((max - low) / 15), code = (x - low) / scale rounded to even, clamped.
-// A scale below the smallest normal number counts as 0 (a constant group:
-// every value reads back as low); a group whose range is not finite gets NaN
-// parameters, so that it reads back as NaN.
+// 1.5 2^23: x + kRound is x rounded to a whole number (half to even), whose
+// value lies in the low bits of the sum.
+constexpr float kRound = 12582912.f;
+constexpr uint32_t kRoundBits = 0x4b400000u;
+
+// 4-bit codes of this lane's 16 elements, as kRoundBits + code, and the
+// parameter word of their group (the G/16 lanes of a group agree on it).  low =
+// bf16(min), scale = bf16((max - low) / 15), code = (x - low) / scale rounded
+// to even, clamped.  A scale below the smallest normal number counts as 0 (a
+// constant group: every value reads back as low); a group whose range is not
+// finite gets NaN parameters, so that it reads back as NaN.
 template <int G>
-__device__ __forceinline__ uint32_t quantise8(const float (&y)[8], int (&code)[8]) {
-  float lo = y[0], hi = y[0];
+__device__ __forceinline__ uint32_t quantise16(const float (&y)[2][8], uint32_t (&code)[2][8]) {
+  float lo = y[0][0], hi = lo;
 #pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    lo = min_nan(lo, y[e]);
-    hi = max_nan(hi, y[e]);
+  for (int e = 1; e < 15; e += 2) {
+    const float a = y[e / 8][e % 8], b = y[(e + 1) / 8][(e + 1) % 8];
+    lo = min_nan(lo, a, b);
+    hi = max_nan(hi, a, b);
   }
+  lo = min_nan(lo, y[1][7]);
+  hi = max_nan(hi, y[1][7]);
 #pragma unroll
-  for (int o = 1; o < G / 8; o <<= 1) {
+  for (int o = 1; o < G / 16; o <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
@@ -139,21 +161,52 @@ __device__ __forceinline__ uint32_t quantise8(const float (&y)[8], int (&code)[8
   const float range = hi - lo;
   const bool finite = fabsf(range) <= 3.402823466e38f;
   uint32_t scale_bits = pack_bf16x2(0.f, __fdiv_rn(fmaxf(range, 0.f), 15.f)) & 0xffff0000u;
-  if (scale_bits < 0x00800000u) scale_bits = 0;
-  if (!finite) scale_bits = 0;
+  if (scale_bits < 0x00800000u || !finite) scale_bits = 0;
   const float scale = __uint_as_float(scale_bits);
-  const float inv = scale_bits ? __frcp_rn(scale) : 0.f;
+  // The code is t / scale, nearly (t the clamped distance from low), rounded:
+  // off only next to a half-way point, where t - code scale, which one fma
+  // gives exactly enough, is half a step or more.  A few of a thousand bf16
+  // values lie exactly there.
+  float inv = 0.f;
+  if (scale_bits) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  const float top = 15.f * scale, half = 0.5f * scale;
+  float off = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float t = y[e] - lo;
-    // t inv is within 2e-6 of the quotient (which is at most 15.1): only next
-    // to a half-way point can its rounding differ from the quotient's, and
-    // there the division decides.  (Dividing always costs a third more.)
-    float u = t * inv;
-    if (fabsf(u - floorf(u) - 0.5f) < 1e-5f) u = __fdiv_rn(t, scale);
-    code[e] = __float2int_rn(fminf(fmaxf(u, 0.f), 15.f));
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float t = fminf(fmaxf(y[i][e] - lo, 0.f), top);
+      const float w = fmaf(t, inv, kRound);
+      code[i][e] = __float_as_uint(w);
+      off = fmaxf(off, fabsf(fmaf(kRound - w, scale, t)));
+    }
+  if (off >= half && scale_bits) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = fminf(fmaxf(y[i][e] - lo, 0.f), top);
+        const float d = fmaf(kRound - __uint_as_float(code[i][e]), scale, t);
+        // Half-way goes to the even code.
+        const bool wrong = fabsf(d) > half || (fabsf(d) == half && (code[i][e] & 1u));
+        if (wrong) code[i][e] += d > 0.f ? 1u : ~0u;
+      }
   }
   return finite ? scale_bits | low_bits : 0x7fc07fc0u;
+}
+
+// The codes in one word, code ORDER(n) in nibble n: the copies of kRoundBits
+// add up to a constant.
+template <bool KEY>
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t (&code)[8]) {
+  uint32_t w = 0, extra = 0;
+#pragma unroll
+  for (int n = 7; n >= 0; --n) {
+    const int e = KEY ? 2 * (n & 3) + (n >> 2) : n;
+    w = w * 16u + code[e];
+    extra = extra * 16u + kRoundBits;
+  }
+  return w - extra;
 }
 
 // Turn fractions and axes of the pairs, formed once per CTA, and the cosines
@@ -173,128 +226,145 @@ __device__ __forceinline__ void load_pairs(const RopeParams& p, RopeShared& sh) 
   }
 }
 
-// What a lane does to the 8 elements it holds of a row: it takes part in
-// pairs `pair0` up, whose other members (of split pairs) lane `partner` holds.
-template <bool IL>
-struct LaneTurn {
-  static constexpr int kPairs = IL ? 4 : 8;
-  bool turns, second;
-  int pair0, partner;
-  float cs[kPairs], sn[kPairs];
+// Cosines and sines of a token's pairs: each lane forms its share of the (at
+// most 64) angles and leaves them in `buf` for the warp.  (Every lane forming
+// those of its own elements cost four times the arithmetic: 41 us instead of
+// 28 for the rotation of 4 x 4096 tokens of 14 heads.)  `position(axis)` gives
+// the token's position.
+template <class Position>
+__device__ __forceinline__ void form_angles(const RopeParams& p, const RopeShared& sh, float2* buf, int lane,
+                                            Position position) {
+  __syncwarp();
+  for (int i = lane; i < p.rot / 2; i += 32) {
+    const uint32_t ax = sh.axis[i];
+    float s, c;
+    turn_sincos(position(static_cast<int>(ax & 3u)), sh.frac[i], s, c);
+    if (ax & 4u) s = c = __uint_as_float(0x7fc00000u);
+    buf[i] = make_float2(c, p.inverse ? -s : s);
+  }
+  __syncwarp();
+}
 
-  __device__ __forceinline__ LaneTurn(int rot, int j, int lane) {
-    turns = 8 * j < rot;
-    second = !IL && 16 * j >= rot;
-    pair0 = IL ? 4 * j : second ? 8 * j - rot / 2 : 8 * j;
-    partner = (!IL && turns) ? lane + (second ? -rot / 16 : rot / 16) : lane;
+// A row held by D/16 lanes, two 16-byte pieces each, both members of 8 pairs
+// (elements e0 .. e0 + 7 and e1 .. e1 + 7), so a rotation stays in the lane;
+// past the rotating part, 16 neighbouring elements.
+template <bool IL>
+struct PairLanes {
+  int e0, e1;
+  bool turns;
+  uint64_t cs[4], sn[4];           // of pairs 2 i, 2 i + 1
+
+  __device__ __forceinline__ PairLanes(int rot, int slot) {
+    turns = 16 * slot < rot;
+    e0 = (IL || !turns) ? 16 * slot : 8 * slot;
+    e1 = (IL || !turns) ? e0 + 8 : e0 + rot / 2;
   }
-  // Cosines and sines of a token's pairs: each lane forms its share of the
-  // (at most 64) angles and the warp exchanges them through `buf` (every lane
-  // forming those of its own elements cost 4 times the arithmetic: 41 us
-  // instead of 26 for the rotation of 4 x 4096 tokens of 14 heads).
-  // `position(axis)` gives the token's position.
-  template <class Position>
-  __device__ __forceinline__ void angles(const RopeParams& p, const RopeShared& sh, float2* buf, int lane,
-                                         Position position) {
-    __syncwarp();
-    for (int i = lane; i < p.rot / 2; i += 32) {
-      const uint32_t ax = sh.axis[i];
-      float s, c;
-      turn_sincos(position(static_cast<int>(ax & 3u)), sh.frac[i], s, c);
-      if (ax & 4u) s = c = __uint_as_float(0x7fc00000u);
-      buf[i] = make_float2(c, p.inverse ? -s : s);
-    }
-    __syncwarp();
-    if (turns) {
+  __device__ __forceinline__ void load_angles(const float2* buf, int slot) {
+    if (!turns) return;
 #pragma unroll
-      for (int e = 0; e < kPairs; e += 2) {
-        const float4 v = *reinterpret_cast<const float4*>(buf + pair0 + e);
-        cs[e] = v.x;
-        sn[e] = v.y;
-        cs[e + 1] = v.z;
-        sn[e + 1] = v.w;
-      }
-      if (!IL && !second) {                      // the first member of a split pair takes -sin times the second
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) sn[e] = -sn[e];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(buf + 8 * slot + 2 * i);
+      cs[i] = f2_pack(v.x, v.z);
+      sn[i] = f2_pack(v.y, v.w);
     }
   }
-  // y = the 8 elements of x, turned (all lanes take part; `rotate` false: as
-  // they are).
-  __device__ __forceinline__ void apply(const uint4& x, float (&y)[8], bool rotate) const {
-    unpack8(x, y);
+  // Two elements of each of x's words, as fp32 pairs.
+  static __device__ __forceinline__ void pairs_of(const uint4& x, uint64_t (&y)[4]) {
+    y[0] = f2_pack(bf_lo(x.x), bf_hi(x.x));
+    y[1] = f2_pack(bf_lo(x.y), bf_hi(x.y));
+    y[2] = f2_pack(bf_lo(x.z), bf_hi(x.z));
+    y[3] = f2_pack(bf_lo(x.w), bf_hi(x.w));
+  }
+  static __device__ __forceinline__ uint32_t round2(uint64_t y) {
+    float lo, hi;
+    f2_unpack(y, lo, hi);
+    return pack_bf16x2(lo, hi);
+  }
+  __device__ __forceinline__ void turn(uint4& x0, uint4& x1) const {
+    if (!turns) return;
+    uint64_t a[4], b[4];
+    pairs_of(x0, a);
+    pairs_of(x1, b);
     if constexpr (IL) {
-      if (turns && rotate) {
+      // x0 holds pairs 0 .. 3 (first, second), x1 pairs 4 .. 7.
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = y[2 * e], b = y[2 * e + 1];
-          y[2 * e] = a * cs[e] - b * sn[e];
-          y[2 * e + 1] = b * cs[e] + a * sn[e];
-        }
+      for (int i = 0; i < 4; ++i) {
+        float c0, c1, s0, s1, u, v;
+        f2_unpack(cs[i], c0, c1);
+        f2_unpack(sn[i], s0, s1);
+        uint64_t& y0 = i < 2 ? a[2 * i] : b[2 * i - 4];
+        uint64_t& y1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+        f2_unpack(y0, u, v);
+        y0 = f2_fma(f2_pack(-v, u), f2_pack(s0, s0), f2_mul(y0, f2_pack(c0, c0)));
+        f2_unpack(y1, u, v);
+        y1 = f2_fma(f2_pack(-v, u), f2_pack(s1, s1), f2_mul(y1, f2_pack(c1, c1)));
       }
     } else {
-      uint4 o;
-      o.x = __shfl_sync(0xffffffffu, x.x, partner);
-      o.y = __shfl_sync(0xffffffffu, x.y, partner);
-      o.z = __shfl_sync(0xffffffffu, x.z, partner);
-      o.w = __shfl_sync(0xffffffffu, x.w, partner);
-      if (turns && rotate) {
-        float z[8];
-        unpack8(o, z);
+      const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = y[e] * cs[e] + z[e] * sn[e];
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t y = a[i];
+        a[i] = f2_fma(f2_mul(b[i], minus), sn[i], f2_mul(y, cs[i]));
+        b[i] = f2_fma(y, sn[i], f2_mul(b[i], cs[i]));
       }
     }
+    x0 = make_uint4(round2(a[0]), round2(a[1]), round2(a[2]), round2(a[3]));
+    x1 = make_uint4(round2(b[0]), round2(b[1]), round2(b[2]), round2(b[3]));
   }
 };
 
-// Rows [r0, r1) of `src` (one token's heads `step` elements apart), turned,
-// to the same rows of `dst`.  All lanes of a warp; kFlight steps of loads are
-// in flight together.
-template <int D, int kFlight, bool IL>
-__device__ __forceinline__ void turn_rows(const LaneTurn<IL>& turn, const __nv_bfloat16* src, long long src_step,
-                                          __nv_bfloat16* dst, long long dst_step, int r0, int r1, int j, int sub) {
-  constexpr int kRows = 256 / D;
-  src += 8 * j;
-  dst += 8 * j;
-  for (int base = r0; base < r1; base += kFlight * kRows) {
-    uint4 x[kFlight];
+// Elements 8 piece .. 8 piece + 7 of a row, turned; `other` holds those that
+// they pair with (split pairs).
+template <bool IL>
+__device__ __forceinline__ void turn_piece(const uint4& x, const uint4& other, const float2* angles, int rot,
+                                           int piece, float (&y)[8]) {
+  unpack8(x, y);
+  if (8 * piece >= rot) return;
+  if constexpr (IL) {
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int r = base + u * kRows + sub;
-      x[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < r1) x[u] = *reinterpret_cast<const uint4*>(src + r * src_step);
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = angles[4 * piece + e];
+      const float a = y[2 * e], b = y[2 * e + 1];
+      y[2 * e] = a * v.x - b * v.y;
+      y[2 * e + 1] = b * v.x + a * v.y;
     }
+  } else {
+    const bool second = 16 * piece >= rot;
+    const float2* cs = angles + 8 * piece - (second ? rot / 2 : 0);
+    float z[8];
+    unpack8(other, z);
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      if (base + u * kRows >= r1) break;         // the same for all lanes
-      const int r = base + u * kRows + sub;
-      float y[8];
-      turn.apply(x[u], y, true);
-      if (r < r1) *reinterpret_cast<uint4*>(dst + r * dst_step) = turn.turns ? pack8(y) : x[u];
+    for (int e = 0; e < 8; e += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(cs + e);
+      // The first member of a pair takes -sin times the second.
+      y[e] = fmaf(second ? z[e] : -z[e], v.y, y[e] * v.x);
+      y[e + 1] = fmaf(second ? z[e + 1] : -z[e + 1], v.w, y[e + 1] * v.z);
     }
   }
 }
 
-// Tasks are (token, slice of its rows), one warp each.
+// Tasks are (token, slice of its rows), one warp each.  Rows of a token:
+// queries, keys, values.
 template <int D, int MODE, int G, bool IL>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kLanes = D / 8;           // lanes of a row
-  constexpr int kRows = 32 / kLanes;      // rows of a warp step
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kSlotLanes = D / 16;             // lanes of a row held in pairs
+  constexpr int kRows = 32 / kSlotLanes;
+  constexpr int kFlight = 2;                     // steps whose loads are in flight together
   __shared__ RopeShared sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = lane % kLanes, sub = lane / kLanes;
+  const int slot = lane % kSlotLanes, sub = lane / kSlotLanes;
 
   pdl_wait_primary();
   pdl_launch_dependents();
   load_pairs(p, sh);
   __syncthreads();
-  LaneTurn<IL> turn(p.rot, j, lane);
+  PairLanes<IL> pl(p.rot, slot);
+  float2* angles = sh.cs[warp];
+  const CellTranspose transpose(lane);
 
   const int tasks = static_cast<int>(p.tasks), stride = gridDim.x * kWarps;
   for (int task = blockIdx.x * kWarps + warp; task < tasks; task += stride) {
-    const int t = task / p.parts;
+    const int t = p.parts == 1 ? task : task / p.parts;
     const int row0 = (task - t * p.parts) * p.rows_per_part;
     const int row1 = min(p.rows, row0 + p.rows_per_part);
 
@@ -321,69 +391,111 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
         continue;
       }
     }
+    const int cache_slot = cache_pos % kSlots;
 
+    // Rows held in pairs: all of them, or with a 4-bit cache the queries.
+    const int end = MODE == kAppendKv4 ? min(row1, p.Hq) : row1;
+    const __nv_bfloat16* qs = p.q.data + batch * p.q.batch + tok * p.q.token;
+    const __nv_bfloat16* ks = p.k.data + batch * p.k.batch + tok * p.k.token;
+    const __nv_bfloat16* vs = MODE == kRotate ? nullptr : p.v.data + tok * p.v.token;
+    uint4 x0[kFlight], x1[kFlight];
+    auto load = [&](int base) {
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int r = base + u * kRows + sub;
+        x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= end) continue;
+        const bool value = MODE == kAppend && r >= p.Hq + p.Hk;
+        const __nv_bfloat16* src = r < p.Hq ? qs + r * p.q.head : value ? vs + (r - p.Hq - p.Hk) * p.v.head
+                                                                       : ks + (r - p.Hq) * p.k.head;
+        x0[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot : pl.e0));
+        x1[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot + 8 : pl.e1));
+      }
+    };
+    if (row0 < end) load(row0);
     if (row0 < p.Hq + p.Hk) {
       const int* pos = p.rope_pos + batch * p.batch_stride + tok;
       const bool own = MODE != kRotate && p.rope_pos == nullptr;
-      turn.angles(p, sh, sh.cs[warp], lane,
-                  [&](int axis) { return own ? cache_pos : pos[axis * p.axis_stride]; });
+      form_angles(p, sh, angles, lane, [&](int axis) { return own ? cache_pos : pos[axis * p.axis_stride]; });
+      if (row0 < end) pl.load_angles(angles, slot);
     }
-    if (row0 < p.Hq)
-      turn_rows<D, 4, IL>(turn, p.q.data + batch * p.q.batch + tok * p.q.token, p.q.head,
-                          p.q_out.data + batch * p.q_out.batch + tok * p.q_out.token, p.q_out.head, row0,
-                          min(row1, p.Hq), j, sub);
-    if (row1 <= p.Hq) continue;
-    const int k0 = max(row0 - p.Hq, 0), k1 = row1 - p.Hq;   // keys, then values
-    if constexpr (MODE == kRotate) {
-      turn_rows<D, 4, IL>(turn, p.k.data + batch * p.k.batch + tok * p.k.token, p.k.head,
-                          p.k_out.data + batch * p.k_out.batch + tok * p.k_out.token, p.k_out.head, k0, k1, j, sub);
-    } else {
-      constexpr int kFlight = 2;
-      const __nv_bfloat16* ks = p.k.data + tok * p.k.token + 8 * j;
-      const __nv_bfloat16* vs = p.v.data + tok * p.v.token + 8 * j;
-      const int slot = cache_pos % kSlots;
-      for (int base = k0; base < k1; base += kFlight * kRows) {
-        uint4 x[kFlight];
+    for (int base = row0; base < end;) {
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-          const int r = base + u * kRows + sub;
-          x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < k1)
-            x[u] = *reinterpret_cast<const uint4*>(r < p.Hk ? ks + r * p.k.head : vs + (r - p.Hk) * p.v.head);
+      for (int u = 0; u < kFlight; ++u) {
+        const int r = base + u * kRows + sub;
+        if (r >= end) continue;
+        const bool value = MODE == kAppend && r >= p.Hq + p.Hk;
+        if (!value) pl.turn(x0[u], x1[u]);
+        __nv_bfloat16* dst;
+        if (r < p.Hq) {
+          dst = p.q_out.data + batch * p.q_out.batch + tok * p.q_out.token + r * p.q_out.head;
+        } else if (MODE == kRotate) {
+          dst = p.k_out.data + batch * p.k_out.batch + tok * p.k_out.token + (r - p.Hq) * p.k_out.head;
+        } else {
+          const int h = value ? r - p.Hq - p.Hk : r - p.Hq;
+          dst = (value ? p.v_cache : p.k_cache) + ((static_cast<size_t>(phys) * p.Hk + h) * kSlots + cache_slot) * D;
         }
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-          if (base + u * kRows >= k1) break;     // the same for all lanes
-          const int r = base + u * kRows + sub;
-          const bool value = r >= p.Hk;
-          const int h = value ? r - p.Hk : r;
-          float y[8];
-          turn.apply(x[u], y, !value);
-          if constexpr (MODE == kAppend) {
-            __nv_bfloat16* dst = (value ? p.v_cache : p.k_cache) +
-                                 ((static_cast<size_t>(phys) * p.Hk + h) * kSlots + slot) * D + 8 * j;
-            if (r < k1) *reinterpret_cast<uint4*>(dst) = (turn.turns && !value) ? pack8(y) : x[u];
-          } else {
-            using Lt = Kv4Layout<D, G>;
-            int code[8];
-            const uint32_t par = quantise8<G>(y, code);
-            uint32_t wk = 0, wv = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              wk |= static_cast<uint32_t>(code[e]) << (4 * ((e >> 1) + 4 * (e & 1)));
-              wv |= static_cast<uint32_t>(code[e]) << (4 * e);
-            }
-            wk = kv4_k_transpose(wk, lane);
-            wv = kv4_v_transpose(wv, lane);
-            if (r < k1) {
-              uint8_t* rec = p.kv_cache + (static_cast<size_t>(phys) * p.Hk + h) * Lt::kBytes;
-              uint32_t* row = reinterpret_cast<uint32_t*>(rec + (value ? Lt::kOffV : 0) + slot * Lt::kRow);
-              row[value ? kv4_v_word<D>(j) : kv4_k_word<D>(j)] = value ? wv : wk;
-              if (j % (G / 8) == 0)
-                reinterpret_cast<uint32_t*>(rec + (value ? Lt::kOffParV : Lt::kOffParK) +
-                                            slot * Lt::kParRow)[j / (G / 8)] = par;
-            }
+        *reinterpret_cast<uint4*>(dst + (value ? 16 * slot : pl.e0)) = x0[u];
+        *reinterpret_cast<uint4*>(dst + (value ? 16 * slot + 8 : pl.e1)) = x1[u];
+      }
+      base += kFlight * kRows;
+      if (base < end) load(base);
+    }
+
+    if constexpr (MODE == kAppendKv4) {
+      // Keys and values for a 4-bit cache: rows of 16 neighbouring elements a
+      // lane, as the groups lie; what they pair with is loaded as well (from
+      // L1).
+      using Lt = Kv4Layout<D, G>;
+      if (row1 <= p.Hq) continue;
+      const int k0 = max(row0 - p.Hq, 0), k1 = row1 - p.Hq;   // keys, then values
+      const int shift = 16 * slot < p.rot / 2 ? p.rot / 2 : -p.rot / 2;         // of piece 2 slot
+      const int shift1 = 16 * slot + 8 < p.rot / 2 ? p.rot / 2 : -p.rot / 2;    // of piece 2 slot + 1
+      for (int base = k0; base < k1; base += kRows) {
+        const int r = base + sub;
+        const bool value = r >= p.Hk;
+        uint4 x[2], z[2];
+        x[0] = x[1] = z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < k1) {
+          const __nv_bfloat16* src = (value ? vs + (r - p.Hk) * p.v.head : ks + r * p.k.head) + 16 * slot;
+          x[0] = *reinterpret_cast<const uint4*>(src);
+          x[1] = *reinterpret_cast<const uint4*>(src + 8);
+          if (!IL && !value) {
+            if (16 * slot < p.rot) z[0] = *reinterpret_cast<const uint4*>(src + shift);
+            if (16 * slot + 8 < p.rot) z[1] = *reinterpret_cast<const uint4*>(src + 8 + shift1);
           }
+        }
+        float y[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (value)
+            unpack8(x[i], y[i]);
+          else
+            turn_piece<IL>(x[i], z[i], angles, p.rot, 2 * slot + i, y[i]);
+        }
+        uint32_t code[2][8], w[2] = {0u, 0u};
+        const uint32_t par = quantise16<G>(y, code);
+        if (base < p.Hk) {                       // some row of this step is a key
+          w[0] = pack_codes<true>(code[0]);
+          w[1] = pack_codes<true>(code[1]);
+          transpose.key(w);
+        }
+        if (base + kRows > p.Hk) {               // some row of this step is a value
+          uint32_t wv[2] = {pack_codes<false>(code[0]), pack_codes<false>(code[1])};
+          transpose.value(wv);
+          if (value) {
+            w[0] = wv[0];
+            w[1] = wv[1];
+          }
+        }
+        if (r < k1) {
+          uint8_t* rec = p.kv_cache + (static_cast<size_t>(phys) * p.Hk + (value ? r - p.Hk : r)) * Lt::kBytes;
+          uint32_t* row = reinterpret_cast<uint32_t*>(rec + (value ? Lt::kOffV : 0) + cache_slot * Lt::kRow);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) row[value ? kv4_v_word<D>(2 * slot + i) : kv4_k_word<D>(2 * slot + i)] = w[i];
+          if (slot % (G / 16) == 0)
+            reinterpret_cast<uint32_t*>(rec + (value ? Lt::kOffParV : Lt::kOffParK) +
+                                        cache_slot * Lt::kParRow)[slot / (G / 16)] = par;
         }
       }
     }
@@ -391,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
 }
 
 // Rows of cached tokens back to bf16: value = code * scale + min, rounded
-// once.  Row 2 h of a token is head h's key, row 2 h + 1 its value.
+// once.  Rows of a token: its keys, then its values.
 struct Kv4ReadParams {
   const uint8_t* kv_cache;
   const int* block_table;
@@ -406,21 +518,21 @@ struct Kv4ReadParams {
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4ReadParams p) {
+__global__ void __launch_bounds__(kThreads, kReadCtas) kv4_read_kernel(const Kv4ReadParams p) {
   using Lt = Kv4Layout<D, G>;
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kFlight = 4;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kFlight = 2;
   const int lane = threadIdx.x & 31;
   const int j = lane % kLanes, sub = lane / kLanes;
   const int rows = 2 * p.Hkv;
+  const CellTranspose transpose(lane);
 
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  const long long stride = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long task = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); task < p.tasks;
-       task += stride) {
-    const long long t = task / p.parts;
-    const int row0 = static_cast<int>(task - t * p.parts) * p.rows_per_part;
+  const int tasks = static_cast<int>(p.tasks), stride = gridDim.x * kWarps;
+  for (int task = blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks; task += stride) {
+    const int t = p.parts == 1 ? task : task / p.parts;
+    const int row0 = (task - t * p.parts) * p.rows_per_part;
     const int row1 = min(rows, row0 + p.rows_per_part);
     const int seq = p.seq_ids[t], pos = p.positions[t];
     if (seq < 0) continue;
@@ -437,37 +549,54 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4ReadParams 
       continue;
     }
     const int slot = pos % kSlots;
+    const uint8_t* recs = p.kv_cache + static_cast<size_t>(phys) * p.Hkv * Lt::kBytes;
     for (int base = row0; base < row1; base += kFlight * kRows) {
-      uint32_t w[kFlight], par[kFlight];
+      uint32_t w[kFlight][2], par[kFlight];
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
         const int r = base + u * kRows + sub;
-        w[u] = par[u] = 0;
+        w[u][0] = w[u][1] = par[u] = 0;
         if (r < row1) {
-          const uint8_t* rec = p.kv_cache + (static_cast<size_t>(phys) * p.Hkv + (r >> 1)) * Lt::kBytes;
-          const bool value = r & 1;
-          w[u] = reinterpret_cast<const uint32_t*>(rec + (value ? Lt::kOffV : 0) + slot * Lt::kRow)[
-              value ? kv4_v_word<D>(j) : kv4_k_word<D>(j)];
+          const bool value = r >= p.Hkv;
+          const uint8_t* rec = recs + static_cast<size_t>(value ? r - p.Hkv : r) * Lt::kBytes;
+          const uint32_t* row = reinterpret_cast<const uint32_t*>(rec + (value ? Lt::kOffV : 0) + slot * Lt::kRow);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[u][i] = row[value ? kv4_v_word<D>(2 * j + i) : kv4_k_word<D>(2 * j + i)];
           par[u] = reinterpret_cast<const uint32_t*>(rec + (value ? Lt::kOffParV : Lt::kOffParK) +
-                                                     slot * Lt::kParRow)[j / (G / 8)];
+                                                     slot * Lt::kParRow)[j / (G / 16)];
         }
       }
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
-        const int r0 = base + u * kRows;
+        const int r0 = base + u * kRows, r = r0 + sub;
         if (r0 >= row1) break;                   // the same for all lanes
-        const int r = r0 + sub;
-        const uint32_t ck = kv4_k_transpose(w[u], lane), cv = kv4_v_transpose(w[u], lane);
+        const bool value = r >= p.Hkv;
+        uint32_t wk[2] = {w[u][0], w[u][1]}, wv[2] = {w[u][0], w[u][1]};
+        if (r0 < p.Hkv) transpose.key(wk);
+        if (r0 + kRows > p.Hkv) transpose.value(wv);
         const float scale = bf_hi(par[u]), low = bf_lo(par[u]);
-        float y[8];
+        uint4 out[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t code = (r & 1) ? cv >> (4 * e) : ck >> (4 * ((e >> 1) + 4 * (e & 1)));
-          y[e] = fmaf(static_cast<float>(code & 15u), scale, low);
+        for (int i = 0; i < 2; ++i) {
+          // Cell n as a float: 2^23 + code, less 2^23.
+          const uint32_t x = value ? wv[i] : wk[i];
+          const uint32_t even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;
+          float n[8];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            n[2 * c] = fmaf(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7440u + c)) - 8388608.f, scale, low);
+            n[2 * c + 1] = fmaf(__uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7440u + c)) - 8388608.f, scale, low);
+          }
+          // Element e of a value is cell e, element 2 c + h of a key cell c + 4 h.
+          const uint32_t k0 = pack_bf16x2(n[0], n[4]), k1 = pack_bf16x2(n[1], n[5]), k2 = pack_bf16x2(n[2], n[6]),
+                         k3 = pack_bf16x2(n[3], n[7]);
+          out[i] = value ? pack8(n) : make_uint4(k0, k1, k2, k3);
         }
         if (r < row1) {
-          __nv_bfloat16* dst = (r & 1) ? p.v : p.k;
-          *reinterpret_cast<uint4*>(dst + (static_cast<size_t>(t) * p.Hkv + (r >> 1)) * D + 8 * j) = pack8(y);
+          uint4* dst = reinterpret_cast<uint4*>(
+              (value ? p.v : p.k) + (static_cast<size_t>(t) * p.Hkv + (value ? r - p.Hkv : r)) * D + 16 * j);
+          dst[0] = out[0];
+          dst[1] = out[1];
         }
       }
     }
@@ -481,7 +610,7 @@ struct Split {
   int parts, rows_per_part;
   unsigned grid;
 };
-Split split_rows(long long tokens, int rows, int rows_per_step, int sms) {
+Split split_rows(long long tokens, int rows, int rows_per_step, int sms, int resident) {
   const long long want = static_cast<long long>(sms) * 16;
   const int most = (rows + rows_per_step - 1) / rows_per_step;
   long long parts = (want + tokens - 1) / tokens;
@@ -491,7 +620,7 @@ Split split_rows(long long tokens, int rows, int rows_per_step, int sms) {
   s.rows_per_part = steps * rows_per_step;
   s.parts = (rows + s.rows_per_part - 1) / s.rows_per_part;
   const long long ctas = (tokens * s.parts + kWarps - 1) / kWarps;
-  const long long cap = static_cast<long long>(sms) * 4;
+  const long long cap = static_cast<long long>(sms) * resident;
   s.grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
   return s;
 }
@@ -516,7 +645,7 @@ void fill_spec(RopeParams& p, const RopeSpec& s) {
 
 template <int D, int MODE, int G>
 cudaError_t launch_t(RopeParams& p, long long tokens, bool interleaved, int sms, cudaStream_t stream) {
-  const Split s = split_rows(tokens, p.rows, 32 / (D / 8), sms);
+  const Split s = split_rows(tokens, p.rows, 32 / (D / 16), sms, ctas_per_sm(MODE));
   p.parts = s.parts;
   p.rows_per_part = s.rows_per_part;
   p.tasks = tokens * s.parts;
@@ -526,7 +655,7 @@ cudaError_t launch_t(RopeParams& p, long long tokens, bool interleaved, int sms,
 
 template <int D, int G>
 cudaError_t launch_read_t(Kv4ReadParams& p, long long tokens, int sms, cudaStream_t stream) {
-  const Split s = split_rows(tokens, 2 * p.Hkv, 32 / (D / 8), sms);
+  const Split s = split_rows(tokens, 2 * p.Hkv, 32 / (D / 16), sms, kReadCtas);
   p.parts = s.parts;
   p.rows_per_part = s.rows_per_part;
   p.tasks = tokens * s.parts;

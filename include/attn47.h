@@ -579,9 +579,10 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  *  workspace  >= attn_decode_paged_kv4_workspace_size(...) bytes, 16-byte
  *             aligned; contents on entry are ignored
  *  q, block_table, seq_lens, o, lse, scale, sizes, empty sequences and device
- *  flags as for attn_decode_paged (Hq / Hkv <= 16).  One kernel; the parts of
- *  a split (sequence, KV head) are merged in a fixed order, so the result is
- *  deterministic for a given device.  Calls that share a workspace must not
+ *  flags as for attn_decode_paged (Hq / Hkv <= 16); attn_set_decode_early_plan
+ *  applies (level 2 acts as 1).  One kernel; the parts of a split (sequence,
+ *  KV head) are merged in a fixed order, so the result is deterministic for a
+ *  given device.  Calls that share a workspace must not
  *  overlap on the GPU.
  */
 attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const int32_t* block_table,
@@ -615,7 +616,7 @@ void attn_set_wait_timeout_ns(unsigned long long ns);
 void attn_set_decode_max_ctas(int ctas);
 
 /*
- * attn_set_decode_early_plan — 1: later decode calls (both entry points)
+ * attn_set_decode_early_plan — 1: later decode calls (every entry point)
  * read seq_lens and the first block-table entries of each CTA's share
  * before the kernel that precedes them in the stream has finished, so that
  * the split plan overlaps that kernel's tail; 2: as 1, and each CTA also

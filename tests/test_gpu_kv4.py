@@ -400,6 +400,39 @@ def test_calls_see_inputs_written_just_before_on_their_stream():
         assert torch.equal(o, ro) and torch.equal(lse, rl)
 
 
+@pytest.mark.parametrize("early", [0, 1, 2])
+def test_early_plan_sees_tokens_appended_just_before(early):
+    """The append that runs just before the decode, on the same stream, writes
+    the newest slots and the queries; lengths and table come from the host."""
+    S, Hq, Hkv, d, group = 6, 12, 2, 128, 32
+    q, rec, table, lens = decode_case([700, 64, 17, 1500, 1, 333], Hq, Hkv, d, group, seed=170)
+    f = workloads.rope_inv_freq(d).to(DEV)
+    tab, ln = dev(table, lens)
+    ids, at = torch.arange(S, dtype=torch.int32, device=DEV), ln - 1
+    steps = [randn(171 + i, S, (Hq + 2 * Hkv) * d).to(DEV) for i in range(3)]
+    want = []
+    kv = rec.to(DEV)
+    for x in steps:
+        qo = attn.rope_append_paged_kv4(*views(x, Hq, Hkv, d), kv, tab, ids, at, group, inv_freq=f)
+        torch.cuda.synchronize()
+        want.append(attn.attn_decode_paged_kv4(qo, kv, tab, ln, group))
+        torch.cuda.synchronize()
+    kv = rec.to(DEV)
+    torch.cuda.synchronize()
+    got = []
+    try:
+        attn.set_decode_early_plan(early)
+        for x in steps:
+            qo = attn.rope_append_paged_kv4(*views(x, Hq, Hkv, d), kv, tab, ids, at, group, inv_freq=f)
+            got.append(attn.attn_decode_paged_kv4(qo, kv, tab, ln, group))
+        torch.cuda.synchronize()
+    finally:
+        attn.set_decode_early_plan(0)
+    assert attn.device_status() == 0
+    for (o, l), (ro, rl) in zip(got, want):
+        assert torch.equal(o, ro) and torch.equal(l, rl)
+
+
 def test_long_cache_beyond_32_bit_offsets():
     """Records past 2^32 bytes from the start of the pool: append, read and
     decode address them."""
