@@ -529,10 +529,10 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
         const float sa = word_scale(kpa[n][g]), sb = word_scale(kpb[n][g]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          s[n][nt][0] = fmaf(sa, acc[n][nt][0], s[n][nt][0]);
-          s[n][nt][1] = fmaf(sa, acc[n][nt][1], s[n][nt][1]);
-          s[n][nt][2] = fmaf(sb, acc[n][nt][2], s[n][nt][2]);
-          s[n][nt][3] = fmaf(sb, acc[n][nt][3], s[n][nt][3]);
+          f2_unpack(f2_fma(f2_pack(sa, sa), f2_pack(acc[n][nt][0], acc[n][nt][1]), f2_pack(s[n][nt][0], s[n][nt][1])),
+                    s[n][nt][0], s[n][nt][1]);
+          f2_unpack(f2_fma(f2_pack(sb, sb), f2_pack(acc[n][nt][2], acc[n][nt][3]), f2_pack(s[n][nt][2], s[n][nt][3])),
+                    s[n][nt][2], s[n][nt][3]);
         }
       }
     }
@@ -592,20 +592,23 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
     uint32_t pw[NT][kGroups][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float p0 = ex2(fmaf(s[n][nt][0], q.back[nt][0], -st.stab[nt][0]));
-      const float p1 = ex2(fmaf(s[n][nt][1], q.back[nt][1], -st.stab[nt][1]));
-      const float p2 = ex2(fmaf(s[n][nt][2], q.back[nt][0], -st.stab[nt][0]));
-      const float p3 = ex2(fmaf(s[n][nt][3], q.back[nt][1], -st.stab[nt][1]));
-      st.l[nt][0] += p0 + p2;
-      st.l[nt][1] += p1 + p3;
+      const uint64_t back = f2_pack(q.back[nt][0], q.back[nt][1]), stab = f2_pack(-st.stab[nt][0], -st.stab[nt][1]);
+      float p0, p1, p2, p3;
+      f2_unpack(f2_fma(f2_pack(s[n][nt][0], s[n][nt][1]), back, stab), p0, p1);
+      f2_unpack(f2_fma(f2_pack(s[n][nt][2], s[n][nt][3]), back, stab), p2, p3);
+      const uint64_t pa = f2_pack(ex2(p0), ex2(p1)), pb = f2_pack(ex2(p2), ex2(p3));
+      f2_unpack(f2_add(f2_pack(st.l[nt][0], st.l[nt][1]), f2_add(pa, pb)), st.l[nt][0], st.l[nt][1]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const float sa = word_scale(vpa[n][g]), sb = word_scale(vpb[n][g]);
         const float ma = word_min(vpa[n][g]), mb = word_min(vpb[n][g]);
-        st.mins[nt][g][0] = fmaf(p0, ma, fmaf(p2, mb, st.mins[nt][g][0]));
-        st.mins[nt][g][1] = fmaf(p1, ma, fmaf(p3, mb, st.mins[nt][g][1]));
-        pw[nt][g][0] = movmatrix_trans(pack_f16x2(p0 * sa, p1 * sa));
-        pw[nt][g][1] = movmatrix_trans(pack_f16x2(p2 * sb, p3 * sb));
+        f2_unpack(f2_fma(pa, f2_pack(ma, ma), f2_fma(pb, f2_pack(mb, mb), f2_pack(st.mins[nt][g][0], st.mins[nt][g][1]))),
+                  st.mins[nt][g][0], st.mins[nt][g][1]);
+        float w0, w1;
+        f2_unpack(f2_mul(pa, f2_pack(sa, sa)), w0, w1);
+        pw[nt][g][0] = movmatrix_trans(pack_f16x2(w0, w1));
+        f2_unpack(f2_mul(pb, f2_pack(sb, sb)), w0, w1);
+        pw[nt][g][1] = movmatrix_trans(pack_f16x2(w0, w1));
       }
     }
 #pragma unroll

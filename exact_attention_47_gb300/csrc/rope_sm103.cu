@@ -36,14 +36,22 @@ enum Mode { kRotate, kAppend, kAppendKv4 };
 constexpr int ctas_per_sm(int mode) { return mode == kAppendKv4 ? 3 : 4; }
 constexpr int kReadCtas = 6;
 
-struct RowPtr {
-  const __nv_bfloat16* data;
-  long long batch, token, head;
+// Rows by strides (in elements; those within a batch in 32 bits, so that an
+// address is one multiply-add).
+template <class T>
+struct Rows {
+  T* data;
+  long long batch;
+  int token, head;
+  __device__ __forceinline__ T* of(int b, int t) const {
+    return data + b * batch + static_cast<long long>(t) * token;
+  }
+  static __device__ __forceinline__ T* row(T* token_rows, int r, int head) {
+    return token_rows + static_cast<long long>(r) * head;
+  }
 };
-struct OutPtr {
-  __nv_bfloat16* data;
-  long long batch, token, head;
-};
+using RowPtr = Rows<const __nv_bfloat16>;
+using OutPtr = Rows<__nv_bfloat16>;
 
 struct RopeParams {
   RowPtr q, k, v;
@@ -252,7 +260,7 @@ template <bool IL>
 struct PairLanes {
   int e0, e1;
   bool turns;
-  uint64_t cs[4], sn[4];           // of pairs 2 i, 2 i + 1
+  float cs[8], sn[8];
 
   __device__ __forceinline__ PairLanes(int rot, int slot) {
     turns = 16 * slot < rot;
@@ -262,54 +270,30 @@ struct PairLanes {
   __device__ __forceinline__ void load_angles(const float2* buf, int slot) {
     if (!turns) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(buf + 8 * slot + 2 * i);
-      cs[i] = f2_pack(v.x, v.z);
-      sn[i] = f2_pack(v.y, v.w);
+    for (int i = 0; i < 8; i += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(buf + 8 * slot + i);
+      cs[i] = v.x;
+      sn[i] = v.y;
+      cs[i + 1] = v.z;
+      sn[i + 1] = v.w;
     }
-  }
-  // Two elements of each of x's words, as fp32 pairs.
-  static __device__ __forceinline__ void pairs_of(const uint4& x, uint64_t (&y)[4]) {
-    y[0] = f2_pack(bf_lo(x.x), bf_hi(x.x));
-    y[1] = f2_pack(bf_lo(x.y), bf_hi(x.y));
-    y[2] = f2_pack(bf_lo(x.z), bf_hi(x.z));
-    y[3] = f2_pack(bf_lo(x.w), bf_hi(x.w));
-  }
-  static __device__ __forceinline__ uint32_t round2(uint64_t y) {
-    float lo, hi;
-    f2_unpack(y, lo, hi);
-    return pack_bf16x2(lo, hi);
   }
   __device__ __forceinline__ void turn(uint4& x0, uint4& x1) const {
     if (!turns) return;
-    uint64_t a[4], b[4];
-    pairs_of(x0, a);
-    pairs_of(x1, b);
-    if constexpr (IL) {
-      // x0 holds pairs 0 .. 3 (first, second), x1 pairs 4 .. 7.
+    float a[8], b[8];
+    unpack8(x0, a);
+    unpack8(x1, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float c0, c1, s0, s1, u, v;
-        f2_unpack(cs[i], c0, c1);
-        f2_unpack(sn[i], s0, s1);
-        uint64_t& y0 = i < 2 ? a[2 * i] : b[2 * i - 4];
-        uint64_t& y1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-        f2_unpack(y0, u, v);
-        y0 = f2_fma(f2_pack(-v, u), f2_pack(s0, s0), f2_mul(y0, f2_pack(c0, c0)));
-        f2_unpack(y1, u, v);
-        y1 = f2_fma(f2_pack(-v, u), f2_pack(s1, s1), f2_mul(y1, f2_pack(c1, c1)));
-      }
-    } else {
-      const uint64_t minus = f2_pack(-1.f, -1.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t y = a[i];
-        a[i] = f2_fma(f2_mul(b[i], minus), sn[i], f2_mul(y, cs[i]));
-        b[i] = f2_fma(y, sn[i], f2_mul(b[i], cs[i]));
-      }
+    for (int i = 0; i < 8; ++i) {
+      // Interleaved, x0 holds pairs 0 .. 3 and x1 pairs 4 .. 7.
+      float& u = IL ? (i < 4 ? a[(2 * i) % 8] : b[(2 * i) % 8]) : a[i];
+      float& v = IL ? (i < 4 ? a[(2 * i) % 8 + 1] : b[(2 * i) % 8 + 1]) : b[i];
+      const float first = u * cs[i] - v * sn[i];
+      v = v * cs[i] + u * sn[i];
+      u = first;
     }
-    x0 = make_uint4(round2(a[0]), round2(a[1]), round2(a[2]), round2(a[3]));
-    x1 = make_uint4(round2(b[0]), round2(b[1]), round2(b[2]), round2(b[3]));
+    x0 = pack8(a);
+    x1 = pack8(b);
   }
 };
 
@@ -368,12 +352,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
     const int row0 = (task - t * p.parts) * p.rows_per_part;
     const int row1 = min(p.rows, row0 + p.rows_per_part);
 
-    long long batch = 0, tok = t;
-    if (MODE == kRotate) {
-      const int b = t / p.N;
-      batch = b;
-      tok = t - b * p.N;
-    }
+    const int batch = MODE == kRotate ? t / p.N : 0;
+    const int tok = t - batch * p.N;
     int cache_pos = 0, phys = 0;
     if (MODE != kRotate) {
       const int seq = p.seq_ids[t];
@@ -395,9 +375,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
 
     // Rows held in pairs: all of them, or with a 4-bit cache the queries.
     const int end = MODE == kAppendKv4 ? min(row1, p.Hq) : row1;
-    const __nv_bfloat16* qs = p.q.data + batch * p.q.batch + tok * p.q.token;
-    const __nv_bfloat16* ks = p.k.data + batch * p.k.batch + tok * p.k.token;
-    const __nv_bfloat16* vs = MODE == kRotate ? nullptr : p.v.data + tok * p.v.token;
+    const __nv_bfloat16 *qs = p.q.of(batch, tok), *ks = p.k.of(batch, tok), *vs = p.v.of(batch, tok);
+    __nv_bfloat16 *qd = p.q_out.of(batch, tok), *kd = p.k_out.of(batch, tok);
     uint4 x0[kFlight], x1[kFlight];
     auto load = [&](int base) {
 #pragma unroll
@@ -406,8 +385,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
         x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
         if (r >= end) continue;
         const bool value = MODE == kAppend && r >= p.Hq + p.Hk;
-        const __nv_bfloat16* src = r < p.Hq ? qs + r * p.q.head : value ? vs + (r - p.Hq - p.Hk) * p.v.head
-                                                                       : ks + (r - p.Hq) * p.k.head;
+        const __nv_bfloat16* src = r < p.Hq ? RowPtr::row(qs, r, p.q.head)
+                                   : value  ? RowPtr::row(vs, r - p.Hq - p.Hk, p.v.head)
+                                            : RowPtr::row(ks, r - p.Hq, p.k.head);
         x0[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot : pl.e0));
         x1[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot + 8 : pl.e1));
       }
@@ -428,9 +408,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
         if (!value) pl.turn(x0[u], x1[u]);
         __nv_bfloat16* dst;
         if (r < p.Hq) {
-          dst = p.q_out.data + batch * p.q_out.batch + tok * p.q_out.token + r * p.q_out.head;
+          dst = OutPtr::row(qd, r, p.q_out.head);
         } else if (MODE == kRotate) {
-          dst = p.k_out.data + batch * p.k_out.batch + tok * p.k_out.token + (r - p.Hq) * p.k_out.head;
+          dst = OutPtr::row(kd, r - p.Hq, p.k_out.head);
         } else {
           const int h = value ? r - p.Hq - p.Hk : r - p.Hq;
           dst = (value ? p.v_cache : p.k_cache) + ((static_cast<size_t>(phys) * p.Hk + h) * kSlots + cache_slot) * D;
@@ -457,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
         uint4 x[2], z[2];
         x[0] = x[1] = z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
         if (r < k1) {
-          const __nv_bfloat16* src = (value ? vs + (r - p.Hk) * p.v.head : ks + r * p.k.head) + 16 * slot;
+          const __nv_bfloat16* src = (value ? RowPtr::row(vs, r - p.Hk, p.v.head) : RowPtr::row(ks, r, p.k.head)) + 16 * slot;
           x[0] = *reinterpret_cast<const uint4*>(src);
           x[1] = *reinterpret_cast<const uint4*>(src + 8);
           if (!IL && !value) {
@@ -626,10 +606,10 @@ Split split_rows(long long tokens, int rows, int rows_per_step, int sms, int res
 }
 
 RowPtr in_rows(const HeadRows& h) {
-  return RowPtr{static_cast<const __nv_bfloat16*>(h.data), h.batch, h.token, h.head};
+  return RowPtr{static_cast<const __nv_bfloat16*>(h.data), h.batch, static_cast<int>(h.token), static_cast<int>(h.head)};
 }
 OutPtr out_rows(const HeadRows& h) {
-  return OutPtr{static_cast<__nv_bfloat16*>(h.data), h.batch, h.token, h.head};
+  return OutPtr{static_cast<__nv_bfloat16*>(h.data), h.batch, static_cast<int>(h.token), static_cast<int>(h.head)};
 }
 
 void fill_spec(RopeParams& p, const RopeSpec& s) {
