@@ -373,8 +373,8 @@ attn_status_t check_heads(const attn_heads_t* h, const char* name, int B, int N,
     if (x.stride < 0 || x.stride % 8 != 0)
       return fail(ATTN_ERR_INVALID_ARG, "%s: strides must be non-negative multiples of 8 elements", name);
     if (x.n > 1 && x.stride > (1LL << 46) / x.n) return fail(ATTN_ERR_INVALID_ARG, "%s: stride too large", name);
-    if (&x != dim && x.n > 1 && x.stride > 0x7fffffffLL)
-      return fail(ATTN_ERR_UNSUPPORTED, "%s: token or head stride of 2^31 elements or more not supported", name);
+    if (&x != dim && x.n > 1 && x.stride >= (1LL << 34))
+      return fail(ATTN_ERR_UNSUPPORTED, "%s: token or head stride of 2^34 elements or more not supported", name);
   }
   if (output) {
     // No two rows may share an element: taken from the smallest stride up,

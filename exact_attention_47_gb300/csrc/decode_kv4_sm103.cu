@@ -32,6 +32,17 @@
 // holds whole is written by it; pieces of a run go to shared memory, are merged
 // per CTA, and if the run reaches into other CTAs the merged part is published
 // and the CTA that arrives last merges the parts.
+//
+// What bounds it (GB300, one column tile, d = 128): further blocks of long
+// contexts stream at 6.5 TB/s, the rate of a copy; about 11.5 us of every call
+// are latency, three dependent reads before the first block (lengths, table,
+// record: 4 us) and, at the end, the merge of a CTA's pieces, the arrival and
+// the merge of published parts (5 to 6 us, over 1 us for each trip to what
+// another SM has written).  8 sequences of 30k .. 131k tokens (195 MB) take
+// 43.7 us, 64 of 128 .. 4096 (44 MB) 19.4 us.  With d = 64 (4.8 TB/s) and with
+// two column tiles (3.3 at d = 64, 4.0 at d = 128) the arithmetic of a block
+// takes longer than its bytes: its instructions wait on one another, at two to
+// three warps a scheduler.
 #include <atomic>
 
 #include <cuda_fp16.h>
@@ -47,6 +58,10 @@ namespace {
 constexpr int kBS = kKv4Slots;
 // CTAs a launch may have (one per SM); the workspace has room for this many.
 constexpr int kMaxCtas = 256;
+// A run costs a warp about this many blocks' time (its queries, its end).
+// Measured with 1, 4 and 8 (us; 64 sequences of 128 .. 4096 tokens, 256 of up
+// to 2048 with 16 heads a KV head, one of 100): 20.9 50.0 6.4, 20.5 46.2 7.2,
+// 20.4 47.2 7.6.
 constexpr int kRunCost = 4;
 // Lazy stabilisers (see attn_decode_paged): the running maximum moves only
 // when a score exceeds it by more than kTau (log2 units).
@@ -61,9 +76,9 @@ template <int D, int G, int NT>
 struct DecKv4Cfg {
   using Rec = Kv4Layout<D, G>;
   // 12 warps with 168 registers each, or 8 with 255 when two column tiles
-  // double the accumulators.  (With one tile, per block of a long context: 12
-  // warps stream 6.1 TB/s, 8 warps 5.6, 16 warps spill; 10, uneven over the
-  // four schedulers, lose to 8.)
+  // double the accumulators.  (With one tile, d = 128, each further block of a
+  // long context streams at 6.1 TB/s with 12 warps and 5.6 with 8; 16 spill,
+  // and 10, uneven over the four schedulers, lose to 8.)
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = D == 128 ? 4 : 8;           // a power of two
@@ -667,7 +682,9 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       if (at < hi) bulk_prefetch_l2(reinterpret_cast<const void*>(at), static_cast<uint32_t>(min(share, static_cast<size_t>(hi - at))));
     };
     prefetch_share(p.seq_lens, static_cast<size_t>(p.num_seqs) * 4);
-    prefetch_share(p.block_table, static_cast<size_t>(p.num_seqs) * p.max_blocks * 4);
+    // (A wide table is mostly padding.)
+    const size_t table = static_cast<size_t>(p.num_seqs) * p.max_blocks * 4;
+    if (table <= (size_t(1) << 20)) prefetch_share(p.block_table, table);
     prefetch_share(p.q, static_cast<size_t>(p.num_seqs) * p.Hq * D * 2);
   }
   // With the early plan, seq_lens and the block table are read before the

@@ -36,18 +36,18 @@ enum Mode { kRotate, kAppend, kAppendKv4 };
 constexpr int ctas_per_sm(int mode) { return mode == kAppendKv4 ? 3 : 4; }
 constexpr int kReadCtas = 6;
 
-// Rows by strides (in elements; those within a batch in 32 bits, so that an
-// address is one multiply-add).
+// Rows by strides: those within a batch in units of 8 elements and 32 bits,
+// so that a row's address takes one multiplication.
 template <class T>
 struct Rows {
   T* data;
   long long batch;
   int token, head;
   __device__ __forceinline__ T* of(int b, int t) const {
-    return data + b * batch + static_cast<long long>(t) * token;
+    return data + b * batch + static_cast<long long>(t) * token * 8;
   }
   static __device__ __forceinline__ T* row(T* token_rows, int r, int head) {
-    return token_rows + static_cast<long long>(r) * head;
+    return token_rows + static_cast<long long>(r) * head * 8;
   }
 };
 using RowPtr = Rows<const __nv_bfloat16>;
@@ -606,10 +606,10 @@ Split split_rows(long long tokens, int rows, int rows_per_step, int sms, int res
 }
 
 RowPtr in_rows(const HeadRows& h) {
-  return RowPtr{static_cast<const __nv_bfloat16*>(h.data), h.batch, static_cast<int>(h.token), static_cast<int>(h.head)};
+  return RowPtr{static_cast<const __nv_bfloat16*>(h.data), h.batch, static_cast<int>(h.token / 8), static_cast<int>(h.head / 8)};
 }
 OutPtr out_rows(const HeadRows& h) {
-  return OutPtr{static_cast<__nv_bfloat16*>(h.data), h.batch, static_cast<int>(h.token), static_cast<int>(h.head)};
+  return OutPtr{static_cast<__nv_bfloat16*>(h.data), h.batch, static_cast<int>(h.token / 8), static_cast<int>(h.head / 8)};
 }
 
 void fill_spec(RopeParams& p, const RopeSpec& s) {

@@ -411,7 +411,7 @@ attn_status_t ssd_chunked_fwd(const void* x, const float* dt, const float* A, co
 /*
  * Rows of d bf16 values, d contiguous: head h of token n of batch b starts
  * `b stride_batch + n stride_token + h stride_head` elements after `data`.
- * Strides are non-negative multiples of 8 (token and head strides below 2^31),
+ * Strides are non-negative multiples of 8 (token and head strides below 2^34),
  * data 16-byte aligned.  A view of a
  * merged projection output (token-major) and the contiguous [B, H, N, d] of
  * attn_fwd are both of this form.

@@ -270,3 +270,32 @@ def test_bad_rows_are_reported_and_skipped(group):
         assert torch.all(rk[2:] == 7) and torch.all(rv[2:] == 7) and torch.all(rk[:2] != 7)
     assert attn.device_status() == attn.ATTN_DEV_BAD_SEQID | attn.ATTN_DEV_BAD_SEQLEN | attn.ATTN_DEV_BAD_BLOCK
     assert torch.all(qo[:2].float().abs().sum(-1) > 0) and torch.all(qo[2:] == 0)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows more than 2^31 elements from the start of their tensor: head-major
+    rotation of a long sequence, and an append of token rows far apart."""
+    d, N = 64, (1 << 25) + 1000
+    f = workloads.rope_inv_freq(d).to(DEV)
+    q = torch.zeros(1, 2, N, d, dtype=BF, device=DEV)
+    tail = randn(41, 1, 2, 700, d).to(DEV)
+    q[:, :, -700:] = tail
+    pos = torch.arange(N, dtype=torch.int32, device=DEV)
+    out, _ = attn.rope_fwd(q, None, pos, f, q_out=q)
+    small, _ = attn.rope_fwd(tail, None, pos[-700:], f)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, :, -700:], small) and not out[:, :, :1000].any()
+    del q, out
+    T, wide, Hkv = 33000, 1 << 16, 2
+    x = torch.zeros(T, wide, dtype=BF, device=DEV)
+    k, v = x[:, : Hkv * d].view(T, Hkv, d), x[:, 512: 512 + Hkv * d].view(T, Hkv, d)
+    k[-50:], v[-50:] = randn(42, 50, Hkv, d).to(DEV), randn(43, 50, Hkv, d).to(DEV)
+    table = torch.arange(-(-T // 16), dtype=torch.int32, device=DEV)[None]
+    ids, at = torch.zeros(T, dtype=torch.int32, device=DEV), torch.arange(T, dtype=torch.int32, device=DEV)
+    kc, vc = (torch.ones(table.shape[1], Hkv, 16, d, dtype=BF, device=DEV) for _ in range(2))
+    attn.rope_append_paged(None, k, v, kc, vc, table, ids, at)
+    torch.cuda.synchronize()
+    assert attn.device_status() == 0
+    rows = torch.arange(T - 50, T)
+    assert torch.equal(kc[rows // 16, :, rows % 16], k[-50:]) and torch.equal(vc[rows // 16, :, rows % 16], v[-50:])
+    assert not kc[0].any()

@@ -101,6 +101,7 @@ def test_rope_refusals(lib, func):
     assert call(q=heads(Q + 8)) == INVALID                           # misaligned
     assert call(q=heads(Q, token=100)) == INVALID                    # stride not a multiple of 8
     assert call(q=heads(Q, token=-128)) == INVALID
+    assert call(q=heads(Q, token=1 << 34)) == UNSUPPORTED
     assert call(q=heads(Q, H=3), qo=heads(QO, H=2)) == INVALID
     assert call(qo=heads(QO, token=64)) == INVALID                   # output rows overlap
     assert "overlap" in lib.attn_last_error().decode()
