@@ -10,12 +10,14 @@ built, every call raises ``RuntimeError``.
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import struct
 
 import torch
 
-from .build_lib import LIB_PATH
+from .build_lib import LIB_PATH, fast_path
 
 ATTN_OK = 0
 ATTN_DEV_TIMEOUT = 0x1
@@ -106,6 +108,27 @@ def load_library(path=None):
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+# The entry points that the fast calls pass on to, in the order of their `bind`.
+_FAST = ("rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "kv4_record_bytes", "kv4_read_paged",
+         "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4")
+
+
+@functools.lru_cache(maxsize=None)
+def _fast():
+    """The module of the fast calls (csrc/fast_calls.cpp), bound to the
+    library.  Each takes the arguments of its namesake here, and does the call
+    or returns None where it is not the usual case."""
+    lib = load_library()
+    path = fast_path()
+    if not os.path.exists(path):
+        raise RuntimeError("%s is not built; run `python -c \"import __graft_entry__ as g; g.build()\"`" % path)
+    loader = importlib.machinery.ExtensionFileLoader("_attn47_fast", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn47_fast", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST))
+    return module
 
 
 def status_string(status):
@@ -485,6 +508,10 @@ def _rope(inv_freq, positions, lead, pair_axis, interleaved, device):
 
 
 def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out, stream):
+    if stream is None:
+        done = _fast().rope(func == "rope_bwd", q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out)
+        if done is not None:
+            return done
     hq = _heads("q", q, None, 4)
     dev = q.device
     B, _, N, d = q.shape
@@ -592,6 +619,11 @@ def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions
     Returns q_out [T,Hq,d] (new unless given; its padding rows are left as
     they were), or None without q.
     """
+    if stream is None and v_cache is not None:
+        done = _fast().append(q, k, v, k_cache, v_cache, block_table, seq_ids, positions, 0, inv_freq, rope_positions,
+                              pair_axis, interleaved, q_out)
+        if done is not None:
+            return done[0]
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
@@ -632,6 +664,11 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
     [num_blocks,Hkv,kv4_record_bytes(d, group)] uint8 (updated in place), 4-bit
     codes with a bf16 (min, scale) per ``group`` (32 or 64) consecutive
     elements of a key or value.  Returns q_out (or None without q)."""
+    if stream is None:
+        done = _fast().append(q, k, v, kv_cache, None, block_table, seq_ids, positions, group, inv_freq, rope_positions,
+                              pair_axis, interleaved, q_out)
+        if done is not None:
+            return done[0]
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
     nb, Hkv = _need_kv4(kv_cache, d, group, dev)
@@ -647,6 +684,10 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
     """The values that cached tokens of a 4-bit cache stand for: row t is
     position positions[t] of sequence seq_ids[t] ([T] int32; negative
     sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16."""
+    if stream is None:
+        done = _fast().read(kv_cache, block_table, seq_ids, positions, d, group, k, v)
+        if done is not None:
+            return done
     if not isinstance(seq_ids, torch.Tensor) or seq_ids.dim() != 1:
         raise ValueError("seq_ids must be a [T] tensor")
     nb, Hkv = _need_kv4(kv_cache, d, group, None)
@@ -672,6 +713,10 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
 
     Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32 or None).
     """
+    if stream is None:
+        done = _fast().decode(q, kv_cache, block_table, seq_lens, group, scale, o, lse, workspace, return_lse)
+        if done is not None:
+            return done
     _need_cuda("q", q, torch.bfloat16)
     dev = q.device
     if q.dim() != 3:

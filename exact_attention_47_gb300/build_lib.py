@@ -4,7 +4,9 @@ Every translation unit is compiled for sm_103a only
 (``-gencode arch=compute_103a,code=sm_103a``), in parallel, then linked into
 one shared object with the CUDA runtime linked statically, so that the
 library loads on a machine without a GPU (e.g. to check its exported
-symbols) and needs only the driver at run time.
+symbols) and needs only the driver at run time.  Beside it g++ builds
+``lib/_attn47_fast_<torch version>.so``, the Python module that marshals the
+usual case of the short calls (csrc/fast_calls.cpp, against torch's headers).
 
 Usage: ``python -m exact_attention_47_gb300.build_lib`` or ``build()``.
 """
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +32,31 @@ SOURCES = ["api.cu", "fwd_sm103.cu", "bwd_sm103.cu", "decode_sm103.cu", "decode_
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = GENCODE + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                     "-I", INCLUDE, "-I", CSRC]
+
+FAST_SOURCE = "fast_calls.cpp"
+
+
+def _torch():
+    """(version, folder) of the installed torch."""
+    import torch
+
+    return str(torch.__version__), os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def fast_path():
+    """Where the module of the fast calls is built for the installed torch."""
+    return os.path.join(LIB_DIR, "_attn47_fast_%s.so" % _torch()[0])
+
+
+def _fast_command(out):
+    home = _torch()[1]
+    include = os.path.join(home, "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", os.path.join(CSRC, FAST_SOURCE),
+             "-o", out]
+            + ["-I" + d for d in (INCLUDE, include, os.path.join(include, "torch", "csrc", "api", "include"),
+                                  sysconfig.get_paths()["include"], os.path.join(cuda, "include"))]
+            + ["-L" + os.path.join(home, "lib")] + ["-l" + n for n in ("torch_python", "torch_cpu", "torch", "c10", "c10_cuda")])
 
 
 def _nvcc():
@@ -69,13 +97,21 @@ def build(verbose=False, ptxas_info=False):
         if ptxas_info or _stale(o, s):
             cmd = [nvcc] + CFLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", s, "-o", o]
             jobs.append(cmd)
+    link = bool(jobs) or not os.path.exists(LIB_PATH)
+    fast = fast_path()
+    if _stale(fast, os.path.join(CSRC, FAST_SOURCE)):
+        jobs.append(_fast_command(fast + ".tmp"))
+    else:
+        fast = None
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
         outs = list(ex.map(_run, jobs))
     if verbose or ptxas_info:
         for out in outs:
             sys.stdout.write(out)
     objs = [os.path.join(BUILD_DIR, s.replace(".cu", ".o")) for s in SOURCES]
-    if jobs or not os.path.exists(LIB_PATH):
+    if fast is not None:
+        os.replace(fast + ".tmp", fast)
+    if link:
         tmp = LIB_PATH + ".tmp"
         _run([nvcc] + GENCODE + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB_PATH)

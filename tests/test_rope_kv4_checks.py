@@ -286,3 +286,19 @@ def test_binding_refuses_append_read_decode(no_library_calls):
                        (dict(workspace=dev((need - 16,), U8)), "workspace has"), (dict(o=dev((S, Hq, 128), BF)), "o must have")]:
         with pytest.raises(ValueError, match=match):
             attn.attn_decode_paged_kv4(**(c | bad))
+
+
+def test_fast_calls_leave_the_unusual_to_the_binding(lib):
+    """CPU tensors, other types and counts: None each time, nothing raised."""
+    fast = _binding._fast()
+    f32, i32 = torch.zeros(8), torch.zeros(8, dtype=I32)
+    for f, n in ((fast.rope, 9), (fast.append, 14), (fast.read, 8), (fast.decode, 10)):
+        for fill in (None, True, 3, 2 ** 80, "x", f32, i32, torch.zeros((2, 4, 8, 64), dtype=BF), f32.to("meta")):
+            for count in (0, n - 1, n, n + 1):
+                assert f(*[fill] * count) is None
+    q = torch.zeros((2, 4, 8, 64), dtype=BF)
+    assert fast.rope(False, q, None, i32, torch.zeros(32), None, False, None, None) is None
+    with pytest.raises(TypeError):
+        fast.bind(1)
+    with pytest.raises(ValueError):
+        fast.bind(*[0] * 8)
