@@ -56,7 +56,8 @@ def _fast_command(out):
              "-o", out]
             + ["-I" + d for d in (INCLUDE, include, os.path.join(include, "torch", "csrc", "api", "include"),
                                   sysconfig.get_paths()["include"], os.path.join(cuda, "include"))]
-            + ["-L" + os.path.join(home, "lib")] + ["-l" + n for n in ("torch_python", "torch_cpu", "torch", "c10", "c10_cuda")])
+            + ["-L" + os.path.join(home, "lib")]
+            + ["-l" + n for n in ("torch_python", "torch_cpu", "torch_cuda", "torch", "c10", "c10_cuda")])
 
 
 def _nvcc():
