@@ -1260,11 +1260,13 @@ attn_status_t kv4_read_paged(const void* kv_cache, int group, const int32_t* blo
   const size_t out = static_cast<size_t>(T) * Hkv * d * 2;
   if (overlap(k, out, v, out) || overlap(k, out, kv_cache, cache) || overlap(v, out, kv_cache, cache))
     return fail(ATTN_ERR_INVALID_ARG, "k, v and kv_cache must not overlap");
+  const size_t ints = static_cast<size_t>(T) * 4, table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4;
+  for (const void* x : {k, v})
+    if (overlap(x, out, block_table, table) || overlap(x, out, seq_ids, ints) || overlap(x, out, positions, ints))
+      return fail(ATTN_ERR_INVALID_ARG, "k and v must not overlap block_table, seq_ids or positions");
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != ATTN_OK) return st;
-  const size_t ints = static_cast<size_t>(T) * 4;
-  if ((st = check_bufs(*dev, {{kv_cache, cache, "kv_cache"},
-                              {block_table, static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, "block_table"},
+  if ((st = check_bufs(*dev, {{kv_cache, cache, "kv_cache"}, {block_table, table, "block_table"},
                               {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"}, {k, out, "k"},
                               {v, out, "v"}})) != ATTN_OK)
     return st;
@@ -1339,6 +1341,12 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
   for (const auto& x : others)
     if (x.n && overlap(workspace, need, x.p, x.n))
       return fail(ATTN_ERR_INVALID_ARG, "workspace overlaps an input or output of the decode");
+  for (int i = 0; i < 4; ++i) {                  // (other warps may still be reading there)
+    if (overlap(o, qb, others[i].p, others[i].n)) return fail(ATTN_ERR_INVALID_ARG, "o overlaps an input of the decode");
+    if (lse && overlap(lse, lb, others[i].p, others[i].n))
+      return fail(ATTN_ERR_INVALID_ARG, "lse overlaps an input of the decode");
+  }
+  if (lse && overlap(o, qb, lse, lb)) return fail(ATTN_ERR_INVALID_ARG, "o overlaps lse");
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != ATTN_OK) return st;
   if ((st = check_bufs(*dev, {{workspace, need, "workspace"}, {q, qb, "q"}, {kv_cache, cache, "kv_cache"},

@@ -483,7 +483,7 @@ attn_status_t rope_bwd(const attn_heads_t* dq_out, const attn_heads_t* dk_out, c
  * prefill: many; both in one batch).  Rows with seq_ids[t] < 0 are padding:
  * nothing is read or written for them.  Other slots of the blocks touched
  * keep what they hold.  Two rows of one call with the same sequence and
- * position leave either one's values.
+ * position leave that slot with values of either one, or a mixture.
  *
  *  q          [T, Hq, d] by strides (stride_batch unused), or NULL
  *  k, v       [T, Hkv, d] by strides
@@ -550,7 +550,8 @@ attn_status_t rope_append_paged_kv4(const attn_heads_t* q, const attn_heads_t* k
  * (for a chunk that attends to what the cache holds, or to move a prefix to a
  * bf16 cache).
  *
- *  k, v       [T, Hkv, d] bf16, contiguous, 16-byte aligned (written)
+ *  k, v       [T, Hkv, d] bf16, contiguous, 16-byte aligned (written); they
+ *             overlap neither each other nor an input
  *  The other arguments, rules and device flags are those of
  *  rope_append_paged_kv4; rows with seq_ids[t] < 0 are left as they were.
  */
@@ -579,7 +580,9 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  *  group      32 or 64
  *  workspace  >= attn_decode_paged_kv4_workspace_size(...) bytes, 16-byte
  *             aligned; contents on entry are ignored
- *  q, block_table, seq_lens, o, lse, scale, sizes, empty sequences and device
+ *  o, lse     as for attn_decode_paged; they overlap neither each other nor an
+ *             input
+ *  q, block_table, seq_lens, scale, sizes, empty sequences and device
  *  flags as for attn_decode_paged (Hq / Hkv <= 16); attn_set_decode_early_plan
  *  applies (level 2 acts as 1).  One kernel; the parts of a split (sequence,
  *  KV head) are merged in a fixed order, so the result is deterministic for a

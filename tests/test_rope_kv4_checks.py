@@ -202,6 +202,27 @@ def test_decode_refusals(lib):
     assert size(0, 12, 2, 128) == 0
 
 
+def test_decode_outputs_keep_off_the_inputs(lib):
+    """O and LSE over the queries, the cache, the table, the lengths or each
+    other: other warps may still be reading there."""
+    need = lib.attn_decode_paged_kv4_workspace_size(2, 12, 2, 128)
+
+    def call(o, lse):
+        return lib.attn_decode_paged_kv4(Q, KC, TAB, IDS, 2, 12, 2, 128, 32, 16, 4, 8, 0.1, o, lse, 0x7000000, need, None)
+
+    assert call(0x5000000, 0x6000000) not in (INVALID, UNSUPPORTED, OK)      # apart: it fails on the missing device
+    for at in (Q, KC.value + 256, TAB.value, IDS.value):
+        assert call(at, None) == INVALID and "o overlaps" in lib.attn_last_error().decode()
+        assert call(0x5000000, at) == INVALID and "lse overlaps" in lib.attn_last_error().decode()
+    assert call(0x5000000, 0x5000000 + 2 * 12 * 128 * 2 - 4) == INVALID
+
+
+def test_read_outputs_keep_off_the_token_map(lib):
+    for at in (TAB.value, IDS.value, POS.value):
+        assert read(lib, k=at) == INVALID and "overlap" in lib.attn_last_error().decode()
+        assert read(lib, v=at) == INVALID
+
+
 # ------------------------------------------------------------------ binding
 class _OnCuda0(torch.Tensor):
     """A CPU tensor that claims to be on cuda:0 (it never reaches the library)."""
