@@ -24,8 +24,8 @@
 // groups up to 8.  P^T changes operand layout with movmatrix.
 //
 // Work split: the blocks of all (sequence, KV head) runs in one flat order,
-// cut into equal costs for every warp of a one-wave grid (a run costs
-// kRunCost blocks more than its blocks, for its queries and its end).  A warp
+// cut into equal costs for every warp of a one-wave grid (a run costs a few
+// blocks more than it has, for its queries and its end).  A warp
 // streams its blocks through a ring of its own in shared memory, one bulk copy
 // per (block, head) record, and keeps its own running softmax, so nothing
 // inside the CTA waits for anything else until the end.  A run that a warp
@@ -34,12 +34,12 @@
 // and the CTA that arrives last merges the parts.
 //
 // What bounds it (GB300, one column tile, d = 128): further blocks of long
-// contexts stream at 6.5 TB/s, the rate of a copy; about 11.5 us of every call
-// are latency, three dependent reads before the first block (lengths, table,
-// record: 4 us) and, at the end, the merge of a CTA's pieces, the arrival and
-// the merge of published parts (5 to 6 us, over 1 us for each trip to what
-// another SM has written).  8 sequences of 30k .. 131k tokens (195 MB) take
-// 43.7 us, 64 of 128 .. 4096 (44 MB) 19.4 us.  With d = 64 (4.8 TB/s) and with
+// contexts stream at 6.4 TB/s, the rate of a copy; about 11.5 us of a call that
+// fills the GPU are latency, three dependent reads before the first block
+// (lengths, table, record: 4 us) and, at the end, the merge of a CTA's pieces,
+// the arrival and the merge of published parts (4 to 5 us, over 1 us for each
+// trip to what another SM has written).  8 sequences of 30k .. 131k tokens (195
+// MB) take 43.9 us, 64 of 128 .. 4096 (44 MB) 17.5 us, one of 100 6.6 us.  With d = 64 (4.8 TB/s) and with
 // two column tiles (3.3 at d = 64, 4.0 at d = 128) the arithmetic of a block
 // takes longer than its bytes: its instructions wait on one another, at two to
 // three warps a scheduler.
@@ -58,11 +58,6 @@ namespace {
 constexpr int kBS = kKv4Slots;
 // CTAs a launch may have (one per SM); the workspace has room for this many.
 constexpr int kMaxCtas = 256;
-// A run costs a warp about this many blocks' time (its queries, its end).
-// Measured with 1, 4 and 8 (us; 64 sequences of 128 .. 4096 tokens, 256 of up
-// to 2048 with 16 heads a KV head, one of 100): 20.9 50.0 6.4, 20.5 46.2 7.2,
-// 20.4 47.2 7.6.
-constexpr int kRunCost = 4;
 // Lazy stabilisers (see attn_decode_paged): the running maximum moves only
 // when a score exceeds it by more than kTau (log2 units).
 constexpr float kTau = 8.f;
@@ -135,7 +130,7 @@ __device__ __forceinline__ int kv4_seq_len(const DecKv4Params& p, int b) {
   return L < 0 ? 0 : min(L, p.max_blocks * kBS);
 }
 
-// Work in cost units: every run (sequence, KV head) is kRunCost units followed
+// Work in cost units: every run (sequence, KV head) is run_cost units followed
 // by one per block, runs in order of (sequence, head).  cost[e] and runs[e]
 // are the units and the runs before entry e, an entry being `per` sequences;
 // blocks[e] the blocks of a head of sequence e (per == 1).
@@ -143,7 +138,7 @@ struct Plan {
   const int* cost;
   const int* runs;
   const int* blocks;
-  int entries, per, total;
+  int entries, per, total, total_blocks, run_cost;
   __device__ __forceinline__ int seq_blocks(const DecKv4Params& p, int b) const {
     return per == 1 ? blocks[b] : (kv4_seq_len(p, b) + kBS - 1) / kBS;
   }
@@ -164,17 +159,17 @@ __device__ __forceinline__ int locate(const DecKv4Params& p, const Plan& plan, i
   at.b = e * plan.per;
   at.nblk = plan.seq_blocks(p, at.b);
   for (int i = 1; i < plan.per; ++i) {           // several sequences to the entry: pass those before x
-    const int c = at.nblk > 0 ? (at.nblk + kRunCost) * p.Hkv : 0;
+    const int c = at.nblk > 0 ? (at.nblk + plan.run_cost) * p.Hkv : 0;
     if (start + c > x) break;
     start += c;
     if (c > 0) runs += p.Hkv;
     at.nblk = plan.seq_blocks(p, ++at.b);
   }
-  const int cost = at.nblk + kRunCost;
+  const int cost = at.nblk + plan.run_cost;
   at.g = (x - start) / cost;
   at.cost = start + at.g * cost;
-  at.blk = max(0, x - at.cost - kRunCost);
-  return at.cost - (runs + at.g) * kRunCost + at.blk;
+  at.blk = max(0, x - at.cost - plan.run_cost);
+  return at.cost - (runs + at.g) * plan.run_cost + at.blk;
 }
 
 // Walk over the runs of a warp's share.
@@ -185,7 +180,7 @@ struct Walk {
   __device__ __forceinline__ void next_run(const DecKv4Params& p, const Plan& plan, int passed) {
     left -= passed;
     at.blk = 0;
-    at.cost += at.nblk + kRunCost;
+    at.cost += at.nblk + plan.run_cost;
     if (++at.g == p.Hkv) {
       at.g = 0;
       do {
@@ -699,6 +694,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
   plan.blocks = seq_blocks;
   plan.per = (p.num_seqs + kPlan - 1) / kPlan;
   plan.entries = (p.num_seqs + plan.per - 1) / plan.per;
+  const int shares = static_cast<int>(gridDim.x) * kWarps;
   {
     // Thread t sums entries [t E, (t + 1) E); warp scan, then the warps' sums.
     constexpr int E = (kPlan + kThreads - 1) / kThreads;
@@ -717,7 +713,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
         const int blocks = ((L < 0 ? 0 : min(L, p.max_blocks * kBS)) + kBS - 1) / kBS;
         if (plan.per == 1) seq_blocks[b] = blocks;
         if (blocks > 0) {
-          c += (blocks + kRunCost) * p.Hkv;
+          c += blocks * p.Hkv;
           r += p.Hkv;
         }
       }
@@ -745,24 +741,29 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       total += v.x;
       total_runs += v.y;
     }
+    // What a run costs beyond its blocks.  A long share spends about 4 blocks'
+    // time on a run (its queries, its end).  A share is at least run_cost + 1
+    // blocks, though, a pass of two blocks takes a warp 0.9 us when it is alone,
+    // and with few blocks most warps have none: then shares of one pass, and
+    // between of two.  Measured with 1, 3 and 4 (us): one sequence of 100 tokens,
+    // 2 KV heads, 6.8 6.9 7.7; 16 of 500, 9.9 12.7 12.8; 32 of 1000, 12.4 11.9
+    // 13.0; 16 of up to 2000, 4 KV heads, 13.4 12.2 12.8; 256 of up to 2048, 45.6
+    // 41.9 40.5.
+    plan.run_cost = total <= shares ? 1 : total <= 8 * shares ? 3 : 4;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int e = tid * each + i;
       if (i >= each || e >= plan.entries) continue;
-      cost[e] = c0 + ec[i];
+      cost[e] = c0 + ec[i] + (r0 + er[i]) * plan.run_cost;
       runs[e] = r0 + er[i];
     }
-    if (tid == 0) {
-      cost[plan.entries] = total;
-      runs[plan.entries] = total_runs;
-    }
-    plan.total = total;
+    plan.total = total + total_runs * plan.run_cost;
+    plan.total_blocks = total;
   }
   __syncthreads();
   // Every share but the last of all holds at least one block (a share longer
   // than a run's start cost cannot lie inside it).
-  const int shares = static_cast<int>(gridDim.x) * kWarps;
-  const int chunk = max(kRunCost + 1, (plan.total - 1) / shares + 1);
+  const int chunk = max(plan.run_cost + 1, (plan.total - 1) / shares + 1);
   const long long mine = (static_cast<long long>(blockIdx.x) * kWarps + warp) * chunk;
 
   const WaitCtl wc{&sh->abort, p.status, p.timeout_ns};
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     at.b = at.g = at.blk = at.nblk = at.cost = 0;
     const long long x = mine + (lane > 0 ? chunk : 0);
     const int flat = x < plan.total ? locate(p, plan, static_cast<int>(x), at)
-                                    : plan.total - runs[plan.entries] * kRunCost;
+                                    : plan.total_blocks;
     const int from = __shfl_sync(0xffffffffu, flat, 0);
     blocks = __shfl_sync(0xffffffffu, flat, 1) - from;
     auto give = [&](int v, int& begin, int& finish) {
@@ -842,13 +843,13 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     if (lane == 0) {
       const long long cta_chunk = static_cast<long long>(chunk) * kWarps;
       auto take_part = [&](int kind, const RunPos& run) {
-        const int first = run.cost + kRunCost;   // cost position of its block 0
+        const int first = run.cost + plan.run_cost;   // cost position of its block 0
         const int cta0 = static_cast<int>(first / cta_chunk), cta1 = static_cast<int>((first + run.nblk - 1) / cta_chunk);
         sh->part_cta0[kind] = cta0;
         sh->part_n[kind] = cta1 - cta0 + 1;
         ready_counter(p.arrive + cta0, p.epoch);
       };
-      if (warp == 0 && w.at.blk > 0 && w.at.cost + kRunCost + w.at.nblk <= mine + cta_chunk) take_part(0, w.at);
+      if (warp == 0 && w.at.blk > 0 && w.at.cost + plan.run_cost + w.at.nblk <= mine + cta_chunk) take_part(0, w.at);
       if (warp == kWarps - 1 && end.blk > 0) take_part(1, end);
     }
 
@@ -863,8 +864,8 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       make_queries<D, G, NT>(p, raw, lane, q);
       st.reset();
       for (const int end = taken + cnt; taken < end;) {
-        const int stage = taken % kStages, stage1 = (taken + 1) % kStages;
         const bool two = taken + 1 < end;
+        const int stage = taken & (kStages - 1), stage1 = (taken + 1) & (kStages - 1);
         if (!wait_warp(bars + stage * 8, (taken / kStages) & 1, wc) ||
             (two && !wait_warp(bars + stage1 * 8, ((taken + 1) / kStages) & 1, wc))) {
           fail = true;
@@ -898,7 +899,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       // one that holds its start, from the piece that the other one, to which
       // it was the first thing to do, has left: with runs about as long as
       // shares that is most of them, and at the CTA's end they would queue.
-      const int run0 = w.at.cost + kRunCost, run1 = run0 + w.at.nblk;
+      const int run0 = w.at.cost + plan.run_cost, run1 = run0 + w.at.nblk;
       const bool to_previous = has_end && !has_start && warp > 0 && run0 >= mine - chunk;
       if (has_start && !has_end && warp + 1 < kWarps && run1 <= mine + 2 * chunk) {
         if (!wait_warp(smem_addr(&sh->ready[warp + 1]), 0, wc)) {
@@ -1034,9 +1035,15 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
   constexpr int W = D / 4;                       // lanes of a head's row, four columns each
   const int sub = lane / W, col = (lane % W) * 4;
   constexpr unsigned kGoesOn = 1u << 31;
+  const int heads = (p.group + 32 / W - 1) & ~(32 / W - 1);
   unsigned todo = ends | (parts_here[1] ? kGoesOn : 0u);
   for (bool parts = false;; parts = true) {
-    for (; todo != 0; todo &= todo - 1) {
+    // The heads of all jobs in one row, 32 / W of them a step, over the warps.
+    // (With the jobs one after another 64 sequences of 128 .. 4096 tokens took
+    // 19.4 us instead of 17.5.)
+    for (int hb = warp * (32 / W);; hb += kWarps * (32 / W)) {
+      for (; todo != 0 && hb >= p.group; todo &= todo - 1) hb -= heads;
+      if (todo == 0) break;
       const int bit = __ffs(todo) - 1;
       const int kind = bit == 31 ? 1 : 0;
       const int wi = kind ? kWarps - 1 : bit;
@@ -1072,7 +1079,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
         m_step = 2 * p.group;
         pitch = D;
       }
-      for (int hb = warp * (32 / W); hb < p.group; hb += kWarps * (32 / W)) {
+      {
         const bool live = hb + sub < p.group;
         const int h = live ? hb + sub : hb;
         float M = -INFINITY, l = 0.f;
