@@ -76,7 +76,9 @@ struct DecKv4Cfg {
   // and 10, uneven over the four schedulers, lose to 8.)
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = D == 128 ? 4 : 8;           // a power of two
+  // A power of two.  (8 with d = 64, as many bytes as 4 with d = 128: 8
+  // sequences of 20000 tokens, 2 KV heads, take 16.9 us instead of 14.6.)
+  static constexpr int kStages = 4;
   static constexpr int kRows = NT * 8;                       // head rows of a piece
   static constexpr int kPitch = D + 4;                       // floats; conflict-free stores
   static constexpr int kPiece = kRows * kPitch * 4;
