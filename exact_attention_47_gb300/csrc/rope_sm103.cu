@@ -24,15 +24,15 @@
 // = 64, three axes (41 MB) 10.3 us; an append of 7 ragged chunks (68 MB) 14.4
 // us.  About 3 us of each are the launch and its first trip to memory; the rest
 // is at the copy rate.  The 4-bit append of 14600 tokens of 16 + 4 heads (158
-// MB) takes 37 us: 1660 warp instructions a token, issued in 54% of the cycles,
+// MB) takes 36 us: 1560 warp instructions a token, issued in half of the cycles,
 // two thirds of them for the quantiser.
 // Copying rows ahead into a ring in shared memory, over the ends of tokens and
 // with equal shares for all warps, was slower (22.4 us instead of 21.5, 17.6
 // instead of 14.4): enough loads are in flight already, and each step then waits
-// for two more trips inside the SM.  So was loading the 4-bit rows before the
-// queries are done (51 us instead of 49 with the read-back), a fourth CTA a SM
-// with its 64 registers (50.7), and paired fp32 arithmetic in the quantiser
-// (52.2).
+// for two more trips inside the SM.  The 4-bit append and its read-back take
+// 47.8 us together; with the 4-bit rows loaded before the queries are done 51 us,
+// and a fourth CTA a SM with its 64 registers gains 0.7 us here and loses 0.25 of
+// 5.6 in a decode step.
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
@@ -186,35 +186,22 @@ __device__ __forceinline__ uint32_t quantise16(const float (&y)[2][8], uint32_t 
   uint32_t scale_bits = pack_bf16x2(0.f, __fdiv_rn(fmaxf(range, 0.f), 15.f)) & 0xffff0000u;
   if (scale_bits < 0x00800000u || !finite) scale_bits = 0;
   const float scale = __uint_as_float(scale_bits);
-  // The code is t / scale, nearly (t the clamped distance from low), rounded:
-  // off only next to a half-way point, where t - code scale, which one fma
-  // gives exactly enough, is half a step or more.  A few of a thousand bf16
-  // values lie exactly there.
+  // code = t / scale (t the clamped distance from low) rounded to even: the
+  // product with an approximate reciprocal, then one step with the remainder,
+  // which one fma gives exactly (Markstein's correction of a quotient), so that a
+  // half-way quotient is met exactly.  Of a thousand bf16 values a few lie
+  // exactly there.
   float inv = 0.f;
   if (scale_bits) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
-  const float top = 15.f * scale, half = 0.5f * scale;
-  float off = 0.f;
+  const float top = 15.f * scale;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float t = fminf(fmaxf(y[i][e] - lo, 0.f), top);
-      const float w = fmaf(t, inv, kRound);
-      code[i][e] = __float_as_uint(w);
-      off = fmaxf(off, fabsf(fmaf(kRound - w, scale, t)));
+      const float near = t * inv;
+      code[i][e] = __float_as_uint(fmaf(fmaf(-near, scale, t), inv, near) + kRound);
     }
-  if (off >= half && scale_bits) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = fminf(fmaxf(y[i][e] - lo, 0.f), top);
-        const float d = fmaf(kRound - __uint_as_float(code[i][e]), scale, t);
-        // Half-way goes to the even code.
-        const bool wrong = fabsf(d) > half || (fabsf(d) == half && (code[i][e] & 1u));
-        if (wrong) code[i][e] += d > 0.f ? 1u : ~0u;
-      }
-  }
   return finite ? scale_bits | low_bits : 0x7fc07fc0u;
 }
 

@@ -66,6 +66,39 @@ def test_unrotated_rows_are_the_oracles_bytes(d, group, Hkv):
         assert np.all(np.abs(to64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -23 * 15 * np.abs(ref).max(-1, keepdims=True))
 
 
+@pytest.mark.parametrize("d,group", [(64, 32), (128, 64)])
+def test_half_way_values_go_to_the_even_code(d, group):
+    """Groups from lowest to lowest + 15 scales whose values all lie half-way
+    between two codes, exactly: (k + 1/2) scale with scale = 1, 3, 5 or 7
+    times a power of two fits in bf16's 8 bits."""
+    T, Hkv = 160, 2
+    gen = torch.Generator().manual_seed(3)
+    shape = (T, Hkv, d // group)
+    scale = 2.0 * torch.randint(0, 4, shape, generator=gen) + 1
+    scale = scale.double() * 2.0 ** torch.randint(-100, 100, shape, generator=gen).double()
+    first = -torch.randint(0, 2, shape, generator=gen).double() * 8          # lowest, in scales
+    steps = torch.randint(0, 15, (*shape, group), generator=gen).double() + 0.5
+    steps[..., 0], steps[..., 1] = 0.0, 15.0
+    x = ((steps + first[..., None]) * scale[..., None]).reshape(T, Hkv, d)
+    assert torch.equal(x.to(BF).double(), x)
+    codes, words = oracle.kv4_quantise(x.float().numpy(), group)
+    whole = steps.reshape(T, Hkv, d).numpy()
+    assert np.array_equal(codes, np.rint(whole).astype(codes.dtype))         # half to even
+    want = np.zeros((T // 16, Hkv, attn.kv4_record_bytes(d, group)), np.uint8)
+    for t in range(T):
+        for h in range(Hkv):
+            for kind in (0, 1):
+                oracle.kv4_store(want[t // 16, h], kind, t % 16, codes[t, h], words[t, h], d, group)
+    kv = torch.zeros(want.shape, dtype=torch.uint8, device=DEV)
+    x = x.to(BF).to(DEV)
+    table = torch.arange(T // 16, dtype=torch.int32, device=DEV)[None]
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    attn.rope_append_paged_kv4(None, x, x, kv, table, torch.zeros_like(pos), pos, group)
+    torch.cuda.synchronize()
+    assert attn.device_status() == 0
+    assert np.array_equal(kv.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("d,group,rot,il,axes", [(128, 32, 128, False, 1), (128, 64, 64, True, 1),
                                                  (64, 32, 64, False, 3), (64, 64, 32, True, 2)])
 def test_rotated_rows_stand_for_the_rotation(d, group, rot, il, axes):
