@@ -30,9 +30,10 @@
 // with equal shares for all warps, was slower (22.4 us instead of 21.5, 17.6
 // instead of 14.4): enough loads are in flight already, and each step then waits
 // for two more trips inside the SM.  The 4-bit append and its read-back take
-// 47.8 us together; with the 4-bit rows loaded before the queries are done 51 us,
+// 46.7 us together; 4-bit rows loaded before the queries are done cost 2 us more,
 // and a fourth CTA a SM with its 64 registers gains 0.7 us here and loses 0.25 of
-// 5.6 in a decode step.
+// 5.6 in a decode step.  Equal shares of steps instead of whole tokens change
+// nothing (21.5, 10.2, 14.5 and 47.3 us).
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
