@@ -152,6 +152,15 @@ def _stream_handle(stream, device=None):
     return stream.cuda_stream
 
 
+def _on_stream(func, stream, tensor, *args):
+    """func(*args) with `stream` current, which is then also the one that what
+    the call allocates belongs to."""
+    if isinstance(tensor, torch.Tensor) and tensor.is_cuda:
+        _stream_handle(stream, tensor.device)
+    with torch.cuda.stream(stream):
+        return func(*args)
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -508,10 +517,12 @@ def _rope(inv_freq, positions, lead, pair_axis, interleaved, device):
 
 
 def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out, stream):
-    if stream is None:
-        done = _fast().rope(func == "rope_bwd", q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out)
-        if done is not None:
-            return done
+    if stream is not None:
+        return _on_stream(_rope_apply, stream, q, func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out,
+                          None)
+    done = _fast().rope(func == "rope_bwd", q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out)
+    if done is not None:
+        return done
     hq = _heads("q", q, None, 4)
     dev = q.device
     B, _, N, d = q.shape
@@ -537,7 +548,7 @@ def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, 
             ho.append(_heads(name, out, dev, 4))
             _need_shape(name, out, x.shape)
         outs.append(out)
-    _call(func, dev, hq, hk, ho[0], ho[1], rope, B, N, d, _stream_handle(stream, dev))
+    _call(func, dev, hq, hk, ho[0], ho[1], rope, B, N, d, _stream_handle(None, dev))
     del keep                                       # the library has read the axis table by now
     return tuple(outs)
 
@@ -619,7 +630,10 @@ def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions
     Returns q_out [T,Hq,d] (new unless given; its padding rows are left as
     they were), or None without q.
     """
-    if stream is None and v_cache is not None:
+    if stream is not None:
+        return _on_stream(rope_append_paged, stream, k, q, k, v, k_cache, v_cache, block_table, seq_ids, positions, inv_freq,
+                          rope_positions, pair_axis, interleaved, q_out)
+    if v_cache is not None:                        # (None: a 4-bit cache)
         done = _fast().append(q, k, v, k_cache, v_cache, block_table, seq_ids, positions, 0, inv_freq, rope_positions,
                               pair_axis, interleaved, q_out)
         if done is not None:
@@ -635,7 +649,7 @@ def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions
         raise ValueError("caches must have k's heads and head dim")
     _call("rope_append_paged", dev, hq, hk, hv, ho, rope[0], _ptr(k_cache), _ptr(v_cache),
           _ptr(block_table), _ptr(seq_ids), _ptr(positions), T, block_table.shape[0], d, bs, block_table.shape[1], nb,
-          _stream_handle(stream, dev))
+          _stream_handle(None, dev))
     return q_out
 
 
@@ -664,11 +678,13 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
     [num_blocks,Hkv,kv4_record_bytes(d, group)] uint8 (updated in place), 4-bit
     codes with a bf16 (min, scale) per ``group`` (32 or 64) consecutive
     elements of a key or value.  Returns q_out (or None without q)."""
-    if stream is None:
-        done = _fast().append(q, k, v, kv_cache, None, block_table, seq_ids, positions, group, inv_freq, rope_positions,
-                              pair_axis, interleaved, q_out)
-        if done is not None:
-            return done[0]
+    if stream is not None:
+        return _on_stream(rope_append_paged_kv4, stream, k, q, k, v, kv_cache, block_table, seq_ids, positions, group,
+                          inv_freq, rope_positions, pair_axis, interleaved, q_out)
+    done = _fast().append(q, k, v, kv_cache, None, block_table, seq_ids, positions, group, inv_freq, rope_positions,
+                          pair_axis, interleaved, q_out)
+    if done is not None:
+        return done[0]
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
     nb, Hkv = _need_kv4(kv_cache, d, group, dev)
@@ -676,7 +692,7 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
         raise ValueError("kv_cache must have k's heads")
     _call("rope_append_paged_kv4", dev, hq, hk, hv, ho, rope[0], _ptr(kv_cache), group,
           _ptr(block_table), _ptr(seq_ids), _ptr(positions), T, block_table.shape[0], d, BLOCK_SIZE,
-          block_table.shape[1], nb, _stream_handle(stream, dev))
+          block_table.shape[1], nb, _stream_handle(None, dev))
     return q_out
 
 
@@ -684,10 +700,11 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
     """The values that cached tokens of a 4-bit cache stand for: row t is
     position positions[t] of sequence seq_ids[t] ([T] int32; negative
     sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16."""
-    if stream is None:
-        done = _fast().read(kv_cache, block_table, seq_ids, positions, d, group, k, v)
-        if done is not None:
-            return done
+    if stream is not None:
+        return _on_stream(kv4_read_paged, stream, kv_cache, kv_cache, block_table, seq_ids, positions, d, group, k, v)
+    done = _fast().read(kv_cache, block_table, seq_ids, positions, d, group, k, v)
+    if done is not None:
+        return done
     if not isinstance(seq_ids, torch.Tensor) or seq_ids.dim() != 1:
         raise ValueError("seq_ids must be a [T] tensor")
     nb, Hkv = _need_kv4(kv_cache, d, group, None)
@@ -696,7 +713,7 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
     k = _output("k", k, (T, Hkv, d), torch.bfloat16, dev)
     v = _output("v", v, (T, Hkv, d), torch.bfloat16, dev)
     _call("kv4_read_paged", dev, _ptr(kv_cache), group, _ptr(block_table), _ptr(seq_ids), _ptr(positions), _ptr(k),
-          _ptr(v), T, block_table.shape[0], Hkv, d, BLOCK_SIZE, block_table.shape[1], nb, _stream_handle(stream, dev))
+          _ptr(v), T, block_table.shape[0], Hkv, d, BLOCK_SIZE, block_table.shape[1], nb, _stream_handle(None, dev))
     return k, v
 
 
@@ -713,10 +730,12 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
 
     Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32 or None).
     """
-    if stream is None:
-        done = _fast().decode(q, kv_cache, block_table, seq_lens, group, scale, o, lse, workspace, return_lse)
-        if done is not None:
-            return done
+    if stream is not None:
+        return _on_stream(attn_decode_paged_kv4, stream, q, q, kv_cache, block_table, seq_lens, group, scale, o, lse,
+                          workspace, return_lse)
+    done = _fast().decode(q, kv_cache, block_table, seq_lens, group, scale, o, lse, workspace, return_lse)
+    if done is not None:
+        return done
     _need_cuda("q", q, torch.bfloat16)
     dev = q.device
     if q.dim() != 3:
@@ -737,7 +756,7 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
     workspace = _workspace("workspace", workspace, attn_decode_paged_kv4_workspace_size(S, Hq, Hkv, d), dev)
     _call("attn_decode_paged_kv4", dev, _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), S, Hq, Hkv, d,
           group, BLOCK_SIZE, table_shape[1], nb, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _stream_handle(stream, dev))
+          workspace.numel() * workspace.element_size(), _stream_handle(None, dev))
     return o, lse
 
 

@@ -1,6 +1,6 @@
 """Both ways of making a rotary, append or 4-bit-cache call give the same
-bytes: the usual case through csrc/fast_calls.cpp (no stream given), and the
-Python one (a stream given).  Errors are the Python way's."""
+bytes: the usual case through csrc/fast_calls.cpp, and the Python one.  Errors
+are the Python way's."""
 
 import threading
 
@@ -18,35 +18,47 @@ DEV = "cuda:0"
 BF = torch.bfloat16
 
 
+class Nothing:
+    """Stands in for the module of the fast calls: nothing is the usual case."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 @pytest.fixture
 def fast_only(monkeypatch):
-    """Fails where a call without a stream takes the Python way."""
-    real = _binding._call
+    """Fails where a call takes the Python way, unless `long_way` is set: then
+    it has to."""
+    real_call, real_fast = _binding._call, _binding._fast
 
     def call(func, device, *args):
-        assert call.allowed, "%s took the long way" % func
-        return real(func, device, *args)
+        assert call.long_way, "%s took the long way" % func
+        return real_call(func, device, *args)
 
-    call.allowed = False
+    call.long_way = False
     monkeypatch.setattr(_binding, "_call", call)
+    monkeypatch.setattr(_binding, "_fast", lambda: Nothing() if call.long_way else real_fast())
     return call
 
 
 def both(flag, f, *caches):
-    """f(stream) by both ways, each on its own copy of the caches."""
+    """f() by both ways and, the fast one, on a stream given, each on its own
+    copy of the caches."""
     got = []
-    for stream in (None, torch.cuda.current_stream()):
-        flag.allowed = stream is not None
+    for long_way, stream in ((False, None), (True, None), (False, torch.cuda.Stream()), (True, torch.cuda.Stream())):
+        flag.long_way = long_way
         mine = [c.clone() for c in caches]
+        torch.cuda.synchronize()
         out = f(stream, *mine)
+        torch.cuda.synchronize()
         got.append([x for x in (out if isinstance(out, tuple) else (out,)) if x is not None] + mine)
-    flag.allowed = False
-    torch.cuda.synchronize()
+    flag.long_way = False
     assert attn.device_status() == 0
-    assert len(got[0]) == len(got[1])
-    for a, b in zip(*got):
-        assert a.shape == b.shape and a.dtype == b.dtype and a.stride() == b.stride()
-        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    for other in got[1:]:
+        assert len(got[0]) == len(other)
+        for a, b in zip(got[0], other):
+            assert a.shape == b.shape and a.dtype == b.dtype and a.stride() == b.stride()
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
     return got[0]
 
 
@@ -155,3 +167,37 @@ def test_threads_on_streams_of_their_own():
         t.join()
     torch.cuda.synchronize()
     assert not bad and attn.device_status() == 0
+
+
+def test_what_a_call_on_a_given_stream_allocates_is_that_streams():
+    """Memory freed on the current stream, where writes to it are still to
+    come, is not handed to a call on another stream."""
+    d, group, S, Hq = 128, 32, 64, 8
+    q, rec, table, lens = (t.to(DEV) for t in decode_case([40] * S, Hq, 2, d, group, seed=8)[:4])
+    want = attn.attn_decode_paged_kv4(q, rec, table, lens, group)[0]
+    x = randn(5, 1, Hq, S, d).to(DEV)
+    f, pos = workloads.rope_inv_freq(d).to(DEV), torch.arange(S, dtype=torch.int32, device=DEV)
+    turned = attn.rope_fwd(x, None, pos, f)[0]
+    side = torch.cuda.Stream()
+    for name, call, ref in (("decode", lambda: attn.attn_decode_paged_kv4(q, rec, table, lens, group, stream=side)[0], want),
+                            ("rope", lambda: attn.rope_fwd(x, None, pos, f, stream=side)[0], turned)):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        held = [torch.empty_like(ref) for _ in range(8)]
+        torch.cuda._sleep(20_000_000)
+        for h in held:
+            h.fill_(7.0)
+        del held, h
+        got = call()
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref), name
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    x = randn(5, 1, 2, 8, 64).to(DEV)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        attn.rope_fwd(x, None, torch.arange(8, dtype=torch.int32, device=DEV), workloads.rope_inv_freq(64).to(DEV),
+                      stream=Elsewhere())
