@@ -25,7 +25,8 @@
 //
 // Work split: the blocks of all (sequence, KV head) runs in one flat order,
 // cut into equal costs for every warp of a one-wave grid (a run costs a few
-// blocks more than it has, for its queries and its end).  A warp
+// blocks more than it has, for its queries and its end), or a run to each CTA
+// where that is shorter.  A warp
 // streams its blocks through a ring of its own in shared memory, one bulk copy
 // per (block, head) record, and keeps its own running softmax, so nothing
 // inside the CTA waits for anything else until the end.  A run that a warp
@@ -39,7 +40,7 @@
 // (lengths, table, record: 4 us) and, at the end, the merge of a CTA's pieces,
 // the arrival and the merge of published parts (4 to 5 us, over 1 us for each
 // trip to what another SM has written).  8 sequences of 30k .. 131k tokens (195
-// MB) take 43.9 us, 64 of 128 .. 4096 (44 MB) 17.5 us, one of 100 6.6 us.  With d = 64 (4.8 TB/s) and with
+// MB) take 44.0 us, 64 of 128 .. 4096 (44 MB) 17.9 us, one of 100 6.2 us.  With d = 64 (4.8 TB/s) and with
 // two column tiles (3.3 at d = 64, 4.0 at d = 128) the arithmetic of a block
 // takes longer than its bytes: its instructions wait on one another, at two to
 // three warps a scheduler.
@@ -102,7 +103,7 @@ struct DecKv4Shared {
   uint64_t full[16][8];
   uint64_t ready[16];              // a warp's first piece is there for the warp before it
   WarpMeta meta[16];
-  int2 scan[16];
+  int4 scan[16];
   int part_cta0[2], part_n[2];     // parts of this CTA (see below): their run's first CTA and part count (0: none)
   int last[2];
   int abort;
@@ -140,7 +141,8 @@ struct Plan {
   const int* cost;
   const int* runs;
   const int* blocks;
-  int entries, per, total, total_blocks, run_cost;
+  int entries, per, total, total_blocks, total_runs, run_cost;
+  bool one_run;                    // CTA i takes run i
   __device__ __forceinline__ int seq_blocks(const DecKv4Params& p, int b) const {
     return per == 1 ? blocks[b] : (kv4_seq_len(p, b) + kBS - 1) / kBS;
   }
@@ -172,6 +174,24 @@ __device__ __forceinline__ int locate(const DecKv4Params& p, const Plan& plan, i
   at.cost = start + at.g * cost;
   at.blk = max(0, x - at.cost - plan.run_cost);
   return at.cost - (runs + at.g) * plan.run_cost + at.blk;
+}
+
+// Run r < the number of runs, from its first block.
+__device__ __forceinline__ void locate_run(const DecKv4Params& p, const Plan& plan, int r, RunPos& at) {
+  int e = 0;                                     // last entry whose runs start at or before r
+  for (int step = 1 << (31 - __clz(plan.entries)); step > 0; step >>= 1)
+    if (e + step < plan.entries && plan.runs[e + step] <= r) e += step;
+  int start = plan.runs[e];
+  at.b = e * plan.per;
+  at.nblk = plan.seq_blocks(p, at.b);
+  for (int i = 1; i < plan.per; ++i) {
+    const int c = at.nblk > 0 ? p.Hkv : 0;
+    if (start + c > r) break;
+    start += c;
+    at.nblk = plan.seq_blocks(p, ++at.b);
+  }
+  at.g = r - start;
+  at.blk = 0;
 }
 
 // Walk over the runs of a warp's share.
@@ -701,7 +721,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     // Thread t sums entries [t E, (t + 1) E); warp scan, then the warps' sums.
     constexpr int E = (kPlan + kThreads - 1) / kThreads;
     const int each = (plan.entries + kThreads - 1) / kThreads;          // <= E
-    int ec[E], er[E], c = 0, r = 0;
+    int ec[E], er[E], c = 0, r = 0, longest = 0;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -714,6 +734,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
         bad |= L < 0 || L > p.max_blocks * kBS;
         const int blocks = ((L < 0 ? 0 : min(L, p.max_blocks * kBS)) + kBS - 1) / kBS;
         if (plan.per == 1) seq_blocks[b] = blocks;
+        longest = max(longest, blocks);
         if (blocks > 0) {
           c += blocks * p.Hkv;
           r += p.Hkv;
@@ -722,6 +743,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, kDevBadSeqLen);
     int cs = c, rs = r;
+    longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int cy = __shfl_up_sync(0xffffffffu, cs, o), ry = __shfl_up_sync(0xffffffffu, rs, o);
@@ -730,19 +752,32 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
         rs += ry;
       }
     }
-    if (lane == 31) sh->scan[warp] = make_int2(cs, rs);
+    if (lane == 31) sh->scan[warp] = make_int4(cs, rs, longest, 0);
     __syncthreads();
     int c0 = cs - c, r0 = rs - r, total = 0, total_runs = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const int2 v = sh->scan[w];
+      const int4 v = sh->scan[w];
       if (w < warp) {
         c0 += v.x;
         r0 += v.y;
       }
       total += v.x;
       total_runs += v.y;
+      longest = max(longest, v.z);
     }
+    plan.total_runs = total_runs;
+    // A run to each CTA, where there are no more of them than CTAs and the
+    // longest takes a CTA's warps no more than 3.5 blocks each (6 with two column
+    // tiles, whose merges cost more, or d = 64, whose blocks cost less) beyond an
+    // equal share of all: that is what merging across CTAs costs.  Measured
+    // against equal shares (us): 4 sequences of 100 .. 300 tokens, 2 KV heads, 6.9
+    // and 9.9; 32 of 400 .. 600, 9.3 and 11.7; 64 of 1500, 13.6 and 16.1; 30 of 900
+    // .. 1000, 4 KV heads of 16, 10.0 and 13.9; and where the rule says no, 4 of
+    // 900, 10.5 and 9.6.
+    constexpr int kSpare = (NT == 1 && D == 128 ? 7 : 12) * kWarps / 2;
+    plan.one_run = total_runs <= static_cast<int>(gridDim.x) &&
+                   static_cast<long long>(longest - kSpare) * static_cast<int>(gridDim.x) <= total;
     // What a run costs beyond its blocks.  A long share spends about 4 blocks'
     // time on a run (its queries, its end).  A share is at least run_cost + 1
     // blocks, though, a pass of two blocks takes a warp 0.9 us when it is alone,
@@ -765,15 +800,25 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
   __syncthreads();
   // Every share but the last of all holds at least one block (a share longer
   // than a run's start cost cannot lie inside it).
-  const int chunk = max(plan.run_cost + 1, (plan.total - 1) / shares + 1);
+  int chunk = max(plan.run_cost + 1, (plan.total - 1) / shares + 1);
+  Walk w;
+  if (plan.one_run) {
+    w.at.nblk = 0;
+    if (static_cast<int>(blockIdx.x) < plan.total_runs) locate_run(p, plan, static_cast<int>(blockIdx.x), w.at);
+    chunk = ((w.at.nblk + kWarps - 1) / kWarps + 1) & ~1;        // whole passes
+  }
   const long long mine = (static_cast<long long>(blockIdx.x) * kWarps + warp) * chunk;
 
   const WaitCtl wc{&sh->abort, p.status, p.timeout_ns};
   WarpMeta meta = {};
   int blocks = 0;
-  Walk w;
   RunPos end;
-  {
+  if (plan.one_run) {
+    end.blk = 0;
+    w.at.cost = static_cast<int>(blockIdx.x) * kWarps * chunk - plan.run_cost;
+    w.at.blk = warp * chunk;
+    blocks = max(0, min(chunk, w.at.nblk - w.at.blk));
+  } else {
     // Lane 0 finds where this warp's share begins, the other lanes where it
     // ends.
     RunPos at;

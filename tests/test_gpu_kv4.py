@@ -214,6 +214,29 @@ def test_one_sequence(n):
     check_decode(o, lse, *case, 0.09, 128, 32, "one sequence")
 
 
+@pytest.mark.parametrize("S,Hq,Hkv,d,group,most", [
+    (1, 8, 1, 128, 32, 700), (7, 15, 3, 128, 32, 110), (20, 16, 2, 64, 64, 600), (76, 4, 2, 128, 64, 400),
+    (152, 1, 1, 64, 32, 300), (153, 1, 1, 64, 32, 300), (38, 64, 4, 64, 32, 250), (30, 9, 3, 128, 32, 1600),
+    (50, 2, 2, 64, 32, 17), (3, 32, 2, 128, 64, 90)])
+def test_a_run_to_each_cta_or_shared(S, Hq, Hkv, d, group, most):
+    """About as many (sequence, KV head) runs as SMs, short ones: each is one
+    CTA's, or cut into equal shares, on either side of the rule."""
+    g = torch.Generator().manual_seed(S)
+    for lens in ([most] * S, torch.randint(0, most + 1, (S,), generator=g).tolist(),
+                 torch.randint(most - most // 4, most + 1, (S,), generator=g).tolist()):
+        q, rec, table, lens = decode_case(lens, Hq, Hkv, d, group, seed=S + 1)
+        check_decode(*run(q, rec, table, lens, group), q, rec, table, lens, d ** -0.5, d, group)
+
+
+def test_few_short_runs_among_many_empty_sequences():
+    """More sequences than the plan has entries, most of them empty."""
+    lens = [0] * 2500
+    for i, n in ((0, 40), (1, 3), (1023, 200), (1024, 1), (1025, 333), (2048, 16), (2499, 17)):
+        lens[i] = n
+    q, rec, table, lens = decode_case(lens, 4, 2, 128, 32, seed=9)
+    check_decode(*run(q, rec, table, lens, 32), q, rec, table, lens, 128 ** -0.5, 128, 32)
+
+
 def test_many_sequences_and_heads():
     gen = torch.Generator().manual_seed(3)
     lens = torch.randint(0, 300, (500,), generator=gen).tolist()
