@@ -25,8 +25,8 @@
 //
 // Work split: the blocks of all (sequence, KV head) runs in one flat order,
 // cut into equal costs for every warp of a one-wave grid (a run costs a few
-// blocks more than it has, for its queries and its end), or a run to each CTA
-// where that is shorter.  A warp
+// blocks more than it has, for its queries and its end), or a team of a CTA's
+// warps to each run where that is shorter.  A warp
 // streams its blocks through a ring of its own in shared memory, one bulk copy
 // per (block, head) record, and keeps its own running softmax, so nothing
 // inside the CTA waits for anything else until the end.  A run that a warp
@@ -35,12 +35,12 @@
 // and the CTA that arrives last merges the parts.
 //
 // What bounds it (GB300, one column tile, d = 128): further blocks of long
-// contexts stream at 6.4 TB/s, the rate of a copy; about 11.5 us of a call that
+// contexts stream at 6.3 TB/s, nearly the rate of a copy; about 11.5 us of a call that
 // fills the GPU are latency, three dependent reads before the first block
 // (lengths, table, record: 4 us) and, at the end, the merge of a CTA's pieces,
 // the arrival and the merge of published parts (4 to 5 us, over 1 us for each
 // trip to what another SM has written).  8 sequences of 30k .. 131k tokens (195
-// MB) take 44.0 us, 64 of 128 .. 4096 (44 MB) 17.9 us, one of 100 6.2 us.  With d = 64 (4.8 TB/s) and with
+// MB) take 44.5 us, 64 of 128 .. 4096 (44 MB) 17.7 us, one of 100 6.1 us.  With d = 64 (4.8 TB/s) and with
 // two column tiles (3.3 at d = 64, 4.0 at d = 128) the arithmetic of a block
 // takes longer than its bytes: its instructions wait on one another, at two to
 // three warps a scheduler.
@@ -100,10 +100,11 @@ struct WarpMeta {
 };
 
 struct DecKv4Shared {
-  uint64_t full[16][8];
+  uint64_t full[16][4];
   uint64_t ready[16];              // a warp's first piece is there for the warp before it
   WarpMeta meta[16];
   int4 scan[16];
+  longlong2 reach[16];             // where the shares of the warps before and behind begin and end
   int part_cta0[2], part_n[2];     // parts of this CTA (see below): their run's first CTA and part count (0: none)
   int last[2];
   int abort;
@@ -142,7 +143,7 @@ struct Plan {
   const int* runs;
   const int* blocks;
   int entries, per, total, total_blocks, total_runs, run_cost;
-  bool one_run;                    // CTA i takes run i
+  int team;                        // warps that share a run (0: equal shares of all)
   __device__ __forceinline__ int seq_blocks(const DecKv4Params& p, int b) const {
     return per == 1 ? blocks[b] : (kv4_seq_len(p, b) + kBS - 1) / kBS;
   }
@@ -684,6 +685,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
     sh->part_n[0] = sh->part_n[1] = 0;
     sh->abort = 0;
   }
+  static_assert(kStages <= 4, "");
   if (lane < kStages) mbar_init(smem_addr(&sh->full[warp][lane]), 1);
   if (lane == kStages) mbar_init(smem_addr(&sh->ready[warp]), 1);
   fence_mbar_init();
@@ -767,17 +769,23 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       longest = max(longest, v.z);
     }
     plan.total_runs = total_runs;
-    // A run to each CTA, where there are no more of them than CTAs and the
-    // longest takes a CTA's warps no more than 3.5 blocks each (6 with two column
-    // tiles, whose merges cost more, or d = 64, whose blocks cost less) beyond an
-    // equal share of all: that is what merging across CTAs costs.  Measured
-    // against equal shares (us): 4 sequences of 100 .. 300 tokens, 2 KV heads, 6.9
-    // and 9.9; 32 of 400 .. 600, 9.3 and 11.7; 64 of 1500, 13.6 and 16.1; 30 of 900
-    // .. 1000, 4 KV heads of 16, 10.0 and 13.9; and where the rule says no, 4 of
-    // 900, 10.5 and 9.6.
-    constexpr int kSpare = (NT == 1 && D == 128 ? 7 : 12) * kWarps / 2;
-    plan.one_run = total_runs <= static_cast<int>(gridDim.x) &&
-                   static_cast<long long>(longest - kSpare) * static_cast<int>(gridDim.x) <= total;
+    // Or a team of warps to each run: as many as there are for it, a CTA's
+    // warps or a half, a third .. of them.  Then nothing has to be merged across
+    // CTAs, which costs about as much as 3.5 blocks (6 with two column tiles,
+    // whose merges cost more, or d = 64, whose blocks cost less): it is taken
+    // where the longest run brings its team no more than that beyond an equal
+    // share of all blocks.  Measured against equal shares (us; sequences x tokens,
+    // KV heads): 4 x 100 .. 300, 2, 7.0 and 9.9; 32 x 400 .. 600, 2, 9.4 and 11.7;
+    // 64 x 1500, 2, 13.7 and 16.1; 256 x 20 .. 90, 2, 9.1 and 12.0; 30 x 900 ..
+    // 1000, 4 of 16 heads, 10.1 and 13.9; 256 x 1 .. 100, the same, 9.8 and 13.7;
+    // and where the rule says no, 4 x 900, 2, 10.5 and 9.6.
+    int team = 0;
+#pragma unroll
+    for (int k = kWarps; k >= 1; --k)
+      if (kWarps % k == 0 && total_runs <= k * static_cast<int>(gridDim.x)) team = kWarps / k;
+    constexpr int kSpare2 = NT == 1 && D == 128 ? 7 : 12;        // in half blocks
+    if (static_cast<long long>(2 * longest - kSpare2 * team) * shares > 2LL * team * total) team = 0;
+    plan.team = team;
     // What a run costs beyond its blocks.  A long share spends about 4 blocks'
     // time on a run (its queries, its end).  A share is at least run_cost + 1
     // blocks, though, a pass of two blocks takes a warp 0.9 us when it is alone,
@@ -802,21 +810,27 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
   // than a run's start cost cannot lie inside it).
   int chunk = max(plan.run_cost + 1, (plan.total - 1) / shares + 1);
   Walk w;
-  if (plan.one_run) {
+  int place = static_cast<int>(blockIdx.x) * kWarps + warp;
+  if (plan.team != 0) {
+    place = warp % plan.team;
+    const int run = static_cast<int>(blockIdx.x) + warp / plan.team * static_cast<int>(gridDim.x);
     w.at.nblk = 0;
-    if (static_cast<int>(blockIdx.x) < plan.total_runs) locate_run(p, plan, static_cast<int>(blockIdx.x), w.at);
-    chunk = ((w.at.nblk + kWarps - 1) / kWarps + 1) & ~1;        // whole passes
+    if (run < plan.total_runs) locate_run(p, plan, run, w.at);
+    chunk = ((w.at.nblk + plan.team - 1) / plan.team + 1) & ~1;  // whole passes
   }
-  const long long mine = (static_cast<long long>(blockIdx.x) * kWarps + warp) * chunk;
+  const long long mine = static_cast<long long>(place) * chunk;
+  // (Read back at a run's end: kept in registers, they cost the loop over the
+  // blocks 1 to 2%.)
+  if (lane == 0) sh->reach[warp] = make_longlong2(mine - chunk, mine + 2LL * chunk);
 
   const WaitCtl wc{&sh->abort, p.status, p.timeout_ns};
   WarpMeta meta = {};
   int blocks = 0;
   RunPos end;
-  if (plan.one_run) {
+  if (plan.team != 0) {
     end.blk = 0;
-    w.at.cost = static_cast<int>(blockIdx.x) * kWarps * chunk - plan.run_cost;
-    w.at.blk = warp * chunk;
+    w.at.cost = -plan.run_cost;                  // positions are those within the run
+    w.at.blk = place * chunk;
     blocks = max(0, min(chunk, w.at.nblk - w.at.blk));
   } else {
     // Lane 0 finds where this warp's share begins, the other lanes where it
@@ -911,8 +925,8 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       make_queries<D, G, NT>(p, raw, lane, q);
       st.reset();
       for (const int end = taken + cnt; taken < end;) {
+        const int stage = taken % kStages, stage1 = (taken + 1) % kStages;
         const bool two = taken + 1 < end;
-        const int stage = taken & (kStages - 1), stage1 = (taken + 1) & (kStages - 1);
         if (!wait_warp(bars + stage * 8, (taken / kStages) & 1, wc) ||
             (two && !wait_warp(bars + stage1 * 8, ((taken + 1) / kStages) & 1, wc))) {
           fail = true;
@@ -947,8 +961,9 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       // it was the first thing to do, has left: with runs about as long as
       // shares that is most of them, and at the CTA's end they would queue.
       const int run0 = w.at.cost + plan.run_cost, run1 = run0 + w.at.nblk;
-      const bool to_previous = has_end && !has_start && warp > 0 && run0 >= mine - chunk;
-      if (has_start && !has_end && warp + 1 < kWarps && run1 <= mine + 2 * chunk) {
+      const longlong2 reach = sh->reach[warp];
+      const bool to_previous = has_end && !has_start && warp > 0 && run0 >= reach.x;
+      if (has_start && !has_end && warp + 1 < kWarps && run1 <= reach.y) {
         if (!wait_warp(smem_addr(&sh->ready[warp + 1]), 0, wc)) {
           fail = true;
           break;

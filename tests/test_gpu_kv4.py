@@ -217,10 +217,12 @@ def test_one_sequence(n):
 @pytest.mark.parametrize("S,Hq,Hkv,d,group,most", [
     (1, 8, 1, 128, 32, 700), (7, 15, 3, 128, 32, 110), (20, 16, 2, 64, 64, 600), (76, 4, 2, 128, 64, 400),
     (152, 1, 1, 64, 32, 300), (153, 1, 1, 64, 32, 300), (38, 64, 4, 64, 32, 250), (30, 9, 3, 128, 32, 1600),
-    (50, 2, 2, 64, 32, 17), (3, 32, 2, 128, 64, 90)])
-def test_a_run_to_each_cta_or_shared(S, Hq, Hkv, d, group, most):
-    """About as many (sequence, KV head) runs as SMs, short ones: each is one
-    CTA's, or cut into equal shares, on either side of the rule."""
+    (50, 2, 2, 64, 32, 17), (3, 32, 2, 128, 64, 90), (100, 6, 3, 128, 32, 100), (110, 4, 4, 64, 64, 130),
+    (300, 2, 2, 128, 64, 60), (900, 2, 2, 64, 32, 33), (100, 64, 4, 64, 32, 100), (250, 36, 4, 64, 64, 70),
+    (95, 32, 2, 128, 32, 200)])
+def test_a_team_of_warps_to_each_run_or_equal_shares(S, Hq, Hkv, d, group, most):
+    """Up to as many (sequence, KV head) runs as warps, short ones: each is some
+    warps', or cut into equal shares, on either side of the rule."""
     g = torch.Generator().manual_seed(S)
     for lens in ([most] * S, torch.randint(0, most + 1, (S,), generator=g).tolist(),
                  torch.randint(most - most // 4, most + 1, (S,), generator=g).tolist()):
