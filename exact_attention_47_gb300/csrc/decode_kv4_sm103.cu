@@ -62,6 +62,7 @@ constexpr int kMaxCtas = 256;
 // Lazy stabilisers (see attn_decode_paged): the running maximum moves only
 // when a score exceeds it by more than kTau (log2 units).
 constexpr float kTau = 8.f;
+constexpr float kGrid = 12288.f;   // 1.5 2^13: x + kGrid - kGrid is x to a multiple of 2^-10
 // Entries of the plan's prefix sums (one per sequence up to this many, then
 // one per several).
 constexpr int kPlan = 1024;
@@ -290,6 +291,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float word_scale(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float word_min(uint32_t w) { return __uint_as_float(w << 16); }
 
+// (stab + log2(l)) ln 2, the whole part of the logarithm added to the
+// stabiliser first (exactly): an LSE near 0 keeps its bits.
+__device__ __forceinline__ float lse_of(float stab, float l) {
+  const int k = static_cast<int>(__float_as_uint(l) >> 23) - 127;
+  if (k <= -127 || k >= 128) return (stab + log2f(l)) * kLn2;    // subnormal, infinite, NaN
+  const float part = __uint_as_float((__float_as_uint(l) & 0x7fffffu) | 0x3f800000u);
+  return ((stab + static_cast<float>(k)) + log2f(part)) * kLn2;
+}
+
 // N words from shared memory at address + OFFSET.
 template <int N, int OFFSET>
 __device__ __forceinline__ void load_words(uint32_t address, uint32_t (&r)[N]) {
@@ -458,7 +468,9 @@ struct RunState {
 #pragma unroll
         for (int o_ = 4; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o_));
         const float top = stab[nt][h] + before;  // the running maximum
-        const float to = (mx > top + kTau ? mx : top) - now;
+        // (To a multiple of 2^-10, so that adding whole numbers to a stabiliser,
+        // here and for the LSE, rounds nothing.)
+        const float to = __fsub_rn(__fadd_rn(mx > top + kTau ? mx : top, kGrid), kGrid) - now;
         f[h] = to == stab[nt][h] ? 1.f : ex2(stab[nt][h] - to);
         stab[nt][h] = to;
         limit[nt][h] = (to + now + kTau) / back[nt][h];
@@ -1009,7 +1021,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
             for (int h = 0; h < 2; ++h) {
               const int hd = nt * 8 + 2 * c + h;
               if (hd < p.group)
-                p.lse[h0 + hd] = st.l[nt][h] == 0.f ? -INFINITY : (st.stab[nt][h] + __log2f(st.l[nt][h])) * kLn2;
+                p.lse[h0 + hd] = st.l[nt][h] == 0.f ? -INFINITY : lse_of(st.stab[nt][h], st.l[nt][h]);
             }
           }
         }
@@ -1201,7 +1213,7 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
           pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
           pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
           *reinterpret_cast<uint2*>(p.o + (h0 + h) * D + col) = pk;
-          if (col == 0 && p.lse != nullptr) p.lse[h0 + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
+          if (col == 0 && p.lse != nullptr) p.lse[h0 + h] = l == 0.f ? -INFINITY : lse_of(M, l);
         } else {
           const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + kind) * p.group + h;
           *reinterpret_cast<float4*>(p.ws_o + slot * D + col) = acc;

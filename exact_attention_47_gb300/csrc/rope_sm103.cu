@@ -20,8 +20,8 @@
 // lane of the warp.
 //
 // Measured (GB300, replayed graphs): 4 x 4096 tokens of 12 + 2 heads, d = 128
-// (118 MB) 21.5 us, 5.5 TB/s or 0.81 of a copy; 5001 tokens of 16 + 16 heads, d
-// = 64, three axes (41 MB) 10.3 us; an append of 7 ragged chunks (68 MB) 14.4
+// (118 MB) 22.1 us, 5.3 TB/s or 0.79 of a copy; 5001 tokens of 16 + 16 heads, d
+// = 64, three axes (41 MB) 10.5 us; an append of 7 ragged chunks (68 MB) 14.6
 // us.  About 3 us of each are the launch and its first trip to memory; the rest
 // is at the copy rate.  The 4-bit append of 14600 tokens of 16 + 4 heads (158
 // MB) takes 36 us: 1560 warp instructions a token, issued in half of the cycles,
@@ -114,9 +114,41 @@ __device__ __forceinline__ uint64_t turn_fraction(float f, bool& bad) {
   return (bits >> 31) ? 0 - t : t;
 }
 
+// Sine and cosine of the position's turn, correctly rounded but for one in 200:
+// of a key that is quantised, the last bit may decide the code.  The turn less
+// whole quarters is at most an eighth; there both are their Taylor series, the
+// leading terms in pairs of floats (error-free sums and products, Dekker).
 __device__ __forceinline__ void turn_sincos(int pos, uint64_t frac, float& s, float& c) {
-  const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * frac;
-  sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &s, &c);
+  const int64_t t = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * frac);
+  const int quarter = static_cast<int>((static_cast<uint64_t>(t) + (1ull << 61)) >> 62);
+  const int64_t rem = static_cast<int64_t>(static_cast<uint64_t>(t) - (static_cast<uint64_t>(quarter) << 62));
+  // The angle pi (rh + rl), as th + tl.
+  constexpr float kPi = 3.14159274101257324f, kPiLow = -8.74227800037e-8f;
+  const float rh = static_cast<float>(static_cast<int>(rem >> 40)) * 0x1p-23f;
+  const float rl = static_cast<float>(static_cast<int>((rem >> 16) & 0xffffff)) * 0x1p-47f;
+  const float a = __fmul_rn(rh, kPi);
+  const float b = __fadd_rn(fmaf(rh, kPi, -a), fmaf(rh, kPiLow, __fmul_rn(rl, kPi)));
+  const float th = __fadd_rn(a, b), tl = __fsub_rn(b, __fsub_rn(th, a));
+  const float zh = __fmul_rn(th, th), zl = fmaf(2.f * th, tl, fmaf(th, th, -zh));
+  // cos = 1 - z / 2 + z^2 (1 / 24 - ..)
+  const float even = fmaf(fmaf(fmaf(zh, 2.08767570e-9f, -2.75573192e-7f), zh, 2.48015873e-5f), zh, -1.38888889e-3f);
+  const float half = 0.5f * zh, ch = __fsub_rn(1.f, half);
+  const float cl = __fadd_rn(__fsub_rn(__fsub_rn(1.f, ch), half),
+                             fmaf(__fmul_rn(zh, zh), fmaf(even, zh, 4.16666667e-2f), -0.5f * zl));
+  const float cosine = __fadd_rn(ch, cl);
+  // sin = theta + theta z (-1 / 6 + z (1 / 120 - ..))
+  constexpr float kSixth = -0.166666671633720398f, kSixthLow = 4.96705373e-9f;
+  const float odd = fmaf(fmaf(fmaf(zh, -2.50521084e-8f, 2.75573192e-6f), zh, -1.98412698e-4f), zh, 8.33333333e-3f);
+  const float zq = __fmul_rn(zh, odd), ph = __fadd_rn(kSixth, zq);
+  const float pl = __fadd_rn(__fsub_rn(zq, __fsub_rn(ph, kSixth)), kSixthLow);
+  const float uh = __fmul_rn(zh, ph), ul = fmaf(zh, pl, fmaf(zl, ph, fmaf(zh, ph, -uh)));
+  const float vh = __fmul_rn(th, uh), vl = fmaf(th, ul, fmaf(tl, uh, fmaf(th, uh, -vh)));
+  const float sh = __fadd_rn(th, vh), sl = __fsub_rn(vh, __fsub_rn(sh, th));
+  const float sine = __fadd_rn(sh, __fadd_rn(sl, __fadd_rn(tl, vl)));
+  s = (quarter & 1) ? cosine : sine;
+  c = (quarter & 1) ? sine : cosine;
+  if (quarter & 2) s = -s;
+  if ((quarter + 1) & 2) c = -c;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -160,7 +192,7 @@ constexpr uint32_t kRoundBits = 0x4b400000u;
 
 // 4-bit codes of this lane's 16 elements, as kRoundBits + code, and the
 // parameter word of their group (the G/16 lanes of a group agree on it).  low =
-// bf16(min), scale = bf16((max - low) / 15), code = (x - low) / scale rounded
+// bf16(min), scale = bf16((max - low) (1 / 15)), code = (x - low) / scale rounded
 // to even, clamped.  A scale below the smallest normal number counts as 0 (a
 // constant group: every value reads back as low); a group whose range is not
 // finite gets NaN parameters, so that it reads back as NaN.
@@ -184,7 +216,7 @@ __device__ __forceinline__ uint32_t quantise16(const float (&y)[2][8], uint32_t 
   lo = __uint_as_float(low_bits << 16);
   const float range = hi - lo;
   const bool finite = fabsf(range) <= 3.402823466e38f;
-  uint32_t scale_bits = pack_bf16x2(0.f, __fdiv_rn(fmaxf(range, 0.f), 15.f)) & 0xffff0000u;
+  uint32_t scale_bits = pack_bf16x2(0.f, __fmul_rn(fmaxf(range, 0.f), 1.f / 15.f)) & 0xffff0000u;
   if (scale_bits < 0x00800000u || !finite) scale_bits = 0;
   const float scale = __uint_as_float(scale_bits);
   // code = t / scale (t the clamped distance from low) rounded to even: the
@@ -301,7 +333,8 @@ struct PairLanes {
 };
 
 // Elements 8 piece .. 8 piece + 7 of a row, turned; `other` holds those that
-// they pair with (split pairs).
+// they pair with (split pairs).  Products and sums are rounded one by one, as
+// the formula reads: codes then agree with those of the fp32 formula.
 template <bool IL>
 __device__ __forceinline__ void turn_piece(const uint4& x, const uint4& other, const float2* angles, int rot,
                                            int piece, float (&y)[8]) {
@@ -312,8 +345,8 @@ __device__ __forceinline__ void turn_piece(const uint4& x, const uint4& other, c
     for (int e = 0; e < 4; ++e) {
       const float2 v = angles[4 * piece + e];
       const float a = y[2 * e], b = y[2 * e + 1];
-      y[2 * e] = a * v.x - b * v.y;
-      y[2 * e + 1] = b * v.x + a * v.y;
+      y[2 * e] = __fsub_rn(__fmul_rn(a, v.x), __fmul_rn(b, v.y));
+      y[2 * e + 1] = __fadd_rn(__fmul_rn(b, v.x), __fmul_rn(a, v.y));
     }
   } else {
     const bool second = 16 * piece >= rot;
@@ -324,8 +357,8 @@ __device__ __forceinline__ void turn_piece(const uint4& x, const uint4& other, c
     for (int e = 0; e < 8; e += 2) {
       const float4 v = *reinterpret_cast<const float4*>(cs + e);
       // The first member of a pair takes -sin times the second.
-      y[e] = fmaf(second ? z[e] : -z[e], v.y, y[e] * v.x);
-      y[e + 1] = fmaf(second ? z[e + 1] : -z[e + 1], v.w, y[e + 1] * v.z);
+      y[e] = __fadd_rn(__fmul_rn(y[e], v.x), __fmul_rn(second ? z[e] : -z[e], v.y));
+      y[e + 1] = __fadd_rn(__fmul_rn(y[e + 1], v.z), __fmul_rn(second ? z[e + 1] : -z[e + 1], v.w));
     }
   }
 }

@@ -513,7 +513,7 @@ attn_status_t rope_append_paged(const attn_heads_t* q, const attn_heads_t* k, co
  *
  * A 4-bit cache is [num_blocks, Hkv, kv4_record_bytes(d, group)] bytes.  Each
  * group of `group` consecutive elements of a key or value has
- *   min = bf16(lowest), scale = bf16((highest - min) / 15),
+ *   min = bf16(lowest), scale = bf16((highest - min) r), r = 1/15 in fp32,
  *   code = (x - min) / scale to the nearest whole number (half to even), 0 .. 15
  * in fp32, and stands for code * scale + min.  So |x - value| <= scale / 2
  * but for the roundings of min and scale (2^-9 of each).  A group whose range

@@ -1,8 +1,8 @@
 """Reference of the 4-bit paged KV cache — TEST INFRASTRUCTURE ONLY.
 
 Every group of ``group`` consecutive elements of a key or value keeps
-min = bf16(lowest), scale = bf16((highest - min) / 15) and a code per
-element, (x - min) / scale to the nearest whole number (half to even) in
+min = bf16(lowest), scale = bf16((highest - min) r), r the fp32 number
+nearest to 1/15, and a code per element, (x - min) / scale to the nearest whole number (half to even) in
 0 .. 15; it stands for code * scale + min.
 
 A record holds the 16 token slots of one KV head of one block:
@@ -42,7 +42,7 @@ def kv4_quantise(x, group):
     low_bits = bf16_bits(y.min(-1))
     low = bf16_value(low_bits)
     spread = np.maximum(y.max(-1) - low, np.float32(0))
-    scale_bits = bf16_bits(spread / np.float32(15))
+    scale_bits = bf16_bits(spread * (np.float32(1) / np.float32(15)))
     scale_bits[scale_bits < 0x80] = 0
     scale = bf16_value(scale_bits)
     with np.errstate(divide="ignore", invalid="ignore"):

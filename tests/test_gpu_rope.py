@@ -1,9 +1,8 @@
 """Rotary positions and the paged appends on the GPU, against the fp64 oracle.
 
 Bound of a rotated value x cos a - y sin a: the angle is formed to 2^-32
-turns and rounded once to fp32 (at most pi 2^-24), sincospi is good to 2 ulp,
-and three fp32 roundings follow: under 2^-20 (|x| + |y|).  Then one rounding
-to bf16, 2^-8 of the value.
+turns, cos and sin are good to 1 ulp, and three fp32 roundings follow: under
+2^-20 (|x| + |y|).  Then one rounding to bf16, 2^-8 of the value.
 """
 
 import numpy as np
