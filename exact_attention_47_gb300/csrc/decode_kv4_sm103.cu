@@ -294,10 +294,10 @@ __device__ __forceinline__ float word_min(uint32_t w) { return __uint_as_float(w
 // (stab + log2(l)) ln 2, the whole part of the logarithm added to the
 // stabiliser first (exactly): an LSE near 0 keeps its bits.
 __device__ __forceinline__ float lse_of(float stab, float l) {
-  const int k = static_cast<int>(__float_as_uint(l) >> 23) - 127;
-  if (k <= -127 || k >= 128) return (stab + log2f(l)) * kLn2;    // subnormal, infinite, NaN
-  const float part = __uint_as_float((__float_as_uint(l) & 0x7fffffu) | 0x3f800000u);
-  return ((stab + static_cast<float>(k)) + log2f(part)) * kLn2;
+  const uint32_t bits = __float_as_uint(l);
+  // (Infinities and NaN stay what they are.)
+  const float part = bits >= 0x7f800000u ? l : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+  return ((stab + static_cast<float>(static_cast<int>(bits >> 23) - 127)) + __log2f(part)) * kLn2;
 }
 
 // N words from shared memory at address + OFFSET.
