@@ -425,7 +425,7 @@ struct RunState {
   float mins[NT][D / G][2];        // sum of p min over this lane's tokens
   float stab[NT][2], l[NT][2];
   float limit[NT][2];              // raw score from which the stabiliser has to move
-  uint32_t cap;                    // largest parameter word the weights have room for
+  float cap;                       // largest parameter word, as a float, that the weights have room for
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -440,24 +440,35 @@ struct RunState {
       limit[nt][0] = limit[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    cap = 0;
+    cap = 0.f;
   }
 
   // The power of two (log2) that the weights carry for V scales up to `cap`:
   // scales of exponent field E are below 2^(E - 126), and 2^(133 - E) brings
   // them under 2^7.  (At most 2^40, which keeps the min terms finite: values
   // all under 2^-50 lose bits.)
-  static __device__ __forceinline__ float room(uint32_t cap_) {
-    const int E = static_cast<int>(cap_ >> 23);
+  static __device__ __forceinline__ float room(float cap_) {
+    const int E = static_cast<int>(__float_as_uint(cap_) >> 23);
     return static_cast<float>(min(133 - E, 40));
   }
 
-  // Moves the stabilisers for raw scores up to s (and V parameter words up to
-  // `big`); rare, and the same for the whole warp.
-  __device__ __forceinline__ void move(const float (&s)[NT][2], const float (&back)[NT][2], uint32_t big) {
+  // Moves the stabilisers for raw scores up to s and these V parameter words;
+  // rare, and the same for the whole warp.  Scales that are no number take no
+  // room: they spoil their own group alone.
+  template <int N>
+  __device__ __forceinline__ void move(const float (&s)[NT][2], const float (&back)[NT][2],
+                                       const uint32_t (&words)[N][2][D / G]) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int g = 0; g < D / G; ++g)
+          if (words[n][i][g] < 0x7f800000u) big = max(big, words[n][i][g]);
     big = __reduce_max_sync(0xffffffffu, big);
     const float before = room(cap);
-    if (big > cap) cap = ((min((big >> 23) & 0xffu, 254u) + 1) << 23) - 1;
+    if (big > __float_as_uint(cap)) cap = __uint_as_float(big | 0x7fffffu);
     const float now = room(cap);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -583,11 +594,11 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
     }
   }
 
-  uint32_t vpa[2][kGroups], vpb[2][kGroups];
+  uint32_t vp[2][2][kGroups];                    // of slots `slot` and slot + 2
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    load_words<kGroups, Rec::kOffParV>(at.par + rec[n], vpa[n]);
-    load_words<kGroups, Rec::kOffParV + 2 * Rec::kParRow>(at.par + rec[n], vpb[n]);
+    load_words<kGroups, Rec::kOffParV>(at.par + rec[n], vp[n][0]);
+    load_words<kGroups, Rec::kOffParV + 2 * Rec::kParRow>(at.par + rec[n], vp[n][1]);
   }
   uint32_t vw[2][4][kVW];
 #pragma unroll
@@ -609,17 +620,19 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
       }
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        if (dead) vpa[n][g] = 0;
-        if (dead8) vpb[n][g] = 0;
+        if (dead) vp[n][0][g] = 0;
+        if (dead8) vp[n][1][g] = 0;
       }
     }
   }
 
-  uint32_t big = 0;
+  // (As floats, the scales with some bits more; NaN drops out.)
+  float big = 0.f;
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) big = max(big, max(vpa[n][g], vpb[n][g]));
+    for (int g = 0; g < kGroups; ++g)
+      big = fmaxf(big, fmaxf(__uint_as_float(vp[n][0][g]), __uint_as_float(vp[n][1][g])));
   bool move = big > st.cap;
   float top[NT][2];
 #pragma unroll
@@ -629,7 +642,7 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
       top[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
       move |= top[nt][h] > st.limit[nt][h];
     }
-  if (__any_sync(0xffffffffu, move)) st.move(top, q.back, big);
+  if (__any_sync(0xffffffffu, move)) st.move(top, q.back, vp);
 
   // --- weights and O^T: rows = elements of V, columns = heads
 #pragma unroll
@@ -645,8 +658,8 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
       f2_unpack(f2_add(f2_pack(st.l[nt][0], st.l[nt][1]), f2_add(pa, pb)), st.l[nt][0], st.l[nt][1]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const float sa = word_scale(vpa[n][g]), sb = word_scale(vpb[n][g]);
-        const float ma = word_min(vpa[n][g]), mb = word_min(vpb[n][g]);
+        const float sa = word_scale(vp[n][0][g]), sb = word_scale(vp[n][1][g]);
+        const float ma = word_min(vp[n][0][g]), mb = word_min(vp[n][1][g]);
         f2_unpack(f2_fma(pa, f2_pack(ma, ma), f2_fma(pb, f2_pack(mb, mb), f2_pack(st.mins[nt][g][0], st.mins[nt][g][1]))),
                   st.mins[nt][g][0], st.mins[nt][g][1]);
         float w0, w1;
