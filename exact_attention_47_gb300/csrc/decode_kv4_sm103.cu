@@ -12,9 +12,12 @@
 // two that loses nothing:
 //   q    scaled per head so its largest element is in [2^14, 2^15): every
 //        bf16 element within 2^-24 of it stays exact;
-//   p scale  the stabiliser of a head's softmax is its running maximum plus
-//        the exponent of the largest V scale met so far (less 7), so weights
-//        stay under 2^15; they are rounded to 11 bits.
+//   p scale  every group of V has a power of two that follows the largest of
+//        its scales met so far, so that the products stay under 2^15 (they are
+//        rounded to 11 bits: with bf16's 8 the error of O would show beside its
+//        own rounding, and a second fp16 for the rest would double the output
+//        MMAs).  A group's power is its own: a group of huge values, or of none
+//        that are numbers, leaves the others and the softmax sums alone.
 // The min terms of the scores are one more MMA (bf16, exact: sum(q_g) is split
 // into three bf16 parts); those of the output are summed in fp32.
 //
@@ -62,6 +65,11 @@ constexpr int kMaxCtas = 256;
 // Lazy stabilisers (see attn_decode_paged): the running maximum moves only
 // when a score exceeds it by more than kTau (log2 units).
 constexpr float kTau = 8.f;
+// The weights p are softmax numerators times 2^-kLow: sums of p V then stay
+// finite in fp32 for values up to 2^123.  With V scales brought under kFull the
+// products p scale are under 2^15, which fp16 holds.
+constexpr float kLow = 20.f;
+constexpr float kFull = 0x1p27f;
 constexpr float kGrid = 12288.f;   // 1.5 2^13: x + kGrid - kGrid is x to a multiple of 2^-10
 // Entries of the plan's prefix sums (one per sequence up to this many, then
 // one per several).
@@ -421,11 +429,13 @@ __device__ __forceinline__ void make_queries(const DecKv4Params& p, const QueryR
 // all in units of 2^stab per head.
 template <int D, int G, int NT>
 struct RunState {
-  float o[NT][D / 16][4];          // rows r and r + 8 (the latter times 16), heads 2c, 2c + 1; times 2^-24
+  float o[NT][D / 16][4];          // rows r and r + 8 (the latter times 16), heads 2c, 2c + 1; times 2^-24 and room
   float mins[NT][D / G][2];        // sum of p min over this lane's tokens
   float stab[NT][2], l[NT][2];
   float limit[NT][2];              // raw score from which the stabiliser has to move
-  float cap;                       // largest parameter word, as a float, that the weights have room for
+  // The power of two of a group of V by which its scales are multiplied for the
+  // products p scale: it keeps the largest scale met so far under kFull.
+  float room[D / G];
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -440,36 +450,30 @@ struct RunState {
       limit[nt][0] = limit[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    cap = 0.f;
+#pragma unroll
+    for (int g = 0; g < D / G; ++g) room[g] = 0x1p126f;
   }
 
-  // The power of two (log2) that the weights carry for V scales up to `cap`:
-  // scales of exponent field E are below 2^(E - 126), and 2^(133 - E) brings
-  // them under 2^7.  (At most 2^40, which keeps the min terms finite: values
-  // all under 2^-50 lose bits.)
-  static __device__ __forceinline__ float room(float cap_) {
-    const int E = static_cast<int>(__float_as_uint(cap_) >> 23);
-    return static_cast<float>(min(133 - E, 40));
-  }
-
-  // Moves the stabilisers for raw scores up to s and these V parameter words;
-  // rare, and the same for the whole warp.  Scales that are no number take no
-  // room: they spoil their own group alone.
+  // Moves the stabilisers for raw scores up to s, and the groups' room for these
+  // V parameter words; rare, and the same for the whole warp.
   template <int N>
   __device__ __forceinline__ void move(const float (&s)[NT][2], const float (&back)[NT][2],
                                        const uint32_t (&words)[N][2][D / G]) {
-    uint32_t big = 0;
+    float less[D / G];                             // what becomes of the products so far
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int g = 0; g < D / G; ++g) {
+      uint32_t big = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int g = 0; g < D / G; ++g)
-          if (words[n][i][g] < 0x7f800000u) big = max(big, words[n][i][g]);
-    big = __reduce_max_sync(0xffffffffu, big);
-    const float before = room(cap);
-    if (big > __float_as_uint(cap)) cap = __uint_as_float(big | 0x7fffffu);
-    const float now = room(cap);
+      for (int n = 0; n < N; ++n) big = max(big, max(words[n][0][g], words[n][1][g]));
+      // Scales of exponent field E are below 2^(E - 126), 2^(151 - E) brings them
+      // under a quarter of kFull, so that somewhat larger ones to come move nothing
+      // (at most 2^126: scales under 2^-102 lose bits; one that is no number takes
+      // its group to the end of the range, and spoils it anyway).
+      const int E = static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 23);
+      const int had = __float_as_int(room[g]), has = min(had, (278 - min(E, 254)) << 23);
+      room[g] = __int_as_float(has);
+      less[g] = __int_as_float(max(has - had + (127 << 23), 0));
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float f[2];
@@ -478,23 +482,27 @@ struct RunState {
         float mx = s[nt][h] * back[nt][h];
 #pragma unroll
         for (int o_ = 4; o_ < 32; o_ <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o_));
-        const float top = stab[nt][h] + before;  // the running maximum
+        const float top = stab[nt][h] - kLow;    // the running maximum
         // (To a multiple of 2^-10, so that adding whole numbers to a stabiliser,
         // here and for the LSE, rounds nothing.)
-        const float to = __fsub_rn(__fadd_rn(mx > top + kTau ? mx : top, kGrid), kGrid) - now;
+        const float to = __fsub_rn(__fadd_rn(mx > top + kTau ? mx : top, kGrid), kGrid) + kLow;
         f[h] = to == stab[nt][h] ? 1.f : ex2(stab[nt][h] - to);
         stab[nt][h] = to;
-        limit[nt][h] = (to + now + kTau) / back[nt][h];
+        limit[nt][h] = (to - kLow + kTau) / back[nt][h];
         l[nt][h] *= f[h];
 #pragma unroll
         for (int g = 0; g < D / G; ++g) mins[nt][g][h] *= f[h];
       }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        o[nt][i][0] *= f[0];
-        o[nt][i][1] *= f[1];
-        o[nt][i][2] *= f[0];
-        o[nt][i][3] *= f[1];
+      for (int g = 0; g < D / G; ++g) {
+        const float f0 = f[0] * less[g], f1 = f[1] * less[g];
+#pragma unroll
+        for (int i = g * (G / 16); i < (g + 1) * (G / 16); ++i) {
+          o[nt][i][0] *= f0;
+          o[nt][i][1] *= f1;
+          o[nt][i][2] *= f0;
+          o[nt][i][3] *= f1;
+        }
       }
     }
   }
@@ -514,10 +522,12 @@ struct RunState {
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
+        // 2^24 / room, and a sixteenth of it.
+        const float u = __int_as_float((278 << 23) - __float_as_int(room[16 * i / G])), u8 = u * 0x1p-4f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          o[nt][i][h] = fmaf(o[nt][i][h], 0x1p24f, mins[nt][16 * i / G][h]);
-          o[nt][i][2 + h] = fmaf(o[nt][i][2 + h], 0x1p20f, mins[nt][16 * i / G][h]);
+          o[nt][i][h] = fmaf(o[nt][i][h], u, mins[nt][16 * i / G][h]);
+          o[nt][i][2 + h] = fmaf(o[nt][i][2 + h], u8, mins[nt][16 * i / G][h]);
         }
       }
     }
@@ -626,14 +636,14 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
     }
   }
 
-  // (As floats, the scales with some bits more; NaN drops out.)
+  // (A word as a float is its scale with some bits more.  NaN drops out.)
   float big = 0.f;
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
-      big = fmaxf(big, fmaxf(__uint_as_float(vp[n][0][g]), __uint_as_float(vp[n][1][g])));
-  bool move = big > st.cap;
+      big = fmaxf(big, fmaxf(__uint_as_float(vp[n][0][g]) * st.room[g], __uint_as_float(vp[n][1][g]) * st.room[g]));
+  bool move = big >= kFull;
   float top[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -658,7 +668,7 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
       f2_unpack(f2_add(f2_pack(st.l[nt][0], st.l[nt][1]), f2_add(pa, pb)), st.l[nt][0], st.l[nt][1]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const float sa = word_scale(vp[n][0][g]), sb = word_scale(vp[n][1][g]);
+        const float sa = word_scale(vp[n][0][g]) * st.room[g], sb = word_scale(vp[n][1][g]) * st.room[g];
         const float ma = word_min(vp[n][0][g]), mb = word_min(vp[n][1][g]);
         f2_unpack(f2_fma(pa, f2_pack(ma, ma), f2_fma(pb, f2_pack(mb, mb), f2_pack(st.mins[nt][g][0], st.mins[nt][g][1]))),
                   st.mins[nt][g][0], st.mins[nt][g][1]);

@@ -525,7 +525,7 @@ attn_status_t rope_append_paged(const attn_heads_t* q, const attn_heads_t* k, co
  * half of a byte first: element e = 32 w + 8 i + 2 c + h of a key is cell
  * 8 ((d/32) c + w) + i + 4 h of its row, element e = r + 8 (8 w + n) of a
  * value cell 8 ((d/64) r + w) + n.  A cache written by other means needs
- * scales >= 0.
+ * scales >= 0, their sign bit clear.
  */
 size_t kv4_record_bytes(int d, int group);
 
@@ -571,8 +571,13 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
 /*
  * attn_decode_paged_kv4 — attn_decode_paged over a 4-bit cache: one query
  * token per sequence, softmax(scale * q . k) v over the values that the
- * cached codes stand for (fp32 accumulation; the softmax numerators are
- * rounded to 11 bits, q, codes and parameters enter exactly).
+ * cached codes stand for (fp32 accumulation).  q, codes and parameters enter
+ * exactly (|q| under 2^120; elements of q under 2^-24 of their head's largest
+ * lose bits).  The product of a softmax numerator and a V scale is rounded to
+ * 11 bits, or to 2^-30 of the largest scale that its group of the KV head has
+ * in the sequence where that is coarser (scales under 2^-102 lose bits).  A V
+ * group that stands for NaN, or with an infinite scale, spoils its own columns
+ * of its sequence and no others; the sums and lse do not depend on V.
  *
  *  kv_cache   [num_blocks, Hkv, kv4_record_bytes(d, group)] bytes, 16-byte
  *             aligned; slots past seq_lens[b] are never used, whatever they

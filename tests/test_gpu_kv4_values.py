@@ -4,8 +4,8 @@ size: a group of V is its own columns' business alone.
 Bounds are those of test_gpu_kv4, with a group's own largest value in place of
 the pool's: a numerator's product with a V scale is rounded to 11 bits, so a
 group's columns are off by at most 2^-11 of 15 scales, under 2^-10 of its
-largest |V| (tokens whose scale is under 2^-21 of the group's largest add
-2^-32 of that each), before the bf16 rounding of O."""
+largest |V| (products under 2^-19 of a numerator of 1 with the group's largest
+scale add 2^-30 of that each), before the bf16 rounding of O."""
 
 import numpy as np
 import pytest
@@ -81,3 +81,53 @@ def test_every_value_group_poisoned_leaves_the_lse():
     o, lse = run(q, bad, table, n, 32, 0.09)
     check_groups(o, lse, q, rec, table, n, 0.09, 128, 32, np.ones(tuple(o.shape), bool))
     assert torch.isnan(o.float()).all()
+
+
+def scaled_words(rec, d, group, powers):
+    """The cache with V groups times 2^powers ([group], or anything that
+    broadcasts against [num_blocks, Hkv, slot, group])."""
+    rec = rec.clone()
+    w = v_words(rec, d, group)
+    pair = w.contiguous().view(torch.bfloat16).unflatten(-1, (d // group, 2)).double()
+    pair = (pair * 2.0 ** torch.as_tensor(powers, dtype=torch.float64)[..., None]).to(torch.bfloat16)
+    w.copy_(pair.flatten(-2).contiguous().view(torch.int32))
+    return rec
+
+
+@pytest.mark.parametrize("powers", [(0, -28), (-24, 20), (100, 0), (-60, -100), (40, -40)])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,group", SHAPES)
+def test_value_groups_of_very_different_size(lens, Hq, Hkv, d, group, powers):
+    q, rec, table, n = decode_case(lens, Hq, Hkv, d, group, seed=221)
+    groups = d // group
+    rec = scaled_words(rec, d, group, (powers * groups)[:groups])
+    o, lse = run(q, rec, table, n, group, 0.09)
+    check_groups(o, lse, q, rec, table, n, 0.09, d, group)
+
+
+@pytest.mark.parametrize("step", [12, 40])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,group", SHAPES)
+def test_value_sizes_that_change_along_a_run(lens, Hq, Hkv, d, group, step):
+    """Values grow along the run in even groups and shrink in odd ones, and
+    the sharp softmax of large scores looks at one place or another."""
+    q, rec, table, n = decode_case(lens, Hq, Hkv, d, group, seed=223)
+    powers = torch.zeros(rec.shape[0], Hkv, 16, d // group)
+    for b, L in enumerate(lens):
+        for j in range(0, L, 16):
+            powers[int(table[b, j // 16])] = ((4 * j // L - 2) * step / 2 * (-1.0) ** torch.arange(d // group)).round()
+    rec = scaled_words(rec, d, group, powers)
+    for scale in (0.02, 2.0):
+        o, lse = run(q, rec, table, n, group, scale)
+        check_groups(o, lse, q, rec, table, n, scale, d, group)
+
+
+@pytest.mark.parametrize("low", [1e30, -3e25, 1e-30])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,group", SHAPES)
+def test_constant_value_groups_of_any_size(lens, Hq, Hkv, d, group, low):
+    """Every V group is constant (scale 0, as the append writes it): O is a
+    mean of what they hold."""
+    q, rec, table, n = decode_case(lens, Hq, Hkv, d, group, seed=227)
+    w = v_words(rec, d, group)
+    mins = (low * (1 + torch.rand(w.shape, generator=torch.Generator().manual_seed(1)))).to(torch.bfloat16)
+    w.copy_(mins.view(torch.int16).int() & 0xFFFF)
+    o, lse = run(q, rec, table, n, group, 0.09)
+    check_groups(o, lse, q, rec, table, n, 0.09, d, group)
