@@ -253,7 +253,10 @@ attn_status_t encode_bf16_strided(CUtensorMap* map, const void* base, int rank, 
 }
 
 attn_status_t launch_result(cudaError_t e, const char* what) {
-  if (e != cudaSuccess) return fail(ATTN_ERR_LAUNCH, "%s launch failed: %s", what, cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();   // reported here: not left for another call to find
+    return fail(ATTN_ERR_LAUNCH, "%s launch failed: %s", what, cudaGetErrorString(e));
+  }
   g_last_error[0] = '\0';
   return ATTN_OK;
 }
@@ -1428,9 +1431,9 @@ attn_status_t attn_selftest_exp2_poly(const float* x, float* y, int n, void* str
   const size_t bytes = static_cast<size_t>(n) * 4;
   if ((st = check_bufs(*dev, {{x, bytes, "x"}, {y, bytes, "y"}})) != ATTN_OK) return st;
   const long long pairs = (static_cast<long long>(n) + 1) / 2;
-  selftest_exp2_poly_kernel<<<static_cast<unsigned>((pairs + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-      x, y, n);
-  return launch_result(cudaGetLastError(), "attn_selftest_exp2_poly");
+  return launch_result(attn47::launch(false, selftest_exp2_poly_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)),
+                                      dim3(256), 0, static_cast<cudaStream_t>(stream), x, y, n),
+                       "attn_selftest_exp2_poly");
 }
 
 attn_status_t attn_selftest_wait_timeout(unsigned long long timeout_ns, void* stream,
@@ -1441,8 +1444,8 @@ attn_status_t attn_selftest_wait_timeout(unsigned long long timeout_ns, void* st
   attn_status_t st = current_device(&dev);
   if (st != ATTN_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  selftest_wait_kernel<<<1, 32, 0, s>>>(dev->status, timeout_ns);
-  st = launch_result(cudaGetLastError(), "selftest");
+  st = launch_result(attn47::launch(false, selftest_wait_kernel, dim3(1), dim3(32), 0, s, dev->status, timeout_ns),
+                     "selftest");
   if (st != ATTN_OK) return st;
   return attn_get_device_status(stream, flags_out);
 }

@@ -954,18 +954,7 @@ cudaError_t launch_t(const DecLaunch& a) {
   // One wave: every CTA resident at once, each with an equal chunk.
   int ctas = a.sms * per_sm;
   if (a.max_ctas > 0 && ctas > a.max_ctas) ctas = a.max_ctas;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Lt::kSmem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, *a.tk, *a.tv, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Lt::kSmem, a.stream, *a.tk, *a.tv, p);
 }
 
 }  // namespace

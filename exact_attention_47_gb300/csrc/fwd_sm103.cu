@@ -817,18 +817,7 @@ cudaError_t launch_t(const FwdLaunch& a) {
   p.max_ctx = PAGED ? a.max_blocks * kPageRows - a.N : 0;
   // Persistent: one CTA per SM (shared memory allows one), each walking units.
   const unsigned grid = static_cast<unsigned>(min(p.num_units, a.sms > 0 ? a.sms : 1));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = L::kSmem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, *a.tq, *a.tk, *a.tv, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), L::kSmem, a.stream, *a.tq, *a.tk, *a.tv, p);
 }
 
 }  // namespace

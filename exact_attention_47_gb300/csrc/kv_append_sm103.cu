@@ -98,8 +98,7 @@ cudaError_t launch_kv_append_sm103(const AppendLaunch& a) {
   // A plain launch: as a programmatic dependent (waiting for the preceding
   // kernel, letting the attention kernel launch early) the chunked prefill
   // measured 2.6 % slower on GB300.
-  attn_kv_append_kernel<<<grid, kThreads, 0, a.stream>>>(p);
-  return cudaGetLastError();
+  return launch(false, attn_kv_append_kernel, dim3(grid), dim3(kThreads), 0, a.stream, p);
 }
 
 }  // namespace attn47

@@ -371,12 +371,12 @@ __device__ __forceinline__ void pdl_wait_primary() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Host side: launch `kern` as a programmatic dependent of the work before it
-// in `stream` (its CTAs may start while that work drains; the kernel calls
-// pdl_wait_primary before it touches global memory).
+// Host side: launch `kern` in `stream`, with `dependent` as a programmatic
+// dependent of the work before it.  What is returned is this launch's own
+// status: cudaGetLastError would bring up one that failed before it.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t stream, Args&&... args) {
+inline cudaError_t launch(bool dependent, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -386,9 +386,15 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+// As a programmatic dependent: its CTAs may start while the work before it
+// drains; the kernel calls pdl_wait_primary before it touches global memory.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, Args&&... args) {
+  return launch(true, kern, grid, block, smem, stream, static_cast<Args&&>(args)...);
 }
 // 16-byte asynchronous global -> shared copy through L2 (cp.async.cg).  With
 // src_bytes = 0 it writes 16 zero bytes and reads nothing.
