@@ -7,8 +7,11 @@
 // given and calls the C entry point of the library (whose addresses `bind`
 // receives), with the GIL released for the last two.  Whatever is not the
 // usual case (tensors of another device, type or layout than wanted, another
-// current device, an error from the library) makes it return None, and the
-// Python function goes its own, longer way, which raises the errors.
+// current device, arguments that the library refuses) makes it return None, and
+// the Python function goes its own, longer way, which raises the errors.  A
+// status that may come after a launch is returned as a number, for the Python
+// function to raise: the call is not made again (a rotation in place would turn
+// twice).
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -148,6 +151,15 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& li
 void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream(); }
 bool current(int device) { return c10::cuda::current_device() == device; }
 
+// This thread's call has reached the library.
+thread_local bool t_called = false;
+
+// For a status other than ATTN_OK: None where nothing was launched.
+PyObject* not_done(attn_status_t st) {
+  if (st == ATTN_ERR_INVALID_ARG || st == ATTN_ERR_UNSUPPORTED || st == ATTN_ERR_WORKSPACE) Py_RETURN_NONE;
+  return PyLong_FromLong(st);
+}
+
 PyObject* pair(const at::Tensor& a, const at::Tensor* b) {
   PyObject* t = PyTuple_New(2);
   if (!t) return nullptr;
@@ -202,10 +214,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ko = k_given ? *k_given : make(k->sizes(), at::kBFloat16, *k);
       heads(ko, &hko);
     }
+    t_called = true;
     st = (back ? g_rope_bwd : g_rope_fwd)(&hq, k ? &hk : nullptr, &ho, k ? &hko : nullptr, &r.r, static_cast<int>(B),
                                           static_cast<int>(N), static_cast<int>(d), stream_of(dev));
   }
-  if (st != ATTN_OK) Py_RETURN_NONE;
+  if (st != ATTN_OK) return not_done(st);
   return pair(qo, k ? &ko : nullptr);
 }
 
@@ -268,12 +281,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       qo = q_given ? *q_given : make(q->sizes(), at::kBFloat16, *q);
       heads(qo, &ho);
     }
+    t_called = true;
     st = kv4 ? g_append_kv4(pq, &hk, &hv, po, pr, data<void>(kc), group, data<int32_t>(table), data<int32_t>(ids),
                             data<int32_t>(pos), t, S, dd, block, mb, nb, stream_of(dev))
              : g_append(pq, &hk, &hv, po, pr, data<void>(kc), data<void>(vc), data<int32_t>(table),
                         data<int32_t>(ids), data<int32_t>(pos), t, S, dd, block, mb, nb, stream_of(dev));
   }
-  if (st != ATTN_OK) Py_RETURN_NONE;
+  if (st != ATTN_OK) return not_done(st);
   PyObject* out = PyTuple_New(1);
   if (out) PyTuple_SET_ITEM(out, 0, q ? THPVariable_Wrap(qo) : Py_NewRef(Py_None));
   return out;
@@ -305,12 +319,13 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Unlocked unlocked;
     k = k_given ? *k_given : make(sizes, at::kBFloat16, *kv);
     v = v_given ? *v_given : make(sizes, at::kBFloat16, *kv);
+    t_called = true;
     st = g_read(data<void>(kv), group, data<int32_t>(table), data<int32_t>(ids), data<int32_t>(pos), data<void>(k),
                 data<void>(v), static_cast<int>(sizes[0]), static_cast<int>(table->size(0)),
                 static_cast<int>(sizes[1]), d, kBlock, static_cast<int>(table->size(1)), static_cast<int>(kv->size(0)),
                 stream_of(dev));
   }
-  if (st != ATTN_OK) Py_RETURN_NONE;
+  if (st != ATTN_OK) return not_done(st);
   return pair(k, &v);
 }
 
@@ -359,22 +374,29 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     o = o_given ? *o_given : make(q->sizes(), at::kBFloat16, *q);
     if (has_lse) lse = lse_given ? *lse_given : make(lse_sizes, at::kFloat, *q);
     ws = ws_given ? *ws_given : make({static_cast<int64_t>(need < 16 ? 16 : need)}, at::kByte, *q);
+    t_called = true;
     st = g_decode(data<void>(q), data<void>(kv), data<int32_t>(table), data<int32_t>(lens), static_cast<int>(S),
                   static_cast<int>(Hq), Hkv, static_cast<int>(d), group, kBlock, static_cast<int>(table->size(1)),
                   static_cast<int>(kv->size(0)), scale, data<void>(o), has_lse ? data<float>(lse) : nullptr,
                   data<void>(ws), ws.nbytes(), stream_of(dev));
   }
-  if (st != ATTN_OK) Py_RETURN_NONE;
+  if (st != ATTN_OK) return not_done(st);
   return pair(o, has_lse ? &lse : nullptr);
 }
 
 // C++ exceptions (an allocation that failed, say) become "not handled": the
-// Python function meets the same and raises it.
+// Python function meets the same and raises it.  Not so once the library has
+// been called.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  t_called = false;
   try {
     return F(self, a, n);
   } catch (...) {
+    if (t_called) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "the call was made, but its results could not be returned");
+      return nullptr;
+    }
     PyErr_Clear();
     Py_RETURN_NONE;
   }

@@ -13,7 +13,9 @@ import torch
 
 import exact_attention_47_gb300 as attn
 import workloads
-from test_gpu_rope import randn
+from exact_attention_47_gb300 import _binding
+from test_gpu_kv4 import decode_case
+from test_gpu_rope import map_case, randn, views
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -80,3 +82,50 @@ def test_other_calls_do_not_report_it(name):
     call()
     torch.cuda.synchronize()
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("status", [3, 4])
+def test_a_call_whose_launch_failed_is_not_made_again(status):
+    """The entry points that the fast calls pass on to, replaced by ones that
+    count: one call each, and its status raised.  (What is refused before a
+    launch goes to the Python way, and is raised there.)"""
+    fast, lib = _binding._fast(), attn.load_library()
+    made = []
+    keep = []
+
+    def stub(name):
+        restype, argtypes = _binding._SIGS[name]
+        if restype is ctypes.c_size_t:
+            return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+        f = ctypes.CFUNCTYPE(restype, *argtypes)(lambda *a: made.append(name) or status)
+        keep.append(f)
+        return ctypes.cast(f, ctypes.c_void_p).value
+
+    d, group = 64, 32
+    q, rec, tab, lens = (t.to(DEV) for t in decode_case([40, 3], 4, 2, d, group, seed=6)[:4])
+    table, ids, pos, nb, x, _, _, _ = map_case([0], [5], 4, 2, d, 3)
+    table, ids, pos, x = (t.to(DEV) for t in (table, ids, pos, x))
+    kv = torch.zeros(nb, 2, attn.kv4_record_bytes(d, group), dtype=torch.uint8, device=DEV)
+    kc, vc = (torch.zeros(nb, 2, 16, d, dtype=BF, device=DEV) for _ in range(2))
+    f = workloads.rope_inv_freq(d).to(DEV)
+    y = randn(7, 1, 2, 9, d).to(DEV)
+    at = torch.arange(9, dtype=torch.int32, device=DEV)
+    attn.attn_decode_paged_kv4(q, rec, tab, lens, group)     # (sizes that are kept by the binding)
+    cases = {"rope_fwd": lambda: attn.rope_fwd(y, None, at, f, q_out=y),
+             "rope_bwd": lambda: attn.rope_bwd(y, None, at, f, dq=y),
+             "rope_append_paged": lambda: attn.rope_append_paged(*views(x, 4, 2, d), kc, vc, table, ids, pos, f),
+             "rope_append_paged_kv4": lambda: attn.rope_append_paged_kv4(*views(x, 4, 2, d), kv, table, ids, pos, group, f),
+             "kv4_read_paged": lambda: attn.kv4_read_paged(kv, table, ids, pos, d, group),
+             "attn_decode_paged_kv4": lambda: attn.attn_decode_paged_kv4(q, rec, tab, lens, group)}
+    before = y.clone()
+    try:
+        fast.bind(*(stub(n) for n in _binding._FAST))
+        for name, call in cases.items():
+            del made[:]
+            with pytest.raises(attn.AttnError, match=name + " failed") as e:
+                call()
+            assert e.value.status == status and made == [name]
+    finally:
+        fast.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _binding._FAST))
+    torch.cuda.synchronize()
+    assert torch.equal(y, before)
