@@ -400,33 +400,84 @@ bool heads_identical(const attn_heads_t& a, const attn_heads_t& b, int B, int N)
          (N == 1 || a.stride_token == b.stride_token) && (a.heads == 1 || a.stride_head == b.stride_head);
 }
 
-// Whether two views certainly share no element: their address ranges are
-// apart, or both repeat with the same token stride and lie beside each other
-// within it (parts of one merged projection output).
-bool heads_disjoint(const attn_heads_t& a, const attn_heads_t& b, int B, int N, int d) {
-  if (!overlap(a.data, static_cast<size_t>(heads_extent(a, B, N, d)) * 2, b.data,
-               static_cast<size_t>(heads_extent(b, B, N, d)) * 2))
-    return true;
-  const long long st = a.stride_token;
-  if (N > 1 || B > 1) {
-    if (st <= 0 || st != b.stride_token) return false;
-    if (B > 1 && (a.stride_batch % st != 0 || b.stride_batch % st != 0)) return false;
-  } else {
+// Memory by strides, in bytes: runs of `run` bytes, n[i] of them stride[i] apart
+// in each of three dimensions.
+struct Strided {
+  const void* p;
+  long long run;
+  long long stride[3], n[3];
+};
+
+Strided strided(const attn_heads_t& h, int B, int N, int d) {
+  return Strided{h.data, 2LL * d, {2 * h.stride_batch, 2 * h.stride_token, 2 * h.stride_head}, {B, N, h.heads}};
+}
+
+// Whether `off` = sum over the dimensions of m step with m in lo .. hi, give or
+// take what two runs reach (lo_run .. hi_run).  Dimensions go from the largest
+// step down, so that few m are left to try where they lie inside one another;
+// `tries` bounds them elsewhere (then: yes).
+struct Meeting {
+  struct Dim {
+    long long step, lo, hi;
+  } dim[6];
+  int dims = 0, tries = 4096;
+  long long lo_run, hi_run;
+
+  void add(long long step, long long lo, long long hi) {
+    if (step == 0 || lo == hi) return;
+    int i = 0;
+    while (i < dims && dim[i].step > step) ++i;
+    if (i < dims && dim[i].step == step) {
+      dim[i].lo += lo;
+      dim[i].hi += hi;
+      return;
+    }
+    for (int j = dims++; j > i; --j) dim[j] = dim[j - 1];
+    dim[i] = Dim{step, lo, hi};
+  }
+  bool search(long long off, int i) {
+    if (--tries < 0) return true;
+    if (i == dims) return off >= lo_run && off <= hi_run;
+    long long least = lo_run, most = hi_run;     // of all that comes after dimension i
+    for (int j = i + 1; j < dims; ++j) {
+      least += dim[j].lo * dim[j].step;
+      most += dim[j].hi * dim[j].step;
+    }
+    const Dim& x = dim[i];
+    auto floor_div = [&](long long v) { return v >= 0 ? v / x.step : -((-v + x.step - 1) / x.step); };
+    long long m = -floor_div(most - off), last = floor_div(off - least);   // least <= off - m step <= most
+    if (m < x.lo) m = x.lo;
+    if (last > x.hi) last = x.hi;
+    for (; m <= last; ++m)
+      if (search(off - m * x.step, i + 1)) return true;
     return false;
   }
-  const long long ea = heads_extent(a, 1, 1, d), eb = heads_extent(b, 1, 1, d);
-  const long long bytes = static_cast<long long>(reinterpret_cast<uintptr_t>(b.data)) -
-                          static_cast<long long>(reinterpret_cast<uintptr_t>(a.data));
-  if (bytes % 2 != 0) return false;
-  const long long off = ((bytes / 2) % st + st) % st;
-  return off >= ea && off + eb <= st;
+};
+
+// Whether two pieces of strided memory share a byte.
+bool meet(const Strided& a, const Strided& b) {
+  long long ea = a.run, eb = b.run;
+  for (int i = 0; i < 3; ++i) {
+    ea += (a.n[i] - 1) * a.stride[i];
+    eb += (b.n[i] - 1) * b.stride[i];
+  }
+  if (!overlap(a.p, static_cast<size_t>(ea), b.p, static_cast<size_t>(eb))) return false;
+  Meeting m;
+  m.lo_run = -(b.run - 1);
+  m.hi_run = a.run - 1;
+  for (int i = 0; i < 3; ++i) {
+    m.add(a.stride[i], 0, a.n[i] - 1);
+    m.add(b.stride[i], -(b.n[i] - 1), 0);
+  }
+  return m.search(static_cast<long long>(reinterpret_cast<uintptr_t>(b.p)) -
+                      static_cast<long long>(reinterpret_cast<uintptr_t>(a.p)), 0);
 }
 
 attn_status_t check_apart(const attn_heads_t* out, const char* out_name, const attn_heads_t* in,
                           const char* in_name, bool may_be_same, int B, int N, int d) {
   if (out == nullptr || in == nullptr) return ATTN_OK;
   if (may_be_same && heads_identical(*out, *in, B, N)) return ATTN_OK;
-  if (!heads_disjoint(*out, *in, B, N, d))
+  if (meet(strided(*out, B, N, d), strided(*in, B, N, d)))
     return fail(ATTN_ERR_INVALID_ARG, "%s overlaps %s", out_name, in_name);
   return ATTN_OK;
 }

@@ -123,6 +123,85 @@ def test_merged_parts_are_told_apart(lib):
     assert fwd(lib, q=q, k=k2, qo=q, ko=k2) == INVALID
 
 
+RUNS = (INVALID, UNSUPPORTED, OK)                # none of these: it got as far as the missing device
+
+
+def part(at, H, token, head=64, batch=0, d=64):
+    return _Heads(at, batch, token, head, H)
+
+
+@pytest.mark.parametrize("token", [0, 512])
+def test_merged_parts_of_one_token_a_batch_are_told_apart(lib, token):
+    """A decode step's [B, 1, (Hq + 2 Hkv) d]: one token, whose stride means
+    nothing."""
+    q, k = part(Q, 2, token, batch=512), part(Q + 2 * 128, 2, token, batch=512)
+    assert fwd(lib, q=q, k=k, qo=q, ko=k, B=4, N=1) not in RUNS
+    over = part(Q + 2 * 64, 2, token, batch=512)
+    assert fwd(lib, q=q, k=over, qo=q, ko=over, B=4, N=1) == INVALID
+    last = part(Q + 2 * 448, 2, token, batch=512)                    # its second head is the next batch's first
+    assert fwd(lib, q=q, k=last, qo=q, ko=last, B=4, N=1) == INVALID
+
+
+def test_head_major_parts_are_told_apart(lib):
+    """Heads of one [B, H, N, d] buffer."""
+    B, N, d = 3, 16, 64
+    for k_first, ok in ((2, True), (1, False), (4, False)):          # of 5 heads, q has 2, k 2
+        q = part(Q, 2, d, head=N * d, batch=5 * N * d)
+        k = part(Q + 2 * k_first * N * d, 2, d, head=N * d, batch=5 * N * d)
+        st = fwd(lib, q=q, k=k, qo=q, ko=k, B=B, N=N)
+        assert (st not in RUNS) if ok else st == INVALID
+    # q and k as halves of every token of a head: [B, H, N, 2, d]
+    q, k = (part(Q + 2 * i * d, 2, 2 * d, head=2 * N * d, batch=4 * N * d) for i in range(2))
+    assert fwd(lib, q=q, k=k, qo=q, ko=k, B=B, N=N) not in RUNS
+
+
+@pytest.mark.parametrize("B,N", [(1, 1), (1, 7), (3, 7), (3, 1)])
+def test_parts_interleaved_by_head_are_told_apart(lib, B, N):
+    """A projection seen as [B, N, H, 3, d]."""
+    H, d = 5, 64
+    qkv = [part(Q + 2 * i * d, H, 3 * H * d, head=3 * d, batch=3 * N * H * d) for i in range(3)]
+    for func in ("rope_fwd", "rope_bwd"):
+        assert fwd(lib, q=qkv[0], k=qkv[1], qo=qkv[0], ko=qkv[1], B=B, N=N, func=func) not in RUNS
+        apart = [heads(QO, H=H, N=N), heads(KO, H=H, N=N)]
+        assert fwd(lib, q=apart[0], k=apart[1], qo=qkv[0], ko=qkv[1], B=B, N=N, func=func) not in RUNS
+        near = part(Q + 2 * (d + 8), H, 3 * H * d, head=3 * d, batch=3 * N * H * d)   # 8 elements into the third part
+        assert fwd(lib, q=qkv[0], k=qkv[1], qo=qkv[2], ko=near, B=B, N=N, func=func) == INVALID
+    if B == 1:
+        assert append(lib, q=qkv[0], k=qkv[1], v=qkv[2], qo=qkv[0], T=N) not in RUNS
+        assert append(lib, q=qkv[0], k=qkv[1], v=qkv[2], qo=qkv[2], T=N) == INVALID
+
+
+def test_views_are_told_apart_as_their_elements_are(lib):
+    """Random small views in one buffer against sets of their elements."""
+    import random
+    rng = random.Random(5)
+    B, N, d = 2, 3, 64
+    seen = [0, 0]
+    for _ in range(3000):
+        base = rng.choice([64, 128, 192, 384])
+        steps = [base, base * rng.choice([2, 3, 5]), base * rng.choice([6, 8, 15])]
+        views = []
+        for v in range(2):
+            token, head, batch = rng.sample(steps, 3) if rng.random() < 0.5 else steps
+            views.append(part(Q + 2 * 8 * rng.randrange(0, 600), rng.choice([1, 2, 4]), token, head, batch))
+
+        def elements(v):
+            return [(v.data - Q) // 2 + b * v.stride_batch + n * v.stride_token + h * v.stride_head + e
+                    for b in range(B) for n in range(N) for h in range(v.heads) for e in range(0, d, 8)]
+
+        mine, other = (elements(v) for v in views)
+        if len(set(mine)) < len(mine):
+            continue                                                 # rows of the output that overlap each other
+        q = part(0x40000000, views[0].heads, 4 * 64, batch=12 * 64)
+        st = fwd(lib, q=q, k=views[1], qo=views[0], ko=part(0x50000000, views[1].heads, 4 * 64, batch=12 * 64), B=B, N=N)
+        if st == INVALID and "rows overlap each other" in lib.attn_last_error().decode():
+            continue
+        shares = not set(mine).isdisjoint(other)
+        assert (st == INVALID) == shares and st not in (UNSUPPORTED, OK)
+        seen[shares] += 1
+    assert min(seen) > 200
+
+
 KC, VC, TAB, IDS, POS = (ctypes.c_void_p(0x20000000 + i * 0x1000000) for i in range(5))
 
 
