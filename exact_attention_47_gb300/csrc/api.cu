@@ -412,6 +412,10 @@ Strided strided(const attn_heads_t& h, int B, int N, int d) {
   return Strided{h.data, 2LL * d, {2 * h.stride_batch, 2 * h.stride_token, 2 * h.stride_head}, {B, N, h.heads}};
 }
 
+Strided flat(const void* p, size_t bytes) {
+  return Strided{p, static_cast<long long>(bytes), {0, 0, 0}, {1, 1, 1}};
+}
+
 // Whether `off` = sum over the dimensions of m step with m in lo .. hi, give or
 // take what two runs reach (lo_run .. hi_run).  Dimensions go from the largest
 // step down, so that few m are left to try where they lie inside one another;
@@ -531,6 +535,27 @@ size_t rope_position_bytes(const attn_rope_t* r, int B, int N) {
   return static_cast<size_t>((r->axes - 1) * r->stride_axis + (B - 1) * r->stride_batch + N) * 4;
 }
 
+// What a call reads beside its rows.
+struct Input {
+  Strided s;
+  const char* name;
+};
+
+// An output keeps off all of it: other warps may still be reading there.
+attn_status_t check_inputs_kept(const Strided& out, const char* out_name, const Input* in, int n) {
+  for (int i = 0; i < n; ++i)
+    if (in[i].s.p != nullptr && meet(out, in[i].s))
+      return fail(ATTN_ERR_INVALID_ARG, "%s overlaps %s", out_name, in[i].name);
+  return ATTN_OK;
+}
+
+// The frequencies and positions of a rotation.
+void rope_inputs(const attn_rope_t* r, int B, int N, Input (&in)[2]) {
+  in[0] = Input{flat(r ? r->inv_freq : nullptr, r ? static_cast<size_t>(r->rot / 2) * 4 : 0), "inv_freq"};
+  in[1] = Input{Strided{r ? r->positions : nullptr, 4LL * N, {r ? 4 * r->stride_axis : 0, r ? 4 * r->stride_batch : 0, 0},
+                        {r ? r->axes : 1, B, 1}}, "the rotation's positions"};
+}
+
 attn_status_t rope_apply(const char* what, const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* q_out,
                          const attn_heads_t* k_out, const attn_rope_t* rope, int B, int N, int d, bool inverse,
                          void* stream) {
@@ -562,6 +587,10 @@ attn_status_t rope_apply(const char* what, const attn_heads_t* q, const attn_hea
   if ((st = check_apart(k_out, "k_out", k, "k", true, B, N, d)) != ATTN_OK) return st;
   if ((st = check_apart(k_out, "k_out", q, "q", false, B, N, d)) != ATTN_OK) return st;
   if ((st = check_apart(k_out, "k_out", q_out, "q_out", false, B, N, d)) != ATTN_OK) return st;
+  Input in[2];
+  rope_inputs(rope, B, N, in);
+  if ((st = check_inputs_kept(strided(*q_out, B, N, d), "q_out", in, 2)) != ATTN_OK) return st;
+  if (k_out != nullptr && (st = check_inputs_kept(strided(*k_out, B, N, d), "k_out", in, 2)) != ATTN_OK) return st;
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != ATTN_OK) return st;
   auto bytes = [&](const attn_heads_t* h) { return h ? static_cast<size_t>(heads_extent(*h, B, N, d)) * 2 : 0; };
@@ -641,15 +670,22 @@ attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_he
             : overlap(k_cache, cache, x.h->data, n) || overlap(v_cache, cache, x.h->data, n))
       return fail(ATTN_ERR_INVALID_ARG, "%s overlaps the cache", x.name);
   }
+  const size_t ints = static_cast<size_t>(T) * 4, table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4;
+  Input turn[2];
+  rope_inputs(rope, 1, T, turn);
+  const Input in[5] = {turn[0], turn[1], {flat(block_table, table), "block_table"}, {flat(seq_ids, ints), "seq_ids"},
+                       {flat(positions, ints), "positions"}};
+  if (q_out != nullptr && (st = check_inputs_kept(strided(*q_out, 1, T, d), "q_out", in, 5)) != ATTN_OK) return st;
+  for (const void* x : {kv4 ? kv_cache : k_cache, kv4 ? nullptr : v_cache})
+    if (x != nullptr && (st = check_inputs_kept(flat(x, cache), "the cache", in, 5)) != ATTN_OK) return st;
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != ATTN_OK) return st;
   auto bytes = [&](const attn_heads_t* h) { return h ? static_cast<size_t>(heads_extent(*h, 1, T, d)) * 2 : 0; };
-  const size_t ints = static_cast<size_t>(T) * 4;
   if ((st = check_bufs(*dev, {{q ? q->data : nullptr, bytes(q), "q"}, {k->data, bytes(k), "k"},
                               {v->data, bytes(v), "v"}, {q_out ? q_out->data : nullptr, bytes(q_out), "q_out"},
                               {k_cache, kv4 ? 0 : cache, "k_cache"}, {v_cache, kv4 ? 0 : cache, "v_cache"},
                               {kv_cache, kv4 ? cache : 0, "kv_cache"},
-                              {block_table, static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, "block_table"},
+                              {block_table, table, "block_table"},
                               {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"},
                               {rope ? rope->inv_freq : nullptr, rope ? static_cast<size_t>(rope->rot / 2) * 4 : 0,
                                "inv_freq"},

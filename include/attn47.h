@@ -456,7 +456,8 @@ typedef struct attn_rope {
  *  q, k           [B, heads, N, d] by their strides; k may be NULL (queries
  *                 only).  Inputs may be broadcast (stride 0).
  *  q_out, k_out   the same shapes (written).  Each is its input (in place) or
- *                 shares no element with any other view of the call.
+ *                 shares no element with any other view of the call; nor do
+ *                 they overlap the frequencies or positions.
  *  d must be 64 or 128.  B == 0 or N == 0: ATTN_OK, nothing launched.  One
  *  kernel, deterministic.
  */
@@ -487,12 +488,13 @@ attn_status_t rope_bwd(const attn_heads_t* dq_out, const attn_heads_t* dk_out, c
  *
  *  q          [T, Hq, d] by strides (stride_batch unused), or NULL
  *  k, v       [T, Hkv, d] by strides
- *  q_out      [T, Hq, d] by strides (written): q itself or memory of its own;
- *             NULL with q
+ *  q_out      [T, Hq, d] by strides (written): q itself, or memory of which no
+ *             other argument has an element; NULL with q
  *  rope       the rotation, or NULL for none (q is then copied).  Its positions
  *             may be NULL: the cache positions; else token t of batch 0
  *  k_cache,
- *  v_cache    [num_blocks, Hkv, 16, d] bf16 (written at the new slots)
+ *  v_cache    [num_blocks, Hkv, 16, d] bf16 (written at the new slots); they
+ *             overlap neither each other nor an input
  *  block_table [num_seqs, max_blocks_per_seq] int32, seq_ids and positions
  *             [T] int32 (device)
  *  block_size must be 16; d 64 or 128.  T == 0: ATTN_OK, nothing launched.

@@ -302,6 +302,41 @@ def test_read_outputs_keep_off_the_token_map(lib):
         assert read(lib, v=at) == INVALID
 
 
+@pytest.mark.parametrize("func", ["rope_fwd", "rope_bwd"])
+def test_rotations_keep_off_positions_and_frequencies(lib, func):
+    """Other warps may still be reading there."""
+    B, N, d, far = 2, 16, 64, 0x9000000
+    for axes, stride_axis, stride_batch in ((1, 0, 16), (1, 0, 0), (3, 64, 16)):
+        r = _Rope(0x8000000, 64, 0, far, axes, stride_axis, stride_batch, bytes(32) if axes > 1 else None)
+        assert fwd(lib, r=r, B=B, func=func) not in RUNS
+        last = far + 4 * ((axes - 1) * stride_axis + (B - 1) * stride_batch) + 4 * (N - 4)   # the last 16 bytes
+        for at in (far, last, 0x8000000, 0x8000000 + 112):
+            for kw in (dict(qo=heads(at)), dict(ko=heads(at))):
+                assert fwd(lib, r=r, B=B, func=func, **kw) == INVALID
+                assert "overlaps" in lib.attn_last_error().decode()
+    # between the positions of two axes, or among rows with room between them: apart
+    r = _Rope(0x8000000, 64, 0, far, 2, 1 << 20, 0, bytes(32))
+    assert fwd(lib, r=r, func=func, qo=heads(far + (1 << 20))) not in RUNS
+    assert fwd(lib, r=rope(pos=QO + 256), func=func, qo=heads(QO, token=512)) not in RUNS
+
+
+@pytest.mark.parametrize("group", [None, 32])
+def test_appends_keep_off_what_they_read(lib, group):
+    T, d = 8, 64
+    cache = 8 * 2 * 16 * d * 2
+    r = rope()
+    for at in (TAB.value, TAB.value + 16, IDS.value, POS.value, POS.value + 16, 0x8000000, 0x9000000):
+        assert append(lib, group=group, qo=heads(at, N=T), r=r) == INVALID
+        assert "q_out overlaps" in lib.attn_last_error().decode()
+        assert append(lib, group=group, kc=ctypes.c_void_p(at), r=r) == INVALID
+        assert "the cache overlaps" in lib.attn_last_error().decode()
+        if group is None:
+            assert append(lib, vc=ctypes.c_void_p(at - cache + 16), r=r) == INVALID
+    own = _Rope(0x8000000, 64, 0, None, 1, 0, 0, None)               # turned by the cache's positions
+    for x in (r, own, None):
+        assert append(lib, group=group, r=x) not in RUNS
+
+
 # ------------------------------------------------------------------ binding
 class _OnCuda0(torch.Tensor):
     """A CPU tensor that claims to be on cuda:0 (it never reaches the library)."""
