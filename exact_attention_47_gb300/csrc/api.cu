@@ -1460,6 +1460,7 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
   a.num_blocks = num_blocks;
   a.sms = dev->sms;
   a.device = dev->index;
+  a.max_ctas = g_decode_max_ctas;
   a.epoch = next_decode_epoch();
   a.early_plan = g_decode_early_plan.load() > 0 ? 1 : 0;
   a.scale = scale;

@@ -1287,7 +1287,8 @@ cudaError_t launch_t(const DecKv4Launch& a) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
-  const int ctas = a.sms < 1 ? 1 : a.sms > kMaxCtas ? kMaxCtas : a.sms;
+  int ctas = a.sms < 1 ? 1 : a.sms > kMaxCtas ? kMaxCtas : a.sms;
+  if (a.max_ctas > 0 && ctas > a.max_ctas) ctas = a.max_ctas;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(Cfg::kThreads), Cfg::kSmem, a.stream, p);
 }
 

@@ -16,6 +16,7 @@ struct DecKv4Launch {
   void* workspace;
   int num_seqs, Hq, Hkv, d, group, max_blocks, num_blocks;
   int sms, device;
+  int max_ctas;                // 0: one CTA per SM
   unsigned int epoch;          // tag of this call's arrival counters (never 0)
   int early_plan;              // >= 1: see attn_set_decode_early_plan
   float scale;

@@ -593,8 +593,8 @@ size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d
  *  flags as for attn_decode_paged (Hq / Hkv <= 16); attn_set_decode_early_plan
  *  applies (level 2 acts as 1).  One kernel; the parts of a split (sequence,
  *  KV head) are merged in a fixed order, so the result is deterministic for a
- *  given device.  Calls that share a workspace must not
- *  overlap on the GPU.
+ *  given device and attn_set_decode_max_ctas setting.  Calls that share a
+ *  workspace must not overlap on the GPU.
  */
 attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const int32_t* block_table,
                                     const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int d,
