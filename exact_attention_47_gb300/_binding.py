@@ -14,6 +14,7 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+import warnings
 
 import torch
 
@@ -115,6 +116,17 @@ _FAST = ("rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "
          "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4")
 
 
+class _NoFastCalls:
+    """In place of the module of the fast calls where it is not built: nothing
+    is the usual case, every call goes the Python way."""
+
+    @staticmethod
+    def rope(*args):
+        return None
+
+    append = read = decode = rope
+
+
 @functools.lru_cache(maxsize=None)
 def _fast():
     """The module of the fast calls (csrc/fast_calls.cpp), bound to the
@@ -124,7 +136,9 @@ def _fast():
     lib = load_library()
     path = fast_path()
     if not os.path.exists(path):
-        raise RuntimeError("%s is not built; run `python -c \"import __graft_entry__ as g; g.build()\"`" % path)
+        warnings.warn("%s is not built (it takes g++ and the headers of Python and torch): the rotary, append and "
+                      "4-bit-cache calls cost more host time" % path, RuntimeWarning, stacklevel=3)
+        return _NoFastCalls
     loader = importlib.machinery.ExtensionFileLoader("_attn47_fast", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn47_fast", loader))
     loader.exec_module(module)

@@ -1,0 +1,43 @@
+"""The module of the fast calls is an addition: without it, or without what it
+is built with, everything else works (CPU)."""
+
+import os
+
+import pytest
+import torch
+
+import exact_attention_47_gb300 as attn
+from exact_attention_47_gb300 import _binding, build_lib
+from test_rope_kv4_checks import BF, F32, I32, dev, lib, no_library_calls  # noqa: F401
+
+
+@pytest.fixture
+def without_module(monkeypatch, tmp_path, lib):  # noqa: F811
+    monkeypatch.setattr(_binding, "fast_path", lambda: str(tmp_path / "absent.so"))
+    _binding._fast.cache_clear()
+    yield
+    _binding._fast.cache_clear()
+
+
+def test_calls_go_the_python_way_without_the_module(without_module, monkeypatch):
+    made = []
+    monkeypatch.setattr(_binding, "_call", lambda func, device, *args: made.append(func))
+    monkeypatch.setattr(_binding, "_stream_handle", lambda *a: 0)
+    T, S, Hq, Hkv, d = 6, 2, 4, 2, 64
+    rec = attn.kv4_record_bytes(d, 32)
+    q, k, f, pos = dev((2, Hq, 8, d), BF), dev((2, Hkv, 8, d), BF), dev((32,), F32), dev((8,), I32)
+    rows = dev((T, Hq, d), BF), dev((T, Hkv, d), BF), dev((T, Hkv, d), BF)
+    kv, table, ids, at = dev((9, Hkv, rec), torch.uint8), dev((S, 4), I32), dev((T,), I32), dev((T,), I32)
+    with pytest.warns(RuntimeWarning, match="absent.so is not built"):
+        attn.rope_fwd(q, k, pos, f, q_out=q, k_out=k)
+    attn.rope_bwd(q, k, pos, f, dq=q, dk=k)
+    attn.rope_append_paged(*rows, dev((9, Hkv, 16, d), BF), dev((9, Hkv, 16, d), BF), table, ids, at, f, q_out=rows[0])
+    attn.rope_append_paged_kv4(*rows, kv, table, ids, at, 32, f, q_out=rows[0])
+    attn.kv4_read_paged(kv, table, ids, at, d, 32, rows[1], rows[2])
+    need = attn.attn_decode_paged_kv4_workspace_size(S, Hq, Hkv, d)
+    attn.attn_decode_paged_kv4(dev((S, Hq, d), BF), kv, table, dev((S,), I32), 32, o=dev((S, Hq, d), BF),
+                               lse=dev((S, Hq), F32), workspace=dev((need,), torch.uint8))
+    assert made == ["rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "kv4_read_paged",
+                    "attn_decode_paged_kv4"]
+    with pytest.raises(ValueError, match="positions of an axis"):
+        attn.rope_fwd(q, k, dev((9,), I32), f, q_out=q, k_out=k)
