@@ -6,7 +6,8 @@ one shared object with the CUDA runtime linked statically, so that the
 library loads on a machine without a GPU (e.g. to check its exported
 symbols) and needs only the driver at run time.  Beside it g++ builds
 ``lib/_attn47_fast_<torch version>.so``, the Python module that marshals the
-usual case of the short calls (csrc/fast_calls.cpp, against torch's headers).
+usual case of the short calls (csrc/fast_calls.cpp, against torch's headers);
+where that cannot be built, the library is, and those calls go another way.
 
 Usage: ``python -m exact_attention_47_gb300.build_lib`` or ``build()``.
 """
@@ -86,6 +87,23 @@ def _stale(obj, src):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_fast():
+    """Compile the module of the fast calls if its sources changed.  The library
+    does not need it: where it cannot be built, that is said, and one from other
+    sources is not left in its place."""
+    fast = None
+    try:
+        fast = fast_path()
+        if _stale(fast, os.path.join(CSRC, FAST_SOURCE)):
+            _run(_fast_command(fast + ".tmp"))
+            os.replace(fast + ".tmp", fast)
+    except (ImportError, OSError, RuntimeError) as e:
+        if fast is not None and os.path.exists(fast):
+            os.remove(fast)
+        sys.stderr.write("the module of the fast calls was not built (the rotary, append and 4-bit-cache calls cost "
+                         "more host time without it): %s\n" % e)
+
+
 def build(verbose=False, ptxas_info=False):
     """Compile (only what changed) and link; returns the library path."""
     nvcc = _nvcc()
@@ -99,19 +117,14 @@ def build(verbose=False, ptxas_info=False):
             cmd = [nvcc] + CFLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", s, "-o", o]
             jobs.append(cmd)
     link = bool(jobs) or not os.path.exists(LIB_PATH)
-    fast = fast_path()
-    if _stale(fast, os.path.join(CSRC, FAST_SOURCE)):
-        jobs.append(_fast_command(fast + ".tmp"))
-    else:
-        fast = None
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        fast = ex.submit(_build_fast)
         outs = list(ex.map(_run, jobs))
+        fast.result()
     if verbose or ptxas_info:
         for out in outs:
             sys.stdout.write(out)
     objs = [os.path.join(BUILD_DIR, s.replace(".cu", ".o")) for s in SOURCES]
-    if fast is not None:
-        os.replace(fast + ".tmp", fast)
     if link:
         tmp = LIB_PATH + ".tmp"
         _run([nvcc] + GENCODE + ["-shared", "-cudart", "static", "-o", tmp] + objs)

@@ -41,3 +41,26 @@ def test_calls_go_the_python_way_without_the_module(without_module, monkeypatch)
                     "attn_decode_paged_kv4"]
     with pytest.raises(ValueError, match="positions of an axis"):
         attn.rope_fwd(q, k, dev((9,), I32), f, q_out=q, k_out=k)
+
+
+@pytest.mark.parametrize("command,told", [(["/nonexistent/g++"], "nonexistent"), (["false"], "command failed")])
+def test_the_library_builds_without_the_module(monkeypatch, tmp_path, capfd, lib, command, told):  # noqa: F811
+    """No compiler for it, or one that fails: the library is there, the reason
+    is told, and a module from older sources is gone."""
+    old = tmp_path / "fast.so"
+    old.write_text("older")
+    os.utime(old, (0, 0))
+    monkeypatch.setattr(build_lib, "fast_path", lambda: str(old))
+    monkeypatch.setattr(build_lib, "_fast_command", lambda out: command)
+    assert os.path.exists(build_lib.build())
+    err = capfd.readouterr().err
+    assert "fast calls was not built" in err and told in err and not old.exists()
+
+
+def test_the_library_builds_without_torch(monkeypatch, capfd, lib):  # noqa: F811
+    def absent():
+        raise ImportError("No module named 'torch'")
+
+    monkeypatch.setattr(build_lib, "_torch", absent)
+    assert os.path.exists(build_lib.build())
+    assert "No module named 'torch'" in capfd.readouterr().err
