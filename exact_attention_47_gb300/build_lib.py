@@ -5,7 +5,7 @@ Every translation unit is compiled for sm_103a only
 one shared object with the CUDA runtime linked statically, so that the
 library loads on a machine without a GPU (e.g. to check its exported
 symbols) and needs only the driver at run time.  Beside it g++ builds
-``lib/_attn47_fast_<torch version>.so``, the Python module that marshals the
+``lib/_attn47_fast_<torch version>.<Python's ABI>.so``, the Python module that marshals the
 usual case of the short calls (csrc/fast_calls.cpp, against torch's headers);
 where that cannot be built, the library is, and those calls go another way.
 
@@ -45,8 +45,9 @@ def _torch():
 
 
 def fast_path():
-    """Where the module of the fast calls is built for the installed torch."""
-    return os.path.join(LIB_DIR, "_attn47_fast_%s.so" % _torch()[0])
+    """Where the module of the fast calls is built for the installed torch and
+    this Python: it fits no other of either."""
+    return os.path.join(LIB_DIR, "_attn47_fast_%s%s" % (_torch()[0], sysconfig.get_config_var("EXT_SUFFIX")))
 
 
 def _fast_command(out):

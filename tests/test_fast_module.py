@@ -64,3 +64,16 @@ def test_the_library_builds_without_torch(monkeypatch, capfd, lib):  # noqa: F81
     monkeypatch.setattr(build_lib, "_torch", absent)
     assert os.path.exists(build_lib.build())
     assert "No module named 'torch'" in capfd.readouterr().err
+
+
+def test_the_module_of_another_interpreter_is_not_loaded(monkeypatch, lib):  # noqa: F811
+    """Each Python has a file of its own, so another's is as good as none."""
+    mine = build_lib.fast_path()
+    monkeypatch.setattr(build_lib.sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")
+    assert build_lib.fast_path() != mine and not os.path.exists(build_lib.fast_path())
+    _binding._fast.cache_clear()
+    try:
+        with pytest.warns(RuntimeWarning, match="cpython-399-other.so is not built"):
+            assert _binding._fast() is _binding._NoFastCalls
+    finally:
+        _binding._fast.cache_clear()
