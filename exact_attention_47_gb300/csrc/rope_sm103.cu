@@ -257,8 +257,9 @@ __device__ __forceinline__ uint32_t pack_codes(const uint32_t (&code)[8]) {
 struct RopeShared {
   uint64_t frac[64];
   uint32_t axis[64];               // bit 2: not finite
-  float2 cs[kWarps][64];
+  alignas(16) float2 cs[kWarps][64];   // read two at a time
 };
+static_assert(alignof(RopeShared) == 16, "16-byte loads of the angles");
 
 __device__ __forceinline__ void load_pairs(const RopeParams& p, RopeShared& sh) {
   for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
