@@ -516,7 +516,6 @@ attn_status_t check_rope(const attn_rope_t* r, int B, int d, bool needs_position
     return fail(ATTN_ERR_INVALID_ARG, "position strides must be non-negative and not too large");
   out->inv_freq = r->inv_freq;
   out->rot = r->rot;
-  out->axes = r->axes;
   out->interleaved = r->interleaved != 0;
   out->positions = r->positions;
   out->axis_stride = r->stride_axis;

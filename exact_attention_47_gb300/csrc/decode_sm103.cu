@@ -198,6 +198,33 @@ struct SegWalk {
   }
 };
 
+// Arrival of one part of a split run on the run's counter (one lane).  The
+// counter holds this call's tag in its high half and the parts arrived in
+// its low half; a value with another tag (a previous call, or workspace
+// contents never written by this library) counts as zero arrivals.  Returns
+// whether this was the last part; the last part resets the counter to zero
+// for the next call (a replayed graph reuses its tag).  The first guess of
+// the counter's value is what the usual order of arrivals gives: part 0 is
+// the last segment of its CTA and arrives after the others.
+__device__ __forceinline__ bool arrive_part(const DecParams& p, unsigned long long* slot, int part,
+                                            int nparts) {
+  const unsigned long long tag = static_cast<unsigned long long>(p.epoch) << 32;
+  unsigned long long cur = part == 0 ? tag | static_cast<unsigned int>(nparts - 1) : 0ull;
+  for (int i = 0; i < 2 * nparts + 2; ++i) {
+    const unsigned long long base = (cur >> 32) == p.epoch ? cur : tag;
+    const unsigned long long next = base + 1;
+    const unsigned long long prev = atomicCAS(slot, cur, next);
+    if (prev == cur) {
+      const bool last = static_cast<int>(next & 0xffffffffu) >= nparts;
+      if (last) atomicExch(slot, 0ull);
+      return last;
+    }
+    cur = prev;
+  }
+  atomicOr(p.status, kDevTimeout);   // more arrivals than parts: cannot happen
+  return false;
+}
+
 // Exact merge of the published parts [s0, s1) of the G query heads
 // hq0 .. hq0+G-1 by one warp: with M = max_s m_s, O = sum_s 2^(m_s - M) O_s
 // / sum_s 2^(m_s - M) l_s and LSE = (M + log2 of the denominator) ln 2.
@@ -392,7 +419,7 @@ __device__ __forceinline__ void merge_segment(const DecParams& p, const float* c
   __threadfence();
   __syncwarp();
   int last = 0;
-  if (lane == 0) last = count_arrival(slot, p.epoch, part, nparts, p.status);
+  if (lane == 0) last = arrive_part(p, slot, part, nparts);
   last = __shfl_sync(0xffffffffu, last, 0);
   if (last) {
     __threadfence();

@@ -639,32 +639,4 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
-// ---------------------------------------- arrival of the parts of a split run
-// Counts one part of a run that is split over CTAs (one lane).  The counter
-// holds a call's tag (never 0) in its high half and the parts arrived in its
-// low half; a value with another tag (a previous call, or memory never
-// written by this library) counts as zero arrivals.  Returns whether this was
-// the last part; the last part resets the counter to zero for the next call
-// (a replayed graph reuses its tag).  The first guess of the counter's value
-// is what the usual order of arrivals gives: part 0 is the last segment of
-// its CTA and arrives after the others.
-__device__ __forceinline__ bool count_arrival(unsigned long long* slot, unsigned int epoch, int part, int nparts,
-                                              unsigned int* status) {
-  const unsigned long long tag = static_cast<unsigned long long>(epoch) << 32;
-  unsigned long long cur = part == 0 ? tag | static_cast<unsigned int>(nparts - 1) : 0ull;
-  for (int i = 0; i < 2 * nparts + 2; ++i) {
-    const unsigned long long base = (cur >> 32) == epoch ? cur : tag;
-    const unsigned long long next = base + 1;
-    const unsigned long long prev = atomicCAS(slot, cur, next);
-    if (prev == cur) {
-      const bool last = static_cast<int>(next & 0xffffffffu) >= nparts;
-      if (last) atomicExch(slot, 0ull);
-      return last;
-    }
-    cur = prev;
-  }
-  atomicOr(status, kDevTimeout);   // more arrivals than parts: cannot happen
-  return false;
-}
-
 }  // namespace attn47

@@ -76,7 +76,7 @@ struct RopeParams {
   const int* rope_pos;               // nullptr: the cache positions (append)
   long long axis_stride, batch_stride;
   uint32_t pair_axis[4];
-  int rot, axes, inverse;
+  int rot, inverse;
   int Hq, Hk, rows;                  // rows of a token: Hq + Hk (+ Hk values when appending)
   int N;                             // tokens per batch (rotation)
   int parts, rows_per_part;
@@ -687,7 +687,6 @@ void fill_spec(RopeParams& p, const RopeSpec& s) {
   p.batch_stride = s.batch_stride;
   for (int i = 0; i < 4; ++i) p.pair_axis[i] = s.pair_axis[i];
   p.rot = s.rot;
-  p.axes = s.axes;
   p.inverse = s.inverse ? 1 : 0;
 }
 

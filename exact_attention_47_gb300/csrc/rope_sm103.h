@@ -19,7 +19,6 @@ struct HeadRows {
 struct RopeSpec {
   const float* inv_freq = nullptr;   // [rot / 2] fp32 (device)
   int rot = 0;                       // leading elements of a head that rotate (a multiple of 16)
-  int axes = 1;                      // position axes (1 .. 4)
   bool interleaved = false;          // pairs (2p, 2p + 1) instead of (p, p + rot / 2)
   bool inverse = false;              // rotate by the negative angle
   uint32_t pair_axis[4] = {0, 0, 0, 0};   // axis of pair p: bits 2p, 2p + 1
