@@ -395,7 +395,8 @@ __device__ __forceinline__ void make_queries(const DecKv4Params& p, const QueryR
     // [2^14, 2^15).
     const int fe = min(268 - static_cast<int>(mx >> 7), 253);
     const float up = __uint_as_float(static_cast<uint32_t>(fe) << 23);
-    const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * 0x1p24f;
+    // (Never 0, which the -inf of slots without a token would make NaN.)
+    const float back = fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * 0x1p24f, 0x1p-126f);
     f.back[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
     f.back[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
     float sum[kGroups];

@@ -131,3 +131,18 @@ def test_constant_value_groups_of_any_size(lens, Hq, Hkv, d, group, low):
     w.copy_(mins.view(torch.int16).int() & 0xFFFF)
     o, lse = run(q, rec, table, n, group, 0.09)
     check_groups(o, lse, q, rec, table, n, 0.09, d, group)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-20, 1e-10])
+def test_queries_of_zero_and_tiny_scales_weigh_all_tokens_alike(scale):
+    q, rec, table, n = decode_case([5, 300, 17, 16], 12, 2, 128, 32, seed=241)
+    q[:, ::3] = 0
+    q[:, 1::3] *= 2.0 ** -100
+    o, lse = run(q, rec, table, n, 32, scale)
+    check_groups(o, lse, q, rec, table, n, scale, 128, 32)
+
+
+def test_one_sequence_of_131072_tokens():
+    q, rec, table, n = decode_case([131072, 100000], 8, 1, 128, 64, seed=243)
+    o, lse = run(q, rec, table, n, 64, 0.09)
+    check_groups(o, lse, q, rec, table, n, 0.09, 128, 64)
