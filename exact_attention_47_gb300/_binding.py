@@ -721,7 +721,8 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
 def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, v=None, stream=None):
     """The values that cached tokens of a 4-bit cache stand for: row t is
     position positions[t] of sequence seq_ids[t] ([T] int32; negative
-    sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16."""
+    sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16, which
+    rope_append_paged puts into a bf16 cache (for attn_prefill_paged, say)."""
     if stream is not None:
         return _on_stream(kv4_read_paged, stream, kv_cache, kv_cache, block_table, seq_ids, positions, d, group, k, v)
     done = _fast().read(kv_cache, block_table, seq_ids, positions, d, group, k, v)

@@ -549,8 +549,9 @@ attn_status_t rope_append_paged_kv4(const attn_heads_t* q, const attn_heads_t* k
 /*
  * kv4_read_paged — the values that cached tokens of a 4-bit cache stand for:
  * row t is the token at logical position positions[t] of sequence seq_ids[t]
- * (for a chunk that attends to what the cache holds, or to move a prefix to a
- * bf16 cache).
+ * (to move a prefix to a bf16 cache: its rows go into rope_append_paged as they
+ * are, without queries or a rotation.  No call lets a prompt chunk attend to a
+ * 4-bit cache itself; attn_prefill_paged does to the prefix so moved).
  *
  *  k, v       [T, Hkv, d] bf16, contiguous, 16-byte aligned (written); they
  *             overlap neither each other nor an input
