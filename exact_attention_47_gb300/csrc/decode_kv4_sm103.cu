@@ -471,7 +471,7 @@ struct RunState {
       // (at most 2^126: scales under 2^-102 lose bits; one that is no number takes
       // its group to the end of the range, and spoils it anyway).
       const int E = static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 23);
-      const int had = __float_as_int(room[g]), has = min(had, (278 - min(E, 254)) << 23);
+      const int had = __float_as_int(room[g]), has = min(had, (278 - min(max(E, 25), 254)) << 23);
       room[g] = __int_as_float(has);
       less[g] = __int_as_float(max(has - had + (127 << 23), 0));
     }

@@ -146,3 +146,22 @@ def test_one_sequence_of_131072_tokens():
     q, rec, table, n = decode_case([131072, 100000], 8, 1, 128, 64, seed=243)
     o, lse = run(q, rec, table, n, 64, 0.09)
     check_groups(o, lse, q, rec, table, n, 0.09, 128, 64)
+
+
+@pytest.mark.parametrize("quiet", [0.0, 2.0 ** -126, 2.0 ** -110])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,group", SHAPES)
+def test_scales_of_next_to_nothing_before_ordinary_ones(lens, Hq, Hkv, d, group, quiet):
+    """Tokens whose V groups are constant (or hardly vary) come first, or lie
+    between others."""
+    q, rec, table, n = decode_case(lens, Hq, Hkv, d, group, seed=233)
+    low = int(torch.tensor(quiet).to(torch.bfloat16).view(torch.int16)) << 16
+    for part in (lambda j, L: j < L // 2, lambda j, L: j // 64 % 2 == 0):
+        mine = rec.clone()
+        w = v_words(mine, d, group)
+        for b, L in enumerate(lens):
+            for j in range(L):
+                if part(j, L):
+                    at = w[int(table[b, j // 16]), :, j % 16]
+                    at.copy_((at & 0xFFFF) | low)
+        o, lse = run(q, mine, table, n, group, 0.09)
+        check_groups(o, lse, q, mine, table, n, 0.09, d, group)
