@@ -637,14 +637,13 @@ __device__ __forceinline__ void take_blocks(const LaneData<D, G>& at, const uint
     }
   }
 
-  // (A word as a float is its scale with some bits more.  NaN drops out.)
-  float big = 0.f;
+  // Whether a scale times its group's room reaches kFull, in the bits of floats
+  // (exponents add up).
+  uint32_t big = 0;
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      big = fmaxf(big, fmaxf(__uint_as_float(vp[n][0][g]) * st.room[g], __uint_as_float(vp[n][1][g]) * st.room[g]));
-  bool move = big >= kFull;
+  for (int g = 0; g < kGroups; ++g)
+    big = __viaddmax_u32(max(max(vp[0][0][g], vp[0][1][g]), max(vp[1][0][g], vp[1][1][g])), __float_as_uint(st.room[g]), big);
+  bool move = big >= (__float_as_uint(kFull) + (127u << 23));
   float top[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
