@@ -146,13 +146,6 @@ def _fast():
     return module
 
 
-def _made(func, done):
-    """What a fast call that was made returned, or its error raised."""
-    if done.__class__ is int:
-        _check(func, done)
-    return done
-
-
 def status_string(status):
     return load_library().attn_status_string(int(status)).decode()
 
@@ -544,7 +537,9 @@ def _rope_apply(func, q, k, positions, inv_freq, pair_axis, interleaved, q_out, 
                           None)
     done = _fast().rope(func == "rope_bwd", q, k, positions, inv_freq, pair_axis, interleaved, q_out, k_out)
     if done is not None:
-        return _made(func, done)
+        if done.__class__ is int:
+            _check(func, done)
+        return done
     hq = _heads("q", q, None, 4)
     dev = q.device
     B, _, N, d = q.shape
@@ -659,7 +654,9 @@ def rope_append_paged(q, k, v, k_cache, v_cache, block_table, seq_ids, positions
         done = _fast().append(q, k, v, k_cache, v_cache, block_table, seq_ids, positions, 0, inv_freq, rope_positions,
                               pair_axis, interleaved, q_out)
         if done is not None:
-            return _made("rope_append_paged", done)[0]
+            if done.__class__ is int:
+                _check("rope_append_paged", done)
+            return done[0]
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
@@ -706,7 +703,9 @@ def rope_append_paged_kv4(q, k, v, kv_cache, block_table, seq_ids, positions, gr
     done = _fast().append(q, k, v, kv_cache, None, block_table, seq_ids, positions, group, inv_freq, rope_positions,
                           pair_axis, interleaved, q_out)
     if done is not None:
-        return _made("rope_append_paged_kv4", done)[0]
+        if done.__class__ is int:
+            _check("rope_append_paged_kv4", done)
+        return done[0]
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
     nb, Hkv = _need_kv4(kv_cache, d, group, dev)
@@ -727,7 +726,9 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
         return _on_stream(kv4_read_paged, stream, kv_cache, kv_cache, block_table, seq_ids, positions, d, group, k, v)
     done = _fast().read(kv_cache, block_table, seq_ids, positions, d, group, k, v)
     if done is not None:
-        return _made("kv4_read_paged", done)
+        if done.__class__ is int:
+            _check("kv4_read_paged", done)
+        return done
     if not isinstance(seq_ids, torch.Tensor) or seq_ids.dim() != 1:
         raise ValueError("seq_ids must be a [T] tensor")
     nb, Hkv = _need_kv4(kv_cache, d, group, None)
@@ -758,7 +759,9 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
                           workspace, return_lse)
     done = _fast().decode(q, kv_cache, block_table, seq_lens, group, scale, o, lse, workspace, return_lse)
     if done is not None:
-        return _made("attn_decode_paged_kv4", done)
+        if done.__class__ is int:
+            _check("attn_decode_paged_kv4", done)
+        return done
     _need_cuda("q", q, torch.bfloat16)
     dev = q.device
     if q.dim() != 3:
