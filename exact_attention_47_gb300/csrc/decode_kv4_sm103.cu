@@ -733,7 +733,10 @@ __global__ void __launch_bounds__(DecKv4Cfg<D, G, NT>::kThreads, 1)
       if (hi <= lo) return;
       const size_t share = ((hi - lo) / gridDim.x + 16) & ~static_cast<size_t>(15);
       const uintptr_t at = lo + share * blockIdx.x;
-      if (at < hi) bulk_prefetch_l2(reinterpret_cast<const void*>(at), static_cast<uint32_t>(min(share, static_cast<size_t>(hi - at))));
+      // (At most 1 MB of each: with few CTAs a share may be far more than L2 is for.)
+      if (at < hi)
+        bulk_prefetch_l2(reinterpret_cast<const void*>(at),
+                         static_cast<uint32_t>(min(min(share, static_cast<size_t>(hi - at)), size_t(1) << 20)));
     };
     prefetch_share(p.seq_lens, static_cast<size_t>(p.num_seqs) * 4);
     // (A wide table is mostly padding.)

@@ -39,3 +39,16 @@ def test_the_bound_is_seen_in_the_workspace():
     ws = torch.full((attn.attn_decode_paged_kv4_workspace_size(1, 6, 1, 128),), 0xA5, dtype=torch.uint8, device=DEV)
     run(*case, 64, 0.09, workspace=ws)
     assert not torch.all(ws[256 * 8 + 4 * 6 * 128 * 4:][:2 * 6 * 128 * 4] == 0xA5)
+
+
+def test_many_queries_with_one_cta():
+    """64 MB of queries: what one CTA asks for ahead is bounded."""
+    S, Hq, Hkv, d, group = 4096, 64, 4, 128, 64
+    case = decode_case([1, 2, 0, 3] * (S // 4), Hq, Hkv, d, group, seed=239)
+    try:
+        attn.set_decode_max_ctas(1)
+        o, lse = run(*case, group, 0.09)
+    finally:
+        attn.set_decode_max_ctas(0)
+    want, want_lse = run(*case, group, 0.09)
+    assert torch.equal(lse, want_lse) and torch.equal(o, want)
