@@ -38,15 +38,17 @@
 // and the CTA that arrives last merges the parts.
 //
 // What bounds it (GB300, one column tile, d = 128): further blocks of long
-// contexts stream at 6.3 TB/s, nearly the rate of a copy; about 11.5 us of a call that
-// fills the GPU are latency, three dependent reads before the first block
-// (lengths, table, record: 4 us) and, at the end, the merge of a CTA's pieces,
-// the arrival and the merge of published parts (4 to 5 us, over 1 us for each
-// trip to what another SM has written).  8 sequences of 30k .. 131k tokens (195
-// MB) take 44.5 us, 64 of 128 .. 4096 (44 MB) 17.7 us, one of 100 6.1 us.  With d = 64 (4.8 TB/s) and with
-// two column tiles (3.3 at d = 64, 4.0 at d = 128) the arithmetic of a block
-// takes longer than its bytes: its instructions wait on one another, at two to
-// three warps a scheduler.
+// contexts stream at 6.1 TB/s (groups of 64; 6.0 with 32), near the rate of a
+// copy; about 12 us of a call that fills the GPU are latency, three dependent
+// reads before the first block (lengths, table, record: 4 us) and, at the end,
+// the merge of a CTA's pieces, the arrival and the merge of published parts (4
+// to 5 us, over 1 us for each trip to what another SM has written).  8 sequences
+// of 30k .. 131k tokens (195 MB) take 45 us, 64 of 128 .. 4096 (44 MB) 18.0 us,
+// one of 100 5.8 to 6.6 us.  With d = 64 (4.6 TB/s) and with two column tiles
+// (3.3 at d = 64, 4.0 at d = 128) the arithmetic of a block takes longer than
+// its bytes: its instructions wait on one another, at two to three warps a
+// scheduler.  (A power of two to each V group instead of one for all costs 1 to
+// 2%: 18.0 us instead of 17.6, 44.9 instead of 44.4.)
 #include <atomic>
 
 #include <cuda_fp16.h>

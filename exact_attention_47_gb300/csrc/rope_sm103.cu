@@ -21,16 +21,17 @@
 //
 // Measured (GB300, replayed graphs): 4 x 4096 tokens of 12 + 2 heads, d = 128
 // (118 MB) 22.1 us, 5.3 TB/s or 0.79 of a copy; 5001 tokens of 16 + 16 heads, d
-// = 64, three axes (41 MB) 10.5 us; an append of 7 ragged chunks (68 MB) 14.6
+// = 64, three axes (41 MB) 10.3 us; an append of 7 ragged chunks (68 MB) 14.5
 // us.  About 3 us of each are the launch and its first trip to memory; the rest
 // is at the copy rate.  The 4-bit append of 14600 tokens of 16 + 4 heads (158
-// MB) takes 36 us: 1560 warp instructions a token, issued in half of the cycles,
-// two thirds of them for the quantiser.
+// MB) takes 37 us: 1640 warp instructions a token, most of them for the
+// quantiser, issued in 57% of the cycles (a warp waits for its rows and then
+// works through them, in turn).
 // Copying rows ahead into a ring in shared memory, over the ends of tokens and
 // with equal shares for all warps, was slower (22.4 us instead of 21.5, 17.6
 // instead of 14.4): enough loads are in flight already, and each step then waits
 // for two more trips inside the SM.  The 4-bit append and its read-back take
-// 46.7 us together; 4-bit rows loaded before the queries are done cost 2 us more,
+// 47 us together; 4-bit rows loaded before the queries are done cost 2 us more,
 // and a fourth CTA a SM with its 64 registers gains 0.7 us here and loses 0.25 of
 // 5.6 in a decode step.  Equal shares of steps instead of whole tokens change
 // nothing (21.5, 10.2, 14.5 and 47.3 us).
