@@ -70,11 +70,11 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 CSRC = os.path.join(ROOT, "exact_attention_47_gb300", "csrc")
 TRAFFIC = {
     # median read + median write of 3 launches
-    "fwd": {"bytes": 67196160 + 5156352, "sources": ("fwd_sm103.cu", "fwd_sm103.h", "ptx.cuh"),
-            "sha256": "c061cce87aac37cddee53f431a14b87c1d506ad4be6b6457a2c5d3c8dc08a1fe"},
+    "fwd": {"bytes": 67192064 + 5373184, "sources": ("fwd_sm103.cu", "fwd_sm103.h", "ptx.cuh"),
+            "sha256": "aba585ac8cdef70f91a9bfef05fa1aeb750e0d50c124f312e62b487dd60311ff"},
     # decode kernel (split parts merged inside it), median read + median write of 3 launches
-    "dec": {"bytes": 132366848 + 414976, "sources": ("decode_sm103.cu", "decode_sm103.h", "ptx.cuh"),
-            "sha256": "f99b6fe8bb0649fd0f754ee35830d2875c82b20eee2a8b35250d418badad3f9b"},
+    "dec": {"bytes": 132367872 + 473856, "sources": ("decode_sm103.cu", "decode_sm103.h", "ptx.cuh"),
+            "sha256": "3054666127aebefdfd2346194dbf2069b46fa8433a95eeb723e38371396fb2f8"},
 }
 
 
