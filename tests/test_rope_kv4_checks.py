@@ -123,7 +123,11 @@ def test_merged_parts_are_told_apart(lib):
     assert fwd(lib, q=q, k=k2, qo=q, ko=k2) == INVALID
 
 
-RUNS = (INVALID, UNSUPPORTED, OK)                # none of these: it got as far as the missing device
+def passes(lib, status):
+    """The arguments are accepted: the call got as far as the missing device or,
+    where there is one, to these addresses not being its memory."""
+    return status == 3 or (status == INVALID and
+                           re.search("is not (device memory|memory of device)", lib.attn_last_error().decode()) is not None)
 
 
 def part(at, H, token, head=64, batch=0, d=64):
@@ -135,7 +139,7 @@ def test_merged_parts_of_one_token_a_batch_are_told_apart(lib, token):
     """A decode step's [B, 1, (Hq + 2 Hkv) d]: one token, whose stride means
     nothing."""
     q, k = part(Q, 2, token, batch=512), part(Q + 2 * 128, 2, token, batch=512)
-    assert fwd(lib, q=q, k=k, qo=q, ko=k, B=4, N=1) not in RUNS
+    assert passes(lib, fwd(lib, q=q, k=k, qo=q, ko=k, B=4, N=1))
     over = part(Q + 2 * 64, 2, token, batch=512)
     assert fwd(lib, q=q, k=over, qo=q, ko=over, B=4, N=1) == INVALID
     last = part(Q + 2 * 448, 2, token, batch=512)                    # its second head is the next batch's first
@@ -149,10 +153,10 @@ def test_head_major_parts_are_told_apart(lib):
         q = part(Q, 2, d, head=N * d, batch=5 * N * d)
         k = part(Q + 2 * k_first * N * d, 2, d, head=N * d, batch=5 * N * d)
         st = fwd(lib, q=q, k=k, qo=q, ko=k, B=B, N=N)
-        assert (st not in RUNS) if ok else st == INVALID
+        assert passes(lib, st) == ok and st != UNSUPPORTED
     # q and k as halves of every token of a head: [B, H, N, 2, d]
     q, k = (part(Q + 2 * i * d, 2, 2 * d, head=2 * N * d, batch=4 * N * d) for i in range(2))
-    assert fwd(lib, q=q, k=k, qo=q, ko=k, B=B, N=N) not in RUNS
+    assert passes(lib, fwd(lib, q=q, k=k, qo=q, ko=k, B=B, N=N))
 
 
 @pytest.mark.parametrize("B,N", [(1, 1), (1, 7), (3, 7), (3, 1)])
@@ -161,13 +165,13 @@ def test_parts_interleaved_by_head_are_told_apart(lib, B, N):
     H, d = 5, 64
     qkv = [part(Q + 2 * i * d, H, 3 * H * d, head=3 * d, batch=3 * N * H * d) for i in range(3)]
     for func in ("rope_fwd", "rope_bwd"):
-        assert fwd(lib, q=qkv[0], k=qkv[1], qo=qkv[0], ko=qkv[1], B=B, N=N, func=func) not in RUNS
+        assert passes(lib, fwd(lib, q=qkv[0], k=qkv[1], qo=qkv[0], ko=qkv[1], B=B, N=N, func=func))
         apart = [heads(QO, H=H, N=N), heads(KO, H=H, N=N)]
-        assert fwd(lib, q=apart[0], k=apart[1], qo=qkv[0], ko=qkv[1], B=B, N=N, func=func) not in RUNS
+        assert passes(lib, fwd(lib, q=apart[0], k=apart[1], qo=qkv[0], ko=qkv[1], B=B, N=N, func=func))
         near = part(Q + 2 * (d + 8), H, 3 * H * d, head=3 * d, batch=3 * N * H * d)   # 8 elements into the third part
         assert fwd(lib, q=qkv[0], k=qkv[1], qo=qkv[2], ko=near, B=B, N=N, func=func) == INVALID
     if B == 1:
-        assert append(lib, q=qkv[0], k=qkv[1], v=qkv[2], qo=qkv[0], T=N) not in RUNS
+        assert passes(lib, append(lib, q=qkv[0], k=qkv[1], v=qkv[2], qo=qkv[0], T=N))
         assert append(lib, q=qkv[0], k=qkv[1], v=qkv[2], qo=qkv[2], T=N) == INVALID
 
 
@@ -197,7 +201,7 @@ def test_views_are_told_apart_as_their_elements_are(lib):
         if st == INVALID and "rows overlap each other" in lib.attn_last_error().decode():
             continue
         shares = not set(mine).isdisjoint(other)
-        assert (st == INVALID) == shares and st not in (UNSUPPORTED, OK)
+        assert passes(lib, st) != shares and st not in (UNSUPPORTED, OK)
         seen[shares] += 1
     assert min(seen) > 200
 
@@ -308,7 +312,7 @@ def test_rotations_keep_off_positions_and_frequencies(lib, func):
     B, N, d, far = 2, 16, 64, 0x9000000
     for axes, stride_axis, stride_batch in ((1, 0, 16), (1, 0, 0), (3, 64, 16)):
         r = _Rope(0x8000000, 64, 0, far, axes, stride_axis, stride_batch, bytes(32) if axes > 1 else None)
-        assert fwd(lib, r=r, B=B, func=func) not in RUNS
+        assert passes(lib, fwd(lib, r=r, B=B, func=func))
         last = far + 4 * ((axes - 1) * stride_axis + (B - 1) * stride_batch) + 4 * (N - 4)   # the last 16 bytes
         for at in (far, last, 0x8000000, 0x8000000 + 112):
             for kw in (dict(qo=heads(at)), dict(ko=heads(at))):
@@ -316,8 +320,8 @@ def test_rotations_keep_off_positions_and_frequencies(lib, func):
                 assert "overlaps" in lib.attn_last_error().decode()
     # between the positions of two axes, or among rows with room between them: apart
     r = _Rope(0x8000000, 64, 0, far, 2, 1 << 20, 0, bytes(32))
-    assert fwd(lib, r=r, func=func, qo=heads(far + (1 << 20))) not in RUNS
-    assert fwd(lib, r=rope(pos=QO + 256), func=func, qo=heads(QO, token=512)) not in RUNS
+    assert passes(lib, fwd(lib, r=r, func=func, qo=heads(far + (1 << 20))))
+    assert passes(lib, fwd(lib, r=rope(pos=QO + 256), func=func, qo=heads(QO, token=512)))
 
 
 @pytest.mark.parametrize("group", [None, 32])
@@ -334,7 +338,7 @@ def test_appends_keep_off_what_they_read(lib, group):
             assert append(lib, vc=ctypes.c_void_p(at - cache + 16), r=r) == INVALID
     own = _Rope(0x8000000, 64, 0, None, 1, 0, 0, None)               # turned by the cache's positions
     for x in (r, own, None):
-        assert append(lib, group=group, r=x) not in RUNS
+        assert passes(lib, append(lib, group=group, r=x))
 
 
 # ------------------------------------------------------------------ binding
