@@ -53,6 +53,9 @@ _SIGS = {
     "rope_append_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "kv4_record_bytes": (ctypes.c_size_t, [_I, _I]),
     "rope_append_paged_kv4": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "kv8_record_bytes": (ctypes.c_size_t, [_I]),
+    "rope_append_paged_kv8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "kv8_read_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "kv4_read_paged": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "attn_decode_paged_kv4_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "attn_decode_paged_kv4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
@@ -113,7 +116,8 @@ def load_library(path=None):
 
 # The entry points that the fast calls pass on to, in the order of their `bind`.
 _FAST = ("rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "kv4_record_bytes", "kv4_read_paged",
-         "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4")
+         "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4", "rope_append_paged_kv8", "kv8_record_bytes",
+         "kv8_read_paged")
 
 
 class _NoFastCalls:
@@ -124,7 +128,7 @@ class _NoFastCalls:
     def rope(*args):
         return None
 
-    append = read = decode = rope
+    append = read = decode = append8 = read8 = rope
 
 
 @functools.lru_cache(maxsize=None)
@@ -738,6 +742,76 @@ def kv4_read_paged(kv_cache, block_table, seq_ids, positions, d, group, k=None, 
     v = _output("v", v, (T, Hkv, d), torch.bfloat16, dev)
     _call("kv4_read_paged", dev, _ptr(kv_cache), group, _ptr(block_table), _ptr(seq_ids), _ptr(positions), _ptr(k),
           _ptr(v), T, block_table.shape[0], Hkv, d, BLOCK_SIZE, block_table.shape[1], nb, _stream_handle(None, dev))
+    return k, v
+
+
+@functools.lru_cache(maxsize=None)
+def kv8_record_bytes(d):
+    """Bytes of one (block, KV head) record of an 8-bit cache."""
+    n = int(load_library().kv8_record_bytes(int(d)))
+    if n == 0:
+        raise ValueError("an 8-bit cache has d 64 or 128, got d %d" % d)
+    return n
+
+
+def _need_kv8(kv_cache, d, device):
+    """(num_blocks, Hkv) of an 8-bit cache."""
+    _need_cuda("kv_cache", kv_cache, torch.uint8, device)
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[2] != kv8_record_bytes(d):
+        raise ValueError("kv_cache must be [num_blocks, Hkv, %d] for d %d, got %s"
+                         % (kv8_record_bytes(d), d, tuple(shape)))
+    return shape[0], shape[1]
+
+
+def rope_append_paged_kv8(q, k, v, kv_cache, block_table, seq_ids, positions, inv_freq=None, rope_positions=None,
+                          pair_axis=None, interleaved=False, q_out=None, stream=None):
+    """rope_append_paged into an 8-bit cache: kv_cache
+    [num_blocks,Hkv,kv8_record_bytes(d)] uint8 (updated in place), e4m3 codes
+    with a scale (a power of two) per block of 16 tokens and head for the keys
+    and one for the values.  Rows that fall into one block stand together, in
+    the order of their positions; a row for a block's first slot begins it anew.
+    Returns q_out (or None without q)."""
+    if stream is not None:
+        return _on_stream(rope_append_paged_kv8, stream, k, q, k, v, kv_cache, block_table, seq_ids, positions,
+                          inv_freq, rope_positions, pair_axis, interleaved, q_out)
+    done = _fast().append8(q, k, v, kv_cache, None, block_table, seq_ids, positions, 0, inv_freq, rope_positions,
+                           pair_axis, interleaved, q_out)
+    if done is not None:
+        if done.__class__ is int:
+            _check("rope_append_paged_kv8", done)
+        return done[0]
+    dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
+        q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
+    nb, Hkv = _need_kv8(kv_cache, d, dev)
+    if Hkv != k.shape[1]:
+        raise ValueError("kv_cache must have k's heads")
+    _call("rope_append_paged_kv8", dev, hq, hk, hv, ho, rope[0], _ptr(kv_cache), _ptr(block_table), _ptr(seq_ids),
+          _ptr(positions), T, block_table.shape[0], d, BLOCK_SIZE, block_table.shape[1], nb,
+          _stream_handle(None, dev))
+    return q_out
+
+
+def kv8_read_paged(kv_cache, block_table, seq_ids, positions, d, k=None, v=None, stream=None):
+    """The values that cached tokens of an 8-bit cache stand for: row t is
+    position positions[t] of sequence seq_ids[t] ([T] int32; negative
+    sequences: rows left as they were).  Returns (k, v) [T,Hkv,d] bf16."""
+    if stream is not None:
+        return _on_stream(kv8_read_paged, stream, kv_cache, kv_cache, block_table, seq_ids, positions, d, k, v)
+    done = _fast().read8(kv_cache, block_table, seq_ids, positions, d, 0, k, v)
+    if done is not None:
+        if done.__class__ is int:
+            _check("kv8_read_paged", done)
+        return done
+    if not isinstance(seq_ids, torch.Tensor) or seq_ids.dim() != 1:
+        raise ValueError("seq_ids must be a [T] tensor")
+    nb, Hkv = _need_kv8(kv_cache, d, None)
+    dev, T = kv_cache.device, seq_ids.shape[0]
+    _token_map(block_table, seq_ids, positions, T, dev)
+    k = _output("k", k, (T, Hkv, d), torch.bfloat16, dev)
+    v = _output("v", v, (T, Hkv, d), torch.bfloat16, dev)
+    _call("kv8_read_paged", dev, _ptr(kv_cache), _ptr(block_table), _ptr(seq_ids), _ptr(positions), _ptr(k), _ptr(v),
+          T, block_table.shape[0], Hkv, d, BLOCK_SIZE, block_table.shape[1], nb, _stream_handle(None, dev))
     return k, v
 
 

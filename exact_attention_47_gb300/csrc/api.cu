@@ -12,6 +12,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "attn47.h"
@@ -22,6 +23,7 @@
 #include "gemm_sm103.h"
 #include "fwd_sm103.h"
 #include "kv4.cuh"
+#include "kv8.cuh"
 #include "rope_sm103.h"
 #include "ssd_sm103.h"
 #include "ptx.cuh"
@@ -612,13 +614,14 @@ attn_status_t rope_apply(const char* what, const attn_heads_t* q, const attn_hea
   return launch_result(attn47::launch_rope_sm103(a), what);
 }
 
-// Both appends: kv_cache == nullptr and group == 0 for the bf16 cache.
-attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+// All appends: into a cache of `bits` bits, 16 (k_cache and v_cache), 8 or 4
+// (kv_cache, and with 4 the group).
+attn_status_t rope_append(const char* what, int bits, const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
                           const attn_heads_t* q_out, const attn_rope_t* rope, void* k_cache, void* v_cache,
                           void* kv_cache, int group, const int32_t* block_table, const int32_t* seq_ids,
                           const int32_t* positions, int T, int num_seqs, int d, int block_size,
                           int max_blocks_per_seq, int num_blocks, void* stream) {
-  const bool kv4 = group != 0;
+  const bool packed = bits != 16;
   if (T < 0 || num_seqs < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
     return fail(ATTN_ERR_INVALID_ARG, "sizes must satisfy T >= 0, num_seqs, max_blocks_per_seq, num_blocks >= 1");
   if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
@@ -649,14 +652,16 @@ attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_he
       (reinterpret_cast<uintptr_t>(positions) & 3u))
     return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_ids and positions must be 4-byte aligned");
   const int Hkv = k->heads;
-  if (kv4 ? (!kv_cache || !aligned16(kv_cache)) : (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)))
+  if (packed ? (!kv_cache || !aligned16(kv_cache)) : (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)))
     return fail(ATTN_ERR_INVALID_ARG, "the cache must be non-null and 16-byte aligned");
   const size_t cache = static_cast<size_t>(num_blocks) * Hkv *
-                       (kv4 ? attn47::kv4_record_bytes_of(d, group) : static_cast<size_t>(16) * d * 2);
+                       (bits == 4   ? attn47::kv4_record_bytes_of(d, group)
+                        : bits == 8 ? attn47::kv8_record_bytes_of(d)
+                                    : static_cast<size_t>(16) * d * 2);
   if ((st = check_apart(q_out, "q_out", q, "q", true, 1, T, d)) != ATTN_OK) return st;
   if ((st = check_apart(q_out, "q_out", k, "k", false, 1, T, d)) != ATTN_OK) return st;
   if ((st = check_apart(q_out, "q_out", v, "v", false, 1, T, d)) != ATTN_OK) return st;
-  if (!kv4 && overlap(k_cache, cache, v_cache, cache))
+  if (!packed && overlap(k_cache, cache, v_cache, cache))
     return fail(ATTN_ERR_INVALID_ARG, "k_cache overlaps v_cache");
   const struct {
     const attn_heads_t* h;
@@ -665,7 +670,7 @@ attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_he
   for (const auto& x : rows) {
     if (x.h == nullptr) continue;
     const size_t n = static_cast<size_t>(heads_extent(*x.h, 1, T, d)) * 2;
-    if (kv4 ? overlap(kv_cache, cache, x.h->data, n)
+    if (packed ? overlap(kv_cache, cache, x.h->data, n)
             : overlap(k_cache, cache, x.h->data, n) || overlap(v_cache, cache, x.h->data, n))
       return fail(ATTN_ERR_INVALID_ARG, "%s overlaps the cache", x.name);
   }
@@ -675,15 +680,15 @@ attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_he
   const Input in[5] = {turn[0], turn[1], {flat(block_table, table), "block_table"}, {flat(seq_ids, ints), "seq_ids"},
                        {flat(positions, ints), "positions"}};
   if (q_out != nullptr && (st = check_inputs_kept(strided(*q_out, 1, T, d), "q_out", in, 5)) != ATTN_OK) return st;
-  for (const void* x : {kv4 ? kv_cache : k_cache, kv4 ? nullptr : v_cache})
+  for (const void* x : {packed ? kv_cache : k_cache, packed ? nullptr : v_cache})
     if (x != nullptr && (st = check_inputs_kept(flat(x, cache), "the cache", in, 5)) != ATTN_OK) return st;
   DeviceInfo* dev = nullptr;
   if ((st = current_device(&dev)) != ATTN_OK) return st;
   auto bytes = [&](const attn_heads_t* h) { return h ? static_cast<size_t>(heads_extent(*h, 1, T, d)) * 2 : 0; };
   if ((st = check_bufs(*dev, {{q ? q->data : nullptr, bytes(q), "q"}, {k->data, bytes(k), "k"},
                               {v->data, bytes(v), "v"}, {q_out ? q_out->data : nullptr, bytes(q_out), "q_out"},
-                              {k_cache, kv4 ? 0 : cache, "k_cache"}, {v_cache, kv4 ? 0 : cache, "v_cache"},
-                              {kv_cache, kv4 ? cache : 0, "kv_cache"},
+                              {k_cache, packed ? 0 : cache, "k_cache"}, {v_cache, packed ? 0 : cache, "v_cache"},
+                              {kv_cache, packed ? cache : 0, "kv_cache"},
                               {block_table, table, "block_table"},
                               {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"},
                               {rope ? rope->inv_freq : nullptr, rope ? static_cast<size_t>(rope->rot / 2) * 4 : 0,
@@ -711,6 +716,70 @@ attn_status_t rope_append(const char* what, const attn_heads_t* q, const attn_he
   a.status = dev->status;
   a.stream = static_cast<cudaStream_t>(stream);
   return launch_result(attn47::launch_rope_append_sm103(a), what);
+}
+
+// Read-back of a cache of `bits` bits, 8 or 4 (and then the group).
+attn_status_t read_paged(const char* what, int bits, const void* kv_cache, int group, const int32_t* block_table,
+                         const int32_t* seq_ids, const int32_t* positions, void* k, void* v, int T, int num_seqs,
+                         int Hkv, int d, int block_size, int max_blocks_per_seq, int num_blocks, void* stream) {
+  if (T < 0 || num_seqs < 1 || Hkv < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
+    return fail(ATTN_ERR_INVALID_ARG, "sizes must satisfy T >= 0, num_seqs, Hkv, max_blocks_per_seq, num_blocks >= 1");
+  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  if (T >= kMaxTokens) return fail(ATTN_ERR_UNSUPPORTED, "T too large");
+  if (T == 0) {
+    g_last_error[0] = '\0';
+    return ATTN_OK;
+  }
+  if (!kv_cache || !block_table || !seq_ids || !positions || !k || !v)
+    return fail(ATTN_ERR_INVALID_ARG, "kv_cache, block_table, seq_ids, positions, k and v must be non-null");
+  if (!aligned16(kv_cache) || !aligned16(k) || !aligned16(v))
+    return fail(ATTN_ERR_INVALID_ARG, "kv_cache, k and v must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_ids and positions must be 4-byte aligned");
+  const size_t cache = static_cast<size_t>(num_blocks) * Hkv *
+                       (bits == 8 ? attn47::kv8_record_bytes_of(d) : attn47::kv4_record_bytes_of(d, group));
+  const size_t out = static_cast<size_t>(T) * Hkv * d * 2;
+  if (overlap(k, out, v, out) || overlap(k, out, kv_cache, cache) || overlap(v, out, kv_cache, cache))
+    return fail(ATTN_ERR_INVALID_ARG, "k, v and kv_cache must not overlap");
+  const size_t ints = static_cast<size_t>(T) * 4, table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4;
+  for (const void* x : {k, v})
+    if (overlap(x, out, block_table, table) || overlap(x, out, seq_ids, ints) || overlap(x, out, positions, ints))
+      return fail(ATTN_ERR_INVALID_ARG, "k and v must not overlap block_table, seq_ids or positions");
+  DeviceInfo* dev = nullptr;
+  attn_status_t st = current_device(&dev);
+  if (st != ATTN_OK) return st;
+  if ((st = check_bufs(*dev, {{kv_cache, cache, "kv_cache"}, {block_table, table, "block_table"},
+                              {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"}, {k, out, "k"},
+                              {v, out, "v"}})) != ATTN_OK)
+    return st;
+  auto launch = [&](auto a) {
+    a.kv_cache = kv_cache;
+    a.block_table = block_table;
+    a.seq_ids = seq_ids;
+    a.positions = positions;
+    a.k = k;
+    a.v = v;
+    a.T = T;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.sms = dev->sms;
+    a.status = dev->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    if constexpr (std::is_same_v<decltype(a), attn47::Kv4ReadLaunch>) {
+      a.group = group;
+      return launch_result(attn47::launch_kv4_read_sm103(a), what);
+    } else {
+      return launch_result(attn47::launch_kv8_read_sm103(a), what);
+    }
+  };
+  return bits == 8 ? launch(attn47::Kv8ReadLaunch()) : launch(attn47::Kv4ReadLaunch());
 }
 
 attn_status_t check_group(int group) {
@@ -1301,7 +1370,7 @@ attn_status_t rope_append_paged(const attn_heads_t* q, const attn_heads_t* k, co
                                 void* v_cache, const int32_t* block_table, const int32_t* seq_ids,
                                 const int32_t* positions, int T, int num_seqs, int d, int block_size,
                                 int max_blocks_per_seq, int num_blocks, void* stream) {
-  return rope_append("rope_append_paged", q, k, v, q_out, rope, k_cache, v_cache, nullptr, 0, block_table, seq_ids,
+  return rope_append("rope_append_paged", 16, q, k, v, q_out, rope, k_cache, v_cache, nullptr, 0, block_table, seq_ids,
                      positions, T, num_seqs, d, block_size, max_blocks_per_seq, num_blocks, stream);
 }
 
@@ -1317,7 +1386,7 @@ attn_status_t rope_append_paged_kv4(const attn_heads_t* q, const attn_heads_t* k
                                     int max_blocks_per_seq, int num_blocks, void* stream) {
   const attn_status_t st = check_group(group);
   if (st != ATTN_OK) return st;
-  return rope_append("rope_append_paged_kv4", q, k, v, q_out, rope, nullptr, nullptr, kv_cache, group, block_table,
+  return rope_append("rope_append_paged_kv4", 4, q, k, v, q_out, rope, nullptr, nullptr, kv_cache, group, block_table,
                      seq_ids, positions, T, num_seqs, d, block_size, max_blocks_per_seq, num_blocks, stream);
 }
 
@@ -1325,58 +1394,28 @@ attn_status_t kv4_read_paged(const void* kv_cache, int group, const int32_t* blo
                              const int32_t* seq_ids, const int32_t* positions, void* k, void* v, int T,
                              int num_seqs, int Hkv, int d, int block_size, int max_blocks_per_seq,
                              int num_blocks, void* stream) {
-  attn_status_t st = check_group(group);
+  const attn_status_t st = check_group(group);
   if (st != ATTN_OK) return st;
-  if (T < 0 || num_seqs < 1 || Hkv < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
-    return fail(ATTN_ERR_INVALID_ARG, "sizes must satisfy T >= 0, num_seqs, Hkv, max_blocks_per_seq, num_blocks >= 1");
-  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
-  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
-  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
-    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
-  if (T >= kMaxTokens) return fail(ATTN_ERR_UNSUPPORTED, "T too large");
-  if (T == 0) {
-    g_last_error[0] = '\0';
-    return ATTN_OK;
-  }
-  if (!kv_cache || !block_table || !seq_ids || !positions || !k || !v)
-    return fail(ATTN_ERR_INVALID_ARG, "kv_cache, block_table, seq_ids, positions, k and v must be non-null");
-  if (!aligned16(kv_cache) || !aligned16(k) || !aligned16(v))
-    return fail(ATTN_ERR_INVALID_ARG, "kv_cache, k and v must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_ids) & 3u) ||
-      (reinterpret_cast<uintptr_t>(positions) & 3u))
-    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_ids and positions must be 4-byte aligned");
-  const size_t cache = static_cast<size_t>(num_blocks) * Hkv * attn47::kv4_record_bytes_of(d, group);
-  const size_t out = static_cast<size_t>(T) * Hkv * d * 2;
-  if (overlap(k, out, v, out) || overlap(k, out, kv_cache, cache) || overlap(v, out, kv_cache, cache))
-    return fail(ATTN_ERR_INVALID_ARG, "k, v and kv_cache must not overlap");
-  const size_t ints = static_cast<size_t>(T) * 4, table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4;
-  for (const void* x : {k, v})
-    if (overlap(x, out, block_table, table) || overlap(x, out, seq_ids, ints) || overlap(x, out, positions, ints))
-      return fail(ATTN_ERR_INVALID_ARG, "k and v must not overlap block_table, seq_ids or positions");
-  DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != ATTN_OK) return st;
-  if ((st = check_bufs(*dev, {{kv_cache, cache, "kv_cache"}, {block_table, table, "block_table"},
-                              {seq_ids, ints, "seq_ids"}, {positions, ints, "positions"}, {k, out, "k"},
-                              {v, out, "v"}})) != ATTN_OK)
-    return st;
-  attn47::Kv4ReadLaunch a;
-  a.kv_cache = kv_cache;
-  a.block_table = block_table;
-  a.seq_ids = seq_ids;
-  a.positions = positions;
-  a.k = k;
-  a.v = v;
-  a.T = T;
-  a.Hkv = Hkv;
-  a.d = d;
-  a.group = group;
-  a.num_seqs = num_seqs;
-  a.max_blocks = max_blocks_per_seq;
-  a.num_blocks = num_blocks;
-  a.sms = dev->sms;
-  a.status = dev->status;
-  a.stream = static_cast<cudaStream_t>(stream);
-  return launch_result(attn47::launch_kv4_read_sm103(a), "kv4_read_paged");
+  return read_paged("kv4_read_paged", 4, kv_cache, group, block_table, seq_ids, positions, k, v, T, num_seqs, Hkv, d,
+                    block_size, max_blocks_per_seq, num_blocks, stream);
+}
+
+size_t kv8_record_bytes(int d) { return d == 64 || d == 128 ? attn47::kv8_record_bytes_of(d) : 0; }
+
+attn_status_t rope_append_paged_kv8(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                                    const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
+                                    const int32_t* block_table, const int32_t* seq_ids, const int32_t* positions,
+                                    int T, int num_seqs, int d, int block_size, int max_blocks_per_seq,
+                                    int num_blocks, void* stream) {
+  return rope_append("rope_append_paged_kv8", 8, q, k, v, q_out, rope, nullptr, nullptr, kv_cache, 0, block_table,
+                     seq_ids, positions, T, num_seqs, d, block_size, max_blocks_per_seq, num_blocks, stream);
+}
+
+attn_status_t kv8_read_paged(const void* kv_cache, const int32_t* block_table, const int32_t* seq_ids,
+                             const int32_t* positions, void* k, void* v, int T, int num_seqs, int Hkv, int d,
+                             int block_size, int max_blocks_per_seq, int num_blocks, void* stream) {
+  return read_paged("kv8_read_paged", 8, kv_cache, 0, block_table, seq_ids, positions, k, v, T, num_seqs, Hkv, d,
+                    block_size, max_blocks_per_seq, num_blocks, stream);
 }
 
 size_t attn_decode_paged_kv4_workspace_size(int num_seqs, int Hq, int Hkv, int d) {

@@ -1,4 +1,4 @@
-// The usual case of the rotary, append and 4-bit-cache calls, marshalled in
+// The usual case of the rotary, append and 8- and 4-bit-cache calls, marshalled in
 // C++: a decode step's kernels take 3 to 8 us each, and checking and passing
 // their tensors from Python took 15 to 20.
 //
@@ -41,6 +41,9 @@ decltype(&kv4_record_bytes) g_record_bytes = nullptr;
 decltype(&kv4_read_paged) g_read = nullptr;
 decltype(&attn_decode_paged_kv4_workspace_size) g_workspace_size = nullptr;
 decltype(&attn_decode_paged_kv4) g_decode = nullptr;
+decltype(&rope_append_paged_kv8) g_append_kv8 = nullptr;
+decltype(&kv8_record_bytes) g_record_bytes_kv8 = nullptr;
+decltype(&kv8_read_paged) g_read_kv8 = nullptr;
 
 constexpr int kBlock = 16;   // cached tokens of a block
 
@@ -222,8 +225,13 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return pair(qo, k ? &ko : nullptr);
 }
 
+// Bytes of a record of a cache of 8 or 4 bits (0: there is none of these).
+size_t record_bytes(bool kv8, int d, int group) { return kv8 ? g_record_bytes_kv8(d) : g_record_bytes(d, group); }
+
 // append(q, k, v, k_cache, v_cache, block_table, seq_ids, positions, group, inv_freq, rope_positions, pair_axis,
-// interleaved, q_out); a 4-bit cache comes as k_cache with v_cache None.  Returns (q_out or None,).
+// interleaved, q_out); a 4-bit cache comes as k_cache with v_cache None, and so does an 8-bit one (append8; its
+// group says nothing).  Returns (q_out or None,).
+template <bool KV8>
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int group = 0;
   if (n != 14 || !g_append || !integer(a[8], &group)) Py_RETURN_NONE;
@@ -239,12 +247,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!table || !ids || !pos || ids->size(0) != T || pos->size(0) != T || !small(T) || !small(Hkv) || !small(d) ||
       !small(table->size(0)) || !small(table->size(1)) || !current(dev))
     Py_RETURN_NONE;
-  const bool kv4 = a[4] == Py_None;
+  const bool codes = KV8 || a[4] == Py_None;
   const at::Tensor *kc, *vc = nullptr;
   int block = kBlock;
-  if (kv4) {
+  if (codes) {
     kc = packed(a[3], at::kByte, dev, 3);
-    const size_t rec = kc ? g_record_bytes(static_cast<int>(d), group) : 0;
+    const size_t rec = kc ? record_bytes(KV8, static_cast<int>(d), group) : 0;
     if (!kc || rec == 0 || kc->size(1) != Hkv || kc->size(2) != static_cast<int64_t>(rec)) Py_RETURN_NONE;
   } else {
     kc = packed(a[3], at::kBFloat16, dev, 4);
@@ -282,7 +290,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       heads(qo, &ho);
     }
     t_called = true;
-    st = kv4 ? g_append_kv4(pq, &hk, &hv, po, pr, data<void>(kc), group, data<int32_t>(table), data<int32_t>(ids),
+    st = KV8 ? g_append_kv8(pq, &hk, &hv, po, pr, data<void>(kc), data<int32_t>(table), data<int32_t>(ids),
+                            data<int32_t>(pos), t, S, dd, block, mb, nb, stream_of(dev))
+         : codes
+             ? g_append_kv4(pq, &hk, &hv, po, pr, data<void>(kc), group, data<int32_t>(table), data<int32_t>(ids),
                             data<int32_t>(pos), t, S, dd, block, mb, nb, stream_of(dev))
              : g_append(pq, &hk, &hv, po, pr, data<void>(kc), data<void>(vc), data<int32_t>(table),
                         data<int32_t>(ids), data<int32_t>(pos), t, S, dd, block, mb, nb, stream_of(dev));
@@ -293,14 +304,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return out;
 }
 
-// read(kv_cache, block_table, seq_ids, positions, d, group, k, v)
+// read(kv_cache, block_table, seq_ids, positions, d, group, k, v); read8 of an 8-bit cache (the group says nothing)
+template <bool KV8>
 PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int d = 0, group = 0;
   if (n != 8 || !g_read || !integer(a[4], &d) || !integer(a[5], &group)) Py_RETURN_NONE;
   const at::Tensor* kv = packed(a[0], at::kByte, -1, 3);
   if (!kv) Py_RETURN_NONE;
   const int dev = static_cast<int>(kv->get_device());
-  const size_t rec = g_record_bytes(d, group);
+  const size_t rec = record_bytes(KV8, d, group);
   const at::Tensor* table = packed(a[1], at::kInt, dev, 2);
   const at::Tensor* ids = packed(a[2], at::kInt, dev, 1);
   const at::Tensor* pos = packed(a[3], at::kInt, dev, 1);
@@ -320,10 +332,16 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     k = k_given ? *k_given : make(sizes, at::kBFloat16, *kv);
     v = v_given ? *v_given : make(sizes, at::kBFloat16, *kv);
     t_called = true;
-    st = g_read(data<void>(kv), group, data<int32_t>(table), data<int32_t>(ids), data<int32_t>(pos), data<void>(k),
-                data<void>(v), static_cast<int>(sizes[0]), static_cast<int>(table->size(0)),
-                static_cast<int>(sizes[1]), d, kBlock, static_cast<int>(table->size(1)), static_cast<int>(kv->size(0)),
-                stream_of(dev));
+    if (KV8)
+      st = g_read_kv8(data<void>(kv), data<int32_t>(table), data<int32_t>(ids), data<int32_t>(pos), data<void>(k),
+                      data<void>(v), static_cast<int>(sizes[0]), static_cast<int>(table->size(0)),
+                      static_cast<int>(sizes[1]), d, kBlock, static_cast<int>(table->size(1)),
+                      static_cast<int>(kv->size(0)), stream_of(dev));
+    else
+      st = g_read(data<void>(kv), group, data<int32_t>(table), data<int32_t>(ids), data<int32_t>(pos), data<void>(k),
+                  data<void>(v), static_cast<int>(sizes[0]), static_cast<int>(table->size(0)),
+                  static_cast<int>(sizes[1]), d, kBlock, static_cast<int>(table->size(1)), static_cast<int>(kv->size(0)),
+                  stream_of(dev));
   }
   if (st != ATTN_OK) return not_done(st);
   return pair(k, &v);
@@ -403,12 +421,13 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 8 addresses");
+  constexpr int kAddresses = 11;
+  if (n != kAddresses) {
+    PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kAddresses);
     return nullptr;
   }
-  void* p[8];
-  for (int i = 0; i < 8; ++i) {
+  void* p[kAddresses];
+  for (int i = 0; i < kAddresses; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -423,14 +442,19 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_read = reinterpret_cast<decltype(g_read)>(p[5]);
   g_workspace_size = reinterpret_cast<decltype(g_workspace_size)>(p[6]);
   g_decode = reinterpret_cast<decltype(g_decode)>(p[7]);
+  g_append_kv8 = reinterpret_cast<decltype(g_append_kv8)>(p[8]);
+  g_record_bytes_kv8 = reinterpret_cast<decltype(g_record_bytes_kv8)>(p[9]);
+  g_read_kv8 = reinterpret_cast<decltype(g_read_kv8)>(p[10]);
   Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                          {"rope", FAST(guarded<rope>), METH_FASTCALL, nullptr},
-                         {"append", FAST(guarded<append>), METH_FASTCALL, nullptr},
-                         {"read", FAST(guarded<read>), METH_FASTCALL, nullptr},
+                         {"append", FAST(guarded<append<false>>), METH_FASTCALL, nullptr},
+                         {"append8", FAST(guarded<append<true>>), METH_FASTCALL, nullptr},
+                         {"read", FAST(guarded<read<false>>), METH_FASTCALL, nullptr},
+                         {"read8", FAST(guarded<read<true>>), METH_FASTCALL, nullptr},
                          {"decode", FAST(guarded<decode>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn47_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -35,9 +35,11 @@
 // and a fourth CTA a SM with its 64 registers gains 0.7 us here and loses 0.25 of
 // 5.6 in a decode step.  Equal shares of steps instead of whole tokens change
 // nothing (21.5, 10.2, 14.5 and 47.3 us).
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"
+#include "kv8.cuh"
 #include "ptx.cuh"
 #include "rope_sm103.h"
 
@@ -47,10 +49,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlots = kKv4Slots;
-enum Mode { kRotate, kAppend, kAppendKv4 };
+enum Mode { kRotate, kAppend, kAppendKv4, kAppendKv8 };
 // Resident CTAs per SM (the register budget follows), and so the size of the
 // persistent grids: one CTA more than fits would be a second wave.
-constexpr int ctas_per_sm(int mode) { return mode == kAppendKv4 ? 3 : 4; }
+constexpr int ctas_per_sm(int mode) { return mode == kAppendKv4 || mode == kAppendKv8 ? 3 : 4; }
 constexpr int kReadCtas = 6;
 
 // Rows by strides: those within a batch in units of 8 elements and 32 bits,
@@ -91,6 +93,8 @@ struct RopeParams {
   const int* positions;
   int num_seqs, max_blocks, num_blocks;
   unsigned int* status;
+  // append to an 8-bit cache: its units of work (see append_kv8_units)
+  int T, kv_units, kv_window, kv_parts, kv_heads_per_part;
 };
 
 // f / (2 pi) mod 1 as a 64-bit fraction (0 for non-finite f, with `bad` set).
@@ -163,6 +167,9 @@ __device__ __forceinline__ void unpack8(const uint4& x, float (&y)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
   return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                     pack_bf16x2(y[6], y[7]));
+}
+__device__ __forceinline__ float2 f16x2_numbers(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 // NaN-propagating extremes, of two and (sm_100+) of three.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -332,6 +339,25 @@ struct PairLanes {
     x0 = pack8(a);
     x1 = pack8(b);
   }
+  // The same of numbers, products and sums rounded one by one, as the formula
+  // reads: codes then agree with those of the fp32 formula.  `angles` are those
+  // of the lane's pairs.
+  __device__ __forceinline__ void turn_rounded(const float2* angles, float (&a)[8], float (&b)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(angles + i);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = i + j;
+        const float c = j ? v.z : v.x, s = j ? v.w : v.y;
+        float& x = IL ? (n < 4 ? a[(2 * n) % 8] : b[(2 * n) % 8]) : a[n];
+        float& y = IL ? (n < 4 ? a[(2 * n) % 8 + 1] : b[(2 * n) % 8 + 1]) : b[n];
+        const float first = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+        y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+        x = first;
+      }
+    }
+  }
 };
 
 // Elements 8 piece .. 8 piece + 7 of a row, turned; `other` holds those that
@@ -365,8 +391,266 @@ __device__ __forceinline__ void turn_piece(const uint4& x, const uint4& other, c
   }
 }
 
+// Four codes times a power of two below 1.
+__device__ __forceinline__ uint32_t kv8_rescale(uint32_t codes, float by) {
+  const float2 lo = f16x2_numbers(e4m3x2_to_f16x2(codes)), hi = f16x2_numbers(e4m3x2_hi_to_f16x2(codes));
+  return to_e4m3x4(lo.x * by, lo.y * by, hi.x * by, hi.y * by);
+}
+
+// Runs that share a block's scale, and what a pass over them needs.
+struct Kv8Append {
+  alignas(16) float2 angles[kSlots][64];   // cosines and sines of a row's pairs
+  int token[kSlots], slot[kSlots], run[kSlots];          // of a row of the pass
+  int phys[kSlots], slot0[kSlots], length[kSlots];       // of a run
+  uint32_t most[2][4][kSlots];             // largest value of a run (bits): [key, value][head of the chunk][run]
+  uint32_t bad[4][kSlots];                 // its rows with elements that are no numbers, as in the record's flags
+  uint32_t scale[2][4][kSlots];
+  float turn[2][4][kSlots];                // what becomes of the block's other codes: 1 as they are, 0 zeros
+};
+
+// New keys and values into an 8-bit cache.  All tokens of a block share a scale
+// per head, so the unit of work is a run: consecutive rows of the batch whose
+// tokens are neighbours in one block (up to 16).  A CTA takes the runs that
+// begin in a window of rows, as many whole runs at a time as make 16 rows, and
+// the heads of its part in chunks: rows to registers, keys turned, the largest
+// value of each run and head to shared memory; then the scales; then the codes.
+// A block that a run enters at its first slot starts anew: its scale is what the
+// run needs, slots not yet written are zeros.  In any other the scale can only
+// grow, and where it does the codes that are there are brought to it.
+template <int D, bool IL>
+__device__ __forceinline__ void append_kv8_units(const RopeParams& p, const RopeShared& sh) {
+  using Lt = Kv8Layout<D>;
+  constexpr int kSlotLanes = D / 16, kRows = 32 / kSlotLanes;
+  constexpr int kSteps = 2, kItems = kWarps * kRows;       // rows of a step
+  constexpr int kChunk = kSteps * kItems / (2 * kSlots);   // heads at a time
+  static_assert(kChunk <= 4, "room in Kv8Append");
+  __shared__ Kv8Append s8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = lane % kSlotLanes, sub = lane / kSlotLanes;
+  const PairLanes<IL> pl(p.rot, slot);
+  for (int i = tid; i < 2 * 4 * kSlots; i += kThreads) (&s8.most[0][0][0])[i] = 0;
+  for (int i = tid; i < 4 * kSlots; i += kThreads) (&s8.bad[0][0])[i] = 0;
+
+  for (int unit = blockIdx.x; unit < p.kv_units; unit += gridDim.x) {
+    const int window = unit / p.kv_parts, part = unit - window * p.kv_parts;
+    const int head0 = part * p.kv_heads_per_part, head1 = min(p.Hk, head0 + p.kv_heads_per_part);
+    // Every warp finds the window's runs: lane i looks at row w0 + i.
+    const int t = window * p.kv_window + lane;
+    int seq = -1, pos = 0;
+    if (t < p.T) {
+      seq = p.seq_ids[t];
+      pos = p.positions[t];
+    }
+    int seq_before = __shfl_up_sync(0xffffffffu, seq, 1), pos_before = __shfl_up_sync(0xffffffffu, pos, 1);
+    if (lane == 0) {
+      seq_before = -1;
+      if (t > 0) {
+        seq_before = p.seq_ids[t - 1];
+        pos_before = p.positions[t - 1];
+      }
+    }
+    const bool valid = seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < p.max_blocks * kSlots;
+    const bool more = valid && pos % kSlots != 0 && seq_before == seq && pos_before == pos - 1;
+    const bool first = valid && !more && lane < p.kv_window;
+    int phys = -1;
+    if (first) {
+      phys = p.block_table[static_cast<size_t>(seq) * p.max_blocks + pos / kSlots];
+      if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
+        phys = -1;
+        atomicOr(p.status, kDevBadBlock);
+      }
+    }
+    if (!valid && seq >= 0 && lane < p.kv_window) atomicOr(p.status, seq >= p.num_seqs ? kDevBadSeqId : kDevBadSeqLen);
+    const unsigned mores = __ballot_sync(0xffffffffu, more);
+    unsigned todo = __ballot_sync(0xffffffffu, phys >= 0);
+    while (todo != 0) {
+      // The next runs that make up to 16 rows.
+      int rows = 0, runs = 0, my_row = -1, my_run = 0;
+      while (todo != 0) {
+        const int at = __ffs(todo) - 1;          // < 16
+        const int n = __ffs(~(mores >> (at + 1)));
+        if (rows + n > kSlots) break;
+        if (lane >= at && lane < at + n) {
+          my_row = rows + lane - at;
+          my_run = runs;
+        }
+        if (warp == 0 && lane == at) {
+          s8.phys[runs] = phys;
+          s8.slot0[runs] = pos % kSlots;
+          s8.length[runs] = n;
+        }
+        rows += n;
+        ++runs;
+        todo &= todo - 1;
+      }
+      if (warp == 0 && my_row >= 0) {
+        s8.token[my_row] = t;
+        s8.slot[my_row] = pos % kSlots;
+        s8.run[my_row] = my_run;
+      }
+      __syncthreads();
+      const int pairs = p.rot / 2;
+      for (int i = tid; i < rows * pairs; i += kThreads) {
+        const int r = i / pairs, pair = i - r * pairs;
+        const uint32_t ax = sh.axis[pair];
+        const int tok = s8.token[r];
+        const int at = p.rope_pos != nullptr ? p.rope_pos[(ax & 3u) * p.axis_stride + tok] : p.positions[tok];
+        float s, c;
+        turn_sincos(at, sh.frac[pair], s, c);
+        if (ax & 4u) s = c = __uint_as_float(0x7fc00000u);
+        s8.angles[r][pair] = make_float2(c, s);
+      }
+      __syncthreads();
+
+      for (int h0 = head0; h0 < head1; h0 += kChunk) {
+        const int heads = min(kChunk, head1 - h0);
+        const int items = 2 * heads * rows;      // keys, then values; rows fastest
+        // What the blocks hold already (one thread for each run and head).
+        const int my = tid / heads, my_head = tid - my * heads;
+        const bool keeper = my < runs;
+        uint4 tail = make_uint4(0u, 0u, 0u, 0u);
+        uint8_t* tail_at = nullptr;
+        if (keeper) {
+          tail_at = p.kv_cache + (static_cast<size_t>(s8.phys[my]) * p.Hk + h0 + my_head) * Lt::kBytes + Lt::kOffTail;
+          if (s8.slot0[my] != 0) tail = *reinterpret_cast<const uint4*>(tail_at);
+        }
+        uint4 x0[kSteps], x1[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int it = u * kItems + warp * kRows + sub;
+          x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (it >= items) continue;
+          const int kh = it / rows, r = it - kh * rows;
+          const bool value = kh >= heads;
+          const int tok = s8.token[r];
+          const __nv_bfloat16* src = value ? RowPtr::row(p.v.of(0, tok), h0 + kh - heads, p.v.head)
+                                           : RowPtr::row(p.k.of(0, tok), h0 + kh, p.k.head);
+          x0[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot : pl.e0));
+          x1[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot + 8 : pl.e1));
+        }
+        // (Turned again for the codes: kept, the numbers would take 32 registers
+        // and the third CTA of an SM.)
+        auto numbers = [&](int u, bool key, int r, float (&a)[8], float (&b)[8]) {
+          unpack8(x0[u], a);
+          unpack8(x1[u], b);
+          if (key && pl.turns) pl.turn_rounded(s8.angles[r] + 8 * slot, a, b);
+        };
+        bool odd[kSteps];                        // some element of the lane's is no finite number
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int it = u * kItems + warp * kRows + sub;
+          const bool live = it < items;
+          const int kh = live ? it / rows : 0, r = live ? it - kh * rows : 0;
+          const bool value = kh >= heads;
+          float a[8], b[8];
+          numbers(u, !value, r, a, b);
+          uint32_t most = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            most = max(most, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
+          odd[u] = most >= 0x7f800000u;
+          const int h = value ? kh - heads : kh;
+          if (odd[u]) {
+            most = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t va = __float_as_uint(a[e]) & 0x7fffffffu, vb = __float_as_uint(b[e]) & 0x7fffffffu;
+              most = max(most, max(va < 0x7f800000u ? va : 0u, vb < 0x7f800000u ? vb : 0u));
+            }
+            atomicOr(&s8.bad[h][s8.run[r]], 1u << (s8.slot[r] + (value ? 16 : 0)));
+          }
+#pragma unroll
+          for (int o = 1; o < kSlotLanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+          if (live && slot == 0) atomicMax(&s8.most[value ? 1 : 0][h][s8.run[r]], most);
+        }
+        __syncthreads();
+        if (keeper) {
+          const bool fresh = s8.slot0[my] == 0;
+          const uint32_t had[2] = {tail.x, tail.y};
+          uint32_t now[2], kept = 0;             // flags of slots that keep their codes
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            now[i] = kv8_scale_for(s8.most[i][my_head][my]);
+            s8.most[i][my_head][my] = 0;
+            float turn = s8.length[my] < kSlots ? 0.f : 1.f;
+            if (!fresh) {
+              // (Anything but a scale: a block that no append has begun.)
+              const float was = __uint_as_float(had[i]);
+              const bool scale = was >= 0x1p-64f && was <= 0x1p64f;
+              turn = scale ? 1.f : 0.f;
+              if (scale) kept |= 0xffffu << (16 * i);
+              if (scale && had[i] > now[i]) now[i] = had[i];
+              if (scale && had[i] < now[i]) turn = was * kv8_inverse(now[i]);
+            }
+            s8.scale[i][my_head][my] = now[i];
+            s8.turn[i][my_head][my] = turn;
+          }
+          const uint32_t slots = ((1u << s8.length[my]) - 1u) << s8.slot0[my];
+          const uint32_t flags = (tail.z & kept & ~(slots * 0x10001u)) | s8.bad[my_head][my];
+          s8.bad[my_head][my] = 0;
+          *reinterpret_cast<uint4*>(tail_at) = make_uint4(now[0], now[1], flags, 0u);
+          if (fresh) *reinterpret_cast<uint4*>(tail_at + 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int it = u * kItems + warp * kRows + sub;
+          if (it >= items) continue;
+          const int kh = it / rows, r = it - kh * rows;
+          const bool value = kh >= heads;
+          const int h = value ? kh - heads : kh, run = s8.run[r];
+          float a[8], b[8];
+          numbers(u, !value, r, a, b);
+          if (odd[u]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (!(fabsf(a[e]) <= 3.402823466e38f)) a[e] = __uint_as_float(0x7fc00000u);
+              if (!(fabsf(b[e]) <= 3.402823466e38f)) b[e] = __uint_as_float(0x7fc00000u);
+            }
+          }
+          const float inv = kv8_inverse(s8.scale[value ? 1 : 0][h][run]);
+          uint8_t* row = p.kv_cache + (static_cast<size_t>(s8.phys[run]) * p.Hk + h0 + h) * Lt::kBytes +
+                         (value ? Lt::kOffV : 0) + s8.slot[r] * Lt::kRow;
+          *reinterpret_cast<uint2*>(row + (value ? 16 * slot : pl.e0)) =
+              make_uint2(to_e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv),
+                         to_e4m3x4(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv));
+          *reinterpret_cast<uint2*>(row + (value ? 16 * slot + 8 : pl.e1)) =
+              make_uint2(to_e4m3x4(b[0] * inv, b[1] * inv, b[2] * inv, b[3] * inv),
+                         to_e4m3x4(b[4] * inv, b[5] * inv, b[6] * inv, b[7] * inv));
+        }
+        // The blocks' other slots, where they do not stay as they are.
+        for (int x = warp; x < 2 * heads * runs; x += kWarps) {
+          const int kh = x / runs, run = x - kh * runs;
+          const bool value = kh >= heads;
+          const int h = value ? kh - heads : kh;
+          const float turn = s8.turn[value ? 1 : 0][h][run];
+          if (turn == 1.f) continue;
+          uint8_t* codes = p.kv_cache + (static_cast<size_t>(s8.phys[run]) * p.Hk + h0 + h) * Lt::kBytes +
+                           (value ? Lt::kOffV : 0);
+          const int from = s8.slot0[run], to = from + s8.length[run];
+          for (int piece = lane; piece < kSlots * kSlotLanes; piece += 32) {
+            const int at = piece / kSlotLanes;
+            if (at >= from && at < to) continue;
+            uint4* dst = reinterpret_cast<uint4*>(codes) + piece;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (turn != 0.f) {
+              w = *dst;
+              w.x = kv8_rescale(w.x, turn);
+              w.y = kv8_rescale(w.y, turn);
+              w.z = kv8_rescale(w.z, turn);
+              w.w = kv8_rescale(w.w, turn);
+            }
+            *dst = w;
+          }
+        }
+      }
+      __syncthreads();                           // the next runs take this pass's place
+    }
+  }
+}
+
 // Tasks are (token, slice of its rows), one warp each.  Rows of a token:
-// queries, keys, values.
+// queries, keys, values (for an 8-bit cache the queries alone).
 template <int D, int MODE, int G, bool IL>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kSlotLanes = D / 16;             // lanes of a row held in pairs
@@ -386,6 +670,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
 
   const int tasks = static_cast<int>(p.tasks), stride = gridDim.x * kWarps;
   int task = blockIdx.x * kWarps + warp;
+  if constexpr (MODE == kAppendKv8) {
+    append_kv8_units<D, IL>(p, sh);
+    // The CTAs that had one unit less begin with the queries.
+    const int late = static_cast<int>(blockIdx.x) - p.kv_units % static_cast<int>(gridDim.x);
+    task = (late < 0 ? late + static_cast<int>(gridDim.x) : late) * kWarps + warp;
+  }
   // Where the next task's token goes is read while this one's rows come.
   int next_seq = 0, next_pos = 0, next_phys = 0;
   auto token = [&](int task_) {
@@ -652,6 +942,104 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) kv4_read_kernel(const Kv4
   }
 }
 
+// Rows of cached tokens of an 8-bit cache back to bf16: value = code * scale,
+// exactly.  Rows of a token: its keys, then its values.
+struct Kv8ReadParams {
+  const uint8_t* kv_cache;
+  const int* block_table;
+  const int* seq_ids;
+  const int* positions;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int Hkv, num_seqs, max_blocks, num_blocks;
+  int parts, rows_per_part;
+  long long tasks;
+  unsigned int* status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kReadCtas) kv8_read_kernel(const Kv8ReadParams p) {
+  using Lt = Kv8Layout<D>;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kFlight = 2;
+  const int lane = threadIdx.x & 31;
+  const int j = lane % kLanes, sub = lane / kLanes;
+  const int rows = 2 * p.Hkv;
+
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  const int tasks = static_cast<int>(p.tasks), stride = gridDim.x * kWarps;
+  int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (task >= tasks) return;
+  // The next task's token and table entry are read while this one's rows come.
+  auto token = [&](int task_, int& seq_, int& pos_) {
+    const int t_ = p.parts == 1 ? task_ : task_ / p.parts;
+    seq_ = p.seq_ids[t_];
+    pos_ = p.positions[t_];
+  };
+  auto entry = [&](int seq_, int pos_) {
+    return seq_ >= 0 && seq_ < p.num_seqs && pos_ >= 0 && pos_ < p.max_blocks * kSlots
+               ? p.block_table[static_cast<size_t>(seq_) * p.max_blocks + pos_ / kSlots] : 0;
+  };
+  int seq, pos, phys;
+  token(task, seq, pos);
+  phys = entry(seq, pos);
+  for (int next; task < tasks; task = next) {
+    next = task + stride;
+    const int t = p.parts == 1 ? task : task / p.parts;
+    const int row0 = (task - t * p.parts) * p.rows_per_part;
+    const int row1 = min(rows, row0 + p.rows_per_part);
+    const int my_seq = seq, my_pos = pos, my_phys = phys;
+    if (next < tasks) token(next, seq, pos);
+    unsigned err = 0;
+    if (my_seq >= p.num_seqs) err = kDevBadSeqId;
+    else if (my_pos < 0 || my_pos >= p.max_blocks * kSlots) err = kDevBadSeqLen;
+    else if (static_cast<unsigned>(my_phys) >= static_cast<unsigned>(p.num_blocks)) err = kDevBadBlock;
+    if (my_seq < 0 || err) {
+      if (my_seq >= 0 && lane == 0) atomicOr(p.status, err);
+      if (next < tasks) phys = entry(seq, pos);
+      continue;
+    }
+    const int slot = my_pos % kSlots;
+    const uint8_t* recs = p.kv_cache + static_cast<size_t>(my_phys) * p.Hkv * Lt::kBytes;
+    for (int base = row0; base < row1; base += kFlight * kRows) {
+      uint4 w[kFlight];
+      float scale[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int r = base + u * kRows + sub;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        scale[u] = 0.f;
+        if (r < row1) {
+          const bool value = r >= p.Hkv;
+          const uint8_t* rec = recs + static_cast<size_t>(value ? r - p.Hkv : r) * Lt::kBytes;
+          w[u] = *reinterpret_cast<const uint4*>(rec + (value ? Lt::kOffV : 0) + slot * Lt::kRow + 16 * j);
+          scale[u] = reinterpret_cast<const float*>(rec + Lt::kOffTail)[value ? 1 : 0];
+        }
+      }
+      if (base == row0 && next < tasks) phys = entry(seq, pos);
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int r = base + u * kRows + sub;
+        if (r >= row1) continue;
+        const bool value = r >= p.Hkv;
+        const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        uint32_t out[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 lo = f16x2_numbers(e4m3x2_to_f16x2(in[i])), hi = f16x2_numbers(e4m3x2_hi_to_f16x2(in[i]));
+          out[2 * i] = pack_bf16x2(lo.x * scale[u], lo.y * scale[u]);
+          out[2 * i + 1] = pack_bf16x2(hi.x * scale[u], hi.y * scale[u]);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(
+            (value ? p.v : p.k) + (static_cast<size_t>(t) * p.Hkv + (value ? r - p.Hkv : r)) * D + 16 * j);
+        dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+      }
+    }
+  }
+}
+
 // Slices of a token's `rows` rows such that `tokens` of them fill the GPU:
 // one warp per token once there are enough tokens, else as many slices as
 // that takes, down to one warp step each.
@@ -699,6 +1087,37 @@ cudaError_t launch_t(RopeParams& p, long long tokens, bool interleaved, int sms,
   p.tasks = tokens * s.parts;
   auto kern = interleaved ? rope_kernel<D, MODE, G, true> : rope_kernel<D, MODE, G, false>;
   return launch_pdl(kern, dim3(s.grid), dim3(kThreads), 0, stream, p);
+}
+
+// An append to an 8-bit cache: units of keys and values beside the tasks of
+// queries.  Windows of 16 rows, or of fewer where that would leave SMs without
+// work, and then parts of the heads.
+template <int D>
+cudaError_t launch_kv8_t(RopeParams& p, bool interleaved, int sms, cudaStream_t stream) {
+  constexpr int kChunk = D == 128 ? 2 : 4;
+  const int want = 2 * sms;
+  int window = kSlots;
+  while (window > 1 && (p.T - 1) / window + 1 < want) window /= 2;
+  const int windows = (p.T - 1) / window + 1, chunks = (p.Hk + kChunk - 1) / kChunk;
+  const int parts = min(chunks, (want + windows - 1) / windows);
+  p.kv_window = window;
+  p.kv_heads_per_part = (chunks + parts - 1) / parts * kChunk;
+  p.kv_parts = (p.Hk + p.kv_heads_per_part - 1) / p.kv_heads_per_part;
+  const long long units = static_cast<long long>(windows) * p.kv_parts;
+  if (units > 0x3fffffff) return cudaErrorInvalidValue;
+  p.kv_units = static_cast<int>(units);
+  Split s = {1, 1, 0};
+  p.parts = p.rows_per_part = 1;
+  p.tasks = 0;
+  if (p.Hq > 0) {
+    s = split_rows(p.T, p.Hq, 32 / (D / 16), sms, ctas_per_sm(kAppendKv8));
+    p.parts = s.parts;
+    p.rows_per_part = s.rows_per_part;
+    p.tasks = static_cast<long long>(p.T) * s.parts;
+  }
+  const long long cap = static_cast<long long>(sms) * ctas_per_sm(kAppendKv8), ctas = units + s.grid;
+  auto kern = interleaved ? rope_kernel<D, kAppendKv8, 0, true> : rope_kernel<D, kAppendKv8, 0, false>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(kThreads), 0, stream, p);
 }
 
 template <int D, int G>
@@ -750,6 +1169,12 @@ cudaError_t launch_rope_append_sm103(const RopeAppendLaunch& a) {
   p.num_blocks = a.num_blocks;
   p.status = a.status;
   const bool il = a.spec.interleaved;
+  if (a.kv_cache != nullptr && a.group == 0) {
+    p.T = a.T;
+    p.rows = p.Hq;
+    if (a.d == 128) return launch_kv8_t<128>(p, il, a.sms, a.stream);
+    return launch_kv8_t<64>(p, il, a.sms, a.stream);
+  }
   if (a.kv_cache == nullptr) {
     if (a.d == 128) return launch_t<128, kAppend, 0>(p, a.T, il, a.sms, a.stream);
     return launch_t<64, kAppend, 0>(p, a.T, il, a.sms, a.stream);
@@ -759,6 +1184,26 @@ cudaError_t launch_rope_append_sm103(const RopeAppendLaunch& a) {
                          : launch_t<128, kAppendKv4, 64>(p, a.T, il, a.sms, a.stream);
   return a.group == 32 ? launch_t<64, kAppendKv4, 32>(p, a.T, il, a.sms, a.stream)
                        : launch_t<64, kAppendKv4, 64>(p, a.T, il, a.sms, a.stream);
+}
+
+cudaError_t launch_kv8_read_sm103(const Kv8ReadLaunch& a) {
+  Kv8ReadParams p;
+  p.kv_cache = static_cast<const uint8_t*>(a.kv_cache);
+  p.block_table = a.block_table;
+  p.seq_ids = a.seq_ids;
+  p.positions = a.positions;
+  p.k = static_cast<__nv_bfloat16*>(a.k);
+  p.v = static_cast<__nv_bfloat16*>(a.v);
+  p.Hkv = a.Hkv;
+  p.num_seqs = a.num_seqs;
+  p.max_blocks = a.max_blocks;
+  p.num_blocks = a.num_blocks;
+  p.status = a.status;
+  const Split s = split_rows(a.T, 2 * p.Hkv, 32 / (a.d / 16), a.sms, kReadCtas);
+  p.parts = s.parts;
+  p.rows_per_part = s.rows_per_part;
+  p.tasks = static_cast<long long>(a.T) * s.parts;
+  return launch_pdl(a.d == 128 ? kv8_read_kernel<128> : kv8_read_kernel<64>, dim3(s.grid), dim3(kThreads), 0, a.stream, p);
 }
 
 cudaError_t launch_kv4_read_sm103(const Kv4ReadLaunch& a) {

@@ -34,8 +34,8 @@ struct RopeLaunch {
   cudaStream_t stream;
 };
 
-// New tokens appended to a paged cache: bf16 (k_cache, v_cache) or 4-bit
-// records (kv_cache, group).  spec.positions == nullptr: rotate by the cache
+// New tokens appended to a paged cache: bf16 (k_cache, v_cache), 4-bit
+// records (kv_cache, group) or 8-bit records (kv_cache, group 0).  spec.positions == nullptr: rotate by the cache
 // positions.
 struct RopeAppendLaunch {
   RopeSpec spec;
@@ -48,6 +48,19 @@ struct RopeAppendLaunch {
   const int* seq_ids;                // [T]
   const int* positions;              // [T]
   int T, num_seqs, max_blocks, num_blocks, d;
+  int sms;
+  unsigned int* status;
+  cudaStream_t stream;
+};
+
+struct Kv8ReadLaunch {
+  const void* kv_cache;              // [num_blocks, Hkv, record] bytes
+  const int* block_table;
+  const int* seq_ids;
+  const int* positions;
+  void* k;                           // [T, Hkv, d] bf16
+  void* v;
+  int T, Hkv, d, num_seqs, max_blocks, num_blocks;
   int sms;
   unsigned int* status;
   cudaStream_t stream;
@@ -68,6 +81,7 @@ struct Kv4ReadLaunch {
 
 cudaError_t launch_rope_sm103(const RopeLaunch& a);
 cudaError_t launch_rope_append_sm103(const RopeAppendLaunch& a);
+cudaError_t launch_kv8_read_sm103(const Kv8ReadLaunch& a);
 cudaError_t launch_kv4_read_sm103(const Kv4ReadLaunch& a);
 
 }  // namespace attn47

@@ -604,6 +604,67 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
                                     size_t workspace_bytes, void* stream);
 
 /*
+ * kv8_record_bytes — bytes of one (block, KV head) record of an 8-bit cache,
+ * 32 d + 32: K codes [16][d], V codes [16][d], then the scale of the K codes
+ * and of the V codes (fp32), a 32-bit word of flags, and zeros.  0 unless d is
+ * 64 or 128.
+ *
+ * An 8-bit cache is [num_blocks, Hkv, kv8_record_bytes(d)] bytes.  A code is
+ * an e4m3 number (bit 7 the sign, 4 bits of exponent with bias 7, 3 of
+ * fraction, no infinities) and stands for itself times the scale of its block,
+ * head and kind (K or V), a power of two: the smallest under which no finite
+ * value of the block's tokens exceeds 448, from 2^-64 to 2^64 (larger values
+ * become 448 times 2^64).  A value is rounded to the nearest code, half to
+ * even: |x - value| <= 2^-4 |x|, or 2^-10 scale where that is more.  All
+ * values are exact in bf16.
+ *
+ * An element that is NaN or infinite is stored as NaN, without effect on the
+ * scale, and flagged: bit s of the flags for slot s's key, bit 16 + s for its
+ * value.  A query that attends to a flagged token gets NaN (all of that head's
+ * o, and lse).  A cache written by other means needs scales that are powers of
+ * two in that range, and the flags of the NaN codes that it holds.
+ */
+size_t kv8_record_bytes(int d);
+
+/*
+ * rope_append_paged_kv8 — rope_append_paged into an 8-bit cache: the rotated
+ * keys and the values are quantised from fp32 (not through bf16).
+ *
+ * The tokens of a block share its scales, so the rows of a call that fall into
+ * one block stand together, in the order of their positions (rows of other
+ * blocks, sequences or padding do not stand between them); if they do not, what
+ * that block then holds is unspecified.  A row for the first slot of a block
+ * begins it anew: the slots of it that the call does not write become zeros.
+ * In any other block the scales stay, or grow where a new value needs it, and
+ * the codes of the other slots are then rounded to the larger scale (which
+ * changes only those that become subnormal); in a block that was never begun
+ * (its scale is not one) those slots become zeros too.
+ *
+ *  kv_cache   [num_blocks, Hkv, kv8_record_bytes(d)] bytes, 16-byte aligned
+ *             (the records of the blocks reached are read and written)
+ *  The other arguments, rules and device flags are those of rope_append_paged.
+ */
+attn_status_t rope_append_paged_kv8(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+                                    const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
+                                    const int32_t* block_table, const int32_t* seq_ids,
+                                    const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                                    int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
+ * kv8_read_paged — the values that cached tokens of an 8-bit cache stand for:
+ * row t is the token at logical position positions[t] of sequence seq_ids[t].
+ *
+ *  k, v       [T, Hkv, d] bf16, contiguous, 16-byte aligned (written); they
+ *             overlap neither each other nor an input
+ *  The other arguments, rules and device flags are those of
+ *  rope_append_paged_kv8 (rows in any order); rows with seq_ids[t] < 0 are left
+ *  as they were.
+ */
+attn_status_t kv8_read_paged(const void* kv_cache, const int32_t* block_table, const int32_t* seq_ids,
+                             const int32_t* positions, void* k, void* v, int T, int num_seqs, int Hkv, int d,
+                             int block_size, int max_blocks_per_seq, int num_blocks, void* stream);
+
+/*
  * attn_get_device_status — synchronises `stream`, copies the current
  * device's status word (ATTN_DEV_* bits) to *flags_out (host pointer) and
  * clears it.  Returns ATTN_ERR_DEVICE if the device is unusable.

@@ -21,7 +21,8 @@ routine and invariants the mathematics fixes: the forward and decode by
 ``tests/test_oracle_backward_pins.py``, the chunked prefill over a paged
 cache by ``tests/test_oracle_paged_prefill_pins.py``, the fusions by
 ``tests/test_oracle_fusion_pins.py``, the SSD by ``tests/test_oracle_ssd_pins.py``, the rotary positions and the
-4-bit cache (plain definitions, no page describes them) by ``tests/test_oracle_rope_kv4_pins.py``.  No
+4-bit cache (plain definitions, no page describes them) by ``tests/test_oracle_rope_kv4_pins.py``, the 8-bit cache
+(the same) by ``tests/test_oracle_kv8_pins.py``.  No
 function is "parity unpinned".
 """
 
@@ -46,6 +47,16 @@ from .kv4 import (  # noqa: F401
     kv4_store,
     kv4_unpack,
     kv4_values,
+)
+from .kv8 import (  # noqa: F401
+    decode_paged_kv8,
+    kv8_append,
+    kv8_code_values,
+    kv8_codes,
+    kv8_record_bytes,
+    kv8_scale,
+    kv8_unpack,
+    prefill_paged_kv8,
 )
 from .rope import rope_rotate  # noqa: F401
 from .ssd import (  # noqa: F401

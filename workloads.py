@@ -277,3 +277,16 @@ def kv4_cache(num_blocks, Hkv, record_bytes, d, group, seed, scale=0.3, spread=0
     low = (-7.5 * s.float() * (1 + 0.15 * _randn(gen, (num_blocks, Hkv, n)))).to(torch.bfloat16)
     rec[..., 2 * BLOCK_SIZE * (d // 2):] = torch.stack([low, s], -1).reshape(num_blocks, Hkv, 2 * n).view(torch.uint8)
     return rec
+
+
+def kv8_cache(num_blocks, Hkv, record_bytes, d, seed, lo=-8, hi=-5):
+    """An 8-bit cache of random codes like those of normalised activations,
+    scales 2^lo .. 2^hi.  uint8 [num_blocks, Hkv, record_bytes] (CPU)."""
+    gen = torch.Generator().manual_seed(int(seed))
+    rec = torch.zeros((num_blocks, Hkv, record_bytes), dtype=torch.uint8)
+    e = torch.randint(lo, hi + 1, (num_blocks, Hkv, 2, 1), generator=gen)
+    x = _randn(gen, (num_blocks, Hkv, 2, BLOCK_SIZE * d)).float() * torch.exp2(-e.float())
+    n = 2 * BLOCK_SIZE * d
+    rec[..., :n] = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).flatten(2)
+    rec[..., n: n + 8] = torch.exp2(e[..., 0].float()).contiguous().view(torch.uint8)
+    return rec
