@@ -3,7 +3,7 @@
 Each case names one operator (``op``) and its sizes:
 
 ``append``   new tokens' queries rotated, their keys rotated and stored with their values in a paged cache
-             held in 8 bits (``rope_append_paged_kv8``), and what the blocks so touched then hold, read
+             held in 8 bits (``kv8_append_paged``), and what the blocks so touched then hold, read
              back (``kv8_read_paged``)
 ``read``     cached tokens of an 8-bit cache expanded to bf16 (``kv8_read_paged``)
 ``decode``   one query per sequence over an 8-bit cache (``attn_decode_paged_kv8``)
@@ -217,7 +217,7 @@ def run(s):
 def _run_append(s):
     if own:
         import exact_attention_47_gb300 as attn
-        attn.rope_append_paged_kv8(s["q"], s["k"], s["v"], s["kv_cache"], s["table"], s["seq_ids"], s["positions"],
+        attn.kv8_append_paged(s["q"], s["k"], s["v"], s["kv_cache"], s["table"], s["seq_ids"], s["positions"],
                                    inv_freq=s["inv_freq"], rope_positions=s["rope_positions"],
                                    pair_axis=s["pair_axis"], interleaved=s["interleaved"], q_out=s["q_out"])
         k, v = attn.kv8_read_paged(s["kv_cache"], s["table"], s["read_ids"], s["read_pos"], s["d"])
