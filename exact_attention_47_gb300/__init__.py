@@ -31,13 +31,13 @@ from ._binding import (  # noqa: F401
     fused_swiglu,
     kv4_read_paged,
     kv4_record_bytes,
+    kv8_append_paged,
     kv8_read_paged,
     kv8_record_bytes,
     library_path,
     load_library,
     rope_append_paged,
     rope_append_paged_kv4,
-    rope_append_paged_kv8,
     rope_bwd,
     rope_fwd,
     selftest_exp2_poly,

@@ -54,7 +54,7 @@ _SIGS = {
     "kv4_record_bytes": (ctypes.c_size_t, [_I, _I]),
     "rope_append_paged_kv4": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "kv8_record_bytes": (ctypes.c_size_t, [_I]),
-    "rope_append_paged_kv8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "kv8_append_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "kv8_read_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "kv4_read_paged": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "attn_decode_paged_kv4_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
@@ -116,8 +116,9 @@ def load_library(path=None):
 
 # The entry points that the fast calls pass on to, in the order of their `bind`.
 _FAST = ("rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "kv4_record_bytes", "kv4_read_paged",
-         "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4", "rope_append_paged_kv8", "kv8_record_bytes",
-         "kv8_read_paged")
+         "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4")
+# Those of the 8-bit cache, in the order of `bind8`.
+_FAST_KV8 = ("kv8_append_paged", "kv8_record_bytes", "kv8_read_paged")
 
 
 class _NoFastCalls:
@@ -147,6 +148,7 @@ def _fast():
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn47_fast", loader))
     loader.exec_module(module)
     module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST))
+    module.bind8(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST_KV8))
     return module
 
 
@@ -764,7 +766,7 @@ def _need_kv8(kv_cache, d, device):
     return shape[0], shape[1]
 
 
-def rope_append_paged_kv8(q, k, v, kv_cache, block_table, seq_ids, positions, inv_freq=None, rope_positions=None,
+def kv8_append_paged(q, k, v, kv_cache, block_table, seq_ids, positions, inv_freq=None, rope_positions=None,
                           pair_axis=None, interleaved=False, q_out=None, stream=None):
     """rope_append_paged into an 8-bit cache: kv_cache
     [num_blocks,Hkv,kv8_record_bytes(d)] uint8 (updated in place), e4m3 codes
@@ -773,20 +775,20 @@ def rope_append_paged_kv8(q, k, v, kv_cache, block_table, seq_ids, positions, in
     the order of their positions; a row for a block's first slot begins it anew.
     Returns q_out (or None without q)."""
     if stream is not None:
-        return _on_stream(rope_append_paged_kv8, stream, k, q, k, v, kv_cache, block_table, seq_ids, positions,
+        return _on_stream(kv8_append_paged, stream, k, q, k, v, kv_cache, block_table, seq_ids, positions,
                           inv_freq, rope_positions, pair_axis, interleaved, q_out)
     done = _fast().append8(q, k, v, kv_cache, None, block_table, seq_ids, positions, 0, inv_freq, rope_positions,
                            pair_axis, interleaved, q_out)
     if done is not None:
         if done.__class__ is int:
-            _check("rope_append_paged_kv8", done)
+            _check("kv8_append_paged", done)
         return done[0]
     dev, T, d, hq, hk, hv, ho, rope, q_out = _append_args(
         q, k, v, block_table, seq_ids, positions, inv_freq, rope_positions, pair_axis, interleaved, q_out)
     nb, Hkv = _need_kv8(kv_cache, d, dev)
     if Hkv != k.shape[1]:
         raise ValueError("kv_cache must have k's heads")
-    _call("rope_append_paged_kv8", dev, hq, hk, hv, ho, rope[0], _ptr(kv_cache), _ptr(block_table), _ptr(seq_ids),
+    _call("kv8_append_paged", dev, hq, hk, hv, ho, rope[0], _ptr(kv_cache), _ptr(block_table), _ptr(seq_ids),
           _ptr(positions), T, block_table.shape[0], d, BLOCK_SIZE, block_table.shape[1], nb,
           _stream_handle(None, dev))
     return q_out

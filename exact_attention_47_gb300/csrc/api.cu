@@ -1402,12 +1402,12 @@ attn_status_t kv4_read_paged(const void* kv_cache, int group, const int32_t* blo
 
 size_t kv8_record_bytes(int d) { return d == 64 || d == 128 ? attn47::kv8_record_bytes_of(d) : 0; }
 
-attn_status_t rope_append_paged_kv8(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+attn_status_t kv8_append_paged(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
                                     const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
                                     const int32_t* block_table, const int32_t* seq_ids, const int32_t* positions,
                                     int T, int num_seqs, int d, int block_size, int max_blocks_per_seq,
                                     int num_blocks, void* stream) {
-  return rope_append("rope_append_paged_kv8", 8, q, k, v, q_out, rope, nullptr, nullptr, kv_cache, 0, block_table,
+  return rope_append("kv8_append_paged", 8, q, k, v, q_out, rope, nullptr, nullptr, kv_cache, 0, block_table,
                      seq_ids, positions, T, num_seqs, d, block_size, max_blocks_per_seq, num_blocks, stream);
 }
 

@@ -41,7 +41,7 @@ decltype(&kv4_record_bytes) g_record_bytes = nullptr;
 decltype(&kv4_read_paged) g_read = nullptr;
 decltype(&attn_decode_paged_kv4_workspace_size) g_workspace_size = nullptr;
 decltype(&attn_decode_paged_kv4) g_decode = nullptr;
-decltype(&rope_append_paged_kv8) g_append_kv8 = nullptr;
+decltype(&kv8_append_paged) g_append_kv8 = nullptr;
 decltype(&kv8_record_bytes) g_record_bytes_kv8 = nullptr;
 decltype(&kv8_read_paged) g_read_kv8 = nullptr;
 
@@ -234,7 +234,7 @@ size_t record_bytes(bool kv8, int d, int group) { return kv8 ? g_record_bytes_kv
 template <bool KV8>
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int group = 0;
-  if (n != 14 || !g_append || !integer(a[8], &group)) Py_RETURN_NONE;
+  if (n != 14 || !(KV8 ? g_append_kv8 != nullptr : g_append != nullptr) || !integer(a[8], &group)) Py_RETURN_NONE;
   const at::Tensor* k = tensor(a[1], at::kBFloat16, -1);
   if (!k || k->dim() != 3) Py_RETURN_NONE;
   const int dev = static_cast<int>(k->get_device());
@@ -308,7 +308,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 template <bool KV8>
 PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int d = 0, group = 0;
-  if (n != 8 || !g_read || !integer(a[4], &d) || !integer(a[5], &group)) Py_RETURN_NONE;
+  if (n != 8 || !(KV8 ? g_read_kv8 != nullptr : g_read != nullptr) || !integer(a[4], &d) || !integer(a[5], &group)) Py_RETURN_NONE;
   const at::Tensor* kv = packed(a[0], at::kByte, -1, 3);
   if (!kv) Py_RETURN_NONE;
   const int dev = static_cast<int>(kv->get_device());
@@ -420,20 +420,25 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   }
 }
 
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kAddresses = 11;
-  if (n != kAddresses) {
-    PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kAddresses);
-    return nullptr;
+// The addresses that `bind` or `bind8` was given, all of them or none.
+bool addresses(PyObject* const* a, Py_ssize_t n, Py_ssize_t wanted, void** p) {
+  if (n != wanted) {
+    PyErr_Format(PyExc_TypeError, "%zd addresses are wanted", wanted);
+    return false;
   }
-  void* p[kAddresses];
-  for (int i = 0; i < kAddresses; ++i) {
+  for (Py_ssize_t i = 0; i < n; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
-      return nullptr;
+      return false;
     }
   }
+  return true;
+}
+
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* p[8];
+  if (!addresses(a, n, 8, p)) return nullptr;
   g_rope_fwd = reinterpret_cast<decltype(g_rope_fwd)>(p[0]);
   g_rope_bwd = reinterpret_cast<decltype(g_rope_bwd)>(p[1]);
   g_append = reinterpret_cast<decltype(g_append)>(p[2]);
@@ -442,14 +447,22 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_read = reinterpret_cast<decltype(g_read)>(p[5]);
   g_workspace_size = reinterpret_cast<decltype(g_workspace_size)>(p[6]);
   g_decode = reinterpret_cast<decltype(g_decode)>(p[7]);
-  g_append_kv8 = reinterpret_cast<decltype(g_append_kv8)>(p[8]);
-  g_record_bytes_kv8 = reinterpret_cast<decltype(g_record_bytes_kv8)>(p[9]);
-  g_read_kv8 = reinterpret_cast<decltype(g_read_kv8)>(p[10]);
+  Py_RETURN_NONE;
+}
+
+// The entry points of the 8-bit cache.
+PyObject* bind8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* p[3];
+  if (!addresses(a, n, 3, p)) return nullptr;
+  g_append_kv8 = reinterpret_cast<decltype(g_append_kv8)>(p[0]);
+  g_record_bytes_kv8 = reinterpret_cast<decltype(g_record_bytes_kv8)>(p[1]);
+  g_read_kv8 = reinterpret_cast<decltype(g_read_kv8)>(p[2]);
   Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
+                         {"bind8", FAST(bind8), METH_FASTCALL, nullptr},
                          {"rope", FAST(guarded<rope>), METH_FASTCALL, nullptr},
                          {"append", FAST(guarded<append<false>>), METH_FASTCALL, nullptr},
                          {"append8", FAST(guarded<append<true>>), METH_FASTCALL, nullptr},

@@ -627,7 +627,7 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
 size_t kv8_record_bytes(int d);
 
 /*
- * rope_append_paged_kv8 — rope_append_paged into an 8-bit cache: the rotated
+ * kv8_append_paged — rope_append_paged into an 8-bit cache: the rotated
  * keys and the values are quantised from fp32 (not through bf16).
  *
  * The tokens of a block share its scales, so the rows of a call that fall into
@@ -644,7 +644,7 @@ size_t kv8_record_bytes(int d);
  *             (the records of the blocks reached are read and written)
  *  The other arguments, rules and device flags are those of rope_append_paged.
  */
-attn_status_t rope_append_paged_kv8(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
+attn_status_t kv8_append_paged(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
                                     const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
                                     const int32_t* block_table, const int32_t* seq_ids,
                                     const int32_t* positions, int T, int num_seqs, int d, int block_size,
@@ -657,7 +657,7 @@ attn_status_t rope_append_paged_kv8(const attn_heads_t* q, const attn_heads_t* k
  *  k, v       [T, Hkv, d] bf16, contiguous, 16-byte aligned (written); they
  *             overlap neither each other nor an input
  *  The other arguments, rules and device flags are those of
- *  rope_append_paged_kv8 (rows in any order); rows with seq_ids[t] < 0 are left
+ *  kv8_append_paged (rows in any order); rows with seq_ids[t] < 0 are left
  *  as they were.
  */
 attn_status_t kv8_read_paged(const void* kv_cache, const int32_t* block_table, const int32_t* seq_ids,

@@ -29,7 +29,7 @@ def dev(*xs):
 def append_both(cache, k, v, table, ids, pos, d, **kw):
     """The same append by the kernel and by the oracle; the records' bytes."""
     kv = torch.as_tensor(cache).to(DEV)
-    attn.rope_append_paged_kv8(None, *dev(k, v), kv, *dev(table, ids, pos), **kw)
+    attn.kv8_append_paged(None, *dev(k, v), kv, *dev(table, ids, pos), **kw)
     torch.cuda.synchronize()
     want = oracle.kv8_append(np.array(cache), k.double().numpy(), v.double().numpy(), table.numpy(), ids.numpy(),
                              pos.numpy(), d)
@@ -187,7 +187,7 @@ def test_rotated_records_are_those_of_the_fp32_formula(d, rot, il, axes):
     y[..., first], y[..., second] = u * c - w * s, w * c + u * s
     kv = torch.zeros(nb, Hkv, attn.kv8_record_bytes(d), dtype=torch.uint8, device=DEV)
     xd = x.to(DEV)
-    qo = attn.rope_append_paged_kv8(*views(xd, Hq, Hkv, d), kv, *dev(table, ids, pos), **kw)
+    qo = attn.kv8_append_paged(*views(xd, Hq, Hkv, d), kv, *dev(table, ids, pos), **kw)
     turned, _ = attn.rope_fwd(views(xd, Hq, Hkv, d)[0].transpose(0, 1)[None], None,
                               kw.get("rope_positions", pos.to(DEV)), f.to(DEV), kw.get("pair_axis"), il)
     torch.cuda.synchronize()
@@ -213,11 +213,11 @@ def test_order_of_sequences_padding_and_views():
     f = workloads.rope_inv_freq(d).to(DEV)
     rec = workloads.kv8_cache(nb, Hkv, attn.kv8_record_bytes(d), d, seed=2).to(DEV)
     a, b = rec.clone(), rec.clone()
-    qa = attn.rope_append_paged_kv8(qv, kk, vv, a, *dev(table, ids, pos), inv_freq=f)
+    qa = attn.kv8_append_paged(qv, kk, vv, a, *dev(table, ids, pos), inv_freq=f)
     rows = wide[:, 1, 8:]
     qb = rows[:, : Hq * d].unflatten(1, (Hq, d))
     before = qb.clone()
-    attn.rope_append_paged_kv8(qb, rows[:, Hq * d: (Hq + Hkv) * d].unflatten(1, (Hkv, d)),
+    attn.kv8_append_paged(qb, rows[:, Hq * d: (Hq + Hkv) * d].unflatten(1, (Hkv, d)),
                                rows[:, (Hq + Hkv) * d:].unflatten(1, (Hkv, d)), b, *dev(table, ids2, pos2), inv_freq=f,
                                q_out=qb)
     torch.cuda.synchronize()
@@ -226,7 +226,7 @@ def test_order_of_sequences_padding_and_views():
     assert torch.equal(qb[7:9], before[7:9])
     assert torch.equal(torch.cat([qb[:7], qb[9:]]), qa[order])
     c = rec.clone()
-    assert attn.rope_append_paged_kv8(None, kk, vv, c, *dev(table, ids, pos), inv_freq=f) is None
+    assert attn.kv8_append_paged(None, kk, vv, c, *dev(table, ids, pos), inv_freq=f) is None
     torch.cuda.synchronize()
     assert torch.equal(a, c)
 
@@ -242,7 +242,7 @@ def test_bad_rows_are_reported_and_skipped():
     rec = workloads.kv8_cache(4, Hkv, attn.kv8_record_bytes(d), d, seed=2)
     kv = rec.to(DEV)
     q_out = torch.full((9, Hq, d), 7.0, dtype=BF, device=DEV)
-    attn.rope_append_paged_kv8(q, k, v, kv, *dev(table, ids, pos), q_out=q_out)
+    attn.kv8_append_paged(q, k, v, kv, *dev(table, ids, pos), q_out=q_out)
     torch.cuda.synchronize()
     assert attn.device_status() == attn.ATTN_DEV_BAD_BLOCK | attn.ATTN_DEV_BAD_SEQID | attn.ATTN_DEV_BAD_SEQLEN
     want = oracle.kv8_append(rec.numpy().copy(), k[good].double().cpu().numpy(), v[good].double().cpu().numpy(),
@@ -282,7 +282,7 @@ def test_records_beyond_32_bits():
     pos = torch.arange(64, dtype=torch.int32)
     k, v = randn(1, 64, Hkv, d), randn(2, 64, Hkv, d)
     ids = torch.zeros_like(pos)
-    attn.rope_append_paged_kv8(None, *dev(k, v), kv, *dev(table, ids, pos))
+    attn.kv8_append_paged(None, *dev(k, v), kv, *dev(table, ids, pos))
     small = np.zeros((4, Hkv, rec), np.uint8)
     want = oracle.kv8_append(small, k.double().numpy(), v.double().numpy(), np.array([[0, 1, 2, 3]]), ids.numpy(), pos.numpy(), d)
     rk, _ = attn.kv8_read_paged(kv, *dev(table, ids, pos), d)
@@ -304,7 +304,7 @@ def test_captured_append_and_read():
     f = workloads.rope_inv_freq(d).to(DEV)
 
     def step():
-        attn.rope_append_paged_kv8(*views(xd, Hq, Hkv, d), kv, table, ids, pos, inv_freq=f, q_out=q_out)
+        attn.kv8_append_paged(*views(xd, Hq, Hkv, d), kv, table, ids, pos, inv_freq=f, q_out=q_out)
         attn.kv8_read_paged(kv, table, ids, pos, d, k=k, v=v)
 
     step()

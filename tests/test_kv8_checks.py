@@ -15,7 +15,7 @@ V, TAB, IDS, POS, KV, OUT = 0x5000000, 0x6000000, 0x6100000, 0x6200000, 0x200000
 
 
 def test_exported_and_sized(lib):  # noqa: F811
-    for n in ("kv8_record_bytes", "rope_append_paged_kv8", "kv8_read_paged"):
+    for n in ("kv8_record_bytes", "kv8_append_paged", "kv8_read_paged"):
         assert hasattr(lib, n) and n in _binding._SIGS
     assert lib.kv8_record_bytes(128) == 4128 and lib.kv8_record_bytes(64) == 2080
     assert lib.kv8_record_bytes(96) == 0 and lib.kv8_record_bytes(0) == 0
@@ -25,7 +25,7 @@ def test_exported_and_sized(lib):  # noqa: F811
 
 def append(lib, q=0, k=0, v=0, qo=0, r=None, kv=KV, tab=TAB, ids=IDS, pos=POS, T=16, S=2, d=64, bs=16, mb=4, nb=8):  # noqa: F811
     q, k, v, qo = (heads(at) if h == 0 else h for at, h in ((Q, q), (K, k), (V, v), (QO, qo)))
-    return lib.rope_append_paged_kv8(ref(q), ref(k), ref(v), ref(qo), ref(r), kv, tab, ids, pos, T, S, d, bs, mb, nb, None)
+    return lib.kv8_append_paged(ref(q), ref(k), ref(v), ref(qo), ref(r), kv, tab, ids, pos, T, S, d, bs, mb, nb, None)
 
 
 def test_append_refusals(lib):  # noqa: F811
@@ -75,7 +75,7 @@ def test_binding_refuses_append_and_read(no_library_calls):  # noqa: F811
                        (dict(kv_cache=dev((9, 3, rec), U8)), "k's heads"),
                        (dict(kv_cache=torch.zeros((9, Hkv, rec), dtype=U8)), "kv_cache must be a CUDA tensor")]:
         with pytest.raises(ValueError, match=match):
-            attn.rope_append_paged_kv8(**(base | bad))
+            attn.kv8_append_paged(**(base | bad))
     r = {n: base[n] for n in ("kv_cache", "block_table", "seq_ids", "positions")}
     r.update(d=d, k=dev((T, Hkv, d), BF), v=dev((T, Hkv, d), BF))
     for bad, match in [(dict(d=128), "kv_cache must be"), (dict(k=dev((T, Hkv, 128), BF)), "k must have shape"),
