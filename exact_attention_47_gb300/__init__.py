@@ -1,6 +1,7 @@
 """GB300 (sm_103a) exact attention: tiled online-softmax prefill, its backward,
 paged-KV decode, chunked prefill over the paged cache, rotary positions and
-the paged appends that rotate on the way, a 4-bit paged cache with its decode,
+the paged appends that rotate on the way, an 8-bit paged cache with attention of
+single queries and chunks, a 4-bit one with its decode,
 and the residual add + RMSNorm and SwiGLU fusions of the same layer.
 
 The compute lives in ``lib/libattn47_sm103.so`` (hand-written CUDA, C-ABI
@@ -22,10 +23,14 @@ from ._binding import (  # noqa: F401
     attn_decode_paged,
     attn_decode_paged_kv4,
     attn_decode_paged_kv4_workspace_size,
+    attn_decode_paged_kv8,
+    attn_decode_paged_kv8_workspace_size,
     attn_decode_paged_noalloc,
     attn_decode_paged_workspace_size,
     attn_fwd,
     attn_prefill_paged,
+    attn_prefill_paged_kv8,
+    attn_prefill_paged_kv8_workspace_size,
     device_status,
     fused_add_rmsnorm,
     fused_swiglu,

@@ -56,6 +56,12 @@ _SIGS = {
     "kv8_record_bytes": (ctypes.c_size_t, [_I]),
     "kv8_append_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "kv8_read_paged": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "attn_decode_paged_kv8_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "attn_decode_paged_kv8": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
+                                   ctypes.c_size_t, _P]),
+    "attn_prefill_paged_kv8_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "attn_prefill_paged_kv8": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
+                                    ctypes.c_size_t, _P]),
     "kv4_read_paged": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "attn_decode_paged_kv4_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "attn_decode_paged_kv4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P,
@@ -118,7 +124,8 @@ def load_library(path=None):
 _FAST = ("rope_fwd", "rope_bwd", "rope_append_paged", "rope_append_paged_kv4", "kv4_record_bytes", "kv4_read_paged",
          "attn_decode_paged_kv4_workspace_size", "attn_decode_paged_kv4")
 # Those of the 8-bit cache, in the order of `bind8`.
-_FAST_KV8 = ("kv8_append_paged", "kv8_record_bytes", "kv8_read_paged")
+_FAST_KV8 = ("kv8_append_paged", "kv8_record_bytes", "kv8_read_paged", "attn_decode_paged_kv8_workspace_size",
+             "attn_decode_paged_kv8", "attn_prefill_paged_kv8_workspace_size", "attn_prefill_paged_kv8")
 
 
 class _NoFastCalls:
@@ -129,7 +136,7 @@ class _NoFastCalls:
     def rope(*args):
         return None
 
-    append = read = decode = append8 = read8 = rope
+    append = read = decode = append8 = read8 = decode8 = prefill8 = rope
 
 
 @functools.lru_cache(maxsize=None)
@@ -860,6 +867,91 @@ def attn_decode_paged_kv4(q, kv_cache, block_table, seq_lens, group, scale=None,
           group, BLOCK_SIZE, table_shape[1], nb, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _stream_handle(None, dev))
     return o, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def attn_decode_paged_kv8_workspace_size(num_seqs, Hq, Hkv, d):
+    return int(load_library().attn_decode_paged_kv8_workspace_size(num_seqs, Hq, Hkv, d))
+
+
+@functools.lru_cache(maxsize=1024)
+def attn_prefill_paged_kv8_workspace_size(num_seqs, Hq, Hkv, N, d):
+    return int(load_library().attn_prefill_paged_kv8_workspace_size(num_seqs, Hq, Hkv, N, d))
+
+
+def _attend_kv8(func, q, kv_cache, block_table, seq_lens, scale, o, lse, workspace, return_lse):
+    """Both attentions over an 8-bit cache, the longer way: q [S,Hq,d] or
+    [S,Hq,N,d]."""
+    _need_cuda("q", q, torch.bfloat16)
+    dev = q.device
+    if func == "attn_decode_paged_kv8":
+        if q.dim() != 3:
+            raise ValueError("q must be [S,Hq,d]")
+        S, Hq, d = q.shape
+        rows, size = (), attn_decode_paged_kv8_workspace_size
+    else:
+        if q.dim() != 4:
+            raise ValueError("q must be [S,Hq,N,d]")
+        S, Hq, N, d = q.shape
+        rows, size = (N,), attn_prefill_paged_kv8_workspace_size
+    nb, Hkv = _need_kv8(kv_cache, d, dev)
+    _need_cuda("block_table", block_table, torch.int32, dev)
+    _need_cuda("seq_lens", seq_lens, torch.int32, dev)
+    table_shape = block_table.shape
+    if len(table_shape) != 2 or table_shape[0] != S:
+        raise ValueError("block_table must be [S, max_blocks]")
+    _need_shape("seq_lens", seq_lens, (S,))
+    o = _output("o", o, q.shape, torch.bfloat16, dev)
+    if lse is not None or return_lse:
+        lse = _output("lse", lse, q.shape[:-1], torch.float32, dev)
+    if scale is None:
+        scale = d ** -0.5
+    workspace = _workspace("workspace", workspace, size(S, Hq, Hkv, *rows, d), dev)
+    _call(func, dev, _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), S, Hq, Hkv, *rows, d, BLOCK_SIZE,
+          table_shape[1], nb, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _stream_handle(None, dev))
+    return o, lse
+
+
+def attn_decode_paged_kv8(q, kv_cache, block_table, seq_lens, scale=None, o=None, lse=None, workspace=None,
+                          return_lse=True, stream=None):
+    """attn_decode_paged over an 8-bit cache.  q [S,Hq,d] bf16; kv_cache
+    [num_blocks,Hkv,kv8_record_bytes(d)] uint8; block_table [S,max_blocks]
+    int32; seq_lens [S] int32 (all on the GPU).
+
+    Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32 or None).
+    """
+    if stream is not None:
+        return _on_stream(attn_decode_paged_kv8, stream, q, q, kv_cache, block_table, seq_lens, scale, o, lse,
+                          workspace, return_lse)
+    done = _fast().decode8(q, kv_cache, block_table, seq_lens, 0, scale, o, lse, workspace, return_lse)
+    if done is not None:
+        if done.__class__ is int:
+            _check("attn_decode_paged_kv8", done)
+        return done
+    return _attend_kv8("attn_decode_paged_kv8", q, kv_cache, block_table, seq_lens, scale, o, lse, workspace, return_lse)
+
+
+def attn_prefill_paged_kv8(q, kv_cache, block_table, seq_lens, scale=None, o=None, lse=None, workspace=None,
+                           return_lse=True, stream=None):
+    """The last N tokens of each sequence attend to an 8-bit cache that holds
+    them already (see kv8_append_paged): a prompt's chunk, or draft tokens.
+    q [S,Hq,N,d] bf16: query i is the token at position seq_lens[b] - N + i and
+    sees the keys up to itself (before position 0: none, o = 0 and lse = -inf);
+    the other arguments are attn_decode_paged_kv8's.
+
+    Returns (o [S,Hq,N,d] bf16, lse [S,Hq,N] fp32 or None).
+    """
+    if stream is not None:
+        return _on_stream(attn_prefill_paged_kv8, stream, q, q, kv_cache, block_table, seq_lens, scale, o, lse,
+                          workspace, return_lse)
+    done = _fast().prefill8(q, kv_cache, block_table, seq_lens, 0, scale, o, lse, workspace, return_lse)
+    if done is not None:
+        if done.__class__ is int:
+            _check("attn_prefill_paged_kv8", done)
+        return done
+    return _attend_kv8("attn_prefill_paged_kv8", q, kv_cache, block_table, seq_lens, scale, o, lse, workspace,
+                       return_lse)
 
 
 def device_status(stream=None):

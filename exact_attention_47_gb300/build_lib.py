@@ -28,7 +28,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB_NAME = "libattn47_sm103.so"
 LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 
-SOURCES = ["api.cu", "fwd_sm103.cu", "bwd_sm103.cu", "decode_sm103.cu", "decode_kv4_sm103.cu", "kv_append_sm103.cu", "rope_sm103.cu",
+SOURCES = ["api.cu", "fwd_sm103.cu", "bwd_sm103.cu", "decode_sm103.cu", "decode_kv4_sm103.cu", "decode_kv8_sm103.cu", "kv_append_sm103.cu", "rope_sm103.cu",
            "fusion_sm103.cu", "gemm_sm103.cu", "ssd_sm103.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = GENCODE + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -101,7 +101,7 @@ def _build_fast():
     except (ImportError, OSError, RuntimeError) as e:
         if fast is not None and os.path.exists(fast):
             os.remove(fast)
-        sys.stderr.write("the module of the fast calls was not built (the rotary, append and 4-bit-cache calls cost "
+        sys.stderr.write("the module of the fast calls was not built (the rotary, append and 8- and 4-bit-cache calls cost "
                          "more host time without it): %s\n" % e)
 
 

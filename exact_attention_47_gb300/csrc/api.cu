@@ -17,6 +17,7 @@
 
 #include "attn47.h"
 #include "decode_kv4_sm103.h"
+#include "decode_kv8_sm103.h"
 #include "decode_sm103.h"
 #include "bwd_sm103.h"
 #include "fusion_sm103.h"
@@ -787,6 +788,123 @@ attn_status_t check_group(int group) {
   return ATTN_OK;
 }
 
+// Host-side checks of attention over a cache of `bits` bits, 8 or 4 (and then the
+// group), by N queries of each sequence: `need` bytes of workspace, `passes` over
+// the blocks of a KV head.  *dev stays null where there is nothing to do.
+attn_status_t check_quantised_attention(int bits, int group, bool decode, const void* q, const void* kv_cache,
+                                        const int32_t* block_table, const int32_t* seq_lens, int num_seqs, int Hq,
+                                        int Hkv, int N, int d, int block_size, int max_blocks_per_seq, int num_blocks,
+                                        float scale, const void* o, const float* lse, const void* workspace,
+                                        size_t workspace_bytes, size_t need, int passes, DeviceInfo** dev) {
+  *dev = nullptr;
+  if (num_seqs < 0 || Hq < 1 || Hkv < 1 || N < 0 || max_blocks_per_seq < 1 || num_blocks < 1)
+    return fail(ATTN_ERR_INVALID_ARG,
+                "sizes must satisfy num_seqs, N >= 0, Hq, Hkv, max_blocks_per_seq, num_blocks >= 1");
+  if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq (%d) is not a multiple of Hkv (%d)", Hq, Hkv);
+  if (!finite_positive(scale)) return fail(ATTN_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
+  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
+  if (decode && Hq / Hkv > 16) return fail(ATTN_ERR_UNSUPPORTED, "Hq/Hkv = %d > 16 not supported", Hq / Hkv);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  // The split counts blocks (and a few more units per run) in 32 bits.
+  if (static_cast<__int128>(num_seqs) * Hq * N >= 0x7fffffff ||
+      static_cast<__int128>(num_seqs) * Hkv * passes * (static_cast<long long>(max_blocks_per_seq) + 64) >= 0x7fffffff)
+    return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
+  if (num_seqs == 0 || N == 0) {
+    g_last_error[0] = '\0';
+    return ATTN_OK;
+  }
+  if (!q || !kv_cache || !block_table || !seq_lens || !o || (need != 0 && !workspace))
+    return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, block_table, seq_lens, o and workspace must be non-null");
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o) || !aligned16(workspace))
+    return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, o and workspace must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
+  if (workspace_bytes < need)
+    return fail(ATTN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  const size_t qb = static_cast<size_t>(num_seqs) * Hq * N * d * 2;
+  const size_t cache = static_cast<size_t>(num_blocks) * Hkv *
+                       (bits == 8 ? attn47::kv8_record_bytes_of(d) : attn47::kv4_record_bytes_of(d, group));
+  const size_t table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, lens = static_cast<size_t>(num_seqs) * 4;
+  const size_t lb = static_cast<size_t>(num_seqs) * Hq * N * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } others[] = {{q, qb}, {kv_cache, cache}, {block_table, table}, {seq_lens, lens}, {o, qb}, {lse, lse ? lb : 0}};
+  for (const auto& x : others)
+    if (need && x.n && overlap(workspace, need, x.p, x.n))
+      return fail(ATTN_ERR_INVALID_ARG, "workspace overlaps an input or output of the attention");
+  for (int i = 0; i < 4; ++i) {                  // (other warps may still be reading there)
+    if (overlap(o, qb, others[i].p, others[i].n)) return fail(ATTN_ERR_INVALID_ARG, "o overlaps an input of the attention");
+    if (lse && overlap(lse, lb, others[i].p, others[i].n))
+      return fail(ATTN_ERR_INVALID_ARG, "lse overlaps an input of the attention");
+  }
+  if (lse && overlap(o, qb, lse, lb)) return fail(ATTN_ERR_INVALID_ARG, "o overlaps lse");
+  attn_status_t st = current_device(dev);
+  if (st == ATTN_OK)
+    st = check_bufs(**dev, {{workspace, need, "workspace"}, {q, qb, "q"}, {kv_cache, cache, "kv_cache"},
+                            {block_table, table, "block_table"}, {seq_lens, lens, "seq_lens"}, {o, qb, "o"},
+                            {lse, lb, "lse"}});
+  return st;
+}
+
+// What the launches of both decodes take alike.
+template <class Launch>
+void fill_quantised_decode(Launch& a, const DeviceInfo& dev, const void* q, const void* kv_cache,
+                           const int32_t* block_table, const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int d,
+                           int max_blocks_per_seq, int num_blocks, float scale, void* o, float* lse, void* workspace,
+                           void* stream) {
+  a.q = q;
+  a.kv_cache = kv_cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.num_seqs = num_seqs;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.sms = dev.sms;
+  a.device = dev.index;
+  a.max_ctas = g_decode_max_ctas;
+  a.epoch = next_decode_epoch();
+  a.early_plan = g_decode_early_plan.load() > 0 ? 1 : 0;
+  a.scale = scale;
+  a.status = dev.status;
+  a.timeout_ns = g_timeout_ns;
+  a.stream = static_cast<cudaStream_t>(stream);
+}
+
+// Both attentions over an 8-bit cache.
+attn_status_t attend_kv8(const char* what, bool decode, const void* q, const void* kv_cache, const int32_t* block_table,
+                         const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d, int block_size,
+                         int max_blocks_per_seq, int num_blocks, float scale, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int passes = 1;
+  if (Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && N > 0) {
+    if (static_cast<long long>(Hq / Hkv) * N >= 0x7fffffffLL)
+      return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
+    need = attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
+    passes = attn47::decode_kv8_rows(Hq, Hkv, N).groups;
+  }
+  DeviceInfo* dev;
+  const attn_status_t st = check_quantised_attention(8, 0, decode, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv,
+                                                     N, d, block_size, max_blocks_per_seq, num_blocks, scale, o, lse,
+                                                     workspace, workspace_bytes, need, passes, &dev);
+  if (st != ATTN_OK || dev == nullptr) return st;
+  attn47::DecKv8Launch a;
+  fill_quantised_decode(a, *dev, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, d, max_blocks_per_seq, num_blocks,
+                        scale, o, lse, workspace, stream);
+  a.N = N;
+  return launch_result(attn47::launch_decode_kv8_sm103(a), what);
+}
+
 __global__ void selftest_wait_kernel(unsigned int* status, unsigned long long timeout_ns) {
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
@@ -1430,82 +1548,43 @@ attn_status_t attn_decode_paged_kv4(const void* q, const void* kv_cache, const i
                                     size_t workspace_bytes, void* stream) {
   attn_status_t st = check_group(group);
   if (st != ATTN_OK) return st;
-  if (num_seqs < 0 || Hq < 1 || Hkv < 1 || max_blocks_per_seq < 1 || num_blocks < 1)
-    return fail(ATTN_ERR_INVALID_ARG,
-                "sizes must satisfy num_seqs >= 0, Hq, Hkv, max_blocks_per_seq, num_blocks >= 1");
-  if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq (%d) is not a multiple of Hkv (%d)", Hq, Hkv);
-  if (!finite_positive(scale)) return fail(ATTN_ERR_INVALID_ARG, "scale must be finite and > 0");
-  if (block_size != 16) return fail(ATTN_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
-  if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", d);
-  if (Hq / Hkv > 16) return fail(ATTN_ERR_UNSUPPORTED, "Hq/Hkv = %d > 16 not supported", Hq / Hkv);
-  if (static_cast<long long>(max_blocks_per_seq) * block_size >= 0x7fffffffLL)
-    return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
-  // The split counts blocks (and a few more units per run) in 32 bits.
-  if (static_cast<long long>(num_seqs) * Hq >= 0x7fffffffLL ||
-      static_cast<__int128>(num_seqs) * Hkv * (static_cast<long long>(max_blocks_per_seq) + 64) >= 0x7fffffff)
-    return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
-  if (num_seqs == 0) {
-    g_last_error[0] = '\0';
-    return ATTN_OK;
-  }
-  if (!q || !kv_cache || !block_table || !seq_lens || !o || !workspace)
-    return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, block_table, seq_lens, o and workspace must be non-null");
-  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o) || !aligned16(workspace))
-    return fail(ATTN_ERR_INVALID_ARG, "q, kv_cache, o and workspace must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return fail(ATTN_ERR_INVALID_ARG, "block_table, seq_lens and lse must be 4-byte aligned");
-  const size_t need = attn47::decode_kv4_workspace_bytes(Hq, Hkv, d);
-  if (workspace_bytes < need)
-    return fail(ATTN_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
-  const size_t qb = static_cast<size_t>(num_seqs) * Hq * d * 2;
-  const size_t cache = static_cast<size_t>(num_blocks) * Hkv * attn47::kv4_record_bytes_of(d, group);
-  const size_t table = static_cast<size_t>(num_seqs) * max_blocks_per_seq * 4, lens = static_cast<size_t>(num_seqs) * 4;
-  const size_t lb = static_cast<size_t>(num_seqs) * Hq * 4;
-  const struct {
-    const void* p;
-    size_t n;
-  } others[] = {{q, qb}, {kv_cache, cache}, {block_table, table}, {seq_lens, lens}, {o, qb}, {lse, lse ? lb : 0}};
-  for (const auto& x : others)
-    if (x.n && overlap(workspace, need, x.p, x.n))
-      return fail(ATTN_ERR_INVALID_ARG, "workspace overlaps an input or output of the decode");
-  for (int i = 0; i < 4; ++i) {                  // (other warps may still be reading there)
-    if (overlap(o, qb, others[i].p, others[i].n)) return fail(ATTN_ERR_INVALID_ARG, "o overlaps an input of the decode");
-    if (lse && overlap(lse, lb, others[i].p, others[i].n))
-      return fail(ATTN_ERR_INVALID_ARG, "lse overlaps an input of the decode");
-  }
-  if (lse && overlap(o, qb, lse, lb)) return fail(ATTN_ERR_INVALID_ARG, "o overlaps lse");
-  DeviceInfo* dev = nullptr;
-  if ((st = current_device(&dev)) != ATTN_OK) return st;
-  if ((st = check_bufs(*dev, {{workspace, need, "workspace"}, {q, qb, "q"}, {kv_cache, cache, "kv_cache"},
-                              {block_table, table, "block_table"}, {seq_lens, lens, "seq_lens"}, {o, qb, "o"},
-                              {lse, lb, "lse"}})) != ATTN_OK)
-    return st;
+  DeviceInfo* dev;
+  const size_t need = Hq > 0 && Hkv > 0 && Hq % Hkv == 0 ? attn47::decode_kv4_workspace_bytes(Hq, Hkv, d) : 0;
+  st = check_quantised_attention(4, group, true, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, 1, d, block_size,
+                                 max_blocks_per_seq, num_blocks, scale, o, lse, workspace, workspace_bytes, need, 1,
+                                 &dev);
+  if (st != ATTN_OK || dev == nullptr) return st;
   attn47::DecKv4Launch a;
-  a.q = q;
-  a.kv_cache = kv_cache;
-  a.block_table = block_table;
-  a.seq_lens = seq_lens;
-  a.o = o;
-  a.lse = lse;
-  a.workspace = workspace;
-  a.num_seqs = num_seqs;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.d = d;
+  fill_quantised_decode(a, *dev, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, d, max_blocks_per_seq, num_blocks,
+                        scale, o, lse, workspace, stream);
   a.group = group;
-  a.max_blocks = max_blocks_per_seq;
-  a.num_blocks = num_blocks;
-  a.sms = dev->sms;
-  a.device = dev->index;
-  a.max_ctas = g_decode_max_ctas;
-  a.epoch = next_decode_epoch();
-  a.early_plan = g_decode_early_plan.load() > 0 ? 1 : 0;
-  a.scale = scale;
-  a.status = dev->status;
-  a.timeout_ns = g_timeout_ns;
-  a.stream = static_cast<cudaStream_t>(stream);
   return launch_result(attn47::launch_decode_kv4_sm103(a), "attn_decode_paged_kv4");
+}
+
+size_t attn_decode_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int d) {
+  if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
+  return attn47::decode_kv8_workspace_bytes(Hq, Hkv, 1, d);
+}
+
+attn_status_t attn_decode_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
+                                    const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int d,
+                                    int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                    void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return attend_kv8("attn_decode_paged_kv8", true, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, 1, d,
+                    block_size, max_blocks_per_seq, num_blocks, scale, o, lse, workspace, workspace_bytes, stream);
+}
+
+size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int N, int d) {
+  if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
+  return attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
+}
+
+attn_status_t attn_prefill_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
+                                     const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d,
+                                     int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                     void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return attend_kv8("attn_prefill_paged_kv8", false, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, N, d,
+                    block_size, max_blocks_per_seq, num_blocks, scale, o, lse, workspace, workspace_bytes, stream);
 }
 
 attn_status_t attn_get_device_status(void* stream, unsigned int* flags_out) {

@@ -44,6 +44,10 @@ decltype(&attn_decode_paged_kv4) g_decode = nullptr;
 decltype(&kv8_append_paged) g_append_kv8 = nullptr;
 decltype(&kv8_record_bytes) g_record_bytes_kv8 = nullptr;
 decltype(&kv8_read_paged) g_read_kv8 = nullptr;
+decltype(&attn_decode_paged_kv8_workspace_size) g_workspace_size_kv8 = nullptr;
+decltype(&attn_decode_paged_kv8) g_decode_kv8 = nullptr;
+decltype(&attn_prefill_paged_kv8_workspace_size) g_prefill_workspace_size_kv8 = nullptr;
+decltype(&attn_prefill_paged_kv8) g_prefill_kv8 = nullptr;
 
 constexpr int kBlock = 16;   // cached tokens of a block
 
@@ -347,21 +351,25 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return pair(k, &v);
 }
 
-// decode(q, kv_cache, block_table, seq_lens, group, scale, o, lse, workspace, return_lse)
+// decode(q, kv_cache, block_table, seq_lens, group, scale, o, lse, workspace, return_lse); decode8 and, with q
+// [S, Hq, N, d], prefill8 over an 8-bit cache (the group says nothing)
+enum Attention { kDecode4, kDecode8, kPrefill8 };
+template <Attention A>
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int group = 0, want_lse = 0;
-  if (n != 10 || !g_decode || !integer(a[4], &group) || !truth(a[9], &want_lse)) Py_RETURN_NONE;
-  const at::Tensor* q = packed(a[0], at::kBFloat16, -1, 3);
+  if (n != 10 || !(A == kDecode4 ? g_decode != nullptr : g_prefill_kv8 != nullptr) || !integer(a[4], &group) || !truth(a[9], &want_lse)) Py_RETURN_NONE;
+  const at::Tensor* q = packed(a[0], at::kBFloat16, -1, A == kPrefill8 ? 4 : 3);
   if (!q) Py_RETURN_NONE;
   const int dev = static_cast<int>(q->get_device());
-  const int64_t S = q->size(0), Hq = q->size(1), d = q->size(2);
+  const int64_t S = q->size(0), Hq = q->size(1), N = A == kPrefill8 ? q->size(2) : 1, d = q->size(q->dim() - 1);
   const at::Tensor* kv = packed(a[1], at::kByte, dev, 3);
   const at::Tensor* table = packed(a[2], at::kInt, dev, 2);
   const at::Tensor* lens = packed(a[3], at::kInt, dev, 1);
-  if (!kv || !table || !lens || table->size(0) != S || lens->size(0) != S || !small(S) || !small(Hq) || !small(d) ||
+  if (!kv || !table || !lens || table->size(0) != S || lens->size(0) != S || !small(S) || !small(Hq) || !small(N) ||
+      !small(d) ||
       !small(kv->size(0)) || !small(kv->size(1)) || !small(table->size(1)) || !current(dev))
     Py_RETURN_NONE;
-  const size_t rec = g_record_bytes(static_cast<int>(d), group);
+  const size_t rec = record_bytes(A != kDecode4, static_cast<int>(d), group);
   if (rec == 0 || kv->size(2) != static_cast<int64_t>(rec)) Py_RETURN_NONE;
   float scale;
   if (a[5] == Py_None)
@@ -371,9 +379,13 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   else
     Py_RETURN_NONE;
   const int Hkv = static_cast<int>(kv->size(1));
-  const int64_t lse_sizes[2] = {S, Hq};
+  const int64_t lse_dims[3] = {S, Hq, N};
+  const at::IntArrayRef lse_sizes(lse_dims, A == kPrefill8 ? 3 : 2);
   const bool has_lse = a[7] != Py_None || want_lse;
-  const size_t need = g_workspace_size(static_cast<int>(S), static_cast<int>(Hq), Hkv, static_cast<int>(d));
+  const int s = static_cast<int>(S), hq = static_cast<int>(Hq), rows = static_cast<int>(N), dd = static_cast<int>(d);
+  const size_t need = A == kDecode4   ? g_workspace_size(s, hq, Hkv, dd)
+                      : A == kDecode8 ? g_workspace_size_kv8(s, hq, Hkv, dd)
+                                      : g_prefill_workspace_size_kv8(s, hq, Hkv, rows, dd);
   const at::Tensor *o_given, *lse_given = nullptr, *ws_given = nullptr;
   if (!output(a[6], q->sizes(), at::kBFloat16, dev, false, &o_given) ||
       (has_lse && !output(a[7], lse_sizes, at::kFloat, dev, false, &lse_given)))
@@ -393,10 +405,17 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (has_lse) lse = lse_given ? *lse_given : make(lse_sizes, at::kFloat, *q);
     ws = ws_given ? *ws_given : make({static_cast<int64_t>(need < 16 ? 16 : need)}, at::kByte, *q);
     t_called = true;
-    st = g_decode(data<void>(q), data<void>(kv), data<int32_t>(table), data<int32_t>(lens), static_cast<int>(S),
-                  static_cast<int>(Hq), Hkv, static_cast<int>(d), group, kBlock, static_cast<int>(table->size(1)),
-                  static_cast<int>(kv->size(0)), scale, data<void>(o), has_lse ? data<float>(lse) : nullptr,
-                  data<void>(ws), ws.nbytes(), stream_of(dev));
+    const int mb = static_cast<int>(table->size(1)), nb = static_cast<int>(kv->size(0));
+    float* pl = has_lse ? data<float>(lse) : nullptr;
+    if constexpr (A == kDecode4)
+      st = g_decode(data<void>(q), data<void>(kv), data<int32_t>(table), data<int32_t>(lens), s, hq, Hkv, dd, group,
+                    kBlock, mb, nb, scale, data<void>(o), pl, data<void>(ws), ws.nbytes(), stream_of(dev));
+    else if constexpr (A == kDecode8)
+      st = g_decode_kv8(data<void>(q), data<void>(kv), data<int32_t>(table), data<int32_t>(lens), s, hq, Hkv, dd, kBlock,
+                        mb, nb, scale, data<void>(o), pl, data<void>(ws), ws.nbytes(), stream_of(dev));
+    else
+      st = g_prefill_kv8(data<void>(q), data<void>(kv), data<int32_t>(table), data<int32_t>(lens), s, hq, Hkv, rows, dd,
+                         kBlock, mb, nb, scale, data<void>(o), pl, data<void>(ws), ws.nbytes(), stream_of(dev));
   }
   if (st != ATTN_OK) return not_done(st);
   return pair(o, has_lse ? &lse : nullptr);
@@ -452,11 +471,15 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The entry points of the 8-bit cache.
 PyObject* bind8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[3];
-  if (!addresses(a, n, 3, p)) return nullptr;
+  void* p[7];
+  if (!addresses(a, n, 7, p)) return nullptr;
   g_append_kv8 = reinterpret_cast<decltype(g_append_kv8)>(p[0]);
   g_record_bytes_kv8 = reinterpret_cast<decltype(g_record_bytes_kv8)>(p[1]);
   g_read_kv8 = reinterpret_cast<decltype(g_read_kv8)>(p[2]);
+  g_workspace_size_kv8 = reinterpret_cast<decltype(g_workspace_size_kv8)>(p[3]);
+  g_decode_kv8 = reinterpret_cast<decltype(g_decode_kv8)>(p[4]);
+  g_prefill_workspace_size_kv8 = reinterpret_cast<decltype(g_prefill_workspace_size_kv8)>(p[5]);
+  g_prefill_kv8 = reinterpret_cast<decltype(g_prefill_kv8)>(p[6]);
   Py_RETURN_NONE;
 }
 
@@ -468,7 +491,9 @@ PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                          {"append8", FAST(guarded<append<true>>), METH_FASTCALL, nullptr},
                          {"read", FAST(guarded<read<false>>), METH_FASTCALL, nullptr},
                          {"read8", FAST(guarded<read<true>>), METH_FASTCALL, nullptr},
-                         {"decode", FAST(guarded<decode>), METH_FASTCALL, nullptr},
+                         {"decode", FAST(guarded<decode<kDecode4>>), METH_FASTCALL, nullptr},
+                         {"decode8", FAST(guarded<decode<kDecode8>>), METH_FASTCALL, nullptr},
+                         {"prefill8", FAST(guarded<decode<kPrefill8>>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn47_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -665,6 +665,72 @@ attn_status_t kv8_read_paged(const void* kv_cache, const int32_t* block_table, c
                              int block_size, int max_blocks_per_seq, int num_blocks, void* stream);
 
 /*
+ * attn_decode_paged_kv8_workspace_size — bytes of device workspace that
+ * attn_decode_paged_kv8 needs: partial results of the query heads of a KV head
+ * and an arrival counter for each of at most 256 CTAs.  It does not depend on
+ * the sequences, but for 0 for an empty problem.
+ */
+size_t attn_decode_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int d);
+
+/*
+ * attn_decode_paged_kv8 — attn_decode_paged over an 8-bit cache: one query
+ * token per sequence, softmax(scale * q . k) v over the values that the cached
+ * codes stand for (fp32 accumulation).  q, codes and scales enter exactly
+ * (elements of q under 2^-31 of their head's largest lose bits); the softmax
+ * numerators are rounded to 11 bits for the product with V, or to 2^-34 of
+ * the largest where that is coarser.
+ *
+ *  kv_cache   [num_blocks, Hkv, kv8_record_bytes(d)] bytes, 16-byte aligned;
+ *             slots past seq_lens[b] are never used, whatever they hold
+ *  workspace  >= attn_decode_paged_kv8_workspace_size(...) bytes, 16-byte
+ *             aligned; contents on entry are ignored
+ *  o, lse     as for attn_decode_paged; they overlap neither each other nor an
+ *             input
+ *  q, block_table, seq_lens, scale, sizes, empty sequences and device
+ *  flags as for attn_decode_paged (Hq / Hkv <= 16); attn_set_decode_early_plan
+ *  applies (level 2 acts as 1).  One kernel; the parts of a split (sequence,
+ *  KV head) are merged in a fixed order, so the result is deterministic for a
+ *  given device and attn_set_decode_max_ctas setting.  Calls that share a
+ *  workspace must not overlap on the GPU.
+ */
+attn_status_t attn_decode_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
+                                    const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int d,
+                                    int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                    void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * attn_prefill_paged_kv8_workspace_size — bytes of device workspace that
+ * attn_prefill_paged_kv8 needs (0: none; the sizes alone decide).
+ */
+size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int N, int d);
+
+/*
+ * attn_prefill_paged_kv8 — the last N tokens of each sequence attend to an
+ * 8-bit cache that holds them already (kv8_append_paged put them there): a
+ * prompt's chunk, draft tokens to be verified, or with N = 1 a decode step.
+ * With L = seq_lens[b], query i of sequence b is its token at position
+ * L - N + i and sees keys 0 .. L - N + i.  A query before position 0 (sequences
+ * shorter than N: a batch padded on the left) sees nothing: o = 0, lse = -inf.
+ *
+ *  q          [num_seqs, Hq, N, d] bf16, 16-byte aligned
+ *  o          [num_seqs, Hq, N, d] bf16 (written)
+ *  lse        [num_seqs, Hq, N] fp32 (written) or NULL
+ *  seq_lens   [num_seqs] int32 (device): cached tokens of each sequence, the N
+ *             new ones among them
+ *  workspace  >= attn_prefill_paged_kv8_workspace_size(...) bytes, 16-byte
+ *             aligned (NULL if that is 0); contents on entry are ignored
+ *  Hq % Hkv == 0, any Hq / Hkv; num_seqs == 0 or N == 0 is an empty problem.
+ *  The other arguments, rules and device flags are those of
+ *  attn_decode_paged_kv8.
+ */
+attn_status_t attn_prefill_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
+                                     const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d,
+                                     int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                     void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * attn_get_device_status — synchronises `stream`, copies the current
  * device's status word (ATTN_DEV_* bits) to *flags_out (host pointer) and
  * clears it.  Returns ATTN_ERR_DEVICE if the device is unusable.

@@ -127,9 +127,9 @@ def prefill_paged_kv8(q, cache, block_table, seq_lens, scale, d):
         L = int(seq_lens[b])
         for h in range(Hq):
             g = h // (Hq // Hkv)
-            at = [(int(block_table[b][j // SLOTS]), g, j % SLOTS) for j in range(L)]
-            keys, vals = np.array([k[a] for a in at]).reshape(L, d), np.array([v[a] for a in at]).reshape(L, d)
-            bad = np.array([flagged[a] for a in at], dtype=bool)
+            j = np.arange(L)
+            at = (np.asarray(block_table)[b, j // SLOTS], g, j % SLOTS)
+            keys, vals, bad = k[at], v[at], flagged[at]
             first = max(0, N - L)                    # rows before it belong to no token
             if first == N:
                 continue
