@@ -880,6 +880,20 @@ void fill_quantised_decode(Launch& a, const DeviceInfo& dev, const void* q, cons
   a.stream = static_cast<cudaStream_t>(stream);
 }
 
+// Tensor map over the codes of 8-bit records, as 128-byte lines in boxes of
+// `lines` lines, 128-byte swizzle.
+attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records, int d, int lines) {
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d / 4), records};
+  const cuuint64_t strides[2] = {128, attn47::kv8_record_bytes_of(d)};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(lines), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ATTN_OK;
+}
+
 // Both attentions over an 8-bit cache.
 attn_status_t attend_kv8(const char* what, bool decode, const void* q, const void* kv_cache, const int32_t* block_table,
                          const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d, int block_size,
@@ -894,6 +908,9 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
     passes = attn47::decode_kv8_rows(Hq, Hkv, N).groups;
   }
   DeviceInfo* dev;
+  // Records are counted in 31 bits.
+  if (static_cast<long long>(num_blocks) * Hkv >= 0x7fffffffLL)
+    return fail(ATTN_ERR_UNSUPPORTED, "KV pool too large (num_blocks * Hkv >= 2^31)");
   const attn_status_t st = check_quantised_attention(8, 0, decode, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv,
                                                      N, d, block_size, max_blocks_per_seq, num_blocks, scale, o, lse,
                                                      workspace, workspace_bytes, need, passes, &dev);
@@ -902,6 +919,10 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
   fill_quantised_decode(a, *dev, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, d, max_blocks_per_seq, num_blocks,
                         scale, o, lse, workspace, stream);
   a.N = N;
+  alignas(64) CUtensorMap records;
+  const attn_status_t enc = encode_kv8(&records, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d, d / 4);
+  if (enc != ATTN_OK) return enc;
+  a.records = &records;
   return launch_result(attn47::launch_decode_kv8_sm103(a), what);
 }
 

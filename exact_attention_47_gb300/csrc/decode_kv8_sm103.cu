@@ -14,21 +14,26 @@
 // V^T P^T): the 16 slots of a block fill the MMA's rows, up to 8 query rows of a
 // KV head its columns; two column tiles make 16.  P^T changes operand layout with
 // movmatrix.  Which elements an MMA's columns of k are is free as long as both
-// operands agree, so a lane takes 16 neighbouring bytes of a row: K rows lane / 4
-// and lane / 4 + 8, V rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9 (c = lane % 4), whose
-// bytes are paired by token with byte permutations.
+// operands agree, and so is which token an MMA row is, so a lane takes
+// neighbouring bytes: with r = lane / 4 and c = lane % 4, D/4 of two K rows
+// (tokens of MMA rows r and r + 8) and D/8 of four V rows (those of MMA rows 2 c,
+// 2 c + 1, 2 c + 8, 2 c + 9), whose bytes are paired by token with byte
+// permutations.
 //
 // The N queries of a sequence (draft tokens: its last N tokens) are rows like the
 // heads that share a KV head, but for the keys they see: row i sees keys up to
 // L - N + i.  More than 16 rows go in several groups, each its own pass.
 //
 // Work split: see decode_split.cuh.  A warp streams the records of its blocks
-// through a ring of its own in shared memory with 16-byte asynchronous copies;
-// every lane copies just the bytes that it will use itself, so there is nothing
-// to wait for but its own copies, whatever the order of rows in the record, and
-// no bank conflict.
+// through a ring of its own in shared memory: the codes as one box of a tensor map
+// over the records, 128-byte lines with TMA's 128-byte swizzle (16-byte piece p of
+// line l at p ^ (l mod 8)), under which the loads above meet no bank twice; the
+// scales as 16 bytes more.  (Copied by the lanes themselves, 16 bytes each of just
+// what they use, 8 sequences of 30k .. 131k tokens took 79 us: a warp's scattered
+// 16-byte copies cost the memory pipe 21 passes where the bytes make 4.)
 #include <atomic>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "decode_kv8_sm103.h"
@@ -52,22 +57,26 @@ struct DecKv8Cfg {
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = D == 64 ? 6 : NT == 1 ? 3 : 4;
-  static constexpr int kStage = Rec::kOffTail + 16;
+  static constexpr int kStage = Rec::kOffTail;               // its scales are apart
   static constexpr int kRows = NT * 8;                       // rows of a piece
   static constexpr int kPitch = D + 4;                       // floats
   static constexpr int kPiece = kRows * kPitch * 4;
   static constexpr int kRing = kStages * kStage;             // per warp
   static constexpr int kOffFirst = kWarps * kRing;           // first pieces, one per warp
-  static constexpr int kOffMl = kOffFirst + kWarps * kPiece; // (max, sum): [warp][2][kRows]
+  static constexpr int kOffTails = kOffFirst + kWarps * kPiece;         // [warp][kStages][16]
+  static constexpr int kOffMl = kOffTails + kWarps * kStages * 16;      // (max, sum): [warp][2][kRows]
   static constexpr int kOffPlan = kOffMl + kWarps * 2 * kRows * 8;
   static constexpr int kOffSrc = kOffPlan + (3 * kPlan + 4) * 4;        // record addresses: [warp][2 batches of 32]
   static constexpr int kOffShared = kOffSrc + kWarps * 64 * 8;
-  static constexpr int kSmem = kOffShared + 2048 + 128;      // + alignment slack
+  static constexpr int kSmem = kOffShared + 3072 + 1024;     // + alignment slack
   static_assert(kRing >= kPiece, "a warp's last piece reuses its ring");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(kStages < 32, "the next batch of addresses is there in time");
+  static_assert(kStages < 32, "the next batch of records is there in time");
 };
-static_assert(sizeof(SplitShared) <= 2048, "shared control block");
+struct DecKv8Shared : SplitShared {
+  uint64_t full[16][8];
+};
+static_assert(sizeof(DecKv8Shared) <= 3072, "shared control block");
 
 struct DecKv8Params {
   const __nv_bfloat16* q;
@@ -104,13 +113,6 @@ struct DecKv8Costs {
   }
 };
 
-__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void load_bytes(uint32_t address, uint32_t (&r)[N]) {
   static_assert(N == 2 || N == 4, "");
@@ -123,48 +125,54 @@ __device__ __forceinline__ void load_bytes(uint32_t address, uint32_t (&r)[N]) {
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(address) : "memory");
 }
 
-// What a lane copies of a record, and where to: pieces of a warp's lanes side by
-// side in the stage.
+// Where a lane's bytes lie in a stage.
 template <int D>
-struct LanePieces {
-  static constexpr int kKPieces = D / 32;        // of 16 bytes: 2 rows, D / 64 in each
-  static constexpr int kVBytes = D / 8;          // of each of 4 rows
-  uint32_t k, v;                                 // offsets in a record
-  __device__ __forceinline__ explicit LanePieces(int lane) {
-    const int r = lane >> 2, c = lane & 3;
-    k = static_cast<uint32_t>(r * D + 16 * c);
-    v = static_cast<uint32_t>(Kv8Layout<D>::kOffV + 2 * c * D + r * kVBytes);
-  }
-  // Piece i < kKPieces: row r + 8 (i / (D / 64)), bytes 64 (i % (D / 64)) + 16 c.
-  static __device__ __forceinline__ uint32_t k_step(int i) { return 8 * D * (i / (D / 64)) + 64 * (i % (D / 64)); }
-  // Row 2 c + (i & 1) + 8 (i >> 1).
-  static __device__ __forceinline__ uint32_t v_step(int i) { return (i & 1) * D + (i >> 1) * 8 * D; }
-  __device__ __forceinline__ void copy(uint32_t stage, const uint8_t* rec, int lane, uint64_t policy) const {
+struct LaneData {
+  static constexpr int kVBytes = D / 8;          // of a V row
+  uint32_t k[D / 64];                            // 16-byte pieces of MMA row r's K row; r + 8's lie k_next() on
+  uint32_t v[2];                                 // V rows of MMA rows 2 c and 2 c + 1; 8 more, v_next() on
+  int slot, slot_v;                              // slot of MMA row r (of r + 8: kNext more), of V row 2 c
+  // D = 128: a line is a row, an MMA row is its slot.  A K load's 8 lanes at a time
+  // are pieces 2 c + j of two neighbouring rows, a V load's are pieces r of rows
+  // 2 c: all eight places each.  D = 64: a line is two rows; MMA rows 2 c, 2 c + 1,
+  // 2 c + 8, 2 c + 9 are slots 4 c .. 4 c + 3, so that the V rows of a load lie in
+  // every other line.
+  static constexpr int kNext = D == 128 ? 8 : 2;
+  __device__ __forceinline__ explicit LaneData(int lane) {
+    const uint32_t r = static_cast<uint32_t>(lane) >> 2, c = static_cast<uint32_t>(lane) & 3u;
+    if constexpr (D == 128) {
+      slot = static_cast<int>(r);
+      slot_v = static_cast<int>(2 * c);
 #pragma unroll
-    for (int i = 0; i < kKPieces; ++i) cp_async16_hint(stage + 512 * i + 16 * lane, rec + k + k_step(i), policy);
+      for (uint32_t j = 0; j < D / 64; ++j) k[j] = 128 * r + 16 * ((2 * c + j) ^ r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t dst = stage + 16 * D + 32 * kVBytes * i + kVBytes * lane;
-      if constexpr (kVBytes == 16)
-        cp_async16_hint(dst, rec + v + v_step(i), policy);
-      else
-        cp_async8(dst, rec + v + v_step(i));
+      for (uint32_t i = 0; i < 2; ++i) v[i] = 16 * D + 128 * (2 * c + i) + 16 * (r ^ (2 * c + i));
+    } else {
+      slot = static_cast<int>(4 * (r >> 1) + (r & 1));
+      slot_v = static_cast<int>(4 * c);
+      const uint32_t line = 2 * (r >> 1);
+      k[0] = 128 * line + 16 * ((4 * (r & 1) + c) ^ line);
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) v[i] = 16 * D + 128 * (2 * c) + 16 * ((4 * i + (r >> 1)) ^ (2 * c)) + 8 * (r & 1);
     }
-    if (lane == 0) cp_async16_hint(stage + Kv8Layout<D>::kOffTail, rec + Kv8Layout<D>::kOffTail, policy);
   }
+  // From MMA row r to r + 8: D = 128: 8 lines on, the same place; D = 64: the next
+  // line, whose number ends in 1 instead of 0.
+  __device__ __forceinline__ uint32_t k_next(int j) const { return D == 128 ? k[j] + 8 * 128 : (k[j] + 128) ^ 16u; }
+  __device__ __forceinline__ uint32_t v_next(int i) const { return D == 128 ? v[i] + 8 * 128 : (v[i] + 128) ^ 16u; }
 };
 
 // Queries of one run as B operands, and what undoes their scaling.
 template <int D, int NT>
 struct QueryFrag {
-  uint32_t b[NT][D / 16][2];       // elements 64 j + 16 c + 4 i + {0, 1}, {2, 3} of row lane / 4 for MMA 4 j + i
+  uint32_t b[NT][D / 16][2];       // elements D/4 c + 4 i + {0, 1}, {2, 3} of row lane / 4 for MMA i
   float back[NT][2];               // score factor of rows 2 c, 2 c + 1
   int behind[NT][2];               // how many of the sequence's last keys those rows do not see
 };
 
 template <int D, int NT>
 struct QueryRaw {
-  uint4 w[NT][D / 64][2];
+  uint4 w[NT][D / 32];
   __device__ __forceinline__ void load(const DecKv8Params& p, int b, int g, int lane) {
     const int rows = p.rows_of(g);
     const __nv_bfloat16* first = p.q + p.row0(b, g) * D;
@@ -172,12 +180,10 @@ struct QueryRaw {
     for (int nt = 0; nt < NT; ++nt) {
       const int row = nt * 8 + (lane >> 2);
       const bool live = row < rows;
-      const uint4* src = reinterpret_cast<const uint4*>(first + static_cast<size_t>(live ? row : 0) * D) + 2 * (lane & 3);
+      const uint4* src = reinterpret_cast<const uint4*>(first + static_cast<size_t>(live ? row : 0) * D) +
+                         D / 32 * (lane & 3);
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        w[nt][j][0] = live ? src[8 * j] : make_uint4(0u, 0u, 0u, 0u);
-        w[nt][j][1] = live ? src[8 * j + 1] : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int j = 0; j < D / 32; ++j) w[nt][j] = live ? src[j] : make_uint4(0u, 0u, 0u, 0u);
     }
   }
 };
@@ -191,15 +197,13 @@ __device__ __forceinline__ void make_queries(const DecKv8Params& p, const QueryR
   for (int nt = 0; nt < NT; ++nt) {
     uint32_t raw[D / 16][2];
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 x = all.w[nt][j][h];
-        raw[4 * j + 2 * h][0] = x.x;
-        raw[4 * j + 2 * h][1] = x.y;
-        raw[4 * j + 2 * h + 1][0] = x.z;
-        raw[4 * j + 2 * h + 1][1] = x.w;
-      }
+    for (int j = 0; j < D / 32; ++j) {
+      const uint4 x = all.w[nt][j];
+      raw[2 * j][0] = x.x;
+      raw[2 * j][1] = x.y;
+      raw[2 * j + 1][0] = x.z;
+      raw[2 * j + 1][1] = x.w;
+    }
     uint32_t mx = 0;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
@@ -291,26 +295,23 @@ struct RunState {
   __device__ __forceinline__ float at(int nt, int k, int h) const { return o[nt][k >> 1][(k & 1) * 2 + h]; }
 };
 
-// One block of a run, 16 slots, in a stage of the ring; `valid` tokens from the
+// One block of a run, 16 slots, in a stage of the ring, its scales at `tail_at`; `valid` tokens from the
 // block's first slot to the sequence's end (16 or more: all slots hold tokens; 0
 // or less: none, whatever the stage holds), `least` of them seen by every row.
 template <int D, int NT>
-__device__ __forceinline__ void take_block(uint32_t stage, int valid, int least, int lane, const QueryFrag<D, NT>& q,
-                                           RunState<D, NT>& st) {
-  using Rec = Kv8Layout<D>;
-  using Lp = LanePieces<D>;
-  constexpr int kHalf = D / 64;                  // 16-byte pieces of a K row in a lane
-  const int r = lane >> 2, c = lane & 3;
+__device__ __forceinline__ void take_block(const LaneData<D>& at, uint32_t stage, uint32_t tail_at, int valid, int least,
+                                           const QueryFrag<D, NT>& q, RunState<D, NT>& st) {
+  using Ld = LaneData<D>;
 
   // --- S^T: rows = slots, columns = query rows
   float s[NT][4];
   {
     float even[NT][4], odd[NT][4];
 #pragma unroll
-    for (int j = 0; j < kHalf; ++j) {
+    for (int j = 0; j < D / 64; ++j) {
       uint32_t a[4], b[4];
-      load_bytes(stage + 512 * j + 16 * lane, a);
-      load_bytes(stage + 512 * (kHalf + j) + 16 * lane, b);
+      load_bytes(stage + at.k[j], a);
+      load_bytes(stage + at.k_next(j), b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t a0 = e4m3x2_to_f16x2(a[i]), a1 = e4m3x2_to_f16x2(b[i]), a2 = e4m3x2_hi_to_f16x2(a[i]),
@@ -332,7 +333,7 @@ __device__ __forceinline__ void take_block(uint32_t stage, int valid, int least,
   }
 
   uint32_t tail[4];
-  load_bytes(stage + Rec::kOffTail, tail);
+  load_bytes(tail_at, tail);
   const float scale_k = __uint_as_float(tail[0]);
   float scale_v = __uint_as_float(tail[1]);
 #pragma unroll
@@ -343,9 +344,9 @@ __device__ __forceinline__ void take_block(uint32_t stage, int valid, int least,
     s[nt][2] *= f0;
     s[nt][3] *= f1;
   }
-  uint32_t v[4][Lp::kVBytes / 4];
+  uint32_t v[4][Ld::kVBytes / 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load_bytes(stage + 16 * D + 32 * Lp::kVBytes * i + Lp::kVBytes * lane, v[i]);
+  for (int i = 0; i < 4; ++i) load_bytes(stage + (i < 2 ? at.v[i & 1] : at.v_next(i & 1)), v[i]);
 
   if (least < kBS || tail[2] != 0) {             // (the same for the whole warp)
     // Slots that a row does not see have no score, those past the end no value;
@@ -356,7 +357,7 @@ __device__ __forceinline__ void take_block(uint32_t stage, int valid, int least,
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int slot = r + (i >> 1) * 8;
+        const int slot = at.slot + (i >> 1) * Ld::kNext;
         if (slot >= valid - q.behind[nt][i & 1])
           s[nt][i] = -INFINITY;
         else if ((bad >> slot) & 1u)
@@ -364,10 +365,10 @@ __device__ __forceinline__ void take_block(uint32_t stage, int valid, int least,
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int slot = 2 * c + (i & 1) + (i >> 1) * 8;
+      const int slot = at.slot_v + (i & 1) + (i >> 1) * Ld::kNext;
       if (slot >= valid || ((bad >> slot) & 1u)) {
 #pragma unroll
-        for (int w = 0; w < Lp::kVBytes / 4; ++w) v[i][w] = 0;
+        for (int w = 0; w < Ld::kVBytes / 4; ++w) v[i][w] = 0;
       }
     }
   }
@@ -396,7 +397,7 @@ __device__ __forceinline__ void take_block(uint32_t stage, int valid, int least,
   }
   const uint64_t sv = f2_pack(scale_v, scale_v);
 #pragma unroll
-  for (int w = 0; w < Lp::kVBytes / 4; ++w) {
+  for (int w = 0; w < Ld::kVBytes / 4; ++w) {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const uint32_t sel = hf ? 0x7362u : 0x5140u;           // (token, next token) of two elements
@@ -419,13 +420,13 @@ __device__ __forceinline__ void take_block(uint32_t stage, int valid, int least,
 
 template <int D, int NT>
 __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
-    attn_decode_kv8_kernel(const __grid_constant__ DecKv8Params p) {
+    attn_decode_kv8_kernel(const __grid_constant__ CUtensorMap records, const __grid_constant__ DecKv8Params p) {
   using Cfg = DecKv8Cfg<D, NT>;
   using Rec = Kv8Layout<D>;
   constexpr int kWarps = Cfg::kWarps, kStages = Cfg::kStages, kRows = Cfg::kRows;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
-  SplitShared* sh = reinterpret_cast<SplitShared*>(smem + Cfg::kOffShared);
+  uint8_t* smem = smem_align1024(smem_raw);
+  DecKv8Shared* sh = reinterpret_cast<DecKv8Shared*>(smem + Cfg::kOffShared);
   int* cost = reinterpret_cast<int*>(smem + Cfg::kOffPlan);             // [kPlan + 1]
   int* runs = cost + kPlan + 2;                                         // [kPlan + 1]
   int* seq_blocks = runs + kPlan + 2;                                   // [kPlan]
@@ -438,9 +439,14 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
     sh->part_n[0] = sh->part_n[1] = 0;
     sh->abort = 0;
   }
-  if (lane == 0) mbar_init(smem_addr(&sh->ready[warp]), 1);
+  static_assert(kStages <= 8, "");
+  if (lane < kStages) mbar_init(smem_addr(&sh->full[warp][lane]), 1);
+  if (lane == kStages) mbar_init(smem_addr(&sh->ready[warp]), 1);
   fence_mbar_init();
-  if (tid == 0) prefetch_inputs<D>(p);
+  if (tid == 0) {
+    prefetch_tmap(&records);
+    prefetch_inputs<D>(p);
+  }
   // With the early plan, seq_lens and the block table are read before the
   // preceding kernel has finished; the queries, the cache and everything that
   // is written come after the wait further down.
@@ -460,23 +466,23 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
     QueryRaw<D, NT> raw;
     if (!p.early_plan) raw.load(p, w.at.b, w.at.g, lane);
     // Lane j looks up block j of every batch of 32, two batches ahead, and
-    // leaves its record's address for the warp (0: not in the pool).  Returns the
-    // batch's mask of blocks that have a record.
+    // leaves its record's number for the issuing lane (-1: not in the pool).
+    // Returns the batch's mask of blocks that have a record.
     Walk ahead = w;
     ahead.skip(p, plan, lane);
-    const uint8_t** src = reinterpret_cast<const uint8_t**>(smem + Cfg::kOffSrc) + warp * 64;
+    int* src = reinterpret_cast<int*>(smem + Cfg::kOffSrc) + warp * 64;
     auto fetch = [&](int batch) {
-      const uint8_t* rec = nullptr;
+      int rec = -1;
       if (ahead.left > 0) {
         const int ph = p.block_table[static_cast<size_t>(ahead.at.b) * p.max_blocks + ahead.at.blk];
         if (static_cast<unsigned>(ph) < static_cast<unsigned>(p.num_blocks))
-          rec = p.kv_cache + (static_cast<size_t>(ph) * p.kv_heads + ahead.at.g / p.groups) * Rec::kBytes;
+          rec = ph * p.kv_heads + ahead.at.g / p.groups;
         else
           atomicOr(p.status, kDevBadBlock);      // outside the pool: that block is skipped
       }
       ahead.skip(p, plan, 32);
       src[(batch & 1) * 32 + lane] = rec;
-      return __ballot_sync(0xffffffffu, rec != nullptr);
+      return __ballot_sync(0xffffffffu, rec >= 0);
     };
     const uint64_t policy = l2_policy_evict_first();
     unsigned present = fetch(0);
@@ -486,19 +492,22 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
     }
     __syncwarp();
     const uint32_t ring_at = smem_addr(smem + warp * Cfg::kRing);
-    const LanePieces<D> pieces(lane);
+    const uint32_t tails = smem_addr(smem + Cfg::kOffTails) + warp * kStages * 16;
+    const uint32_t bars = smem_addr(&sh->full[warp][0]);
+    const LaneData<D> at(lane);
     // Block i of the share goes to stage i % kStages; blocks [0, taken + kStages)
-    // are issued, a group of copies each (empty for those without a record and
-    // past the end, so that the groups can be counted).
+    // are issued.  (One lane.)
     auto issue = [&](int i, int stage) {
-      if (i < blocks) {
-        const uint8_t* from = src[i & 63];
-        if (from != nullptr) pieces.copy(ring_at + stage * Cfg::kStage, from, lane, policy);
+      const int rec = src[i & 63];
+      const uint32_t bar = bars + stage * 8;
+      mbar_arrive_expect_tx(bar, rec >= 0 ? Cfg::kStage + 16 : 0);
+      if (rec >= 0) {
+        tma_load_3d_hint(ring_at + stage * Cfg::kStage, &records, bar, 0, 0, rec, policy);
+        bulk_load_hint(tails + stage * 16, p.kv_cache + static_cast<size_t>(rec) * Rec::kBytes + Rec::kOffTail, 16, bar,
+                       policy);
       }
-      cp_async_commit();
     };
-#pragma unroll 1
-    for (int i = 0; i < kStages; ++i) issue(i, i);
+    if (lane < min(blocks, kStages)) issue(lane, lane);
     unsigned next_present = blocks > 32 ? fetch(1) : 0u;
     __syncwarp();
     announce_parts<kWarps>(p, plan, sh, share);
@@ -506,20 +515,27 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
     QueryFrag<D, NT> q;
     RunState<D, NT> st;
     int taken = 0, stage = 0;
-    while (w.left > 0) {
+    uint32_t parity = 0;
+    bool fail = false;
+    while (w.left > 0 && !fail) {
       const int cnt = w.count();
       int valid = seq_len_of(p, w.at.b) - w.at.blk * kBS;       // tokens from this block on
       if (taken > 0) raw.load(p, w.at.b, w.at.g, lane);
       make_queries<D, NT>(p, raw, w.at.g, lane, q);
       st.reset();
       for (const int end = taken + cnt; taken < end; ++taken) {
-        cp_async_wait_group<kStages - 1>();
-        __syncwarp();                            // (the record's last bytes are lane 0's copy)
+        if (!wait_warp(bars + stage * 8, parity, wc)) {
+          fail = true;
+          break;
+        }
         const int alive = (present >> (taken & 31)) & 1u ? valid : 0;
-        take_block<D, NT>(ring_at + stage * Cfg::kStage, alive, alive - (p.N - 1), lane, q, st);
+        take_block<D, NT>(at, ring_at + stage * Cfg::kStage, tails + stage * 16, alive, alive - (p.N - 1), q, st);
         __syncwarp();                            // every lane has read the stage
-        issue(taken + kStages, stage);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (lane == 0 && taken + kStages < blocks) issue(taken + kStages, stage);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
         valid -= kBS;
         if ((taken & 31) == 31) {                // (what is issued is less than a batch ahead)
           present = next_present;
@@ -527,6 +543,7 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
           __syncwarp();
         }
       }
+      if (fail) break;
       st.finish();
       const bool has_start = w.at.blk == 0, has_end = w.at.blk + cnt == w.at.nblk;
       const int c = lane & 3, r = lane >> 2;
@@ -539,7 +556,10 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
       const longlong2 reach = sh->reach[warp];
       const bool to_previous = has_end && !has_start && warp > 0 && run0 >= reach.x;
       if (has_start && !has_end && warp + 1 < kWarps && run1 <= reach.y) {
-        if (!wait_warp(smem_addr(&sh->ready[warp + 1]), 0, wc)) break;   // (it was the share's last run)
+        if (!wait_warp(smem_addr(&sh->ready[warp + 1]), 0, wc)) {
+          fail = true;
+          break;
+        }
         const float* from = first_piece(warp + 1) + r * (D / 8);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -622,7 +642,14 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
       }
       w.next_run(p, plan, cnt);
     }
-    cp_async_wait_all();                         // (groups without copies)
+    if (fail) {
+      // Copies in flight must land before the CTA may exit.
+      for (int s = 0; s < kStages; ++s) {
+        const int issued = min(blocks, taken + kStages);
+        const int fills = issued / kStages + (s < issued % kStages ? 1 : 0);
+        if (fills > 0) mbar_wait_warp_drain(bars + s * 8, static_cast<uint32_t>((fills - 1) & 1), wc);
+      }
+    }
   }
   if (p.early_plan) pdl_wait_primary();          // (warps without work)
   if (lane == 0) sh->meta[warp] = meta;
@@ -670,7 +697,7 @@ cudaError_t launch_t(const DecKv8Launch& a, const Kv8Rows& rows) {
   p.timeout_ns = a.timeout_ns;
   int ctas = a.sms < 1 ? 1 : a.sms > kMaxCtas ? kMaxCtas : a.sms;
   if (a.max_ctas > 0 && ctas > a.max_ctas) ctas = a.max_ctas;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(Cfg::kThreads), Cfg::kSmem, a.stream, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(Cfg::kThreads), Cfg::kSmem, a.stream, *a.records, p);
 }
 
 }  // namespace

@@ -2,12 +2,15 @@
 // part of the C-ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace attn47 {
 
 struct DecKv8Launch {
   const void* q;               // [S, Hq, N, d] bf16
+  const CUtensorMap* records;  // the records' codes: bytes [num_blocks Hkv][d / 4 lines][128], a record to a box,
+                               // 128-byte swizzle
   const void* kv_cache;        // [num_blocks, Hkv, record] bytes
   const int* block_table;      // [S, max_blocks] int32
   const int* seq_lens;         // [S] int32
