@@ -894,6 +894,10 @@ attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records,
   return ATTN_OK;
 }
 
+// Whether queries go in tiles of 128 rows (the tensor cores' work) or by passes of
+// up to 16 rows over the blocks (the memory's).
+bool kv8_in_tiles(int Hq, int Hkv, int N) { return Hq / Hkv * N > 32; }
+
 // Both attentions over an 8-bit cache.
 attn_status_t attend_kv8(const char* what, bool decode, const void* q, const void* kv_cache, const int32_t* block_table,
                          const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d, int block_size,
@@ -901,11 +905,15 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
                          size_t workspace_bytes, void* stream) {
   size_t need = 0;
   int passes = 1;
+  bool tiles = false;
   if (Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && N > 0) {
-    if (static_cast<long long>(Hq / Hkv) * N >= 0x7fffffffLL)
+    if (static_cast<long long>(Hq / Hkv) * N >= 0x7fffff00LL)
       return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
-    need = attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
-    passes = attn47::decode_kv8_rows(Hq, Hkv, N).groups;
+    tiles = !decode && kv8_in_tiles(Hq, Hkv, N);
+    if (!tiles) {
+      need = attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
+      passes = attn47::decode_kv8_rows(Hq, Hkv, N).groups;
+    }
   }
   DeviceInfo* dev;
   // Records are counted in 31 bits.
@@ -915,6 +923,43 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
                                                      N, d, block_size, max_blocks_per_seq, num_blocks, scale, o, lse,
                                                      workspace, workspace_bytes, need, passes, &dev);
   if (st != ATTN_OK || dev == nullptr) return st;
+  if (tiles) {
+    // The heads of a group in one row of query blocks where N is short.
+    const bool packed = N < 2 * attn47::fwd_box_rows();
+    const int heads = packed ? Hkv : Hq, rows = packed ? Hq / Hkv * N : N;
+    const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(attn47::fwd_box_rows()), 1};
+    const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                                 static_cast<cuuint64_t>(num_seqs) * heads};
+    alignas(64) CUtensorMap tq, blocks;
+    attn_status_t enc = encode_bf16(&tq, q, 3, qdims, qbox);
+    if (enc == ATTN_OK) enc = encode_kv8(&blocks, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d, d / 8);
+    if (enc != ATTN_OK) return enc;
+    attn47::FwdLaunch f;
+    f.tq = &tq;
+    f.tk = &blocks;
+    f.tv = &blocks;   // (not used)
+    f.o = o;
+    f.lse = lse;
+    f.B = num_seqs;
+    f.Hq = heads;
+    f.Hkv = Hkv;
+    f.N = rows;
+    f.d = d;
+    f.causal = true;
+    f.scale = scale;
+    f.sms = dev->sms;
+    f.status = dev->status;
+    f.timeout_ns = g_timeout_ns;
+    f.stream = static_cast<cudaStream_t>(stream);
+    f.paged = true;
+    f.block_table = block_table;
+    f.ctx_lens = seq_lens;
+    f.max_blocks = max_blocks_per_seq;
+    f.num_blocks = num_blocks;
+    f.kv_cache = kv_cache;
+    f.rows = N;
+    return launch_result(attn47::launch_fwd_sm103(f), what);
+  }
   attn47::DecKv8Launch a;
   fill_quantised_decode(a, *dev, q, kv_cache, block_table, seq_lens, num_seqs, Hq, Hkv, d, max_blocks_per_seq, num_blocks,
                         scale, o, lse, workspace, stream);
@@ -1596,7 +1641,9 @@ attn_status_t attn_decode_paged_kv8(const void* q, const void* kv_cache, const i
 }
 
 size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int N, int d) {
-  if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
+  if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0 || Hq % Hkv != 0 ||
+      static_cast<long long>(Hq / Hkv) * N >= 0x7fffff00LL || kv8_in_tiles(Hq, Hkv, N))
+    return 0;
   return attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
 }
 

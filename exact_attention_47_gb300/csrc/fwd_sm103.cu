@@ -53,9 +53,27 @@
 // ctx_b + its query block's first row, so units are walked in decreasing
 // order of that key (every CTA ranks the (sequence, query block) pairs the
 // same way at start-up) instead of query block by query block.
+//
+// Paged mode over an 8-bit cache (kPagedKv8): the same, but the cache holds the
+// new tokens already, sequence b's row i is the token at position seq_lens[b] -
+// N + i (before position 0 it sees nothing: O = 0, LSE = -inf), and the gather
+// turns codes into bf16 on the way.  The records' codes come by TMA into a small
+// ring of raw blocks (128-byte swizzle), from there a warp takes 16 codes a lane,
+// spreads them to bf16 with their exponents 120 too low (sign, 4 bits of exponent
+// and 3 of fraction fit where they are), multiplies by 2^120 times the block's
+// scale (both powers of two: exact, e4m3's subnormal numbers too) and stores them
+// into the swizzled tile.  So the tile holds the very numbers that the codes stand
+// for, and nothing else in the kernel changes.  It is kGather warps to an operand,
+// in a fourth warpgroup.  A code that is NaN becomes a finite number there; the
+// records' flags say which tokens have one, the gather keeps the first position of
+// such a token, and a row that sees that position gets NaN in the epilogue.
+// With fewer than 256 new tokens the rows of all query heads that share a KV head
+// make one row of query blocks (row = head in the group times N + token), so that
+// a 256-row unit is not mostly empty.
 #include <cuda_runtime.h>
 
 #include "fwd_sm103.h"
+#include "kv8.cuh"
 #include "ptx.cuh"
 
 namespace attn47 {
@@ -65,25 +83,30 @@ constexpr int kBM = 128;            // rows per query tile (= TMEM lanes)
 constexpr int kBN = 128;            // keys per K/V tile
 constexpr int kTiles = 2;           // query tiles per CTA
 constexpr int kRowsPerCta = kBM * kTiles;
-constexpr int kThreads = 384;       // 2 softmax warpgroups + 1 producer/MMA warpgroup
+// 2 softmax warpgroups + 1 producer/MMA warpgroup (+ 1 for the gather of an 8-bit cache)
+enum Source { kContiguous, kPagedBf16, kPagedKv8 };
+__host__ __device__ constexpr int threads_of(int source) { return source == kPagedKv8 ? 512 : 384; }
 constexpr int kWarpLoad = 8;
 constexpr int kWarpMma = 9;
 // Launched at 168 registers a thread (384 x 168 = 64512); the softmax
 // warpgroups then take 216 and the producer/MMA warpgroup keeps 72:
 // 256 x 216 + 128 x 72 = 64512, and per sub-partition 216 + 216 + 72 = 504
 // = 3 x 168, so the increase never waits for registers nobody frees.
-constexpr uint32_t kRegsSoftmax = 216;
-constexpr uint32_t kRegsOther = 72;
+// With the gather's warpgroup: 512 at 128 registers, 256 x 208 + 256 x 48 = 65536.
+__host__ __device__ constexpr uint32_t regs_softmax(int source) { return source == kPagedKv8 ? 208 : 216; }
+__host__ __device__ constexpr uint32_t regs_other(int source) { return source == kPagedKv8 ? 48 : 72; }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
+
+constexpr int kGather = 2;          // 8-bit cache: gather warps to an operand
 
 // SUMV (d = 64 with contiguous K/V): the row sums of P come from the tensor
 // core.  Every V stage gets a second 64-column chunk, written once, whose
 // first column is all ones, and P V runs with N = d + 16: columns d .. d+15
 // of O_X then hold P times that column, the row sums of the bf16 P that P V
 // uses, at no extra MMA instruction (three stages instead of four make room).
-template <int D, bool SUMV = false>
+template <int D, bool SUMV = false, int SOURCE = kContiguous>
 struct FwdLayout {
   static constexpr int kChunks = D / 64;                 // 128-byte swizzle atoms per row
   static constexpr int kStages = (D == 128) ? 2 : SUMV ? 3 : 4;
@@ -99,7 +122,11 @@ struct FwdLayout {
   static constexpr int kOffBar = kOffV + kStages * kVStage;
   static constexpr int kOffCtx = kOffBar + 512;          // paged: ctx_b of each sequence
   static constexpr int kOffOrder = kOffCtx + 4 * 256;    // paged: (b << 16 | qblk) of each cost rank
-  static constexpr int kSmem = kOffOrder + 4 * 2048 + 1024;   // + alignment slack
+  // 8-bit cache: raw blocks (a K or V half of a record) of each gather warp.
+  static constexpr int kRawStages = SOURCE == kPagedKv8 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kRaw = 16 * D;
+  static constexpr int kOffRaw = (kOffOrder + 4 * 2048 + 1023) / 1024 * 1024;
+  static constexpr int kSmem = kOffRaw + 2 * kGather * kRawStages * kRaw + 1024;   // + alignment slack
   static constexpr uint32_t kColS0 = 0, kColS1 = 128;
   static constexpr uint32_t kColO0 = 256, kColO1 = SUMV ? 384 : 256 + D;
 };
@@ -110,9 +137,15 @@ struct FwdBarriers {
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t o_free[2];                 // O_X read out by the epilogue of the previous unit
   uint64_t mma_final;
+  uint64_t raw_full[2 * kGather][4];  // 8-bit cache: raw block x of a gather warp has come
   uint32_t tmem_base;
   int abort;
+  // 8-bit cache: the first position of a flagged token of unit u (of the CTA's), as
+  // each K gather warp has found it, at u % 8: a gather is at most kStages tiles
+  // ahead of the MMAs, and those at most a unit ahead of the epilogue.
+  int first_flagged[kGather][8];
 };
+static_assert(sizeof(FwdBarriers) <= 512, "room in the layout");
 
 struct FwdParams {
   void* o;
@@ -128,6 +161,12 @@ struct FwdParams {
   const int* ctx_lens;      // [B] tokens cached before the N new ones
   int max_blocks, num_blocks;
   int max_ctx;              // max_blocks * 16 - N: largest valid ctx_lens entry
+  // 8-bit cache: ctx_lens are the sequences' lengths, new tokens included; a
+  // "query head" is a KV head's whole group where `rows` tokens are fewer than 256
+  // (then N is group * rows, and row r is token r % rows).
+  const uint8_t* kv_cache;
+  int rows;
+  bool packed;
 };
 
 // Cost ordering of the paged mode fits in shared memory up to these sizes
@@ -139,14 +178,27 @@ constexpr int kPageRows = 16;                        // token slots per cache bl
 constexpr int kPagesPerTile = kBN / kPageRows;
 constexpr int kWarpGatherK = 10;                     // paged mode: K / V gather warps
 constexpr int kWarpGatherV = 11;
+constexpr int kWarpGather8 = 12;                     // of an 8-bit cache: K, V, K, V
+static_assert(kGather == 2, "the gather's warpgroup");
 
-template <int D, bool CAUSAL, bool PAGED, bool SORTED>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <int D, bool CAUSAL, int SOURCE, bool SORTED>
+__global__ void __launch_bounds__(threads_of(SOURCE), 1)
     attn_fwd_sm103_kernel(const __grid_constant__ CUtensorMap tq,
                           const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const FwdParams p) {
+  constexpr bool PAGED = SOURCE != kContiguous, KV8 = SOURCE == kPagedKv8;
+  constexpr int kThreads = threads_of(SOURCE);
   constexpr bool SUMV = D == 64 && !PAGED;
-  using L = FwdLayout<D, SUMV>;
+  using L = FwdLayout<D, SUMV, SOURCE>;
   extern __shared__ uint8_t smem_raw[];
   // Aligned through an integer round trip (the pointer becomes generic):
   // measured faster for this kernel than smem_align1024.
@@ -193,7 +245,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     u.b = bh / p.Hq;
     u.kvh = (bh % p.Hq) / p.group;
     u.zkv = u.b * p.Hkv + u.kvh;
-    if constexpr (PAGED) {
+    if constexpr (KV8) {
+      const int len = min(max(__ldg(p.ctx_lens + u.b), 0), p.max_blocks * kPageRows);
+      u.pos0 = len - p.rows;                           // (negative: rows that see nothing)
+      // The last token among rows r0 .. r1 (packed: they may span heads).
+      auto last = [&](int r0, int r1) {
+        r1 = min(r1, p.N - 1);
+        const int i0 = r0 % p.rows;
+        return i0 + r1 - r0 >= p.rows ? p.rows - 1 : i0 + r1 - r0;
+      };
+      const int r0 = u.qblk * kRowsPerCta;
+      const int lastA = last(r0, r0 + kBM - 1), lastB = r0 + kBM < p.N ? last(r0 + kBM, r0 + 2 * kBM - 1) : lastA;
+      u.nA = max(u.pos0 + lastA, 0) / kBN + 1;
+      u.nB = max(max(u.pos0 + lastB, 0) / kBN + 1, u.nA);
+      u.nblk = (len + kPageRows - 1) / kPageRows;
+    } else if constexpr (PAGED) {
       // A ctx_lens entry outside [0, max_ctx] was reported by the append
       // kernel; it is clamped here so every loop stays bounded.
       u.pos0 = min(max(__ldg(p.ctx_lens + u.b), 0), p.max_ctx);
@@ -220,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < L::kStages; ++s) {
       // Paged: every lane of a gather warp arrives once its copies landed.
-      mbar_init(smem_addr(&bar->k_full[s]), PAGED ? 32 : 1);
-      mbar_init(smem_addr(&bar->v_full[s]), PAGED ? 32 : 1);
+      mbar_init(smem_addr(&bar->k_full[s]), KV8 ? 32 * kGather : PAGED ? 32 : 1);
+      mbar_init(smem_addr(&bar->v_full[s]), KV8 ? 32 * kGather : PAGED ? 32 : 1);
       mbar_init(smem_addr(&bar->k_empty[s]), 1);
       mbar_init(smem_addr(&bar->v_empty[s]), 1);
     }
@@ -231,6 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&bar->o_done[x]), 1);
     }
     mbar_init(smem_addr(&bar->mma_final), 1);
+    if constexpr (KV8) {
+      for (int x = 0; x < 2 * kGather * 4; ++x) mbar_init(smem_addr(&bar->raw_full[0][0] + x), 1);
+    }
     bar->abort = 0;
     fence_mbar_init();
   }
@@ -254,6 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of the kernel before this one in the stream; nothing in global memory
   // is read or written before that kernel has finished.
   pdl_wait_primary();
+  if constexpr (KV8) {
+    // (The append reports bad lengths for a bf16 cache; this call has none.)
+    if (cta == 0) {
+      bool bad = false;
+      for (int b = threadIdx.x; b < p.bh_total / p.Hq; b += kThreads) {
+        const int len = __ldg(p.ctx_lens + b);
+        bad |= len < 0 || len > p.max_blocks * kPageRows;
+      }
+      if (bad) atomicOr(p.status, kDevBadSeqLen);
+    }
+  }
   if constexpr (SORTED) {
     {
       // Cost key of pair (b, qblk): ctx_b + 256 * qblk (the K/V tiles of the
@@ -262,12 +342,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int S = p.bh_total / p.Hq;
       const int nq = p.num_q_blocks;
       int* ctx_w = reinterpret_cast<int*>(smem + L::kOffCtx);
-      for (int b = threadIdx.x; b < S; b += kThreads) ctx_w[b] = min(max(__ldg(p.ctx_lens + b), 0), p.max_ctx);
+      for (int b = threadIdx.x; b < S; b += kThreads)
+        ctx_w[b] = min(max(__ldg(p.ctx_lens + b), 0), KV8 ? p.max_blocks * kPageRows : p.max_ctx);
       __syncthreads();
       int* order_w = reinterpret_cast<int*>(smem + L::kOffOrder);
       for (int i = threadIdx.x; i < S * nq; i += kThreads) {
-        const int key = s_ctx[i / nq] + kRowsPerCta * (i % nq);
         int rank = 0;
+        if (KV8 && p.packed) {                     // all blocks of a sequence cost the same
+          const int key = s_ctx[i / nq];
+          for (int b = 0; b < S; ++b)
+            if (s_ctx[b] > key || (s_ctx[b] == key && b < i / nq)) rank += nq;
+          order_w[rank + i % nq] = ((i / nq) << 16) | (i % nq);
+          continue;
+        }
+        const int key = s_ctx[i / nq] + kRowsPerCta * (i % nq);
         for (int b = 0; b < S; ++b) {
           const int dk = key - s_ctx[b];
           if (dk < 0) {
@@ -288,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bar->tmem_base;
   const WaitCtl wc{&bar->abort, p.status, p.timeout_ns};
   if (warp >= 8) {
-  regs_decrease<kRegsOther>();
+  regs_decrease<regs_other(SOURCE)>();
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -508,7 +596,193 @@ __global__ void __launch_bounds__(kThreads, 1)
       __all_sync(0xffffffffu, mbar_wait(smem_addr(&bar->mma_final), 0, wc, true));
     }
   }
-  if constexpr (PAGED) {
+  if constexpr (KV8) {
+    if (warp >= kWarpGather8) {
+      // ------------------------------------- paged K / V gather, 8-bit records
+      const int me = warp - kWarpGather8;                      // even: K, odd: V
+      const bool is_v = me & 1;
+      const int part = me >> 1;
+      const uint32_t s_base = is_v ? sV : sK;
+      const uint32_t full0 = smem_addr(is_v ? &bar->v_full[0] : &bar->k_full[0]);
+      const uint32_t empty0 = smem_addr(is_v ? &bar->v_empty[0] : &bar->k_empty[0]);
+      const uint32_t raw = smem_addr(smem + L::kOffRaw) + me * L::kRawStages * L::kRaw;
+      const uint32_t raw_full = smem_addr(&bar->raw_full[me][0]);
+      constexpr int kMine = kPagesPerTile / kGather;           // blocks of a tile
+      constexpr int kRawStages = L::kRawStages;
+      static_assert(kRawStages <= kMine && kRawStages <= 4, "a raw block is at most a tile ahead");
+      // Lane i < kMine holds block part + kGather i of a tile.  Records are looked
+      // up two tiles ahead, their scales one tile ahead, raw blocks kRawStages
+      // blocks ahead.
+      int band = 0, j = 0, left = 0, nblk = 0, kvh = 0;        // of the tile to look up next
+      const int* row = nullptr;
+      auto open_unit = [&]() {
+        const int k = unit_at(band);
+        left = 0;
+        if (k >= p.num_units) return;
+        const Unit u = unit_info(k);
+        left = u.nB;
+        nblk = u.nblk;
+        kvh = u.kvh;
+        row = p.block_table + static_cast<size_t>(u.b) * p.max_blocks;
+        j = 0;
+      };
+      open_unit();
+      // A tile: its blocks' records (-1: none, read as zeros), whether it is there
+      // at all, whether it is its unit's last, and its number in the unit.
+      struct Tile {
+        int rec, number;
+        bool there, last;
+      };
+      auto look_up = [&]() {
+        Tile x;
+        x.rec = -1;
+        x.number = j;
+        x.there = left > 0;
+        x.last = left == 1;
+        if (!x.there) return x;
+        const int lb = j * kPagesPerTile + part + kGather * lane;
+        if (lane < kMine && lb < nblk) {
+          const int e = __ldg(row + lb);
+          if (static_cast<unsigned>(e) < static_cast<unsigned>(p.num_blocks))
+            x.rec = e * p.Hkv + kvh;
+          else
+            atomicOr(p.status, kDevBadBlock);                  // reported, read as zeros
+        }
+        ++j;
+        if (--left == 0) {
+          ++band;
+          open_unit();
+        }
+        return x;
+      };
+      auto tail_of = [&](const Tile& x) {                      // (K scale, V scale, flags)
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (x.rec >= 0)
+          v = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + static_cast<size_t>(x.rec) * Kv8Layout<D>::kBytes +
+                                                   Kv8Layout<D>::kOffTail));
+        return v;
+      };
+      int issued = 0;                                          // raw blocks asked for
+      uint32_t in_flight = 0;                                  // stages whose block has not been waited for
+      auto issue = [&](int rec) {
+        const int s = issued % kRawStages;
+        ++issued;
+        if (rec < 0) return;
+        in_flight |= 1u << s;
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(raw_full + 8u * s, L::kRaw);
+        tma_load_3d(raw + s * L::kRaw, &tk, raw_full + 8u * s, 0, is_v ? D / 8 : 0, rec);
+      };
+      // Completions of a raw stage's barrier (a block without a record makes none).
+      uint32_t phases = 0;
+      // 16 codes of a lane: those of 8 neighbouring lanes are the same columns of 8
+      // rows, which the swizzles spread over all banks, here and in the tile.
+      const int r = lane & 7, c = lane >> 3;
+      uint32_t raw_at[2 * (D / 64)], dst_at[2 * (D / 64)];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          const int slot = r + 8 * h, col = c + 4 * x, i = h * (D / 64) + x;
+          const int line = D == 128 ? slot : slot >> 1, piece = D == 128 ? col : 4 * (slot & 1) + col;
+          raw_at[i] = 128 * line + 16 * (piece ^ (line & 7));
+          // As bf16: 16-byte columns 2 col and 2 col + 1, 8 of them to a 128-byte row.
+          dst_at[i] = (col >> 2) * L::kKVChunk + slot * 128 + (((2 * col) & 7) ^ (slot & 7)) * 16;
+        }
+      auto convert = [&](uint32_t dst, uint32_t src, uint32_t scale) {
+        // 2^120 times the scale, in bf16 as two factors (2^127 is the largest).
+        const uint32_t field = (scale >> 23) + 120u;
+        const uint32_t f = (min(field, 254u) << 7) * 0x10001u;
+        const uint32_t f_more = (field > 254u ? (field - 254u + 127u) << 7 : 0x3f80u) * 0x10001u;
+#pragma unroll
+        for (int i = 0; i < 2 * (D / 64); ++i) {
+          uint32_t w[4], y[8];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(src + raw_at[i])
+                       : "memory");
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t x = __byte_perm(w[e >> 1], 0u, e & 1 ? 0x3424u : 0x1404u);
+            y[e] = mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
+          }
+          if (f_more != 0x3f803f80u) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f_more);
+          }
+          st_shared_v4(dst + dst_at[i], y[0], y[1], y[2], y[3]);
+          st_shared_v4(dst + (dst_at[i] ^ 16u), y[4], y[5], y[6], y[7]);
+        }
+      };
+      Tile now = look_up(), next = look_up();
+      uint4 tail = tail_of(now);
+      if (now.there) {
+#pragma unroll
+        for (int i = 0; i < kRawStages; ++i) issue(__shfl_sync(0xffffffffu, now.rec, i));
+      }
+      int g = 0, taken = 0, unit = 0, flagged = 0x7fffffff;
+      bool ok = true;
+      while (now.there) {
+        const Tile after = look_up();
+        const uint4 next_tail = tail_of(next);
+        if (!is_v) {
+          // The first flagged token: the lowest bit of its block's flags.
+          const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
+          int at = bits != 0 && now.rec >= 0
+                       ? (now.number * kPagesPerTile + part + kGather * lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
+          flagged = min(flagged, __reduce_min_sync(0xffffffffu, at));
+          if (now.last) {
+            if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged[part])[unit & 7] = flagged;
+            flagged = 0x7fffffff;
+            ++unit;
+          }
+        }
+        const int st = g % L::kStages;
+        if (!(ok = mbar_wait_warp(empty0 + 8u * st, ((g / L::kStages) & 1) ^ 1, wc))) break;
+        const uint32_t dst0 = s_base + st * L::kKV;
+#pragma unroll 1
+        for (int i = 0; i < kMine; ++i) {
+          const int rec = __shfl_sync(0xffffffffu, now.rec, i);
+          const uint32_t scale = __shfl_sync(0xffffffffu, is_v ? tail.y : tail.x, i);
+          const int s = taken % kRawStages;
+          ++taken;
+          const uint32_t dst = dst0 + (part + kGather * i) * kPageRows * 128;
+          if (rec >= 0) {
+            if (!(ok = mbar_wait_warp(raw_full + 8u * s, (phases >> s) & 1u, wc))) break;
+            phases ^= 1u << s;
+            in_flight &= ~(1u << s);
+            convert(dst, raw + s * L::kRaw, scale);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2 * (D / 64); ++x) {
+              st_shared_v4(dst + dst_at[x], 0u, 0u, 0u, 0u);
+              st_shared_v4(dst + (dst_at[x] ^ 16u), 0u, 0u, 0u, 0u);
+            }
+          }
+          __syncwarp();                                        // every lane has read the raw block
+          const int ahead = i + kRawStages;
+          const int more = __shfl_sync(0xffffffffu, ahead < kMine ? now.rec : next.rec, ahead % kMine);
+          if (ahead < kMine || next.there) issue(more);
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        mbar_arrive(full0 + 8u * st);
+        ++g;
+        now = next;
+        next = after;
+        tail = next_tail;
+      }
+      if (!ok) {
+        // Raw blocks in flight must land before the CTA may exit: their barriers
+        // have one completion more than was waited for.
+        __syncwarp();
+        for (int s = 0; s < kRawStages; ++s) {
+          if (lane == 0 && (in_flight >> s) & 1u) mbar_wait(raw_full + 8u * s, (phases >> s) & 1u, wc, true);
+        }
+        __syncwarp();
+      }
+    }
+  } else if constexpr (PAGED) {
     if (warp == kWarpGatherK || warp == kWarpGatherV) {
       // ------------------------------------------------- paged K / V gather
       const bool is_v = warp == kWarpGatherV;
@@ -573,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_dealloc(tmem, kTmemCols);
     }
   } else {
-    regs_increase<kRegsSoftmax>();
+    regs_increase<regs_softmax(SOURCE)>();
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2;                       // query tile of this warpgroup
     const int quarter = warp & 3;                  // TMEM lane quarter of this warp
@@ -592,8 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qrow = u.qblk * kRowsPerCta + x * kBM + row;
     const int n_kv = x ? u.nB : u.nA;
     const int diag = 2 * u.qblk + x;               // causal: the tile holding key == row
-    const int qpos = u.pos0 + qrow;                // paged: position of this row's token
-    const int qpos_first = u.pos0 + u.qblk * kRowsPerCta + x * kBM;
+    // Paged: position of this row's token, and the lowest of the tile's rows'.
+    const int qpos = u.pos0 + (KV8 ? qrow % p.rows : qrow);
+    const int first = u.qblk * kRowsPerCta + x * kBM;
+    const int qpos_first = u.pos0 + (!KV8 || !p.packed ? first : first % p.rows + kBM <= p.rows ? first % p.rows : 0);
     const int zq = u.zq;
     float m = 0.f;                                 // stabiliser in use (exp2 domain)
     float l = 0.f;                                 // denominator relative to m (fp32 terms)
@@ -752,7 +1028,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ATTN47_TMEM_LD_WAIT(rs);
         lsum = __uint_as_float(rs[0]);
       }
-      const float inv_l = 1.f / lsum;
+      float inv_l = 1.f / lsum;
+      bool spoilt = false;
+      if constexpr (KV8) {
+        // (The gather wrote this before the unit's last tile was full.)
+        const volatile int* flagged = &bar->first_flagged[0][0];
+        spoilt = qpos >= min(flagged[units & 7], flagged[8 + (units & 7)]);
+        if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
+        if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
+      }
       const bool in_range = qrow < p.N;
       __nv_bfloat16* orow =
           reinterpret_cast<__nv_bfloat16*>(p.o) + (static_cast<size_t>(zq) * p.N + qrow) * D;
@@ -773,7 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (in_range && p.lse != nullptr)
-        p.lse[static_cast<size_t>(zq) * p.N + qrow] = (m + __log2f(l)) * kLn2;
+        p.lse[static_cast<size_t>(zq) * p.N + qrow] =
+            KV8 && spoilt ? __uint_as_float(0x7fc00000u) : (m + __log2f(l)) * kLn2;
       // O_X has been read out: the next unit's first P V may overwrite it.
       tc_fence_before();
       __syncwarp();
@@ -789,10 +1074,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool CAUSAL, bool PAGED, bool SORTED = false>
+template <int D, bool CAUSAL, int SOURCE, bool SORTED = false>
 cudaError_t launch_t(const FwdLaunch& a) {
-  using L = FwdLayout<D, D == 64 && !PAGED>;
-  auto kern = attn_fwd_sm103_kernel<D, CAUSAL, PAGED, SORTED>;
+  constexpr bool PAGED = SOURCE != kContiguous;
+  using L = FwdLayout<D, D == 64 && !PAGED, SOURCE>;
+  static_assert(L::kSmem <= 227 * 1024, "shared memory");
+  auto kern = attn_fwd_sm103_kernel<D, CAUSAL, SOURCE, SORTED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   FwdParams p;
@@ -815,9 +1102,12 @@ cudaError_t launch_t(const FwdLaunch& a) {
   p.max_blocks = a.max_blocks;
   p.num_blocks = a.num_blocks;
   p.max_ctx = PAGED ? a.max_blocks * kPageRows - a.N : 0;
+  p.kv_cache = static_cast<const uint8_t*>(a.kv_cache);
+  p.rows = a.rows;
+  p.packed = a.rows != a.N;
   // Persistent: one CTA per SM (shared memory allows one), each walking units.
   const unsigned grid = static_cast<unsigned>(min(p.num_units, a.sms > 0 ? a.sms : 1));
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), L::kSmem, a.stream, *a.tq, *a.tk, *a.tv, p);
+  return launch_pdl(kern, dim3(grid), dim3(threads_of(SOURCE)), L::kSmem, a.stream, *a.tq, *a.tk, *a.tv, p);
 }
 
 }  // namespace
@@ -827,12 +1117,16 @@ int fwd_box_rows() { return kBM; }
 cudaError_t launch_fwd_sm103(const FwdLaunch& a) {
   if (a.paged) {
     const long long pairs = static_cast<long long>(a.B) * ((a.N + kRowsPerCta - 1) / kRowsPerCta);
-    if (a.B <= kSortMaxSeqs && pairs <= kSortMaxPairs)
-      return a.d == 128 ? launch_t<128, true, true, true>(a) : launch_t<64, true, true, true>(a);
-    return a.d == 128 ? launch_t<128, true, true, false>(a) : launch_t<64, true, true, false>(a);
+    const bool sorted = a.B <= kSortMaxSeqs && pairs <= kSortMaxPairs;
+    if (a.kv_cache != nullptr) {
+      if (a.d == 128) return sorted ? launch_t<128, true, kPagedKv8, true>(a) : launch_t<128, true, kPagedKv8>(a);
+      return sorted ? launch_t<64, true, kPagedKv8, true>(a) : launch_t<64, true, kPagedKv8>(a);
+    }
+    if (a.d == 128) return sorted ? launch_t<128, true, kPagedBf16, true>(a) : launch_t<128, true, kPagedBf16>(a);
+    return sorted ? launch_t<64, true, kPagedBf16, true>(a) : launch_t<64, true, kPagedBf16>(a);
   }
-  if (a.d == 128) return a.causal ? launch_t<128, true, false>(a) : launch_t<128, false, false>(a);
-  return a.causal ? launch_t<64, true, false>(a) : launch_t<64, false, false>(a);
+  if (a.d == 128) return a.causal ? launch_t<128, true, kContiguous>(a) : launch_t<128, false, kContiguous>(a);
+  return a.causal ? launch_t<64, true, kContiguous>(a) : launch_t<64, false, kContiguous>(a);
 }
 
 }  // namespace attn47
