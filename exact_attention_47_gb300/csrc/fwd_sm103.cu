@@ -1006,7 +1006,8 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
         }
         numerators();
         if (j == 0 || pass == 1) break;
-        const bool big = !(lt <= 0x1p100f);
+        // (Values of an 8-bit cache reach 2^73: 2^40 keeps the sums of P V finite.)
+        const bool big = !(lt <= (KV8 ? 0x1p40f : 0x1p100f));
         if (!__any_sync(0xffffffffu, big)) break;
       }
       l += lt;
