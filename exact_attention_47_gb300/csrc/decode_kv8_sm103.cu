@@ -50,26 +50,26 @@ constexpr float kTau = 4.f;
 // A numerator is 2^kHigh for a score at the maximum, at most 2^(kHigh + kTau).
 constexpr float kHigh = 10.f;
 
-// NT: column tiles of 8 query rows (1 or 2).
+// NT: column tiles of 8 query rows (1 .. 4).
 template <int D, int NT>
 struct DecKv8Cfg {
   using Rec = Kv8Layout<D>;
-  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kWarps = D == 64 ? (NT <= 2 ? 12 : 8) : NT == 1 ? 12 : NT <= 3 ? 8 : 6;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = D == 64 ? 6 : NT == 1 ? 3 : 4;
+  static constexpr int kStages = D == 64 || NT == 2 || NT == 4 ? 4 : 3;
   static constexpr int kStage = Rec::kOffTail;               // its scales are apart
   static constexpr int kRows = NT * 8;                       // rows of a piece
   static constexpr int kPitch = D + 4;                       // floats
   static constexpr int kPiece = kRows * kPitch * 4;
-  static constexpr int kRing = kStages * kStage;             // per warp
+  // Per warp; its last piece takes the ring's place.
+  static constexpr int kRing = kStages * kStage > kPiece ? kStages * kStage : (kPiece + 1023) / 1024 * 1024;
   static constexpr int kOffFirst = kWarps * kRing;           // first pieces, one per warp
   static constexpr int kOffTails = kOffFirst + kWarps * kPiece;         // [warp][kStages][16]
   static constexpr int kOffMl = kOffTails + kWarps * kStages * 16;      // (max, sum): [warp][2][kRows]
   static constexpr int kOffPlan = kOffMl + kWarps * 2 * kRows * 8;
-  static constexpr int kOffSrc = kOffPlan + (3 * kPlan + 4) * 4;        // record addresses: [warp][2 batches of 32]
-  static constexpr int kOffShared = kOffSrc + kWarps * 64 * 8;
+  static constexpr int kOffSrc = kOffPlan + (3 * kPlan + 4) * 4;        // record numbers: [warp][2 batches of 32]
+  static constexpr int kOffShared = (kOffSrc + kWarps * 64 * 4 + 15) / 16 * 16;
   static constexpr int kSmem = kOffShared + 3072 + 1024;     // + alignment slack
-  static_assert(kRing >= kPiece, "a warp's last piece reuses its ring");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages < 32, "the next batch of records is there in time");
 };
@@ -703,7 +703,7 @@ cudaError_t launch_t(const DecKv8Launch& a, const Kv8Rows& rows) {
 }  // namespace
 
 Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N) {
-  const int rows = Hq / Hkv * N, groups = (rows + 15) / 16;
+  const int rows = Hq / Hkv * N, groups = (rows + 31) / 32;
   return Kv8Rows{(rows + groups - 1) / groups, groups};
 }
 
@@ -714,8 +714,12 @@ size_t decode_kv8_workspace_bytes(int Hq, int Hkv, int N, int d) {
 
 cudaError_t launch_decode_kv8_sm103(const DecKv8Launch& a) {
   const Kv8Rows rows = decode_kv8_rows(a.Hq, a.Hkv, a.N);
-  if (a.d == 128) return rows.group <= 8 ? launch_t<128, 1>(a, rows) : launch_t<128, 2>(a, rows);
-  return rows.group <= 8 ? launch_t<64, 1>(a, rows) : launch_t<64, 2>(a, rows);
+  const int tiles = (rows.group + 7) / 8;
+  if (a.d == 128)
+    return tiles == 1 ? launch_t<128, 1>(a, rows) : tiles == 2 ? launch_t<128, 2>(a, rows)
+         : tiles == 3 ? launch_t<128, 3>(a, rows) : launch_t<128, 4>(a, rows);
+  return tiles == 1 ? launch_t<64, 1>(a, rows) : tiles == 2 ? launch_t<64, 2>(a, rows)
+       : tiles == 3 ? launch_t<64, 3>(a, rows) : launch_t<64, 4>(a, rows);
 }
 
 }  // namespace attn47
