@@ -57,6 +57,7 @@ struct DecKv8Cfg {
   static constexpr int kWarps = D == 64 ? (NT <= 2 ? 12 : 8) : NT == 1 ? 12 : NT <= 3 ? 8 : 6;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = D == 64 || NT == 2 || NT == 4 ? 4 : 3;
+  static constexpr int kBlocks = D == 64 && NT <= 2 ? 2 : 1; // taken at a time
   static constexpr int kStage = Rec::kOffTail;               // its scales are apart
   static constexpr int kRows = NT * 8;                       // rows of a piece
   static constexpr int kPitch = D + 4;                       // floats
@@ -295,23 +296,26 @@ struct RunState {
   __device__ __forceinline__ float at(int nt, int k, int h) const { return o[nt][k >> 1][(k & 1) * 2 + h]; }
 };
 
-// One block of a run, 16 slots, in a stage of the ring, its scales at `tail_at`; `valid` tokens from the
-// block's first slot to the sequence's end (16 or more: all slots hold tokens; 0
-// or less: none, whatever the stage holds), `least` of them seen by every row.
-template <int D, int NT>
-__device__ __forceinline__ void take_block(const LaneData<D>& at, uint32_t stage, uint32_t tail_at, int valid, int least,
-                                           const QueryFrag<D, NT>& q, RunState<D, NT>& st) {
+// NB blocks of a run, 16 slots each, in stages of the ring, their scales at
+// `tail_at`; `valid` tokens from a block's first slot to the sequence's end (16 or
+// more: all slots hold tokens; 0 or less: none, whatever the stage holds), in each
+// block at least `least` of them seen by every row.
+template <int D, int NT, int NB>
+__device__ __forceinline__ void take_blocks(const LaneData<D>& at, const uint32_t (&stage)[NB],
+                                            const uint32_t (&tail_at)[NB], const int (&valid)[NB], int least,
+                                            const QueryFrag<D, NT>& q, RunState<D, NT>& st) {
   using Ld = LaneData<D>;
 
   // --- S^T: rows = slots, columns = query rows
-  float s[NT][4];
-  {
+  float s[NB][NT][4];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
     float even[NT][4], odd[NT][4];
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       uint32_t a[4], b[4];
-      load_bytes(stage + at.k[j], a);
-      load_bytes(stage + at.k_next(j), b);
+      load_bytes(stage[n] + at.k[j], a);
+      load_bytes(stage[n] + at.k_next(j), b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t a0 = e4m3x2_to_f16x2(a[i]), a1 = e4m3x2_to_f16x2(b[i]), a2 = e4m3x2_hi_to_f16x2(a[i]),
@@ -329,46 +333,58 @@ __device__ __forceinline__ void take_block(const LaneData<D>& at, uint32_t stage
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[nt][i] = even[nt][i] + odd[nt][i];
+      for (int i = 0; i < 4; ++i) s[n][nt][i] = even[nt][i] + odd[nt][i];
   }
 
-  uint32_t tail[4];
-  load_bytes(tail_at, tail);
-  const float scale_k = __uint_as_float(tail[0]);
-  float scale_v = __uint_as_float(tail[1]);
+  float scale_v[NB];
+  uint32_t flags[NB], any_flags = 0;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float f0 = q.back[nt][0] * scale_k, f1 = q.back[nt][1] * scale_k;
-    s[nt][0] *= f0;
-    s[nt][1] *= f1;
-    s[nt][2] *= f0;
-    s[nt][3] *= f1;
+  for (int n = 0; n < NB; ++n) {
+    uint32_t tail[4];
+    load_bytes(tail_at[n], tail);
+    const float scale_k = __uint_as_float(tail[0]);
+    scale_v[n] = __uint_as_float(tail[1]);
+    flags[n] = tail[2];
+    any_flags |= tail[2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f0 = q.back[nt][0] * scale_k, f1 = q.back[nt][1] * scale_k;
+      s[n][nt][0] *= f0;
+      s[n][nt][1] *= f1;
+      s[n][nt][2] *= f0;
+      s[n][nt][3] *= f1;
+    }
   }
-  uint32_t v[4][Ld::kVBytes / 4];
+  uint32_t v[NB][4][Ld::kVBytes / 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load_bytes(stage + (i < 2 ? at.v[i & 1] : at.v_next(i & 1)), v[i]);
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_bytes(stage[n] + (i < 2 ? at.v[i & 1] : at.v_next(i & 1)), v[n][i]);
 
-  if (least < kBS || tail[2] != 0) {             // (the same for the whole warp)
+  if (least < kBS || any_flags != 0) {           // (the same for the whole warp)
     // Slots that a row does not see have no score, those past the end no value;
     // a row that sees a flagged token has NaN for a score.
-    const uint32_t bad = valid > 0 ? tail[2] | (tail[2] >> 16) : 0u;
-    if (valid <= 0) scale_v = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int n = 0; n < NB; ++n) {
+      const uint32_t bad = valid[n] > 0 ? flags[n] | (flags[n] >> 16) : 0u;
+      if (valid[n] <= 0) scale_v[n] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int slot = at.slot + (i >> 1) * Ld::kNext;
+          if (slot >= valid[n] - q.behind[nt][i & 1])
+            s[n][nt][i] = -INFINITY;
+          else if ((bad >> slot) & 1u)
+            s[n][nt][i] = __uint_as_float(0x7fc00000u);
+        }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int slot = at.slot + (i >> 1) * Ld::kNext;
-        if (slot >= valid - q.behind[nt][i & 1])
-          s[nt][i] = -INFINITY;
-        else if ((bad >> slot) & 1u)
-          s[nt][i] = __uint_as_float(0x7fc00000u);
-      }
+        const int slot = at.slot_v + (i & 1) + (i >> 1) * Ld::kNext;
+        if (slot >= valid[n] || ((bad >> slot) & 1u)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int slot = at.slot_v + (i & 1) + (i >> 1) * Ld::kNext;
-      if (slot >= valid || ((bad >> slot) & 1u)) {
-#pragma unroll
-        for (int w = 0; w < Ld::kVBytes / 4; ++w) v[i][w] = 0;
+          for (int w = 0; w < Ld::kVBytes / 4; ++w) v[n][i][w] = 0;
+        }
       }
     }
   }
@@ -379,40 +395,48 @@ __device__ __forceinline__ void take_block(const LaneData<D>& at, uint32_t stage
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      top[nt][h] = fmaxf(s[nt][h], s[nt][2 + h]);
+      top[nt][h] = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
+#pragma unroll
+      for (int n = 1; n < NB; ++n) top[nt][h] = fmax3(top[nt][h], s[n][nt][h], s[n][nt][2 + h]);
       move |= top[nt][h] > st.limit[nt][h];
     }
   if (__any_sync(0xffffffffu, move)) st.move(top);
 
   // --- numerators and O^T: rows = elements of V, columns = query rows
-  uint32_t pw[NT][2];
+  uint32_t pw[NB][NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float p0 = ex2(s[nt][0] - st.stab[nt][0]), p1 = ex2(s[nt][1] - st.stab[nt][1]);
-    const float p2 = ex2(s[nt][2] - st.stab[nt][0]), p3 = ex2(s[nt][3] - st.stab[nt][1]);
-    st.l[nt][0] += p0 + p2;
-    st.l[nt][1] += p1 + p3;
-    pw[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
-    pw[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+  for (int n = 0; n < NB; ++n) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float p0 = ex2(s[n][nt][0] - st.stab[nt][0]), p1 = ex2(s[n][nt][1] - st.stab[nt][1]);
+      const float p2 = ex2(s[n][nt][2] - st.stab[nt][0]), p3 = ex2(s[n][nt][3] - st.stab[nt][1]);
+      st.l[nt][0] += p0 + p2;
+      st.l[nt][1] += p1 + p3;
+      pw[n][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+      pw[n][nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+    }
   }
-  const uint64_t sv = f2_pack(scale_v, scale_v);
 #pragma unroll
-  for (int w = 0; w < Ld::kVBytes / 4; ++w) {
+  for (int n = 0; n < NB; ++n) {
+    const uint64_t sv = f2_pack(scale_v[n], scale_v[n]);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t sel = hf ? 0x7362u : 0x5140u;           // (token, next token) of two elements
-      const uint32_t x = __byte_perm(v[0][w], v[1][w], sel), y = __byte_perm(v[2][w], v[3][w], sel);
-      const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_hi_to_f16x2(x), a2 = e4m3x2_to_f16x2(y),
-                     a3 = e4m3x2_hi_to_f16x2(y);
-      const int i = 2 * w + hf;
+    for (int w = 0; w < Ld::kVBytes / 4; ++w) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float acc[4];
-        mma_16816_f16_first(acc, a0, a1, a2, a3, pw[nt][0], pw[nt][1]);
-        f2_unpack(f2_fma(f2_pack(acc[0], acc[1]), sv, f2_pack(st.o[nt][i][0], st.o[nt][i][1])), st.o[nt][i][0],
-                  st.o[nt][i][1]);
-        f2_unpack(f2_fma(f2_pack(acc[2], acc[3]), sv, f2_pack(st.o[nt][i][2], st.o[nt][i][3])), st.o[nt][i][2],
-                  st.o[nt][i][3]);
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t sel = hf ? 0x7362u : 0x5140u;         // (token, next token) of two elements
+        const uint32_t x = __byte_perm(v[n][0][w], v[n][1][w], sel), y = __byte_perm(v[n][2][w], v[n][3][w], sel);
+        const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_hi_to_f16x2(x), a2 = e4m3x2_to_f16x2(y),
+                       a3 = e4m3x2_hi_to_f16x2(y);
+        const int i = 2 * w + hf;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4];
+          mma_16816_f16_first(acc, a0, a1, a2, a3, pw[n][nt][0], pw[n][nt][1]);
+          f2_unpack(f2_fma(f2_pack(acc[0], acc[1]), sv, f2_pack(st.o[nt][i][0], st.o[nt][i][1])), st.o[nt][i][0],
+                    st.o[nt][i][1]);
+          f2_unpack(f2_fma(f2_pack(acc[2], acc[3]), sv, f2_pack(st.o[nt][i][2], st.o[nt][i][3])), st.o[nt][i][2],
+                    st.o[nt][i][3]);
+        }
       }
     }
   }
@@ -423,7 +447,7 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
     attn_decode_kv8_kernel(const __grid_constant__ CUtensorMap records, const __grid_constant__ DecKv8Params p) {
   using Cfg = DecKv8Cfg<D, NT>;
   using Rec = Kv8Layout<D>;
-  constexpr int kWarps = Cfg::kWarps, kStages = Cfg::kStages, kRows = Cfg::kRows;
+  constexpr int kWarps = Cfg::kWarps, kStages = Cfg::kStages, kRows = Cfg::kRows, NB = Cfg::kBlocks;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
   DecKv8Shared* sh = reinterpret_cast<DecKv8Shared*>(smem + Cfg::kOffShared);
@@ -523,24 +547,43 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
       if (taken > 0) raw.load(p, w.at.b, w.at.g, lane);
       make_queries<D, NT>(p, raw, w.at.g, lane, q);
       st.reset();
-      for (const int end = taken + cnt; taken < end; ++taken) {
-        if (!wait_warp(bars + stage * 8, parity, wc)) {
+      for (const int end = taken + cnt; taken < end;) {
+        // Without a second block the first one's stage stands in, with no slot of
+        // it alive.
+        const bool two = NB == 2 && taken + 1 < end;
+        const int next_stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (!wait_warp(bars + stage * 8, parity, wc) ||
+            (two && !wait_warp(bars + next_stage * 8, next_stage == 0 ? parity ^ 1 : parity, wc))) {
           fail = true;
           break;
         }
-        const int alive = (present >> (taken & 31)) & 1u ? valid : 0;
-        take_block<D, NT>(at, ring_at + stage * Cfg::kStage, tails + stage * 16, alive, alive - (p.N - 1), q, st);
-        __syncwarp();                            // every lane has read the stage
-        if (lane == 0 && taken + kStages < blocks) issue(taken + kStages, stage);
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1;
+        uint32_t rec_at[NB], tail_at[NB];
+        int alive[NB];
+        rec_at[0] = ring_at + stage * Cfg::kStage;
+        tail_at[0] = tails + stage * 16;
+        alive[0] = (present >> (taken & 31)) & 1u ? valid : 0;
+        int least = alive[0];
+        if constexpr (NB == 2) {
+          rec_at[1] = two ? ring_at + next_stage * Cfg::kStage : rec_at[0];
+          tail_at[1] = two ? tails + next_stage * 16 : tail_at[0];
+          alive[1] = two && ((taken & 31) == 31 ? next_present & 1u : (present >> ((taken + 1) & 31)) & 1u) ? valid - kBS : 0;
+          least = min(least, alive[1]);
         }
-        valid -= kBS;
-        if ((taken & 31) == 31) {                // (what is issued is less than a batch ahead)
+        take_blocks<D, NT, NB>(at, rec_at, tail_at, alive, least - (p.N - 1), q, st);
+        __syncwarp();                            // every lane has read the stages
+        const int n = two ? 2 : 1;
+        if (lane < n && taken + lane + kStages < blocks) issue(taken + lane + kStages, lane ? next_stage : stage);
+        valid -= n * kBS;
+        if (((taken + n) ^ taken) & 32) {        // (what is issued is less than a batch ahead)
           present = next_present;
-          next_present = ((taken + 1) & ~31) + 32 < blocks ? fetch(((taken + 1) >> 5) + 1) : 0u;
+          next_present = ((taken + n) & ~31) + 32 < blocks ? fetch(((taken + n) >> 5) + 1) : 0u;
           __syncwarp();
+        }
+        taken += n;
+        stage += n;
+        if (stage >= kStages) {
+          stage -= kStages;
+          parity ^= 1;
         }
       }
       if (fail) break;
