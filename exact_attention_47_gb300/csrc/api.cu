@@ -912,7 +912,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
     tiles = !decode && kv8_in_tiles(Hq, Hkv, N);
     if (!tiles) {
       need = attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
-      passes = attn47::decode_kv8_rows(Hq, Hkv, N).groups;
+      passes = attn47::decode_kv8_rows(Hq, Hkv, N, d).groups;
     }
   }
   DeviceInfo* dev;

@@ -50,13 +50,13 @@ constexpr float kTau = 4.f;
 // A numerator is 2^kHigh for a score at the maximum, at most 2^(kHigh + kTau).
 constexpr float kHigh = 10.f;
 
-// NT: column tiles of 8 query rows (1 .. 4).
+// NT: column tiles of 8 query rows (1 .. 4 with D = 64, 1 or 2 with D = 128).
 template <int D, int NT>
 struct DecKv8Cfg {
   using Rec = Kv8Layout<D>;
-  static constexpr int kWarps = D == 64 ? (NT <= 2 ? 12 : 8) : NT == 1 ? 12 : NT <= 3 ? 8 : 6;
+  static constexpr int kWarps = (D == 64 && NT <= 2) || NT == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = D == 64 || NT == 2 || NT == 4 ? 4 : 3;
+  static constexpr int kStages = D == 64 || NT == 2 ? 4 : 3;
   static constexpr int kBlocks = D == 64 && NT <= 2 ? 2 : 1; // taken at a time
   static constexpr int kStage = Rec::kOffTail;               // its scales are apart
   static constexpr int kRows = NT * 8;                       // rows of a piece
@@ -745,22 +745,24 @@ cudaError_t launch_t(const DecKv8Launch& a, const Kv8Rows& rows) {
 
 }  // namespace
 
-Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N) {
-  const int rows = Hq / Hkv * N, groups = (rows + 31) / 32;
+Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N, int d) {
+  // Up to four column tiles a pass with d = 64, two with d = 128, whose accumulators
+  // for more do not fit beside enough warps (24 rows of 32 sequences of 500 .. 6000
+  // tokens, 2 KV heads: two passes of 12 take 33.3 us, one of 24 35.9).
+  const int most = d == 64 ? 32 : 16, rows = Hq / Hkv * N, groups = (rows + most - 1) / most;
   return Kv8Rows{(rows + groups - 1) / groups, groups};
 }
 
 size_t decode_kv8_workspace_bytes(int Hq, int Hkv, int N, int d) {
   return static_cast<size_t>(kMaxCtas) * sizeof(unsigned long long) +
-         static_cast<size_t>(2) * kMaxCtas * decode_kv8_rows(Hq, Hkv, N).group * (static_cast<size_t>(d) + 2) * sizeof(float);
+         static_cast<size_t>(2) * kMaxCtas * decode_kv8_rows(Hq, Hkv, N, d).group * (static_cast<size_t>(d) + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_kv8_sm103(const DecKv8Launch& a) {
-  const Kv8Rows rows = decode_kv8_rows(a.Hq, a.Hkv, a.N);
+  const Kv8Rows rows = decode_kv8_rows(a.Hq, a.Hkv, a.N, a.d);
   const int tiles = (rows.group + 7) / 8;
   if (a.d == 128)
-    return tiles == 1 ? launch_t<128, 1>(a, rows) : tiles == 2 ? launch_t<128, 2>(a, rows)
-         : tiles == 3 ? launch_t<128, 3>(a, rows) : launch_t<128, 4>(a, rows);
+    return tiles == 1 ? launch_t<128, 1>(a, rows) : launch_t<128, 2>(a, rows);
   return tiles == 1 ? launch_t<64, 1>(a, rows) : tiles == 2 ? launch_t<64, 2>(a, rows)
        : tiles == 3 ? launch_t<64, 3>(a, rows) : launch_t<64, 4>(a, rows);
 }

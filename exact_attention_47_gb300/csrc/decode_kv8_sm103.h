@@ -33,7 +33,7 @@ struct DecKv8Launch {
 struct Kv8Rows {
   int group, groups;
 };
-Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N);
+Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N, int d);
 // Bytes of workspace: two partial results of a group's rows and one counter for
 // each CTA a launch can have.
 size_t decode_kv8_workspace_bytes(int Hq, int Hkv, int N, int d);

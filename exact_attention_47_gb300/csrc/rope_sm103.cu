@@ -340,12 +340,12 @@ struct PairLanes {
     x1 = pack8(b);
   }
   // The same of numbers, products and sums rounded one by one, as the formula
-  // reads: codes then agree with those of the fp32 formula.  `angles` are those
-  // of the lane's pairs.
+  // reads: codes then agree with those of the fp32 formula.  `angles`: those of the
+  // lane's pairs, two at a time, 16 apart.
   __device__ __forceinline__ void turn_rounded(const float2* angles, float (&a)[8], float (&b)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float4 v = *reinterpret_cast<const float4*>(angles + i);
+      const float4 v = *reinterpret_cast<const float4*>(angles + 8 * i);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int n = i + j;
@@ -399,7 +399,9 @@ __device__ __forceinline__ uint32_t kv8_rescale(uint32_t codes, float by) {
 
 // Runs that share a block's scale, and what a pass over them needs.
 struct Kv8Append {
-  alignas(16) float2 angles[kSlots][64];   // cosines and sines of a row's pairs
+  // Cosines and sines of a row's pairs; pair 8 s + i at 16 (i / 2) + 2 s + i % 2, so
+  // that lanes s = 0 .. 7 read neighbouring 16 bytes.
+  alignas(16) float2 angles[kSlots][64];
   int token[kSlots], slot[kSlots], run[kSlots];          // of a row of the pass
   int phys[kSlots], slot0[kSlots], length[kSlots];       // of a run
   uint32_t most[2][4][kSlots];             // largest value of a run (bits): [key, value][head of the chunk][run]
@@ -498,13 +500,12 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         float s, c;
         turn_sincos(at, sh.frac[pair], s, c);
         if (ax & 4u) s = c = __uint_as_float(0x7fc00000u);
-        s8.angles[r][pair] = make_float2(c, s);
+        s8.angles[r][((pair & 7) >> 1) * 16 + (pair >> 3) * 2 + (pair & 1)] = make_float2(c, s);
       }
       __syncthreads();
 
       for (int h0 = head0; h0 < head1; h0 += kChunk) {
         const int heads = min(kChunk, head1 - h0);
-        const int items = 2 * heads * rows;      // keys, then values; rows fastest
         // What the blocks hold already (one thread for each run and head).
         const int my = tid / heads, my_head = tid - my * heads;
         const bool keeper = my < runs;
@@ -514,13 +515,15 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
           tail_at = p.kv_cache + (static_cast<size_t>(s8.phys[my]) * p.Hk + h0 + my_head) * Lt::kBytes + Lt::kOffTail;
           if (s8.slot0[my] != 0) tail = *reinterpret_cast<const uint4*>(tail_at);
         }
+        // Items are rows of 16 of each head's keys, then of its values: a warp's are
+        // neighbouring rows of one of them.
         uint4 x0[kSteps], x1[kSteps];
+        bool odd[kSteps];                        // some element of the lane's is no finite number
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-          const int it = u * kItems + warp * kRows + sub;
+          const int it = u * kItems + warp * kRows, kh = it / kSlots, r = it % kSlots + sub;
           x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (it >= items) continue;
-          const int kh = it / rows, r = it - kh * rows;
+          if (kh >= 2 * heads || r >= rows) continue;
           const bool value = kh >= heads;
           const int tok = s8.token[r];
           const __nv_bfloat16* src = value ? RowPtr::row(p.v.of(0, tok), h0 + kh - heads, p.v.head)
@@ -533,35 +536,50 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         auto numbers = [&](int u, bool key, int r, float (&a)[8], float (&b)[8]) {
           unpack8(x0[u], a);
           unpack8(x1[u], b);
-          if (key && pl.turns) pl.turn_rounded(s8.angles[r] + 8 * slot, a, b);
+          if (key && pl.turns) pl.turn_rounded(s8.angles[r] + 2 * slot, a, b);
         };
-        bool odd[kSteps];                        // some element of the lane's is no finite number
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-          const int it = u * kItems + warp * kRows + sub;
-          const bool live = it < items;
-          const int kh = live ? it / rows : 0, r = live ? it - kh * rows : 0;
-          const bool value = kh >= heads;
-          float a[8], b[8];
-          numbers(u, !value, r, a, b);
-          uint32_t most = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            most = max(most, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
-          odd[u] = most >= 0x7f800000u;
+          const int it = u * kItems + warp * kRows, kh = it / kSlots, r0 = it % kSlots, r = r0 + sub;
+          odd[u] = false;
+          if (kh >= 2 * heads || r0 >= rows) continue;         // (the same for the whole warp)
+          const bool value = kh >= heads, live = r < rows;
           const int h = value ? kh - heads : kh;
+          uint32_t most = 0;                     // bits of the largest size
+          if (value) {
+            const uint32_t w[8] = {x0[u].x, x0[u].y, x0[u].z, x0[u].w, x1[u].x, x1[u].y, x1[u].z, x1[u].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = __vmaxu2(most, w[i] & 0x7fff7fffu);
+            most = max(most & 0xffff0000u, most << 16);
+          } else {
+            float a[8], b[8];
+            numbers(u, true, live ? r : 0, a, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              most = max(most, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
+          }
+          if (!live) most = 0;
+          odd[u] = most >= 0x7f800000u;
+          const int run = s8.run[live ? r : r0];
           if (odd[u]) {
+            float a[8], b[8];
+            numbers(u, !value, r, a, b);
             most = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint32_t va = __float_as_uint(a[e]) & 0x7fffffffu, vb = __float_as_uint(b[e]) & 0x7fffffffu;
               most = max(most, max(va < 0x7f800000u ? va : 0u, vb < 0x7f800000u ? vb : 0u));
             }
-            atomicOr(&s8.bad[h][s8.run[r]], 1u << (s8.slot[r] + (value ? 16 : 0)));
+            atomicOr(&s8.bad[h][run], 1u << (s8.slot[r] + (value ? 16 : 0)));
           }
+          if (s8.run[r0] == s8.run[min(r0 + kRows, rows) - 1]) {   // one run: the usual case of a long batch
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) atomicMax(&s8.most[value ? 1 : 0][h][run], most);
+          } else {
 #pragma unroll
-          for (int o = 1; o < kSlotLanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-          if (live && slot == 0) atomicMax(&s8.most[value ? 1 : 0][h][s8.run[r]], most);
+            for (int o = 1; o < kSlotLanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+            if (live && slot == 0) atomicMax(&s8.most[value ? 1 : 0][h][run], most);
+          }
         }
         __syncthreads();
         if (keeper) {
@@ -594,9 +612,8 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-          const int it = u * kItems + warp * kRows + sub;
-          if (it >= items) continue;
-          const int kh = it / rows, r = it - kh * rows;
+          const int it = u * kItems + warp * kRows, kh = it / kSlots, r = it % kSlots + sub;
+          if (kh >= 2 * heads || r >= rows) continue;
           const bool value = kh >= heads;
           const int h = value ? kh - heads : kh, run = s8.run[r];
           float a[8], b[8];
