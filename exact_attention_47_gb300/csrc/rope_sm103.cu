@@ -35,6 +35,8 @@
 // and a fourth CTA a SM with its 64 registers gains 0.7 us here and loses 0.25 of
 // 5.6 in a decode step.  Equal shares of steps instead of whole tokens change
 // nothing (21.5, 10.2, 14.5 and 47.3 us).
+#include <type_traits>
+
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -420,13 +422,12 @@ struct Kv8Append {
 // run needs, slots not yet written are zeros.  In any other the scale can only
 // grow, and where it does the codes that are there are brought to it.
 template <int D, bool IL>
-__device__ __forceinline__ void append_kv8_units(const RopeParams& p, const RopeShared& sh) {
+__device__ __forceinline__ void append_kv8_units(const RopeParams& p, const RopeShared& sh, Kv8Append& s8) {
   using Lt = Kv8Layout<D>;
   constexpr int kSlotLanes = D / 16, kRows = 32 / kSlotLanes;
   constexpr int kSteps = 2, kItems = kWarps * kRows;       // rows of a step
   constexpr int kChunk = kSteps * kItems / (2 * kSlots);   // heads at a time
   static_assert(kChunk <= 4, "room in Kv8Append");
-  __shared__ Kv8Append s8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = lane % kSlotLanes, sub = lane / kSlotLanes;
   const PairLanes<IL> pl(p.rot, slot);
@@ -674,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
   constexpr int kRows = 32 / kSlotLanes;
   constexpr int kFlight = 2;                     // steps whose loads are in flight together
   __shared__ RopeShared sh;
+  __shared__ std::conditional_t<MODE == kAppendKv8, Kv8Append, int> s8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = lane % kSlotLanes, sub = lane / kSlotLanes;
 
@@ -687,8 +689,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
 
   const int tasks = static_cast<int>(p.tasks), stride = gridDim.x * kWarps;
   int task = blockIdx.x * kWarps + warp;
+  // Append to an 8-bit cache: a unit of keys and values is a chain of waits, so part
+  // of the CTAs does its units while the others are at the queries.
+  const bool units_first = blockIdx.x < gridDim.x / 3;
   if constexpr (MODE == kAppendKv8) {
-    append_kv8_units<D, IL>(p, sh);
+    if (units_first) append_kv8_units<D, IL>(p, sh, s8);
     // The CTAs that had one unit less begin with the queries.
     const int late = static_cast<int>(blockIdx.x) - p.kv_units % static_cast<int>(gridDim.x);
     task = (late < 0 ? late + static_cast<int>(gridDim.x) : late) * kWarps + warp;
@@ -837,6 +842,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) rope_kernel(const
         }
       }
     }
+  }
+  if constexpr (MODE == kAppendKv8) {
+    if (!units_first) append_kv8_units<D, IL>(p, sh, s8);
   }
 }
 
