@@ -492,6 +492,26 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         s8.run[my_row] = my_run;
       }
       __syncthreads();
+      // Items are rows of 16 of each head's keys, then of its values: a warp's are
+      // neighbouring rows of one of them.  The first heads' rows come while the
+      // angles are formed, the next ones' while these are written.
+      uint4 x0[kSteps], x1[kSteps];
+      auto load_rows = [&](int h0) {
+        const int heads = min(kChunk, head1 - h0);
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const int it = u * kItems + warp * kRows, kh = it / kSlots, r = it % kSlots + sub;
+          x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (kh >= 2 * heads || r >= rows) continue;
+          const bool value = kh >= heads;
+          const int tok = s8.token[r];
+          const __nv_bfloat16* src = value ? RowPtr::row(p.v.of(0, tok), h0 + kh - heads, p.v.head)
+                                           : RowPtr::row(p.k.of(0, tok), h0 + kh, p.k.head);
+          x0[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot : pl.e0));
+          x1[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot + 8 : pl.e1));
+        }
+      };
+      load_rows(head0);
       const int pairs = p.rot / 2;
       for (int i = tid; i < rows * pairs; i += kThreads) {
         const int r = i / pairs, pair = i - r * pairs;
@@ -516,22 +536,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
           tail_at = p.kv_cache + (static_cast<size_t>(s8.phys[my]) * p.Hk + h0 + my_head) * Lt::kBytes + Lt::kOffTail;
           if (s8.slot0[my] != 0) tail = *reinterpret_cast<const uint4*>(tail_at);
         }
-        // Items are rows of 16 of each head's keys, then of its values: a warp's are
-        // neighbouring rows of one of them.
-        uint4 x0[kSteps], x1[kSteps];
         bool odd[kSteps];                        // some element of the lane's is no finite number
-#pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-          const int it = u * kItems + warp * kRows, kh = it / kSlots, r = it % kSlots + sub;
-          x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (kh >= 2 * heads || r >= rows) continue;
-          const bool value = kh >= heads;
-          const int tok = s8.token[r];
-          const __nv_bfloat16* src = value ? RowPtr::row(p.v.of(0, tok), h0 + kh - heads, p.v.head)
-                                           : RowPtr::row(p.k.of(0, tok), h0 + kh, p.k.head);
-          x0[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot : pl.e0));
-          x1[u] = *reinterpret_cast<const uint4*>(src + (value ? 16 * slot + 8 : pl.e1));
-        }
         // (Turned again for the codes: kept, the numbers would take 32 registers
         // and the third CTA of an SM.)
         auto numbers = [&](int u, bool key, int r, float (&a)[8], float (&b)[8]) {
@@ -636,6 +641,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
               make_uint2(to_e4m3x4(b[0] * inv, b[1] * inv, b[2] * inv, b[3] * inv),
                          to_e4m3x4(b[4] * inv, b[5] * inv, b[6] * inv, b[7] * inv));
         }
+        if (h0 + kChunk < head1) load_rows(h0 + kChunk);
         // The blocks' other slots, where they do not stay as they are.
         for (int x = warp; x < 2 * heads * runs; x += kWarps) {
           const int kh = x / runs, run = x - kh * runs;
