@@ -16,7 +16,6 @@
 #pragma once
 
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
@@ -201,11 +200,6 @@ __device__ __noinline__ bool wait_warp_slow(uint32_t bar, uint32_t parity, const
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& w) {
   if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   return wait_warp_slow(bar, parity, w);
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // (stab + log2(l)) ln 2, the whole part of the logarithm added to the

@@ -56,17 +56,26 @@
 //
 // Paged mode over an 8-bit cache (kPagedKv8): the same, but the cache holds the
 // new tokens already, sequence b's row i is the token at position seq_lens[b] -
-// N + i (before position 0 it sees nothing: O = 0, LSE = -inf), and the gather
-// turns codes into bf16 on the way.  The records' codes come by TMA into a small
-// ring of raw blocks (128-byte swizzle), from there a warp takes 16 codes a lane,
-// spreads them to bf16 with their exponents 120 too low (sign, 4 bits of exponent
-// and 3 of fraction fit where they are), multiplies by 2^120 times the block's
-// scale (both powers of two: exact, e4m3's subnormal numbers too) and stores them
-// into the swizzled tile.  So the tile holds the very numbers that the codes stand
-// for, and nothing else in the kernel changes.  It is kGather warps to an operand,
-// in a fourth warpgroup.  A code that is NaN becomes a finite number there; the
-// records' flags say which tokens have one, the gather keeps the first position of
-// such a token, and a row that sees that position gets NaN in the epilogue.
+// N + i (before position 0 it sees nothing: O = 0, LSE = -inf), and everything is
+// fp16 in place of bf16: an e4m3 code is an fp16 number, one conversion
+// instruction makes two, and the gather has nothing else to do (in bf16 it took
+// four integer steps and a product more, and the whole 337 us where this takes
+// 243).  The scales, powers of two for each 16 keys, act where they cost
+// least.  With S the product with the K codes, b a 16-key block, back the row's
+// factor (below) and e_b = log2 of the V scale:
+//   P'_j = 2^(S_j scale_Kb back + e_b - m),   O = sum P'_j code_j / l,
+//   l = sum over blocks 2^-e_b sum P'_j
+// so a block's scales are the two constants of the FMA before the exponential, and
+// one more FMA for a block's sum.  P' is at most 2^16 (its sum over a tile is
+// checked, a tile beyond is redone with m moved), 2^8 at the maximum; what rounds
+// to zero in fp16 is 2^-32 of the largest contribution.  The rows of Q are turned
+// into fp16 in shared memory, each by a power of two of its own that brings its
+// largest element to [2^14, 2^15) (warp 8 tile A, warp 10 tile B, which also load
+// them).  Warp 11 looks up the blocks and their scales, two warps to an operand, of
+// a fourth warpgroup, load codes two blocks ahead, convert and store them into the
+// swizzled tile.  NaN codes of V are cleared where there can be any (a sequence's
+// last block, flagged blocks); warp 11 keeps the first position of a flagged token,
+// and a row that sees that position gets NaN in the epilogue.
 // With fewer than 256 new tokens the rows of all query heads that share a KV head
 // make one row of query blocks (row = head in the group times N + token), so that
 // a 256-row unit is not mostly empty.
@@ -83,23 +92,24 @@ constexpr int kBM = 128;            // rows per query tile (= TMEM lanes)
 constexpr int kBN = 128;            // keys per K/V tile
 constexpr int kTiles = 2;           // query tiles per CTA
 constexpr int kRowsPerCta = kBM * kTiles;
-// 2 softmax warpgroups + 1 producer/MMA warpgroup (+ 1 for the gather of an 8-bit cache)
+constexpr int kThreads = 384;       // 2 softmax warpgroups + 1 producer/MMA warpgroup
 enum Source { kContiguous, kPagedBf16, kPagedKv8 };
-__host__ __device__ constexpr int threads_of(int source) { return source == kPagedKv8 ? 512 : 384; }
 constexpr int kWarpLoad = 8;
 constexpr int kWarpMma = 9;
 // Launched at 168 registers a thread (384 x 168 = 64512); the softmax
 // warpgroups then take 216 and the producer/MMA warpgroup keeps 72:
 // 256 x 216 + 128 x 72 = 64512, and per sub-partition 216 + 216 + 72 = 504
 // = 3 x 168, so the increase never waits for registers nobody frees.
-// With the gather's warpgroup: 512 at 128 registers, 256 x 208 + 256 x 48 = 65536.
-__host__ __device__ constexpr uint32_t regs_softmax(int source) { return source == kPagedKv8 ? 208 : 216; }
-__host__ __device__ constexpr uint32_t regs_other(int source) { return source == kPagedKv8 ? 48 : 72; }
+constexpr uint32_t kRegsSoftmax = 216;
+constexpr uint32_t kRegsOther = 72;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
+constexpr float kHigh8 = 8.0f;      // 8-bit cache: log2 of P' at the maximum
 
-constexpr int kGather = 2;          // 8-bit cache: gather warps to an operand
+__host__ __device__ constexpr int sort_max_pairs(int source) { return source == kPagedKv8 ? 1024 : 2048; }
+constexpr int kRawStages = 6;       // 8-bit cache: raw blocks in flight of K and of V
+constexpr int kScaleTiles = 16;     // tiles whose scales are kept
 
 // SUMV (d = 64 with contiguous K/V): the row sums of P come from the tensor
 // core.  Every V stage gets a second 64-column chunk, written once, whose
@@ -120,13 +130,14 @@ struct FwdLayout {
   static constexpr int kOffK = kOffQ + kTiles * kQTile;
   static constexpr int kOffV = kOffK + kStages * kKV;
   static constexpr int kOffBar = kOffV + kStages * kVStage;
-  static constexpr int kOffCtx = kOffBar + 512;          // paged: ctx_b of each sequence
+  static constexpr int kOffCtx = kOffBar + 640;          // paged: ctx_b of each sequence
   static constexpr int kOffOrder = kOffCtx + 4 * 256;    // paged: (b << 16 | qblk) of each cost rank
-  // 8-bit cache: raw blocks (a K or V half of a record) of each gather warp.
-  static constexpr int kRawStages = SOURCE == kPagedKv8 ? (D == 128 ? 3 : 4) : 0;
-  static constexpr int kRaw = 16 * D;
-  static constexpr int kOffRaw = (kOffOrder + 4 * 2048 + 1023) / 1024 * 1024;
-  static constexpr int kSmem = kOffRaw + 2 * kGather * kRawStages * kRaw + 1024;   // + alignment slack
+  // 8-bit cache: (K scale times scale log2 e, log2 of V's, 1 / V's) of the 8 blocks
+  // of tile t at t % kScaleTiles; rings of raw blocks of K and V.
+  static constexpr int kOffScales = kOffOrder + 4 * sort_max_pairs(SOURCE);
+  static constexpr int kOffRaw = (kOffScales + kScaleTiles * 8 * 16 + 1023) / 1024 * 1024;
+  static constexpr int kRaw = 16 * D;                         // a record's K or V codes
+  static constexpr int kSmem = (SOURCE == kPagedKv8 ? kOffRaw + 2 * kRawStages * kRaw : kOffScales) + 1024;   // + alignment slack
   static constexpr uint32_t kColS0 = 0, kColS1 = 128;
   static constexpr uint32_t kColO0 = 256, kColO1 = SUMV ? 384 : 256 + D;
 };
@@ -137,15 +148,20 @@ struct FwdBarriers {
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t o_free[2];                 // O_X read out by the epilogue of the previous unit
   uint64_t mma_final;
-  uint64_t raw_full[2 * kGather][4];  // 8-bit cache: raw block x of a gather warp has come
+  // 8-bit cache: Q tile x is fp16; raw block s of K / V has come / has been read, and
+  // what it is.
+  uint64_t q_ready[2], raw_full[2][kRawStages], raw_empty[2][kRawStages];
   uint32_t tmem_base;
   int abort;
-  // 8-bit cache: the first position of a flagged token of unit u (of the CTA's), as
-  // each K gather warp has found it, at u % 8: a gather is at most kStages tiles
-  // ahead of the MMAs, and those at most a unit ahead of the epilogue.
-  int first_flagged[kGather][8];
+  int raw_kind[2][kRawStages], raw_fills[2][kRawStages];
+  // The first position of a flagged token in unit u (of the CTA's), at u % 16: the
+  // look-up is at most two tiles ahead of the gather, that kStages ahead of the MMAs,
+  // and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1), which also bounds
+  // the scales' ring.
+  int first_flagged[16];
 };
-static_assert(sizeof(FwdBarriers) <= 512, "room in the layout");
+enum RawKind { kRawNone, kRawCodes, kRawCareful, kRawEnd };   // none: zeros; careful: there may be NaN codes
+static_assert(sizeof(FwdBarriers) <= 640, "room in the layout");
 
 struct FwdParams {
   void* o;
@@ -172,31 +188,31 @@ struct FwdParams {
 // Cost ordering of the paged mode fits in shared memory up to these sizes
 // (beyond them a second instantiation keeps the query-block-major order).
 constexpr int kSortMaxSeqs = 256;
-constexpr int kSortMaxPairs = 2048;
 
 constexpr int kPageRows = 16;                        // token slots per cache block
 constexpr int kPagesPerTile = kBN / kPageRows;
 constexpr int kWarpGatherK = 10;                     // paged mode: K / V gather warps
 constexpr int kWarpGatherV = 11;
-constexpr int kWarpGather8 = 12;                     // of an 8-bit cache: K, V, K, V
-static_assert(kGather == 2, "the gather's warpgroup");
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// Four e4m3 codes, those that are NaN as 0.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in the byte of a 0x7f or 0xff
+  return w & ~(nan * 0xffu);
+}
 
 template <int D, bool CAUSAL, int SOURCE, bool SORTED>
-__global__ void __launch_bounds__(threads_of(SOURCE), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_sm103_kernel(const __grid_constant__ CUtensorMap tq,
                           const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const FwdParams p) {
   constexpr bool PAGED = SOURCE != kContiguous, KV8 = SOURCE == kPagedKv8;
-  constexpr int kThreads = threads_of(SOURCE);
   constexpr bool SUMV = D == 64 && !PAGED;
   using L = FwdLayout<D, SUMV, SOURCE>;
   extern __shared__ uint8_t smem_raw[];
@@ -286,8 +302,8 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
     }
     for (int s = 0; s < L::kStages; ++s) {
       // Paged: every lane of a gather warp arrives once its copies landed.
-      mbar_init(smem_addr(&bar->k_full[s]), KV8 ? 32 * kGather : PAGED ? 32 : 1);
-      mbar_init(smem_addr(&bar->v_full[s]), KV8 ? 32 * kGather : PAGED ? 32 : 1);
+      mbar_init(smem_addr(&bar->k_full[s]), PAGED ? 32 : 1);
+      mbar_init(smem_addr(&bar->v_full[s]), PAGED ? 32 : 1);
       mbar_init(smem_addr(&bar->k_empty[s]), 1);
       mbar_init(smem_addr(&bar->v_empty[s]), 1);
     }
@@ -298,7 +314,12 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
     }
     mbar_init(smem_addr(&bar->mma_final), 1);
     if constexpr (KV8) {
-      for (int x = 0; x < 2 * kGather * 4; ++x) mbar_init(smem_addr(&bar->raw_full[0][0] + x), 1);
+      for (int x = 0; x < 2; ++x) mbar_init(smem_addr(&bar->q_ready[x]), kBM);
+      for (int x = 0; x < 2 * kRawStages; ++x) {
+        mbar_init(smem_addr(&bar->raw_full[0][0] + x), 1);
+        mbar_init(smem_addr(&bar->raw_empty[0][0] + x), 1);
+        (&bar->raw_fills[0][0])[x] = 0;
+      }
     }
     bar->abort = 0;
     fence_mbar_init();
@@ -375,9 +396,143 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   const WaitCtl wc{&bar->abort, p.status, p.timeout_ns};
+  // Warps that wait long sleep where a gather needs the issue slots.
+  auto wait_long = [&](uint32_t b, uint32_t parity) {
+    return KV8 ? mbar_wait_sleep_warp(b, parity, wc) : mbar_wait_warp(b, parity, wc);
+  };
   if (warp >= 8) {
-  regs_decrease<regs_other(SOURCE)>();
-  if (warp == kWarpLoad) {
+  regs_decrease<kRegsOther>();
+  if (KV8 && warp == kWarpLoad) {
+    // --------------------------------------- the blocks of the tiles, 8-bit records
+    // Lane i < 8 looks up block i of a tile.  Table entries are read two tiles
+    // ahead of their use here, scales one tile ahead.
+    int band = 0, j = 0, left = 0, nblk = 0, kvh = 0;        // of the tile to read next
+    const int* row = nullptr;
+    auto open_unit = [&]() {
+      const int k = unit_at(band);
+      left = 0;
+      if (k >= p.num_units) return;
+      const Unit u = unit_info(k);
+      left = u.nB;
+      nblk = u.nblk;
+      kvh = u.kvh;
+      row = p.block_table + static_cast<size_t>(u.b) * p.max_blocks;
+      j = 0;
+    };
+    open_unit();
+    // A tile: the table entry of this lane's block and its KV head (-1: no such
+    // block), then its record; its number in its unit (-1: there is no tile),
+    // whether it is the last, and whether the block is the sequence's last.
+    struct Tile {
+      int entry, kvh, number;
+      bool last, ends;
+    };
+    auto read_table = [&]() {
+      Tile x;
+      x.entry = -1;
+      x.kvh = -1;
+      x.number = left > 0 ? j : -1;
+      x.last = left == 1;
+      x.ends = false;
+      if (left > 0) {
+        const int lb = j * kPagesPerTile + lane;
+        if (lane < kPagesPerTile && lb < nblk) {
+          x.entry = __ldg(row + lb);
+          x.kvh = kvh;
+          x.ends = lb == nblk - 1;
+        }
+        ++j;
+        if (--left == 0) {
+          ++band;
+          open_unit();
+        }
+      }
+      return x;
+    };
+    // The record of the lane's block, -1 for none (read as zeros).
+    auto record = [&](const Tile& x) {
+      if (static_cast<unsigned>(x.entry) < static_cast<unsigned>(p.num_blocks)) return x.entry * p.Hkv + x.kvh;
+      if (x.kvh >= 0) atomicOr(p.status, kDevBadBlock);
+      return -1;
+    };
+    auto tail_of = [&](int rec) {                            // (K scale, V scale, flags)
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (rec >= 0)
+        v = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + static_cast<size_t>(rec) * Kv8Layout<D>::kBytes +
+                                                 Kv8Layout<D>::kOffTail));
+      return v;
+    };
+    Tile next = read_table();
+    int now_rec = record(next), now_number = next.number;
+    bool now_last = next.last, now_ends = next.ends;
+    uint4 tail = tail_of(now_rec);
+    next = read_table();
+    int unit = 0, flagged = 0x7fffffff, n = 0;
+    bool ok = true;
+    // Block number `at` of an operand into its ring.
+    auto fill = [&](int op, int at, int rec, int what) {
+      const int s = at % kRawStages;
+      const uint32_t full = smem_addr(&bar->raw_full[op][s]);
+      if (!mbar_wait_sleep(smem_addr(&bar->raw_empty[op][s]), ((at / kRawStages) & 1) ^ 1, wc)) return false;
+      reinterpret_cast<volatile int*>(bar->raw_kind[op])[s] = what;
+      ++bar->raw_fills[op][s];
+      mbar_arrive_expect_tx(full, rec >= 0 ? L::kRaw : 0);
+      if (rec >= 0)
+        tma_load_3d(smem_addr(smem + L::kOffRaw) + (op * kRawStages + s) * L::kRaw, &tk, full, 0, op * (D / 8), rec);
+      return true;
+    };
+    for (;; ++n) {
+      const int next_rec = record(next), next_number = next.number;
+      const bool next_last = next.last, next_ends = next.ends;
+      const uint4 next_tail = tail_of(next_rec);
+      next = read_table();
+      // The first flagged token: the lowest bit of its block's flags.
+      const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
+      if (__any_sync(0xffffffffu, bits != 0)) {
+        const int at = bits != 0 ? (now_number * kPagesPerTile + lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
+        flagged = min(flagged, __reduce_min_sync(0xffffffffu, at));
+      }
+      if (now_last) {
+        if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
+        flagged = 0x7fffffff;
+        ++unit;
+      }
+      if (now_number < 0) break;
+      if (lane < kPagesPerTile) {
+        // (No block, zeros: any scales.)
+        reinterpret_cast<float4*>(smem + L::kOffScales)[n % kScaleTiles * 8 + lane] =
+            make_float4(now_rec >= 0 ? __uint_as_float(tail.x) * p.scale_log2 : 1.f,
+                        now_rec >= 0 ? static_cast<float>(static_cast<int>(tail.y >> 23) - 127) : 0.f,
+                        now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, 0.f);
+      }
+      const int kind = now_rec < 0 ? kRawNone : now_ends || bits != 0 ? kRawCareful : kRawCodes;
+      // Blocks three at a time (half a ring), K and V at once: lane 3 op + i.
+      for (int first = 0; ok && first < kPagesPerTile; first += 3) {
+        const int op = lane / 3, i = first + lane % 3;
+        const int rec = __shfl_sync(0xffffffffu, now_rec, i), what = __shfl_sync(0xffffffffu, kind, i);
+        if (lane < 6 && i < kPagesPerTile) ok = fill(op, n * kPagesPerTile + i, rec, what);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) break;
+      now_rec = next_rec;
+      now_number = next_number;
+      now_last = next_last;
+      now_ends = next_ends;
+      tail = next_tail;
+    }
+    // The end, for both gather warps; then the next kernel in the stream may set up.
+    if (ok && lane < 2) ok = fill(lane, n * kPagesPerTile, -1, kRawEnd);
+    ok = __all_sync(0xffffffffu, ok);
+    pdl_launch_dependents();
+    __syncwarp();
+    if (!ok) {
+      // Raw blocks in flight must land before the CTA may exit.
+      for (int s = 0; s < 2 * kRawStages; ++s) {
+        const int fills = (&bar->raw_fills[0][0])[s];
+        if (fills) mbar_wait_warp_drain(smem_addr(&bar->raw_full[0][0] + s), (fills - 1) & 1, wc);
+      }
+    }
+  } else if (!KV8 && warp == kWarpLoad) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       prefetch_tmap(&tq);
@@ -446,8 +601,9 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
   } else if (warp == kWarpMma) {
     // --------------------------------------------------------- MMA issuer
     {
-      constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, false);
-      constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, L::kNPV, true);
+      constexpr uint32_t kFp16 = KV8 ? ~((1u << 7) | (1u << 10)) : ~0u;    // A and B formats: fp16 is 0
+      constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, false) & kFp16;
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, L::kNPV, true) & kFp16;
       constexpr int kSteps = D / 16;               // MMAs in an S group (K = d)
       constexpr int kPSteps = kBN / 16;            // MMAs in a PV group (K = keys)
       const uint32_t kF = smem_addr(&bar->k_full[0]);
@@ -516,14 +672,15 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
         const Unit u = unit_info(k);
         const int nA = u.nA, nB = u.nB;
         const uint32_t upar = static_cast<uint32_t>(units & 1);
-        ok = mbar_wait_warp(smem_addr(&bar->q_full[0]), upar, wc) &&
+        uint64_t* const q_there = KV8 ? bar->q_ready : bar->q_full;
+        ok = mbar_wait_warp(smem_addr(&q_there[0]), upar, wc) &&
              mbar_wait_warp(kfull(0), ph(0), wc);
         if (ok) {
           tc_fence_after();
           probe_kind = 0;
           group_s(0, 0);
           if (nA == 1) umma_commit_warp(smem_addr(&bar->q_empty[0]));
-          ok = mbar_wait_warp(smem_addr(&bar->q_full[1]), upar, wc);
+          ok = mbar_wait_warp(smem_addr(&q_there[1]), upar, wc);
         }
         if (ok) {
           tc_fence_after();
@@ -597,189 +754,71 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
     }
   }
   if constexpr (KV8) {
-    if (warp >= kWarpGather8) {
-      // ------------------------------------- paged K / V gather, 8-bit records
-      const int me = warp - kWarpGather8;                      // even: K, odd: V
-      const bool is_v = me & 1;
-      const int part = me >> 1;
-      const uint32_t s_base = is_v ? sV : sK;
-      const uint32_t full0 = smem_addr(is_v ? &bar->v_full[0] : &bar->k_full[0]);
-      const uint32_t empty0 = smem_addr(is_v ? &bar->v_empty[0] : &bar->k_empty[0]);
-      const uint32_t raw = smem_addr(smem + L::kOffRaw) + me * L::kRawStages * L::kRaw;
-      const uint32_t raw_full = smem_addr(&bar->raw_full[me][0]);
-      constexpr int kMine = kPagesPerTile / kGather;           // blocks of a tile
-      constexpr int kRawStages = L::kRawStages;
-      static_assert(kRawStages <= kMine && kRawStages <= 4, "a raw block is at most a tile ahead");
-      // Lane i < kMine holds block part + kGather i of a tile.  Records are looked
-      // up two tiles ahead, their scales one tile ahead, raw blocks kRawStages
-      // blocks ahead.
-      int band = 0, j = 0, left = 0, nblk = 0, kvh = 0;        // of the tile to look up next
-      const int* row = nullptr;
-      auto open_unit = [&]() {
-        const int k = unit_at(band);
-        left = 0;
-        if (k >= p.num_units) return;
-        const Unit u = unit_info(k);
-        left = u.nB;
-        nblk = u.nblk;
-        kvh = u.kvh;
-        row = p.block_table + static_cast<size_t>(u.b) * p.max_blocks;
-        j = 0;
-      };
-      open_unit();
-      // A tile: its blocks' records (-1: none, read as zeros), whether it is there
-      // at all, whether it is its unit's last, and its number in the unit.
-      struct Tile {
-        int rec, number;
-        bool there, last;
-      };
-      auto look_up = [&]() {
-        Tile x;
-        x.rec = -1;
-        x.number = j;
-        x.there = left > 0;
-        x.last = left == 1;
-        if (!x.there) return x;
-        const int lb = j * kPagesPerTile + part + kGather * lane;
-        if (lane < kMine && lb < nblk) {
-          const int e = __ldg(row + lb);
-          if (static_cast<unsigned>(e) < static_cast<unsigned>(p.num_blocks))
-            x.rec = e * p.Hkv + kvh;
-          else
-            atomicOr(p.status, kDevBadBlock);                  // reported, read as zeros
-        }
-        ++j;
-        if (--left == 0) {
-          ++band;
-          open_unit();
-        }
-        return x;
-      };
-      auto tail_of = [&](const Tile& x) {                      // (K scale, V scale, flags)
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (x.rec >= 0)
-          v = __ldg(reinterpret_cast<const uint4*>(p.kv_cache + static_cast<size_t>(x.rec) * Kv8Layout<D>::kBytes +
-                                                   Kv8Layout<D>::kOffTail));
-        return v;
-      };
-      int issued = 0;                                          // raw blocks asked for
-      uint32_t in_flight = 0;                                  // stages whose block has not been waited for
-      auto issue = [&](int rec) {
-        const int s = issued % kRawStages;
-        ++issued;
-        if (rec < 0) return;
-        in_flight |= 1u << s;
-        if (lane != 0) return;
-        mbar_arrive_expect_tx(raw_full + 8u * s, L::kRaw);
-        tma_load_3d(raw + s * L::kRaw, &tk, raw_full + 8u * s, 0, is_v ? D / 8 : 0, rec);
-      };
-      // Completions of a raw stage's barrier (a block without a record makes none).
-      uint32_t phases = 0;
+    if (warp == kWarpGatherK || warp == kWarpGatherV) {
+      // -------------------------------------- raw blocks into fp16 K / V tiles
+      const int op = warp - kWarpGatherK;                      // 0: K, 1: V
+      const uint32_t raw = smem_addr(smem + L::kOffRaw) + op * kRawStages * L::kRaw;
+      const uint32_t full = smem_addr(&bar->raw_full[op][0]), empty = smem_addr(&bar->raw_empty[op][0]);
+      const volatile int* kinds = bar->raw_kind[op];
+      const uint32_t tile0 = op ? sV : sK;
+      const uint32_t tile_full = smem_addr(op ? &bar->v_full[0] : &bar->k_full[0]);
+      const uint32_t tile_empty = smem_addr(op ? &bar->v_empty[0] : &bar->k_empty[0]);
+      constexpr int kPieces = 2 * (D / 64);                    // of 16 codes: rows r, r + 8, columns c (, c + 4)
       // 16 codes of a lane: those of 8 neighbouring lanes are the same columns of 8
       // rows, which the swizzles spread over all banks, here and in the tile.
       const int r = lane & 7, c = lane >> 3;
-      uint32_t raw_at[2 * (D / 64)], dst_at[2 * (D / 64)];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const int slot = r + 8 * h, col = c + 4 * x, i = h * (D / 64) + x;
-          const int line = D == 128 ? slot : slot >> 1, piece = D == 128 ? col : 4 * (slot & 1) + col;
-          raw_at[i] = 128 * line + 16 * (piece ^ (line & 7));
-          // As bf16: 16-byte columns 2 col and 2 col + 1, 8 of them to a 128-byte row.
-          dst_at[i] = (col >> 2) * L::kKVChunk + slot * 128 + (((2 * col) & 7) ^ (slot & 7)) * 16;
-        }
-      auto convert = [&](uint32_t dst, uint32_t src, uint32_t scale) {
-        // 2^120 times the scale, in bf16 as two factors (2^127 is the largest).
-        const uint32_t field = (scale >> 23) + 120u;
-        const uint32_t f = (min(field, 254u) << 7) * 0x10001u;
-        const uint32_t f_more = (field > 254u ? (field - 254u + 127u) << 7 : 0x3f80u) * 0x10001u;
-#pragma unroll
-        for (int i = 0; i < 2 * (D / 64); ++i) {
-          uint32_t w[4], y[8];
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(src + raw_at[i])
-                       : "memory");
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t x = __byte_perm(w[e >> 1], 0u, e & 1 ? 0x3424u : 0x1404u);
-            y[e] = mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), f);
-          }
-          if (f_more != 0x3f803f80u) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = mul_bf16x2(y[e], f_more);
-          }
-          st_shared_v4(dst + dst_at[i], y[0], y[1], y[2], y[3]);
-          st_shared_v4(dst + (dst_at[i] ^ 16u), y[4], y[5], y[6], y[7]);
-        }
+      const uint32_t raw_at = D == 128 ? 128 * r + 16 * (c ^ r) : 128 * (r >> 1) + 16 * ((4 * (r & 1) + c) ^ (r >> 1));
+      // As fp16, 16-byte columns 2 c and 2 c + 1 of a 128-byte row.
+      const uint32_t dst_at = 128 * r + 16 * ((2 * c) ^ r);
+      auto raw_of = [&](int x) {
+        if constexpr (D == 128) return (raw_at ^ (64u * (x & 1))) + 1024u * (x >> 1);
+        return x ? (raw_at ^ 64u) + 512u : raw_at;             // (4 lines on)
       };
-      Tile now = look_up(), next = look_up();
-      uint4 tail = tail_of(now);
-      if (now.there) {
-#pragma unroll
-        for (int i = 0; i < kRawStages; ++i) issue(__shfl_sync(0xffffffffu, now.rec, i));
-      }
-      int g = 0, taken = 0, unit = 0, flagged = 0x7fffffff;
+      auto dst_of = [&](int x) {
+        return D == 128 ? dst_at + L::kKVChunk * (x & 1) + 1024u * (x >> 1) : dst_at + 1024u * x;
+      };
       bool ok = true;
-      while (now.there) {
-        const Tile after = look_up();
-        const uint4 next_tail = tail_of(next);
-        if (!is_v) {
-          // The first flagged token: the lowest bit of its block's flags.
-          const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
-          int at = bits != 0 && now.rec >= 0
-                       ? (now.number * kPagesPerTile + part + kGather * lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
-          flagged = min(flagged, __reduce_min_sync(0xffffffffu, at));
-          if (now.last) {
-            if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged[part])[unit & 7] = flagged;
-            flagged = 0x7fffffff;
-            ++unit;
-          }
-        }
+      int s = 0;                                               // raw stage and its barrier's phase
+      uint32_t phase = 0;
+      for (int g = 0; ok; ++g) {
         const int st = g % L::kStages;
-        if (!(ok = mbar_wait_warp(empty0 + 8u * st, ((g / L::kStages) & 1) ^ 1, wc))) break;
-        const uint32_t dst0 = s_base + st * L::kKV;
+        bool end = false;
 #pragma unroll 1
-        for (int i = 0; i < kMine; ++i) {
-          const int rec = __shfl_sync(0xffffffffu, now.rec, i);
-          const uint32_t scale = __shfl_sync(0xffffffffu, is_v ? tail.y : tail.x, i);
-          const int s = taken % kRawStages;
-          ++taken;
-          const uint32_t dst = dst0 + (part + kGather * i) * kPageRows * 128;
-          if (rec >= 0) {
-            if (!(ok = mbar_wait_warp(raw_full + 8u * s, (phases >> s) & 1u, wc))) break;
-            phases ^= 1u << s;
-            in_flight &= ~(1u << s);
-            convert(dst, raw + s * L::kRaw, scale);
-          } else {
+        for (int i = 0; i < kPagesPerTile; ++i) {
+          if (!(ok = mbar_wait_warp(full + 8u * s, phase, wc))) break;
+          const int kind = kinds[s];
+          if (kind == kRawEnd) {
+            end = true;
+            break;
+          }
+          uint4 w[kPieces];
 #pragma unroll
-            for (int x = 0; x < 2 * (D / 64); ++x) {
-              st_shared_v4(dst + dst_at[x], 0u, 0u, 0u, 0u);
-              st_shared_v4(dst + (dst_at[x] ^ 16u), 0u, 0u, 0u, 0u);
-            }
+          for (int x = 0; x < kPieces; ++x) w[x] = ld_shared_v4(raw + s * L::kRaw + raw_of(x));
+          if (i == 0 && !(ok = wait_long(tile_empty + 8u * st, ((g / L::kStages) & 1) ^ 1))) break;
+          if (kind != kRawCodes) {                             // (the same for the whole warp)
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x)
+              w[x] = kind == kRawNone ? make_uint4(0u, 0u, 0u, 0u)
+                                      : make_uint4(without_nan(w[x].x), without_nan(w[x].y), without_nan(w[x].z), without_nan(w[x].w));
+          }
+          const uint32_t dst = tile0 + st * L::kKV + i * (kPageRows * 128);
+#pragma unroll
+          for (int x = 0; x < kPieces; ++x) {
+            st_shared_v4(dst + dst_of(x), e4m3x2_to_f16x2(w[x].x), e4m3x2_hi_to_f16x2(w[x].x), e4m3x2_to_f16x2(w[x].y),
+                         e4m3x2_hi_to_f16x2(w[x].y));
+            st_shared_v4(dst + (dst_of(x) ^ 16u), e4m3x2_to_f16x2(w[x].z), e4m3x2_hi_to_f16x2(w[x].z),
+                         e4m3x2_to_f16x2(w[x].w), e4m3x2_hi_to_f16x2(w[x].w));
           }
           __syncwarp();                                        // every lane has read the raw block
-          const int ahead = i + kRawStages;
-          const int more = __shfl_sync(0xffffffffu, ahead < kMine ? now.rec : next.rec, ahead % kMine);
-          if (ahead < kMine || next.there) issue(more);
+          if (lane == 0) mbar_arrive(empty + 8u * s);
+          if (++s == kRawStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (!ok) break;
+        if (!ok || end) break;
         fence_proxy_async_smem();
-        mbar_arrive(full0 + 8u * st);
-        ++g;
-        now = next;
-        next = after;
-        tail = next_tail;
-      }
-      if (!ok) {
-        // Raw blocks in flight must land before the CTA may exit: their barriers
-        // have one completion more than was waited for.
-        __syncwarp();
-        for (int s = 0; s < kRawStages; ++s) {
-          if (lane == 0 && (in_flight >> s) & 1u) mbar_wait(raw_full + 8u * s, (phases >> s) & 1u, wc, true);
-        }
-        __syncwarp();
+        mbar_arrive(tile_full + 8u * st);
       }
     }
   } else if constexpr (PAGED) {
@@ -847,7 +886,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
       tmem_dealloc(tmem, kTmemCols);
     }
   } else {
-    regs_increase<regs_softmax(SOURCE)>();
+    regs_increase<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2;                       // query tile of this warpgroup
     const int quarter = warp & 3;                  // TMEM lane quarter of this warp
@@ -858,6 +897,47 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
     const float sl2 = p.scale_log2;
     bool ok = true;
     int sx0 = 0;                                   // S_X tiles consumed in earlier units
+    int kv0 = 0;                                   // K/V tiles of earlier units
+    // 8-bit cache: each softmax warpgroup loads its Q tile (its first thread, as soon
+    // as the last S of the unit before is there), and each thread turns its row into
+    // fp16 in place.
+    const uint32_t q_tile = sQ + x * L::kQTile, q_full = smem_addr(&bar->q_full[x]);
+    auto load_q = [&](int band) {
+      const int k = unit_at(band);
+      if (quarter != 0 || lane != 0 || k >= p.num_units) return;
+      const Unit u = unit_info(k);
+      mbar_arrive_expect_tx(q_full, L::kQTile);
+      for (int c = 0; c < L::kChunks; ++c)
+        tma_load_3d(q_tile + c * L::kQChunk, &tq, q_full, c * 64, u.qblk * kRowsPerCta + x * kBM, u.zq);
+    };
+    // Returns what undoes the row's scaling.
+    auto turn_q = [&]() {
+      auto piece = [&](int i) { return q_tile + (i >> 3) * L::kQChunk + row * 128 + (((i & 7) ^ (row & 7)) << 4); };
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = ld_shared_v4(piece(i));
+        mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu),
+                      __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+      }
+      mx = max(mx & 0xffffu, mx >> 16);
+      // Largest element in [2^(E-127), 2^(E-126)); times 2^(141-E) it is in
+      // [2^14, 2^15).
+      const int fe = min(268 - static_cast<int>(mx >> 7), 253);
+      const float up = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+      auto turn = [&](uint32_t w) {
+        return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+      };
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = ld_shared_v4(piece(i));
+        st_shared_v4(piece(i), turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_addr(&bar->q_ready[x]));
+      return __uint_as_float(static_cast<uint32_t>(254 - fe) << 23);
+    };
+    if constexpr (KV8) load_q(0);
     int units = 0;
     for (int band = 0; ok; ++band) {
     const int k = unit_at(band);
@@ -874,13 +954,25 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
     float m = 0.f;                                 // stabiliser in use (exp2 domain)
     float l = 0.f;                                 // denominator relative to m (fp32 terms)
     float lr = 0.f;                                // same, bf16-rounded terms
+    float back = 1.f;                              // 8-bit cache: the factor of this row of Q
+    if constexpr (KV8) {
+      if (!mbar_wait_warp(q_full, units & 1, wc)) {
+        if (lane == 0 && quarter == 0) mbar_wait(q_full, units & 1, wc, true);
+        ok = false;
+        break;
+      }
+      back = turn_q();
+    }
 
     for (int j = 0; j < n_kv; ++j) {
-      if (!mbar_wait_warp(smem_addr(&bar->s_full[x]), static_cast<uint32_t>(sx0 + j) & 1u, wc)) {
+      if (!wait_long(smem_addr(&bar->s_full[x]), static_cast<uint32_t>(sx0 + j) & 1u)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      if constexpr (KV8) {
+        if (j == n_kv - 1) load_q(band + 1);       // (Q has been read for the last time)
+      }
       uint32_t r0[32], r1[32], r2[32], r3[32];
       ATTN47_TMEM_LD32(tl + colS + 0, r0);
       ATTN47_TMEM_LD32(tl + colS + 32, r1);
@@ -910,8 +1002,27 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
           s[c] = masked ? -INFINITY : s[c];
         }
       }
-      // Row maximum: a depth-5 tree of three-input maxima.
+      // 8-bit cache: a block's scales (see kOffScales) and its scores' factor
+      // (never 0, which the -inf of masked keys would make NaN).
+      auto scales = [&](int blk) {
+        return reinterpret_cast<const float4*>(smem + L::kOffScales)[(kv0 + j) % kScaleTiles * 8 + blk];
+      };
+      auto factor = [&](const float4& w) { return fmaxf(w.x * back, 1e-37f); };
+      // Row maximum: a depth-5 tree of three-input maxima.  (8-bit cache: of the
+      // exponents of P'.)
       auto row_max = [&]() {
+        if constexpr (KV8) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int blk = 0; blk < 8; ++blk) {
+            const float* y = s + 16 * blk;
+            const float a = fmax3(fmax3(y[0], y[1], y[2]), fmax3(y[3], y[4], y[5]), fmax3(y[6], y[7], y[8]));
+            const float b = fmax3(fmax3(y[9], y[10], y[11]), fmax3(y[12], y[13], y[14]), y[15]);
+            const float4 w = scales(blk);
+            mx = fmaxf(mx, fmaf(fmaxf(a, b), factor(w), w.y));
+          }
+          return mx;
+        }
         float t[43], u[15];
 #pragma unroll
         for (int i = 0; i < 42; ++i) t[i] = fmax3(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
@@ -930,8 +1041,38 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
       // fp32 numerators and gives the LSE.  P_X goes over the first 64
       // columns of S_X (keys 2c, 2c+1 in column c), the first half while the
       // second is computed.
-      float lt, lrt;                               // this tile's two sums
+      float lt, lrt;                               // this tile's two sums (8-bit cache: lrt is that of P')
       auto numerators = [&]() {
+        if constexpr (KV8) {
+          lt = lrt = 0.f;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+              const float4 w = scales(half * 4 + blk);
+              const float a = factor(w), b = w.y - m;
+              const uint64_t sc2 = f2_pack(a, a), add2 = f2_pack(b, b);
+              uint64_t acc[2] = {0, 0};
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const int i = half * 64 + blk * 16 + 2 * c;
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(s[i], s[i + 1]), sc2, add2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                acc[c & 1] = f2_add(acc[c & 1], f2_pack(p0, p1));
+                pk[blk * 8 + c] = pack_f16x2(p0, p1);
+              }
+              float e0, e1;
+              f2_unpack(f2_add(acc[0], acc[1]), e0, e1);
+              const float sum = e0 + e1;
+              lrt += sum;
+              lt = fmaf(sum, w.z, lt);
+            }
+            ATTN47_TMEM_ST32(tl + colS + half * 32, pk);
+          }
+          return;
+        }
         const uint64_t sc2 = f2_pack(sl2, sl2);
         const uint64_t nm2 = f2_pack(-m, -m);
         uint64_t accE[4] = {0, 0, 0, 0};
@@ -964,7 +1105,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
       // more than kTau, rescaling the sums and O_X (which holds PV_X(0..j-1),
       // complete since S_X(j) completed after it).
       auto restabilise = [&](float mt) {
-        const bool need = mt > m + kTau;
+        const bool need = mt > m + (KV8 ? 0.f : kTau);
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? mt : m;
           const float alpha = ex2(m - m_new);
@@ -998,7 +1139,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
         if (j == 0 || pass == 1) {                 // the tile's maximum is needed
-          const float mt = row_max() * sl2;
+          const float mt = KV8 ? row_max() - kHigh8 : row_max() * sl2;
           if (j == 0)
             m = (mt == -INFINITY) ? 0.f : mt;
           else
@@ -1006,8 +1147,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
         }
         numerators();
         if (j == 0 || pass == 1) break;
-        // (Values of an 8-bit cache reach 2^73: 2^40 keeps the sums of P V finite.)
-        const bool big = !(lt <= (KV8 ? 0x1p40f : 0x1p100f));
+        const bool big = !(KV8 ? lrt <= 65504.f : lt <= 0x1p100f);   // (P' has to fit in fp16)
         if (!__any_sync(0xffffffffu, big)) break;
       }
       l += lt;
@@ -1022,7 +1162,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
     ok = __all_sync(0xffffffffu, ok);
     if (ok && mbar_wait_warp(smem_addr(&bar->o_done[x]), static_cast<uint32_t>(units & 1), wc)) {
       tc_fence_after();
-      float lsum = lr;
+      float lsum = KV8 ? l : lr;
       if constexpr (SUMV) {
         uint32_t rs[32];
         ATTN47_TMEM_LD32(tl + colO + D, rs);
@@ -1033,8 +1173,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
       bool spoilt = false;
       if constexpr (KV8) {
         // (The gather wrote this before the unit's last tile was full.)
-        const volatile int* flagged = &bar->first_flagged[0][0];
-        spoilt = qpos >= min(flagged[units & 7], flagged[8 + (units & 7)]);
+        spoilt = qpos >= reinterpret_cast<const volatile int*>(bar->first_flagged)[units & 15];
         if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
         if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
       }
@@ -1068,6 +1207,7 @@ __global__ void __launch_bounds__(threads_of(SOURCE), 1)
       ok = false;
     }
     sx0 += n_kv;
+    kv0 += u.nB;
     ++units;
     }
     tc_fence_before();
@@ -1108,7 +1248,7 @@ cudaError_t launch_t(const FwdLaunch& a) {
   p.packed = a.rows != a.N;
   // Persistent: one CTA per SM (shared memory allows one), each walking units.
   const unsigned grid = static_cast<unsigned>(min(p.num_units, a.sms > 0 ? a.sms : 1));
-  return launch_pdl(kern, dim3(grid), dim3(threads_of(SOURCE)), L::kSmem, a.stream, *a.tq, *a.tk, *a.tv, p);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), L::kSmem, a.stream, *a.tq, *a.tk, *a.tv, p);
 }
 
 }  // namespace
@@ -1118,7 +1258,7 @@ int fwd_box_rows() { return kBM; }
 cudaError_t launch_fwd_sm103(const FwdLaunch& a) {
   if (a.paged) {
     const long long pairs = static_cast<long long>(a.B) * ((a.N + kRowsPerCta - 1) / kRowsPerCta);
-    const bool sorted = a.B <= kSortMaxSeqs && pairs <= kSortMaxPairs;
+    const bool sorted = a.B <= kSortMaxSeqs && pairs <= sort_max_pairs(a.kv_cache != nullptr ? kPagedKv8 : kPagedBf16);
     if (a.kv_cache != nullptr) {
       if (a.d == 128) return sorted ? launch_t<128, true, kPagedKv8, true>(a) : launch_t<128, true, kPagedKv8>(a);
       return sorted ? launch_t<64, true, kPagedKv8, true>(a) : launch_t<64, true, kPagedKv8>(a);
