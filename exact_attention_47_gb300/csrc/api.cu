@@ -932,7 +932,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
                                  static_cast<cuuint64_t>(num_seqs) * heads};
     alignas(64) CUtensorMap tq, blocks;
     attn_status_t enc = encode_bf16(&tq, q, 3, qdims, qbox);
-    if (enc == ATTN_OK) enc = encode_kv8(&blocks, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d, d / 8);
+    if (enc == ATTN_OK) enc = encode_kv8(&blocks, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d, d / 4);
     if (enc != ATTN_OK) return enc;
     attn47::FwdLaunch f;
     f.tq = &tq;

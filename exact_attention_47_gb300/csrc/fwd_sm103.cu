@@ -57,28 +57,34 @@
 // Paged mode over an 8-bit cache (kPagedKv8): the same, but the cache holds the
 // new tokens already, sequence b's row i is the token at position seq_lens[b] -
 // N + i (before position 0 it sees nothing: O = 0, LSE = -inf), and everything is
-// fp16 in place of bf16: an e4m3 code is an fp16 number, one conversion
-// instruction makes two, and the gather has nothing else to do (in bf16 it took
-// four integer steps and a product more, and the whole 337 us where this takes
-// 243).  The scales, powers of two for each 16 keys, act where they cost
-// least.  With S the product with the K codes, b a 16-key block, back the row's
+// fp16 in place of bf16: an e4m3 code is an fp16 number, and one conversion
+// instruction makes two.  The scales, powers of two for each 16 keys, act where they
+// cost least.  With S the product with the K codes, b a 16-key block, back the row's
 // factor (below) and e_b = log2 of the V scale:
 //   P'_j = 2^(S_j scale_Kb back + e_b - m),   O = sum P'_j code_j / l,
 //   l = sum over blocks 2^-e_b sum P'_j
 // so a block's scales are the two constants of the FMA before the exponential, and
 // one more FMA for a block's sum.  P' is at most 2^16 (its sum over a tile is
 // checked, a tile beyond is redone with m moved), 2^8 at the maximum; what rounds
-// to zero in fp16 is 2^-32 of the largest contribution.  The rows of Q are turned
-// into fp16 in shared memory, each by a power of two of its own that brings its
-// largest element to [2^14, 2^15) (warp 8 tile A, warp 10 tile B, which also load
-// them).  Warp 11 looks up the blocks and their scales, two warps to an operand, of
-// a fourth warpgroup, load codes two blocks ahead, convert and store them into the
-// swizzled tile.  NaN codes of V are cleared where there can be any (a sequence's
-// last block, flagged blocks); warp 11 keeps the first position of a flagged token,
-// and a row that sees that position gets NaN in the epilogue.
+// to zero in fp16 is 2^-32 of the largest contribution.  The rows of Q, which each
+// softmax warpgroup loads for itself, are turned into fp16 in shared memory, each by
+// a power of two of its own that brings its largest element to [2^14, 2^15).
+// Warp 8 looks up the blocks and their scales, a tile ahead, and has the TMA bring
+// their codes into a ring of six; warps 10 (K) and 11 (V) take two at a time from
+// there, convert them and store them into the swizzled tile.  NaN codes are cleared
+// where there can be any (a sequence's last block, flagged blocks); the look-up keeps
+// the first position of a flagged token, and a row that sees that position gets NaN
+// in the epilogue.
 // With fewer than 256 new tokens the rows of all query heads that share a KV head
 // make one row of query blocks (row = head in the group times N + token), so that
 // a 256-row unit is not mostly empty.
+// What bounds it is the conversion: two instructions a warp shares with the softmax
+// warps of its scheduler, 2400 (K) and 4000 (V) of a tile's 4700 cycles.  Converting
+// by shifts and masks was slower (7 instructions for 4 codes instead of 4: 284 us and
+// up where this takes 231), so was converting in place in the stage (300 us: a stage
+// is then held for the whole way), each gather warp issuing its own TMA copies (291)
+// and a fourth warpgroup with two warps to an operand (300: too few registers are
+// left for the softmax).
 #include <cuda_runtime.h>
 
 #include "fwd_sm103.h"
@@ -100,15 +106,18 @@ constexpr int kWarpMma = 9;
 // warpgroups then take 216 and the producer/MMA warpgroup keeps 72:
 // 256 x 216 + 128 x 72 = 64512, and per sub-partition 216 + 216 + 72 = 504
 // = 3 x 168, so the increase never waits for registers nobody frees.
-constexpr uint32_t kRegsSoftmax = 216;
-constexpr uint32_t kRegsOther = 72;
+// (8-bit cache: the gather spills at 72.  Timed with 216 + 72, 208 + 88 and 200 +
+// 104: d = 128 takes 263, 237 and 231 us for 256-token chunks of 6 sequences, d = 64
+// 22.9, 22.7 and 23.1 us for a padded batch.)
+__host__ __device__ constexpr uint32_t regs_softmax(bool kv8, int d) { return !kv8 ? 216 : d == 128 ? 200 : 208; }
+__host__ __device__ constexpr uint32_t regs_other(bool kv8, int d) { return !kv8 ? 72 : d == 128 ? 104 : 88; }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
 constexpr float kHigh8 = 8.0f;      // 8-bit cache: log2 of P' at the maximum
 
 __host__ __device__ constexpr int sort_max_pairs(int source) { return source == kPagedKv8 ? 1024 : 2048; }
-constexpr int kRawStages = 6;       // 8-bit cache: raw blocks in flight of K and of V
+constexpr int kRawStages = 6;       // 8-bit cache: raw blocks (K and V codes) in flight, taken in pairs
 constexpr int kScaleTiles = 16;     // tiles whose scales are kept
 
 // SUMV (d = 64 with contiguous K/V): the row sums of P come from the tensor
@@ -133,11 +142,12 @@ struct FwdLayout {
   static constexpr int kOffCtx = kOffBar + 640;          // paged: ctx_b of each sequence
   static constexpr int kOffOrder = kOffCtx + 4 * 256;    // paged: (b << 16 | qblk) of each cost rank
   // 8-bit cache: (K scale times scale log2 e, log2 of V's, 1 / V's) of the 8 blocks
-  // of tile t at t % kScaleTiles; rings of raw blocks of K and V.
+  // of tile t at t % kScaleTiles; a ring of raw blocks.
   static constexpr int kOffScales = kOffOrder + 4 * sort_max_pairs(SOURCE);
   static constexpr int kOffRaw = (kOffScales + kScaleTiles * 8 * 16 + 1023) / 1024 * 1024;
-  static constexpr int kRaw = 16 * D;                         // a record's K or V codes
-  static constexpr int kSmem = (SOURCE == kPagedKv8 ? kOffRaw + 2 * kRawStages * kRaw : kOffScales) + 1024;   // + alignment slack
+  static constexpr int kRawHalf = 16 * D;                     // a record's K or V codes
+  static constexpr int kRaw = 2 * kRawHalf;
+  static constexpr int kSmem = (SOURCE == kPagedKv8 ? kOffRaw + kRawStages * kRaw : kOffScales) + 1024;   // + alignment slack
   static constexpr uint32_t kColS0 = 0, kColS1 = 128;
   static constexpr uint32_t kColO0 = 256, kColO1 = SUMV ? 384 : 256 + D;
 };
@@ -148,12 +158,12 @@ struct FwdBarriers {
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t o_free[2];                 // O_X read out by the epilogue of the previous unit
   uint64_t mma_final;
-  // 8-bit cache: Q tile x is fp16; raw block s of K / V has come / has been read, and
+  // 8-bit cache: Q tile x is fp16; raw block s has come / has been read, and
   // what it is.
-  uint64_t q_ready[2], raw_full[2][kRawStages], raw_empty[2][kRawStages];
+  uint64_t q_ready[2], raw_full[kRawStages], raw_empty[kRawStages];
   uint32_t tmem_base;
   int abort;
-  int raw_kind[2][kRawStages], raw_fills[2][kRawStages];
+  int raw_kind[kRawStages], raw_fills[kRawStages];
   // The first position of a flagged token in unit u (of the CTA's), at u % 16: the
   // look-up is at most two tiles ahead of the gather, that kStages ahead of the MMAs,
   // and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1), which also bounds
@@ -315,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&bar->mma_final), 1);
     if constexpr (KV8) {
       for (int x = 0; x < 2; ++x) mbar_init(smem_addr(&bar->q_ready[x]), kBM);
-      for (int x = 0; x < 2 * kRawStages; ++x) {
-        mbar_init(smem_addr(&bar->raw_full[0][0] + x), 1);
-        mbar_init(smem_addr(&bar->raw_empty[0][0] + x), 1);
-        (&bar->raw_fills[0][0])[x] = 0;
+      for (int x = 0; x < kRawStages; ++x) {
+        mbar_init(smem_addr(&bar->raw_full[x]), 1);
+        mbar_init(smem_addr(&bar->raw_empty[x]), 2);
+        bar->raw_fills[x] = 0;
       }
     }
     bar->abort = 0;
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return KV8 ? mbar_wait_sleep_warp(b, parity, wc) : mbar_wait_warp(b, parity, wc);
   };
   if (warp >= 8) {
-  regs_decrease<kRegsOther>();
+  regs_decrease<regs_other(KV8, D)>();
   if (KV8 && warp == kWarpLoad) {
     // --------------------------------------- the blocks of the tiles, 8-bit records
     // Lane i < 8 looks up block i of a tile.  Table entries are read two tiles
@@ -469,16 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     next = read_table();
     int unit = 0, flagged = 0x7fffffff, n = 0;
     bool ok = true;
-    // Block number `at` of an operand into its ring.
-    auto fill = [&](int op, int at, int rec, int what) {
+    // Block number `at` into the ring.
+    auto fill = [&](int at, int rec, int what) {
       const int s = at % kRawStages;
-      const uint32_t full = smem_addr(&bar->raw_full[op][s]);
-      if (!mbar_wait_sleep(smem_addr(&bar->raw_empty[op][s]), ((at / kRawStages) & 1) ^ 1, wc)) return false;
-      reinterpret_cast<volatile int*>(bar->raw_kind[op])[s] = what;
-      ++bar->raw_fills[op][s];
+      const uint32_t full = smem_addr(&bar->raw_full[s]);
+      if (!mbar_wait_sleep(smem_addr(&bar->raw_empty[s]), ((at / kRawStages) & 1) ^ 1, wc)) return false;
+      reinterpret_cast<volatile int*>(bar->raw_kind)[s] = what;
+      ++bar->raw_fills[s];
       mbar_arrive_expect_tx(full, rec >= 0 ? L::kRaw : 0);
-      if (rec >= 0)
-        tma_load_3d(smem_addr(smem + L::kOffRaw) + (op * kRawStages + s) * L::kRaw, &tk, full, 0, op * (D / 8), rec);
+      if (rec >= 0) tma_load_3d(smem_addr(smem + L::kOffRaw) + s * L::kRaw, &tk, full, 0, 0, rec);
       return true;
     };
     for (;; ++n) {
@@ -506,11 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, 0.f);
       }
       const int kind = now_rec < 0 ? kRawNone : now_ends || bits != 0 ? kRawCareful : kRawCodes;
-      // Blocks three at a time (half a ring), K and V at once: lane 3 op + i.
-      for (int first = 0; ok && first < kPagesPerTile; first += 3) {
-        const int op = lane / 3, i = first + lane % 3;
+      // Two blocks at a time.
+      for (int first = 0; ok && first < kPagesPerTile; first += 2) {
+        const int i = first + (lane & 1);
         const int rec = __shfl_sync(0xffffffffu, now_rec, i), what = __shfl_sync(0xffffffffu, kind, i);
-        if (lane < 6 && i < kPagesPerTile) ok = fill(op, n * kPagesPerTile + i, rec, what);
+        if (lane < 2) ok = fill(n * kPagesPerTile + i, rec, what);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
@@ -521,15 +530,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tail = next_tail;
     }
     // The end, for both gather warps; then the next kernel in the stream may set up.
-    if (ok && lane < 2) ok = fill(lane, n * kPagesPerTile, -1, kRawEnd);
+    if (ok && lane < 2) ok = fill(n * kPagesPerTile + lane, -1, kRawEnd);
     ok = __all_sync(0xffffffffu, ok);
     pdl_launch_dependents();
     __syncwarp();
     if (!ok) {
       // Raw blocks in flight must land before the CTA may exit.
-      for (int s = 0; s < 2 * kRawStages; ++s) {
-        const int fills = (&bar->raw_fills[0][0])[s];
-        if (fills) mbar_wait_warp_drain(smem_addr(&bar->raw_full[0][0] + s), (fills - 1) & 1, wc);
+      for (int s = 0; s < kRawStages; ++s) {
+        const int fills = bar->raw_fills[s];
+        if (fills) mbar_wait_warp_drain(smem_addr(&bar->raw_full[s]), (fills - 1) & 1, wc);
       }
     }
   } else if (!KV8 && warp == kWarpLoad) {
@@ -757,9 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpGatherK || warp == kWarpGatherV) {
       // -------------------------------------- raw blocks into fp16 K / V tiles
       const int op = warp - kWarpGatherK;                      // 0: K, 1: V
-      const uint32_t raw = smem_addr(smem + L::kOffRaw) + op * kRawStages * L::kRaw;
-      const uint32_t full = smem_addr(&bar->raw_full[op][0]), empty = smem_addr(&bar->raw_empty[op][0]);
-      const volatile int* kinds = bar->raw_kind[op];
+      const uint32_t raw = smem_addr(smem + L::kOffRaw) + op * L::kRawHalf;
+      const uint32_t full = smem_addr(&bar->raw_full[0]), empty = smem_addr(&bar->raw_empty[0]);
+      const volatile int* kinds = bar->raw_kind;
       const uint32_t tile0 = op ? sV : sK;
       const uint32_t tile_full = smem_addr(op ? &bar->v_full[0] : &bar->k_full[0]);
       const uint32_t tile_empty = smem_addr(op ? &bar->v_empty[0] : &bar->k_empty[0]);
@@ -784,34 +793,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = g % L::kStages;
         bool end = false;
 #pragma unroll 1
-        for (int i = 0; i < kPagesPerTile; ++i) {
+        for (int i = 0; i < kPagesPerTile; i += 2) {
           if (!(ok = mbar_wait_warp(full + 8u * s, phase, wc))) break;
-          const int kind = kinds[s];
-          if (kind == kRawEnd) {
+          if (!(ok = mbar_wait_warp(full + 8u * (s + 1), phase, wc))) break;
+          const int kind[2] = {kinds[s], kinds[s + 1]};
+          if (kind[0] == kRawEnd) {
             end = true;
             break;
           }
-          uint4 w[kPieces];
+          uint4 w[2 * kPieces];
 #pragma unroll
-          for (int x = 0; x < kPieces; ++x) w[x] = ld_shared_v4(raw + s * L::kRaw + raw_of(x));
+          for (int x = 0; x < 2 * kPieces; ++x) w[x] = ld_shared_v4(raw + (s + x / kPieces) * L::kRaw + raw_of(x % kPieces));
           if (i == 0 && !(ok = wait_long(tile_empty + 8u * st, ((g / L::kStages) & 1) ^ 1))) break;
-          if (kind != kRawCodes) {                             // (the same for the whole warp)
+          if (kind[0] != kRawCodes || kind[1] != kRawCodes) {  // (the same for the whole warp)
 #pragma unroll
-            for (int x = 0; x < kPieces; ++x)
-              w[x] = kind == kRawNone ? make_uint4(0u, 0u, 0u, 0u)
-                                      : make_uint4(without_nan(w[x].x), without_nan(w[x].y), without_nan(w[x].z), without_nan(w[x].w));
+            for (int x = 0; x < 2 * kPieces; ++x)
+              w[x] = kind[x / kPieces] == kRawNone
+                         ? make_uint4(0u, 0u, 0u, 0u)
+                         : make_uint4(without_nan(w[x].x), without_nan(w[x].y), without_nan(w[x].z), without_nan(w[x].w));
           }
           const uint32_t dst = tile0 + st * L::kKV + i * (kPageRows * 128);
 #pragma unroll
-          for (int x = 0; x < kPieces; ++x) {
-            st_shared_v4(dst + dst_of(x), e4m3x2_to_f16x2(w[x].x), e4m3x2_hi_to_f16x2(w[x].x), e4m3x2_to_f16x2(w[x].y),
-                         e4m3x2_hi_to_f16x2(w[x].y));
-            st_shared_v4(dst + (dst_of(x) ^ 16u), e4m3x2_to_f16x2(w[x].z), e4m3x2_hi_to_f16x2(w[x].z),
+          for (int x = 0; x < 2 * kPieces; ++x) {
+            const uint32_t to = dst + x / kPieces * (kPageRows * 128);
+            st_shared_v4(to + dst_of(x % kPieces), e4m3x2_to_f16x2(w[x].x), e4m3x2_hi_to_f16x2(w[x].x),
+                         e4m3x2_to_f16x2(w[x].y), e4m3x2_hi_to_f16x2(w[x].y));
+            st_shared_v4(to + (dst_of(x % kPieces) ^ 16u), e4m3x2_to_f16x2(w[x].z), e4m3x2_hi_to_f16x2(w[x].z),
                          e4m3x2_to_f16x2(w[x].w), e4m3x2_hi_to_f16x2(w[x].w));
           }
-          __syncwarp();                                        // every lane has read the raw block
-          if (lane == 0) mbar_arrive(empty + 8u * s);
-          if (++s == kRawStages) {
+          __syncwarp();                                        // every lane has read the raw blocks
+          if (lane < 2) mbar_arrive(empty + 8u * (s + lane));
+          if ((s += 2) == kRawStages) {
             s = 0;
             phase ^= 1;
           }
@@ -886,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_dealloc(tmem, kTmemCols);
     }
   } else {
-    regs_increase<kRegsSoftmax>();
+    regs_increase<regs_softmax(KV8, D)>();
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2;                       // query tile of this warpgroup
     const int quarter = warp & 3;                  // TMEM lane quarter of this warp
