@@ -894,9 +894,24 @@ attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records,
   return ATTN_OK;
 }
 
-// Whether queries go in tiles of 128 rows (the tensor cores' work) or by passes of
-// up to 16 rows over the blocks (the memory's).
-bool kv8_in_tiles(int Hq, int Hkv, int N) { return Hq / Hkv * N > 32; }
+// Whether an 8-bit prefill goes through the tiles of the forward kernel or, `group`
+// query rows of a KV head at a time, through passes of the decode kernel.  Both take
+// time in proportion to the lengths: a wave of 152 CTAs about 2.7 us for 128 keys, a
+// pass of one KV head of one sequence, split over all SMs, 5.5 ns.  So a pass is
+// 1 / 480 of a wave, and the tiles are taken where there are more than 3 * 152 passes
+// to a wave.  Measured, passes against tiles: 12 heads over 2 KV heads, d = 128, 6000
+// keys, 4 sequences of 8 new tokens 29 and 129 us, of 128 121 and 131; 16 sequences
+// of 32 121 and 135, of 64 217 and 133; 32 heads over 8, 64 sequences of 8 new tokens
+// and 1000 keys (4 waves) 68 and 115, of 32 201 and 121; 16 heads over 4, d = 64,
+// 16 sequences of 32 new tokens and 6000 keys 94 and 125, of 64 168 and 127.
+bool kv8_packed(int N) { return N < 2 * attn47::fwd_box_rows(); }
+bool kv8_in_tiles(int num_seqs, int Hq, int Hkv, int N, int d) {
+  constexpr long long kCtas = 152;
+  const long long seqs = num_seqs, rows = static_cast<long long>(Hq / Hkv) * N, tile = 2 * attn47::fwd_box_rows();
+  const long long units = kv8_packed(N) ? seqs * Hkv * ((rows + tile - 1) / tile) : seqs * Hq * ((N + tile - 1) / tile);
+  const long long waves = (units + kCtas - 1) / kCtas;
+  return seqs * Hkv * attn47::decode_kv8_rows(Hq, Hkv, N, d).groups > 3 * kCtas * waves;
+}
 
 // Both attentions over an 8-bit cache.
 attn_status_t attend_kv8(const char* what, bool decode, const void* q, const void* kv_cache, const int32_t* block_table,
@@ -909,7 +924,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
   if (Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && N > 0) {
     if (static_cast<long long>(Hq / Hkv) * N >= 0x7fffff00LL)
       return fail(ATTN_ERR_UNSUPPORTED, "problem too large for one launch");
-    tiles = !decode && kv8_in_tiles(Hq, Hkv, N);
+    tiles = !decode && kv8_in_tiles(num_seqs, Hq, Hkv, N, d);
     if (!tiles) {
       need = attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
       passes = attn47::decode_kv8_rows(Hq, Hkv, N, d).groups;
@@ -925,7 +940,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
   if (st != ATTN_OK || dev == nullptr) return st;
   if (tiles) {
     // The heads of a group in one row of query blocks where N is short.
-    const bool packed = N < 2 * attn47::fwd_box_rows();
+    const bool packed = kv8_packed(N);
     const int heads = packed ? Hkv : Hq, rows = packed ? Hq / Hkv * N : N;
     const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(attn47::fwd_box_rows()), 1};
     const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
@@ -1642,7 +1657,7 @@ attn_status_t attn_decode_paged_kv8(const void* q, const void* kv_cache, const i
 
 size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int N, int d) {
   if (num_seqs <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0 || Hq % Hkv != 0 ||
-      static_cast<long long>(Hq / Hkv) * N >= 0x7fffff00LL || kv8_in_tiles(Hq, Hkv, N))
+      static_cast<long long>(Hq / Hkv) * N >= 0x7fffff00LL || kv8_in_tiles(num_seqs, Hq, Hkv, N, d))
     return 0;
   return attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
 }

@@ -3,10 +3,7 @@ one query per sequence, and the last N tokens of each.
 
 Bounds.  q, codes and scales enter exactly and the scores are fp32 sums: with
 these inputs their error is under 2^-12, and 2 2^-12 of max|V| in O.  Numerators
-are rounded to 11 bits (a decode and few rows): 2^-11 of max|V|; or to bf16's 8
-bits, their sum of the rounded ones (tiles of 128 rows): a change of 2^-8 in each
-weight moves O by up to 2^-8 max|V - O|, under 2^-7 max|V|.  Then O's own rounding
-to bf16, 2^-8 |O|.  The LSE uses the unrounded numerators: 2^-16 covers the fp32
+are rounded to 11 bits: 2^-11 of max|V|.  Then O's own rounding to bf16, 2^-8 |O|.  The LSE uses the unrounded numerators: 2^-16 covers the fp32
 sums, relative to its size where that is more than 16.
 """
 
@@ -45,7 +42,29 @@ def case(lens, Hq, Hkv, d, seed, N=None, garbage=0xFF):
     return randn(seed + 2, *shape), cache, table, torch.tensor(lens, dtype=torch.int32)
 
 
-def compare(o, lse, ref, cache, d, tile=False, what=""):
+def prefill(args, times=1, **kw):
+    """The call on GPU tensors, its batch `times` over: the copies come out alike."""
+    q, cache, table, lens = args
+    S = q.shape[0]
+    o, lse = attn.attn_prefill_paged_kv8(q.repeat(times, 1, 1, 1), cache, table.repeat(times, 1), lens.repeat(times), **kw)
+    torch.cuda.synchronize()
+    same = lambda a, b: torch.equal(torch.nan_to_num(a, 7.0), torch.nan_to_num(b, 7.0))
+    for i in range(1, times):
+        assert same(o[i * S: i * S + S], o[:S]) and same(lse[i * S: i * S + S], lse[:S])
+    return o[:S], lse[:S]
+
+
+def ways(S, Hq, Hkv, N, d):
+    """How often a batch has to be repeated for each way through it: passes over the
+    cache, which use a workspace, and tiles of query rows, for many rows in all,
+    which use none."""
+    found = {}
+    for r in list(range(1, 25)) + [50, 100, 200, 500]:
+        found.setdefault(attn.attn_prefill_paged_kv8_workspace_size(S * r, Hq, Hkv, N, d) == 0, r)
+    return list(found.values())
+
+
+def compare(o, lse, ref, cache, d, what=""):
     o_ref, lse_ref = ref
     o, lse = to64(o), lse.double().cpu().numpy()
     nan = np.isnan(lse_ref)
@@ -55,7 +74,7 @@ def compare(o, lse, ref, cache, d, tile=False, what=""):
     assert np.array_equal(np.isneginf(lse), none) and np.all(o[none] == 0), what
     top = max(np.nanmax(np.abs(np.where(np.isfinite(x), x, 0))) for x in oracle.kv8_unpack(cache, d)[1:2])
     fine = ~nan & ~none
-    lim = 2.0 ** -8 * np.abs(o_ref[fine]) + (2.0 ** -7 + 2.0 ** -11 if tile else 2.0 ** -10) * top
+    lim = 2.0 ** -8 * np.abs(o_ref[fine]) + 2.0 ** -10 * top
     err = np.abs(o[fine] - o_ref[fine])
     assert np.all(err <= lim), "%s: O at %.3g of its bound" % (what, (err / lim).max())
     lerr = np.abs(lse[fine] - lse_ref[fine])
@@ -104,11 +123,16 @@ def test_prefill_against_the_oracle(lens, Hq, Hkv, N, d, garbage):
     """Rows of sequences shorter than N among them; garbage past the ends is NaN
     or the largest numbers."""
     q, cache, table, sl = case(lens, Hq, Hkv, d, seed=N, N=N, garbage=garbage)
-    o, lse = attn.attn_prefill_paged_kv8(*(x.to(DEV) for x in (q, cache, table, sl)))
-    torch.cuda.synchronize()
-    assert attn.device_status() == 0
     ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), lens, d ** -0.5, d)
-    compare(o, lse, ref, cache.numpy(), d, tile=Hq // Hkv * N > 16)
+    for times in ways(len(lens), Hq, Hkv, N, d):
+        o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
+        assert attn.device_status() == 0
+        compare(o, lse, ref, cache.numpy(), d, what="%d times" % times)
+
+
+def test_the_two_ways_are_both_tested():
+    both = [c for c in PREFILLS if len(ways(len(c[0]), *c[1:])) == 2]
+    assert {c[4] for c in both} == {64, 128} and {c[3] >= 256 for c in both} == {True, False}
 
 
 def test_a_query_alone_is_a_decode():
@@ -134,17 +158,18 @@ def test_flagged_tokens(N, d):
         word = rec[32 * d + 8: 32 * d + 12].view(torch.int32)
         word |= 1 << (16 * kind + p % 16)
     args = [x.to(DEV) for x in (q, cache, table, sl)]
-    o, lse = attn.attn_decode_paged_kv8(*args) if N is None else attn.attn_prefill_paged_kv8(*args)
-    torch.cuda.synchronize()
     f = oracle.decode_paged_kv8 if N is None else oracle.prefill_paged_kv8
     ref = f(q.double().numpy(), cache.numpy(), table.numpy(), lens, d ** -0.5, d)
     assert np.isnan(ref[1]).any() and not np.isnan(ref[1]).all()
-    compare(o, lse, ref, cache.numpy(), d, tile=N == 60)
+    for times in (0,) if N is None else ways(4, Hq, Hkv, N, d):
+        o, lse = attn.attn_decode_paged_kv8(*args) if N is None else prefill(args, times)
+        torch.cuda.synchronize()
+        compare(o, lse, ref, cache.numpy(), d)
     assert attn.device_status() == 0
 
 
-@pytest.mark.parametrize("N", [None, 3, 40])
-def test_bad_blocks_and_lengths_are_reported(N):
+@pytest.mark.parametrize("N,times", [(None, 0), (3, 1), (64, 1), (64, 50)])
+def test_bad_blocks_and_lengths_are_reported(N, times):
     """A block outside the pool counts as keys and values of zero in tiles, and
     is left out by the others; a length outside the table is clamped.  What is
     beside them is as ever."""
@@ -152,7 +177,7 @@ def test_bad_blocks_and_lengths_are_reported(N):
     lens = [90, 50, 200]
     q, cache, table, sl = case(lens, Hq, Hkv, d, seed=5, N=N)
     args = [x.to(DEV) for x in (q, cache, table, sl)]
-    call = attn.attn_decode_paged_kv8 if N is None else attn.attn_prefill_paged_kv8
+    call = attn.attn_decode_paged_kv8 if N is None else lambda *x: prefill(x, times)
     good, _ = call(*args)
     bad = table.clone()
     bad[0, 1], bad[0, 3] = cache.shape[0], -1
@@ -168,7 +193,7 @@ def test_bad_blocks_and_lengths_are_reported(N):
     assert torch.equal(got[0], good[0])
 
 
-@pytest.mark.parametrize("N", [None, 2, 33])
+@pytest.mark.parametrize("N", [None, 2, 33, 66])
 @pytest.mark.parametrize("qs,ks,vs", [(1.0, 0, 0), (2.0 ** 20, -30, 40), (2.0 ** -30, 20, -60), (1e-36, 64, 64), (0.0, 0, 0),
                                       (6.0, 1, -3)])
 def test_values_of_every_size(N, qs, ks, vs):
@@ -182,11 +207,12 @@ def test_values_of_every_size(N, qs, ks, vs):
     cache[..., 32 * d: 32 * d + 8] = tail.contiguous().view(torch.uint8)
     scale = d ** -0.5 * (2.0 ** 10 if qs == 2.0 ** 20 else 1.0)
     args = [x.to(DEV) for x in (q, cache, table, sl)]
-    o, lse = (attn.attn_decode_paged_kv8 if N is None else attn.attn_prefill_paged_kv8)(*args, scale=scale)
-    torch.cuda.synchronize()
     f = oracle.decode_paged_kv8 if N is None else oracle.prefill_paged_kv8
     ref = f(q.double().numpy(), cache.numpy(), table.numpy(), lens, np.float32(scale).astype(np.float64), d)
-    compare(o, lse, ref, cache.numpy(), d, tile=N == 33)
+    for times in (0,) if N is None else ways(2, Hq, Hkv, N, d):
+        o, lse = attn.attn_decode_paged_kv8(*args, scale=scale) if N is None else prefill(args, times, scale=scale)
+        torch.cuda.synchronize()
+        compare(o, lse, ref, cache.numpy(), d)
     assert attn.device_status() == 0
 
 
@@ -207,29 +233,32 @@ def test_scores_that_jump(N):
         t[0] *= 2.0 ** float(e[i])
         t[1] *= 2.0 ** (30 * (i % 3 - 1))
     args = [x.to(DEV) for x in (q, cache, table, sl)]
-    o, lse = (attn.attn_decode_paged_kv8 if N is None else attn.attn_prefill_paged_kv8)(*args)
-    torch.cuda.synchronize()
     f = oracle.decode_paged_kv8 if N is None else oracle.prefill_paged_kv8
     o_ref, lse_ref = f(q.double().numpy(), cache.numpy(), table.numpy(), [L], d ** -0.5, d)
     # Scores up to some 1000 (their fp32 sums are off by up to 128 2^-24 of the
     # sum of their terms' sizes, 2^-9 here), so weights by 2^-8.
     top = np.abs(oracle.kv8_unpack(cache.numpy(), d)[1]).max()
-    assert np.all(np.abs(to64(o) - o_ref) <= 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -6 * top)
-    assert np.all(np.abs(lse.double().cpu().numpy() - lse_ref) <= 2.0 ** -9)
+    for times in (0,) if N is None else ways(1, Hq, Hkv, N, d):
+        o, lse = attn.attn_decode_paged_kv8(*args) if N is None else prefill(args, times)
+        torch.cuda.synchronize()
+        assert np.all(np.abs(to64(o) - o_ref) <= 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -6 * top)
+        assert np.all(np.abs(lse.double().cpu().numpy() - lse_ref) <= 2.0 ** -9)
     assert attn.device_status() == 0
 
 
-@pytest.mark.parametrize("N", [None, 3])
+@pytest.mark.parametrize("N", [None, 3, 64])
 def test_workspaces_levels_streams_and_graphs(N):
     """Garbage and reused workspaces, both early-plan levels, given outputs, a
     given stream, a captured graph replayed on other contents: the same bits."""
     d, Hq, Hkv = 128, 12, 2
-    lens = [4000, 17, 0, 900, 900, 2500]
+    more = 2 if N == 64 else 1                       # (enough for tiles)
+    lens = [4000, 17, 0, 900, 900, 2500] * more
     q, cache, table, sl = case(lens, Hq, Hkv, d, seed=4, N=N)
     args = [x.to(DEV) for x in (q, cache, table, sl)]
     call = attn.attn_decode_paged_kv8 if N is None else attn.attn_prefill_paged_kv8
-    need = (attn.attn_decode_paged_kv8_workspace_size(6, Hq, Hkv, d) if N is None
-            else attn.attn_prefill_paged_kv8_workspace_size(6, Hq, Hkv, N, d))
+    need = (attn.attn_decode_paged_kv8_workspace_size(len(lens), Hq, Hkv, d) if N is None
+            else attn.attn_prefill_paged_kv8_workspace_size(len(lens), Hq, Hkv, N, d))
+    assert (need == 0) == (N == 64)
     o, lse = call(*args)
     for fill in (0, 0xFF, 0x5A):
         ws = torch.full((need + 16,), fill, dtype=torch.uint8, device=DEV)
@@ -256,7 +285,7 @@ def test_workspaces_levels_streams_and_graphs(N):
     torch.cuda.synchronize()
     assert torch.equal(out, o) and torch.equal(lse2, lse)
     live.copy_(q2)
-    lens2.copy_(torch.tensor([64, 3000, 5, 0, 1, 16], dtype=torch.int32).clamp(max=sl))
+    lens2.copy_(torch.tensor([64, 3000, 5, 0, 1, 16] * more, dtype=torch.int32).clamp(max=sl))
     graph.replay()
     want = call(q2, *args[1:3], lens2)
     torch.cuda.synchronize()
@@ -293,7 +322,7 @@ def test_a_prompt_in_chunks_then_drafts_then_steps():
             o, lse = attn.attn_prefill_paged_kv8(q, kv, table.to(DEV), lens.to(DEV))
         torch.cuda.synchronize()
         ref = oracle.prefill_paged_kv8(to64(q), kv.cpu().numpy(), table.numpy(), at, d ** -0.5, d)
-        compare(o, lse, ref, kv.cpu().numpy(), d, tile=Hq // Hkv * N > 16, what="N %d" % N)
+        compare(o, lse, ref, kv.cpu().numpy(), d, what="N %d" % N)
         if N == 4:                                   # some drafts are not taken
             at = [a - b for a, b in zip(at, (0, 1, 3))]
     assert attn.device_status() == 0
@@ -311,8 +340,46 @@ def test_cache_beyond_32_bits():
     lens = torch.tensor([61], dtype=torch.int32)
     for n in (1, 2, 40):
         x = q[:, :, :n].contiguous()
-        o, lse = attn.attn_prefill_paged_kv8(x.to(DEV), kv, table.to(DEV), lens.to(DEV))
-        torch.cuda.synchronize()
         ref = oracle.prefill_paged_kv8(x.double().numpy(), small.numpy(), np.array([[0, 1, 2, 3]]), [61], d ** -0.5, d)
-        compare(o, lse, ref, small.numpy(), d, tile=n > 8)
+        for times in ways(1, Hq, Hkv, n, d):
+            o, lse = prefill([y.to(DEV) for y in (x, kv, table, lens)], times)
+            compare(o, lse, ref, small.numpy(), d)
+    assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("S,Hq,Hkv,N,d", [(300, 4, 2, 64, 64), (260, 2, 1, 300, 128), (250, 1, 1, 1250, 64)])
+def test_more_sequences_and_query_blocks_than_are_ordered(S, Hq, Hkv, N, d):
+    """In tiles, beyond the numbers of sequences and of query blocks that the kernel
+    orders by their cost; most sequences shorter than their N rows."""
+    lens = [(37 * i) % 41 for i in range(S)]
+    lens[7], lens[S - 1] = 333, 130
+    q, cache, table, sl = case(lens, Hq, Hkv, d, seed=N, N=N)
+    assert attn.attn_prefill_paged_kv8_workspace_size(S, Hq, Hkv, N, d) == 0
+    o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)])
+    assert attn.device_status() == 0
+    ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), lens, d ** -0.5, d)
+    compare(o, lse, ref, cache.numpy(), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_every_code(kind, d):
+    """Keys (or values) that take every code in every dimension.  A row that sees
+    one token has its value, rounded to bf16, which holds every e4m3 number."""
+    codes = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8)
+    L = len(codes)
+    N, Hq = 260, 2
+    table, _, _, nb = workloads.token_map([0], [L], 5)
+    cache = workloads.kv8_cache(nb, 1, attn.kv8_record_bytes(d), d, 6)
+    for p in range(L):
+        at = (16 * kind + p % 16) * d
+        cache[table[0, p // 16].long(), 0, at: at + d] = codes[(p + torch.arange(d)) % L]
+    q = randn(7, 1, Hq, N, d)
+    sl = torch.tensor([L], dtype=torch.int32)
+    ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), [L], d ** -0.5, d)
+    for times in ways(1, Hq, 1, N, d):
+        o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
+        compare(o, lse, ref, cache.numpy(), d)
+        # The row that sees the first token alone.
+        assert torch.equal(o[0, :, N - L].cpu(), torch.from_numpy(ref[0][0, :, N - L]).to(BF))
     assert attn.device_status() == 0
