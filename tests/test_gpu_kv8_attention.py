@@ -130,6 +130,22 @@ def test_prefill_against_the_oracle(lens, Hq, Hkv, N, d, garbage):
         compare(o, lse, ref, cache.numpy(), d, what="%d times" % times)
 
 
+@pytest.mark.parametrize("ctas", [1, 7])
+@pytest.mark.parametrize("d,N", [(128, 9), (64, 20)])
+def test_passes_over_few_ctas(ctas, d, N):
+    """Several groups of rows of several sequences, split over a few CTAs."""
+    lens = [700, 0, 33, 1200]
+    q, cache, table, sl = case(lens, 12, 2, d, seed=2, N=N)
+    attn.set_decode_max_ctas(ctas)
+    try:
+        o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)])
+    finally:
+        attn.set_decode_max_ctas(0)
+    assert attn.device_status() == 0
+    ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), lens, d ** -0.5, d)
+    compare(o, lse, ref, cache.numpy(), d)
+
+
 def test_the_two_ways_are_both_tested():
     both = [c for c in PREFILLS if len(ways(len(c[0]), *c[1:])) == 2]
     assert {c[4] for c in both} == {64, 128} and {c[3] >= 256 for c in both} == {True, False}
