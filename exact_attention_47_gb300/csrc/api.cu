@@ -896,14 +896,14 @@ attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records,
 
 // Whether an 8-bit prefill goes through the tiles of the forward kernel or, `group`
 // query rows of a KV head at a time, through passes of the decode kernel.  Both take
-// time in proportion to the lengths: a wave of 152 CTAs about 2.7 us for 128 keys, a
+// time in proportion to the lengths: a wave of 152 CTAs about 2.5 us for 128 keys, a
 // pass of one KV head of one sequence, split over all SMs, 5.5 ns.  So a pass is
-// 1 / 480 of a wave, and the tiles are taken where there are more than 3 * 152 passes
+// 1 / 450 of a wave, and the tiles are taken where there are more than 3 * 152 passes
 // to a wave.  Measured, passes against tiles: 12 heads over 2 KV heads, d = 128, 6000
-// keys, 4 sequences of 8 new tokens 29 and 129 us, of 128 121 and 131; 16 sequences
-// of 32 121 and 135, of 64 217 and 133; 32 heads over 8, 64 sequences of 8 new tokens
-// and 1000 keys (4 waves) 68 and 115, of 32 201 and 121; 16 heads over 4, d = 64,
-// 16 sequences of 32 new tokens and 6000 keys 94 and 125, of 64 168 and 127.
+// keys, 4 sequences of 8 new tokens 29 and 121 us, of 128 121 and 121; 16 sequences
+// of 32 121 and 125, of 64 217 and 123; 32 heads over 8, 64 sequences of 8 new tokens
+// and 1000 keys (4 waves) 68 and 111, of 32 201 and 115; 16 heads over 4, d = 64,
+// 16 sequences of 32 new tokens and 6000 keys 96 and 106, of 64 168 and 106.
 bool kv8_packed(int N) { return N < 2 * attn47::fwd_box_rows(); }
 bool kv8_in_tiles(int num_seqs, int Hq, int Hkv, int N, int d) {
   constexpr long long kCtas = 152;

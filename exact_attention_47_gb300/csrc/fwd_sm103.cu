@@ -70,7 +70,7 @@
 // softmax warpgroup loads for itself, are turned into fp16 in shared memory, each by
 // a power of two of its own that brings its largest element to [2^14, 2^15).
 // Warp 8 looks up the blocks and their scales, a tile ahead, and has the TMA bring
-// their codes into a ring of six; warps 10 (K) and 11 (V) take two at a time from
+// their codes into a ring; warps 10 (K) and 11 (V) take two at a time from
 // there, convert them and store them into the swizzled tile.  NaN codes are cleared
 // where there can be any (a sequence's last block, flagged blocks); the look-up keeps
 // the first position of a flagged token, and a row that sees that position gets NaN
@@ -78,13 +78,15 @@
 // With fewer than 256 new tokens the rows of all query heads that share a KV head
 // make one row of query blocks (row = head in the group times N + token), so that
 // a 256-row unit is not mostly empty.
-// What bounds it is the conversion: two instructions a warp shares with the softmax
-// warps of its scheduler, 2400 (K) and 4000 (V) of a tile's 4700 cycles.  Converting
-// by shifts and masks was slower (7 instructions for 4 codes instead of 4: 284 us and
-// up where this takes 231), so was converting in place in the stage (300 us: a stage
-// is then held for the whole way), each gather warp issuing its own TMA copies (291)
-// and a fourth warpgroup with two warps to an operand (300: too few registers are
-// left for the softmax).
+// A tile takes some 4500 cycles with d = 128 (4 sequences of up to 8192 keys, 2048 new
+// tokens of 12 heads over 2: 228 us) where the tensor core is busy for 2850 of them
+// and a softmax warp for 2100; the gather takes 2100 a tile and waits 1700 for codes,
+// of which no more fit in flight.  Tried and slower: converting by shifts and masks
+// (7 instructions for 4 codes instead of 4; a gather warp shares its scheduler with
+// two softmax warps: 284 us and up), converting in place in the stage (300: a stage is
+// held all the way from the copy to the MMA), copies issued by the gather warps
+// themselves (291), a fourth warpgroup with two warps to an operand (300: the softmax
+// has too few registers left).
 #include <cuda_runtime.h>
 
 #include "fwd_sm103.h"
@@ -107,8 +109,8 @@ constexpr int kWarpMma = 9;
 // 256 x 216 + 128 x 72 = 64512, and per sub-partition 216 + 216 + 72 = 504
 // = 3 x 168, so the increase never waits for registers nobody frees.
 // (8-bit cache: the gather spills at 72.  Timed with 216 + 72, 208 + 88 and 200 +
-// 104: d = 128 takes 263, 237 and 231 us for 256-token chunks of 6 sequences, d = 64
-// 22.9, 22.7 and 23.1 us for a padded batch.)
+// 104: d = 128, 4 chunks of 2048 tokens, takes 263, 237 and 231 us; d = 64, 24
+// left-padded chunks of 100, 22.9, 22.7 and 23.1.)
 __host__ __device__ constexpr uint32_t regs_softmax(bool kv8, int d) { return !kv8 ? 216 : d == 128 ? 200 : 208; }
 __host__ __device__ constexpr uint32_t regs_other(bool kv8, int d) { return !kv8 ? 72 : d == 128 ? 104 : 88; }
 constexpr uint32_t kTmemCols = 512;
@@ -117,7 +119,10 @@ constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
 constexpr float kHigh8 = 8.0f;      // 8-bit cache: log2 of P' at the maximum
 
 __host__ __device__ constexpr int sort_max_pairs(int source) { return source == kPagedKv8 ? 1024 : 2048; }
-constexpr int kRawStages = 6;       // 8-bit cache: raw blocks (K and V codes) in flight, taken in pairs
+// 8-bit cache: raw blocks (K and V codes) in flight, taken in pairs; as many as there
+// is room for (d = 64: 16 sequences of 6000 tokens took 125 us with 6, 108 with 14).
+__host__ __device__ constexpr int raw_stages(int d) { return d == 128 ? 6 : 14; }
+constexpr int kMaxRawStages = 14;
 constexpr int kScaleTiles = 16;     // tiles whose scales are kept
 
 // SUMV (d = 64 with contiguous K/V): the row sums of P come from the tensor
@@ -139,7 +144,7 @@ struct FwdLayout {
   static constexpr int kOffK = kOffQ + kTiles * kQTile;
   static constexpr int kOffV = kOffK + kStages * kKV;
   static constexpr int kOffBar = kOffV + kStages * kVStage;
-  static constexpr int kOffCtx = kOffBar + 640;          // paged: ctx_b of each sequence
+  static constexpr int kOffCtx = kOffBar + 768;          // paged: ctx_b of each sequence
   static constexpr int kOffOrder = kOffCtx + 4 * 256;    // paged: (b << 16 | qblk) of each cost rank
   // 8-bit cache: (K scale times scale log2 e, log2 of V's, 1 / V's) of the 8 blocks
   // of tile t at t % kScaleTiles; a ring of raw blocks.
@@ -147,6 +152,7 @@ struct FwdLayout {
   static constexpr int kOffRaw = (kOffScales + kScaleTiles * 8 * 16 + 1023) / 1024 * 1024;
   static constexpr int kRawHalf = 16 * D;                     // a record's K or V codes
   static constexpr int kRaw = 2 * kRawHalf;
+  static constexpr int kRawStages = raw_stages(D);
   static constexpr int kSmem = (SOURCE == kPagedKv8 ? kOffRaw + kRawStages * kRaw : kOffScales) + 1024;   // + alignment slack
   static constexpr uint32_t kColS0 = 0, kColS1 = 128;
   static constexpr uint32_t kColO0 = 256, kColO1 = SUMV ? 384 : 256 + D;
@@ -160,10 +166,10 @@ struct FwdBarriers {
   uint64_t mma_final;
   // 8-bit cache: Q tile x is fp16; raw block s has come / has been read, and
   // what it is.
-  uint64_t q_ready[2], raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t q_ready[2], raw_full[kMaxRawStages], raw_empty[kMaxRawStages];
   uint32_t tmem_base;
   int abort;
-  int raw_kind[kRawStages], raw_fills[kRawStages];
+  int raw_kind[kMaxRawStages], raw_fills[kMaxRawStages];
   // The first position of a flagged token in unit u (of the CTA's), at u % 16: the
   // look-up is at most two tiles ahead of the gather, that kStages ahead of the MMAs,
   // and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1), which also bounds
@@ -171,7 +177,7 @@ struct FwdBarriers {
   int first_flagged[16];
 };
 enum RawKind { kRawNone, kRawCodes, kRawCareful, kRawEnd };   // none: zeros; careful: there may be NaN codes
-static_assert(sizeof(FwdBarriers) <= 640, "room in the layout");
+static_assert(sizeof(FwdBarriers) <= 768, "room in the layout");
 
 struct FwdParams {
   void* o;
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&bar->mma_final), 1);
     if constexpr (KV8) {
       for (int x = 0; x < 2; ++x) mbar_init(smem_addr(&bar->q_ready[x]), kBM);
-      for (int x = 0; x < kRawStages; ++x) {
+      for (int x = 0; x < L::kRawStages; ++x) {
         mbar_init(smem_addr(&bar->raw_full[x]), 1);
         mbar_init(smem_addr(&bar->raw_empty[x]), 2);
         bar->raw_fills[x] = 0;
@@ -481,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // Block number `at` into the ring.
     auto fill = [&](int at, int rec, int what) {
-      const int s = at % kRawStages;
+      const int s = at % L::kRawStages;
       const uint32_t full = smem_addr(&bar->raw_full[s]);
-      if (!mbar_wait_sleep(smem_addr(&bar->raw_empty[s]), ((at / kRawStages) & 1) ^ 1, wc)) return false;
+      if (!mbar_wait_sleep(smem_addr(&bar->raw_empty[s]), ((at / L::kRawStages) & 1) ^ 1, wc)) return false;
       reinterpret_cast<volatile int*>(bar->raw_kind)[s] = what;
       ++bar->raw_fills[s];
       mbar_arrive_expect_tx(full, rec >= 0 ? L::kRaw : 0);
@@ -494,6 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int next_rec = record(next), next_number = next.number;
       const bool next_last = next.last, next_ends = next.ends;
       const uint4 next_tail = tail_of(next_rec);
+      // (d = 128, whose ring is short: 16 sequences of 6000 tokens, 64 queries of 4
+      // heads each over 8 KV heads, 143 -> 131 us.)
+      if (D == 128 && next_rec >= 0)
+        bulk_prefetch_l2(p.kv_cache + static_cast<size_t>(next_rec) * Kv8Layout<D>::kBytes, L::kRaw);
       next = read_table();
       // The first flagged token: the lowest bit of its block's flags.
       const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (!ok) {
       // Raw blocks in flight must land before the CTA may exit.
-      for (int s = 0; s < kRawStages; ++s) {
+      for (int s = 0; s < L::kRawStages; ++s) {
         const int fills = bar->raw_fills[s];
         if (fills) mbar_wait_warp_drain(smem_addr(&bar->raw_full[s]), (fills - 1) & 1, wc);
       }
@@ -823,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();                                        // every lane has read the raw blocks
           if (lane < 2) mbar_arrive(empty + 8u * (s + lane));
-          if ((s += 2) == kRawStages) {
+          if ((s += 2) == L::kRawStages) {
             s = 0;
             phase ^= 1;
           }
