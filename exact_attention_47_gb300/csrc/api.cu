@@ -906,11 +906,11 @@ attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records,
 // 16 sequences of 32 new tokens and 6000 keys 96 and 106, of 64 168 and 106.
 bool kv8_packed(int N) { return N < 2 * attn47::fwd_box_rows(); }
 bool kv8_in_tiles(int num_seqs, int Hq, int Hkv, int N, int d) {
-  constexpr long long kCtas = 152;
-  const long long seqs = num_seqs, rows = static_cast<long long>(Hq / Hkv) * N, tile = 2 * attn47::fwd_box_rows();
-  const long long units = kv8_packed(N) ? seqs * Hkv * ((rows + tile - 1) / tile) : seqs * Hq * ((N + tile - 1) / tile);
-  const long long waves = (units + kCtas - 1) / kCtas;
-  return seqs * Hkv * attn47::decode_kv8_rows(Hq, Hkv, N, d).groups > 3 * kCtas * waves;
+  constexpr double kCtas = 152;
+  const long long rows = static_cast<long long>(Hq / Hkv) * N, tile = 2 * attn47::fwd_box_rows();
+  const double seqs = num_seqs;
+  const double units = kv8_packed(N) ? seqs * Hkv * ((rows + tile - 1) / tile) : seqs * Hq * ((N + tile - 1) / tile);
+  return seqs * Hkv * attn47::decode_kv8_rows(Hq, Hkv, N, d).groups > 3 * kCtas * std::ceil(units / kCtas);
 }
 
 // Both attentions over an 8-bit cache.
@@ -928,6 +928,12 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
     if (!tiles) {
       need = attn47::decode_kv8_workspace_bytes(Hq, Hkv, N, d);
       passes = attn47::decode_kv8_rows(Hq, Hkv, N, d).groups;
+      // Tiles too where the passes' blocks are more than their split can count.
+      if (passes > 1 && static_cast<__int128>(num_seqs) * Hkv * passes * (static_cast<long long>(max_blocks_per_seq) + 64) >= 0x7fffffff) {
+        tiles = true;
+        need = 0;
+        passes = 1;
+      }
     }
   }
   DeviceInfo* dev;

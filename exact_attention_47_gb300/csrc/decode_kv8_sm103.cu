@@ -31,6 +31,14 @@
 // scales as 16 bytes more.  (Copied by the lanes themselves, 16 bytes each of just
 // what they use, 8 sequences of 30k .. 131k tokens took 79 us: a warp's scattered
 // 16-byte copies cost the memory pipe 21 passes where the bytes make 4.)
+//
+// Measured (GB300, replayed graphs): 8 sequences of 30000 .. 131072 tokens, 16 heads
+// over 2, d = 128 (346 MB) 64.3 us, 5.4 TB/s or 0.81 of a copy; 64 of 128 .. 4096, 12
+// heads over 2 (70 MB) 19.2 us, of which 4 are dependent reads before the first block
+// and 4 to 5 the merges at the end; 256 of 0 .. 2048, 64 heads over 4, d = 64 (139 MB)
+// 40.7 us: two column tiles, 250 instructions a block issued in 48 % of the cycles by
+// the three warps that a scheduler's registers hold; one sequence of 100 tokens 6.4
+// us, a chain of dependent steps.
 #include <atomic>
 
 #include <cuda.h>
@@ -106,12 +114,20 @@ struct DecKv8Params {
   __device__ __forceinline__ int rows_of(int g) const { return min(group, rows - g % groups * group); }
 };
 
-template <int D, int NT>
+template <int D>
 struct DecKv8Costs {
-  static constexpr int spare2 = NT == 1 && D == 128 ? 7 : 12;
-  __device__ __forceinline__ int run_cost(int total, int shares) const {
-    return total <= shares ? 1 : total <= 8 * shares ? 3 : 4;
-  }
+  // What a merge across CTAs costs, in half blocks.  Teams against equal shares, where
+  // 14 decides for teams and 7 does not (us; sequences x tokens, KV heads): 32 x 500 ..
+  // 1000, 8, 16.1 and 16.7; 32 x 500 .. 1000, 2, 11.6 and 12.5; 24 instead of 12 with
+  // d = 64 changes nothing.
+  static constexpr int spare2 = D == 128 ? 14 : 12;
+  // What a run costs beyond its blocks: a long share spends about 4 blocks' time on
+  // one (its queries, its end).  A share is at least this and one more, though, so
+  // with fewer blocks than shares it is 1.  Measured with 1, 3 and 4 (us): 256
+  // sequences of up to 2048 tokens, 4 KV heads, d = 64, 46.6 42.2 40.6 (6: 40.6); 64 of
+  // 128 .. 4096, 2 heads, d = 128, 19.8 19.4 19.4; with 1 and 4 always, 3 of 2000, 2
+  // heads, d = 64, 9.3 11.0.
+  __device__ __forceinline__ int run_cost(int total, int shares) const { return total <= shares ? 1 : 4; }
 };
 
 template <int N>
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(DecKv8Cfg<D, NT>::kThreads, 1)
   // is written come after the wait further down.
   if (!p.early_plan) pdl_wait_primary();
 
-  const Plan plan = build_plan<kWarps>(p, sh, cost, runs, seq_blocks, DecKv8Costs<D, NT>());
+  const Plan plan = build_plan<kWarps>(p, sh, cost, runs, seq_blocks, DecKv8Costs<D>());
   __syncthreads();
   Share share = take_share<kWarps>(p, plan, sh);
   Walk& w = share.w;

@@ -129,6 +129,12 @@ def test_prefill_of_its_own(lib):  # noqa: F811
     assert attend(lib, 1 << 30) == UNSUPPORTED and attend(lib, 1 << 20, S=1 << 10) == UNSUPPORTED
     # More than 16 query heads to a KV head: the prefill's alone.
     assert attend(lib, None, Hq=34) == UNSUPPORTED and passes(lib, attend(lib, 1, Hq=34))
+    # More blocks in all passes than 31 bits count: tiles.
+    wide = dict(S=1000, Hq=32, Hkv=8, d=64, mb=1 << 17, nb=1 << 20, q=0x10000000000, o=0x20000000000, lse=None,
+                kv=0x30000000000, tab=0x40000000000)
+    assert passes(lib, attend(lib, 20, **wide)) and passes(lib, attend(lib, 20, ws=None, ws_bytes=0, **wide))
+    assert attend(lib, 8, ws=None, ws_bytes=0, **wide) == INVALID
+    assert attend(lib, 20, **(wide | dict(S=1 << 12))) == UNSUPPORTED
     # Many rows in all go in tiles, without a workspace.
     assert passes(lib, attend(lib, 2000, S=4, o=0x40000000, lse=None, ws=None, ws_bytes=0))
 
