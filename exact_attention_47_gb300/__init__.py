@@ -1,8 +1,8 @@
 """GB300 (sm_103a) exact attention: tiled online-softmax prefill, its backward,
 paged-KV decode, chunked prefill over the paged cache, rotary positions and
-the paged appends that rotate on the way, an 8-bit paged cache with attention of
-single queries and chunks, a 4-bit one with its decode,
-and the residual add + RMSNorm and SwiGLU fusions of the same layer.
+the paged appends that rotate on the way, an 8-bit paged cache with the attention
+of single queries, draft tokens and chunks, a 4-bit one with its decode, and the
+residual add + RMSNorm and SwiGLU fusions of the same layer.
 
 The compute lives in ``lib/libattn47_sm103.so`` (hand-written CUDA, C-ABI
 declared in ``include/attn47.h``); this package is its Python binding.

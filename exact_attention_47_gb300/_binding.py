@@ -148,8 +148,8 @@ def _fast():
     lib = load_library()
     path = fast_path()
     if not os.path.exists(path):
-        warnings.warn("%s is not built (it takes g++ and the headers of Python and torch): the rotary, append and "
-                      "4-bit-cache calls cost more host time" % path, RuntimeWarning, stacklevel=3)
+        warnings.warn("%s is not built (it takes g++ and the headers of Python and torch): the rotary, append, "
+                      "8- and 4-bit-cache calls cost more host time" % path, RuntimeWarning, stacklevel=3)
         return _NoFastCalls
     loader = importlib.machinery.ExtensionFileLoader("_attn47_fast", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn47_fast", loader))

@@ -63,6 +63,10 @@
  *  rope_append_paged_kv4, kv4_read_paged, attn_decode_paged_kv4
  *                     the same append into a cache held in 4 bits, the
  *                     read-back of its rows, and the decode over it
+ *  kv8_append_paged, kv8_read_paged, attn_decode_paged_kv8,
+ *  attn_prefill_paged_kv8
+ *                     the same for a cache held in 8 bits, and the attention
+ *                     of prompt chunks and draft tokens over it
  *
  * Conventions shared by every call
  *  - Pointers are DEVICE pointers of the current CUDA device unless stated.
@@ -117,9 +121,9 @@ typedef enum attn_status {
                                     > max_blocks_per_seq*block_size - N (chunked prefill);
                                     it was clamped into range, outputs of that sequence invalid;
                                     or a token's cache position was outside its table (rope_append_*,
-                                    kv4_read_paged): nothing was written for that token */
+                                    kv8_append_paged, kv4_read_paged, kv8_read_paged): nothing was written for that token */
 #define ATTN_DEV_BAD_SEQID 0x8u  /* a token's seq_ids entry was >= num_seqs (rope_append_*,
-                                    kv4_read_paged): nothing was written for that token */
+                                    kv8_append_paged, kv4_read_paged, kv8_read_paged): nothing was written for that token */
 
 /*
  * attn_fwd — exact attention forward (prefill).
@@ -723,6 +727,12 @@ size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int 
  *  Hq % Hkv == 0, any Hq / Hkv; num_seqs == 0 or N == 0 is an empty problem.
  *  The other arguments, rules and device flags are those of
  *  attn_decode_paged_kv8.
+ *
+ * Few query rows in all go through the decode's kernel, 16 or 32 rows of a KV
+ * head at a time, each time over the whole sequence; many (where the workspace
+ * size is 0) through tiles of 128 rows by 128 keys.  In tiles the numerators
+ * are rounded to 11 bits or 2^-32 of the largest, and a block outside the pool
+ * counts as keys and values of zero instead of being left out.
  */
 attn_status_t attn_prefill_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
                                      const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d,
