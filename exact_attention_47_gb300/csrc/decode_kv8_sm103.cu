@@ -65,7 +65,7 @@ struct DecKv8Cfg {
   static constexpr int kWarps = (D == 64 && NT <= 2) || NT == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = D == 64 || NT == 2 ? 4 : 3;
-  static constexpr int kBlocks = D == 64 && NT <= 2 ? 2 : 1; // taken at a time
+  static constexpr int kBlocks = D == 64 || NT == 2 ? 2 : 1;      // taken at a time
   static constexpr int kStage = Rec::kOffTail;               // its scales are apart
   static constexpr int kRows = NT * 8;                       // rows of a piece
   static constexpr int kPitch = D + 4;                       // floats
