@@ -160,11 +160,14 @@ def test_threads_on_streams_of_their_own(N):
     bad = []
 
     def work(i):
-        with torch.cuda.stream(torch.cuda.Stream()):
-            for _ in range(50):
-                o, lse = call(*cases[i])
-                if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
-                    bad.append(i)
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    o, lse = call(*cases[i])
+                    if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
+                        bad.append(i)
+        except Exception as e:                               # (a thread's would be a warning)
+            bad.append(e)
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
     for t in threads:
@@ -173,6 +176,37 @@ def test_threads_on_streams_of_their_own(N):
         t.join()
     torch.cuda.synchronize()
     assert not bad and attn.device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["fwd", "decode", "decode8", "passes8", "tiles8"])
+def test_the_first_call_of_a_thread(name):
+    """A thread that has made no CUDA call has no context bound to it."""
+    d = 64
+    q, rec, table, lens = on_gpu([40, 3] * 8, 4, 2, d, seed=6)
+    one = torch.zeros(1, 2, 40, d, dtype=BF, device=DEV)
+    bf = torch.zeros(rec.shape[0], 2, 16, d, dtype=BF, device=DEV)
+    few, many = (torch.zeros(16, 4, n, d, dtype=BF, device=DEV) for n in (2, 300))
+    assert attn.attn_prefill_paged_kv8_workspace_size(16, 4, 2, 300, d) == 0
+    call = dict(fwd=lambda: attn.attn_fwd(one, one, one), decode=lambda: attn.attn_decode_paged(q, bf, bf, table, lens),
+                decode8=lambda: attn.attn_decode_paged_kv8(q, rec, table, lens),
+                passes8=lambda: attn.attn_prefill_paged_kv8(few, rec, table, lens),
+                tiles8=lambda: attn.attn_prefill_paged_kv8(many, rec, table, lens))[name]
+    want = call()
+    torch.cuda.synchronize()
+    got = []
+
+    def work():
+        try:
+            got.append(call())
+        except Exception as e:
+            got.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert isinstance(got[0], tuple), got[0]
+    assert torch.equal(torch.nan_to_num(got[0][0]), torch.nan_to_num(want[0])) and attn.device_status() == 0
 
 
 def test_what_a_call_on_a_given_stream_allocates_is_that_streams():
