@@ -423,9 +423,9 @@ struct Kv8Append {
 // grow, and where it does the codes that are there are brought to it.
 //
 // Measured, the append with its queries and the read-back of the blocks it reached: 5
-// ragged chunks of 500 .. 5001 tokens, 16 + 4 heads, three axes (209 MB in all) 55.9
-// us, some 45 of them the append; 7 of 100 .. 2300, 12 + 2 heads (77 MB) 25.5; a decode
-// step of 64 sequences 9.2.  The append issues in 56 % of the cycles, 1780 warp
+// ragged chunks of 500 .. 5001 tokens, 16 + 4 heads, three axes (209 MB in all) 53.9
+// us, 42 of them the append; 7 of 100 .. 2300, 12 + 2 heads (77 MB) 24.6, 16.5 of them
+// the append; a decode step of 64 sequences 6.2 (4.3).  The append issues in 56 % of the cycles, 1780 warp
 // instructions a token with its queries, with 6 warps to a scheduler; what it waits for
 // are the rows, which it then works through.  What helped: rows of a warp share their
 // head and largest values go by warp reductions (64 -> 59 for the three axes), a third
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) kv4_read_kernel(const Kv4
 // Rows of cached tokens of an 8-bit cache back to bf16: value = code * scale,
 // exactly.  Rows of a token: its keys, then its values.  15500 tokens of 4 heads, d =
 // 128, take 11.7 us (48 MB, 0.61 of a copy with the launch and three dependent
-// reads), 1567 of 2 heads, d = 64, 6.
+// reads), 1567 of 2 heads, d = 64, 1.9.
 struct Kv8ReadParams {
   const uint8_t* kv_cache;
   const int* block_table;
