@@ -79,7 +79,7 @@
 // make one row of query blocks (row = head in the group times N + token), so that
 // a 256-row unit is not mostly empty.
 // A tile takes some 4500 cycles with d = 128 (4 sequences of up to 8192 keys, 2048 new
-// tokens of 12 heads over 2: 228 us) where the tensor core is busy for 2850 of them
+// tokens of 12 heads over 2: 225 us) where the tensor core is busy for 2850 of them
 // and a softmax warp for 2100; the gather takes 2100 a tile and waits 1700 for codes,
 // of which no more fit in flight.  Tried and slower: converting by shifts and masks
 // (7 instructions for 4 codes instead of 4; a gather warp shares its scheduler with
@@ -412,10 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   const WaitCtl wc{&bar->abort, p.status, p.timeout_ns};
-  // Warps that wait long sleep where a gather needs the issue slots.
-  auto wait_long = [&](uint32_t b, uint32_t parity) {
-    return KV8 ? mbar_wait_sleep_warp(b, parity, wc) : mbar_wait_warp(b, parity, wc);
-  };
   if (warp >= 8) {
   regs_decrease<regs_other(KV8, D)>();
   if (KV8 && warp == kWarpLoad) {
@@ -814,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 w[2 * kPieces];
 #pragma unroll
           for (int x = 0; x < 2 * kPieces; ++x) w[x] = ld_shared_v4(raw + (s + x / kPieces) * L::kRaw + raw_of(x % kPieces));
-          if (i == 0 && !(ok = wait_long(tile_empty + 8u * st, ((g / L::kStages) & 1) ^ 1))) break;
+          if (i == 0 && !(ok = mbar_wait_warp(tile_empty + 8u * st, ((g / L::kStages) & 1) ^ 1, wc))) break;
           if (kind[0] != kRawCodes || kind[1] != kRawCodes) {  // (the same for the whole warp)
 #pragma unroll
             for (int x = 0; x < 2 * kPieces; ++x)
@@ -987,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     for (int j = 0; j < n_kv; ++j) {
-      if (!wait_long(smem_addr(&bar->s_full[x]), static_cast<uint32_t>(sx0 + j) & 1u)) {
+      if (!mbar_wait_warp(smem_addr(&bar->s_full[x]), static_cast<uint32_t>(sx0 + j) & 1u, wc)) {
         ok = false;
         break;
       }
