@@ -70,11 +70,11 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 CSRC = os.path.join(ROOT, "exact_attention_47_gb300", "csrc")
 TRAFFIC = {
     # median read + median write of 3 launches
-    "fwd": {"bytes": 67192064 + 5373184, "sources": ("fwd_sm103.cu", "fwd_sm103.h", "ptx.cuh"),
-            "sha256": "aba585ac8cdef70f91a9bfef05fa1aeb750e0d50c124f312e62b487dd60311ff"},
+    "fwd": {"bytes": 67191296 + 5316608, "sources": ("fwd_sm103.cu", "fwd_sm103.h", "ptx.cuh"),
+            "sha256": "b6650b0cbe91a5848f73a6f4b3d0dd39dfb71cfeaef5d804b8ebd514b13befaf"},
     # decode kernel (split parts merged inside it), median read + median write of 3 launches
-    "dec": {"bytes": 132367872 + 473856, "sources": ("decode_sm103.cu", "decode_sm103.h", "ptx.cuh"),
-            "sha256": "3054666127aebefdfd2346194dbf2069b46fa8433a95eeb723e38371396fb2f8"},
+    "dec": {"bytes": 132364800 + 122368, "sources": ("decode_sm103.cu", "decode_sm103.h", "ptx.cuh"),
+            "sha256": "075ecbe37e0a1a17e2a12ef5f407dd3103cf8a333cb719d554cb84b193bfc5eb"},
 }
 
 
