@@ -774,7 +774,7 @@ def _need_kv8(kv_cache, d, device):
 
 
 def kv8_append_paged(q, k, v, kv_cache, block_table, seq_ids, positions, inv_freq=None, rope_positions=None,
-                          pair_axis=None, interleaved=False, q_out=None, stream=None):
+                     pair_axis=None, interleaved=False, q_out=None, stream=None):
     """rope_append_paged into an 8-bit cache: kv_cache
     [num_blocks,Hkv,kv8_record_bytes(d)] uint8 (updated in place), e4m3 codes
     with a scale (a power of two) per block of 16 tokens and head for the keys

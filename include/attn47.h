@@ -649,10 +649,10 @@ size_t kv8_record_bytes(int d);
  *  The other arguments, rules and device flags are those of rope_append_paged.
  */
 attn_status_t kv8_append_paged(const attn_heads_t* q, const attn_heads_t* k, const attn_heads_t* v,
-                                    const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
-                                    const int32_t* block_table, const int32_t* seq_ids,
-                                    const int32_t* positions, int T, int num_seqs, int d, int block_size,
-                                    int max_blocks_per_seq, int num_blocks, void* stream);
+                               const attn_heads_t* q_out, const attn_rope_t* rope, void* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_ids,
+                               const int32_t* positions, int T, int num_seqs, int d, int block_size,
+                               int max_blocks_per_seq, int num_blocks, void* stream);
 
 /*
  * kv8_read_paged — the values that cached tokens of an 8-bit cache stand for:
