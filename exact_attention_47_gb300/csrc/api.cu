@@ -901,23 +901,27 @@ attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records,
   return ATTN_OK;
 }
 
-// Whether an 8-bit prefill goes through the tiles of the forward kernel or, `group`
+// Whether an 8-bit prefill goes through the tiles of the forward kernel or, a group of
 // query rows of a KV head at a time, through passes of the decode kernel.  Both take
-// time in proportion to the lengths: a wave of 152 CTAs about 2.5 us for 128 keys, a
-// pass of one KV head of one sequence, split over all SMs, 5.5 ns.  So a pass is
-// 1 / 450 of a wave, and the tiles are taken where there are more than 3 * 152 passes
-// to a wave.  Measured, passes against tiles: 12 heads over 2 KV heads, d = 128, 6000
-// keys, 4 sequences of 8 new tokens 29 and 121 us, of 128 121 and 121; 16 sequences
-// of 32 121 and 125, of 64 217 and 123; 32 heads over 8, 64 sequences of 8 new tokens
-// and 1000 keys (4 waves) 68 and 111, of 32 201 and 115; 16 heads over 4, d = 64,
-// 16 sequences of 32 new tokens and 6000 keys 96 and 106, of 64 168 and 106.
+// time in proportion to the lengths: for 1000 keys a wave of 152 CTAs about 20 us (d =
+// 64: 17), a pass of one KV head of one sequence, split over all SMs, 42 ns (d = 64:
+// 23, with three column tiles 31).  So as many passes as CTAs of all waves, times
+// `share`, take as long as the tiles, which are taken beyond that.  Measured, passes
+// against tiles: d = 128, 12 heads over 2 KV heads, 6000 keys, 4 sequences of 8 new
+// tokens 29 and 121 us, of 128 121 and 121; 16 sequences of 32 121 and 125, of 64 217
+// and 123; 32 heads over 8, 64 sequences of 8 new tokens and 1000 keys (4 waves) 68
+// and 111, of 32 201 and 115; d = 64, 16 heads over 4, 6000 keys, 4 sequences of 64
+// new tokens 53 and 104, of 128 90 and 104; 16 of 32 90 and 106, of 64 160 and 106;
+// 64 of 1000 keys (2 waves) and 16 new tokens 47 and 53, 32 68 and 53.
 bool kv8_packed(int N) { return N < 2 * attn47::fwd_box_rows(); }
 bool kv8_in_tiles(int num_seqs, int Hq, int Hkv, int N, int d) {
   constexpr double kCtas = 152;
   const long long rows = static_cast<long long>(Hq / Hkv) * N, tile = 2 * attn47::fwd_box_rows();
   const double seqs = num_seqs;
   const double units = kv8_packed(N) ? seqs * Hkv * ((rows + tile - 1) / tile) : seqs * Hq * ((N + tile - 1) / tile);
-  return seqs * Hkv * attn47::decode_kv8_rows(Hq, Hkv, N, d).groups > 3 * kCtas * std::ceil(units / kCtas);
+  const attn47::Kv8Rows pass = attn47::decode_kv8_rows(Hq, Hkv, N, d);
+  const double share = d == 128 ? 3 : pass.group <= 16 ? 5 : 3.5;   // passes that take a CTA as long as its part of a wave
+  return seqs * Hkv * pass.groups > share * kCtas * std::ceil(units / kCtas);
 }
 
 // Both attentions over an 8-bit cache.

@@ -58,7 +58,7 @@ constexpr float kTau = 4.f;
 // A numerator is 2^kHigh for a score at the maximum, at most 2^(kHigh + kTau).
 constexpr float kHigh = 10.f;
 
-// NT: column tiles of 8 query rows (1 .. 4 with D = 64, 1 or 2 with D = 128).
+// NT: column tiles of 8 query rows (1 .. 3 with D = 64, 1 or 2 with D = 128).
 template <int D, int NT>
 struct DecKv8Cfg {
   using Rec = Kv8Layout<D>;
@@ -762,11 +762,15 @@ cudaError_t launch_t(const DecKv8Launch& a, const Kv8Rows& rows) {
 }  // namespace
 
 Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N, int d) {
-  // Up to four column tiles a pass with d = 64, two with d = 128, whose accumulators
-  // for more do not fit beside enough warps (24 rows of 32 sequences of 500 .. 6000
-  // tokens, 2 KV heads: two passes of 12 take 33.3 us, one of 24 35.9).
-  const int most = d == 64 ? 32 : 16, rows = Hq / Hkv * N, groups = (rows + most - 1) / most;
-  return Kv8Rows{(rows + groups - 1) / groups, groups};
+  // Two column tiles a pass; three with d = 64 where their fewer passes pay (one takes
+  // 1.46 times as long: 16 sequences of 6000 tokens, 4 KV heads, 24 rows in one pass
+  // 30.8 us, in two 32.8; 64 rows in three 57.3, in four 53.2; 32 rows in one pass of
+  // four tiles 38.9, in two of two 32.8).  With d = 128 the accumulators of three do
+  // not fit beside enough warps (24 rows of 32 sequences of 500 .. 6000 tokens, 2 KV
+  // heads: two passes of 12 33.3 us, one of 24 35.9).
+  const int rows = Hq / Hkv * N, by16 = (rows - 1) / 16 + 1, by24 = (rows - 1) / 24 + 1;
+  const int groups = d == 64 && 1.46 * by24 < by16 ? by24 : by16;
+  return Kv8Rows{(rows - 1) / groups + 1, groups};
 }
 
 size_t decode_kv8_workspace_bytes(int Hq, int Hkv, int N, int d) {
@@ -779,8 +783,7 @@ cudaError_t launch_decode_kv8_sm103(const DecKv8Launch& a) {
   const int tiles = (rows.group + 7) / 8;
   if (a.d == 128)
     return tiles == 1 ? launch_t<128, 1>(a, rows) : launch_t<128, 2>(a, rows);
-  return tiles == 1 ? launch_t<64, 1>(a, rows) : tiles == 2 ? launch_t<64, 2>(a, rows)
-       : tiles == 3 ? launch_t<64, 3>(a, rows) : launch_t<64, 4>(a, rows);
+  return tiles == 1 ? launch_t<64, 1>(a, rows) : tiles == 2 ? launch_t<64, 2>(a, rows) : launch_t<64, 3>(a, rows);
 }
 
 }  // namespace attn47

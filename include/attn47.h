@@ -728,7 +728,7 @@ size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int 
  *  The other arguments, rules and device flags are those of
  *  attn_decode_paged_kv8.
  *
- * Few query rows in all go through the decode's kernel, 16 or 32 rows of a KV
+ * Few query rows in all go through the decode's kernel, 16 or 24 rows of a KV
  * head at a time, each time over the whole sequence; many (where the workspace
  * size is 0) through tiles of 128 rows by 128 keys.  In tiles the numerators
  * are rounded to 11 bits or 2^-32 of the largest, and a block outside the pool
