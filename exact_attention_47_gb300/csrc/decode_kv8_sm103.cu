@@ -767,7 +767,10 @@ Kv8Rows decode_kv8_rows(int Hq, int Hkv, int N, int d) {
   // 30.8 us, in two 32.8; 64 rows in three 57.3, in four 53.2; 32 rows in one pass of
   // four tiles 38.9, in two of two 32.8).  With d = 128 the accumulators of three do
   // not fit beside enough warps (24 rows of 32 sequences of 500 .. 6000 tokens, 2 KV
-  // heads: two passes of 12 33.3 us, one of 24 35.9).
+  // heads: two passes of 12 33.3 us, one of 24 35.9); one tile a pass, with 12 warps
+  // instead of 8, is faster over few tokens (24 rows of 4 of 6000: 22.5 us in three
+  // passes, 26.6 in two) and slower over many (16 of 6000, 8 KV heads, more than L2
+  // holds: 117 and 86).
   const int rows = Hq / Hkv * N, by16 = (rows - 1) / 16 + 1, by24 = (rows - 1) / 24 + 1;
   const int groups = d == 64 && 1.46 * by24 < by16 ? by24 : by16;
   return Kv8Rows{(rows - 1) / groups + 1, groups};

@@ -141,13 +141,13 @@ def test_prefill_of_its_own(lib):  # noqa: F811
 
 def test_workspace_sizes(lib):  # noqa: F811
     decode, prefill = lib.attn_decode_paged_kv8_workspace_size, lib.attn_prefill_paged_kv8_workspace_size
-    for d, most in ((64, 24), (128, 16)):
+    for d, passes in ((64, {16: 1, 17: 1, 24: 1, 25: 2, 32: 2, 64: 4, 71: 3, 240: 10}),
+                      (128, {8: 1, 16: 1, 17: 2, 32: 2, 47: 3, 160: 10})):
         for group in (1, 6, 16):
             assert decode(5, 2 * group, 2, d) == decode(500, 2 * group, 2, d) == 256 * 8 + 512 * group * (d + 2) * 4
             assert prefill(5, 2 * group, 2, 1, d) == decode(5, 2 * group, 2, d)
         # Groups of as equal sizes as can be.
-        for rows in (most, most + 1, 3 * most - 1, 10 * most):
-            groups = -(-rows // most)
+        for rows, groups in passes.items():
             assert prefill(1, 1, 1, rows, d) == 256 * 8 + 512 * -(-rows // groups) * (d + 2) * 4
     for bad in ((0, 12, 2, 128), (2, 12, 5, 128), (2, 0, 2, 128), (2, 12, 2, 0)):
         assert decode(*bad) == 0 and prefill(*bad[:3], 4, bad[3]) == 0
