@@ -520,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         now_rec >= 0 ? static_cast<float>(static_cast<int>(tail.y >> 23) - 127) : 0.f,
                         now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, 0.f);
       }
+      __syncwarp();                              // (lanes 0 and 1 release what all of them have stored)
       const int kind = now_rec < 0 ? kRawNone : now_ends || bits != 0 ? kRawCareful : kRawCodes;
       // Two blocks at a time.
       for (int first = 0; ok && first < kPagesPerTile; first += 2) {
