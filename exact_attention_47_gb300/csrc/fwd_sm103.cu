@@ -170,10 +170,10 @@ struct FwdBarriers {
   uint32_t tmem_base;
   int abort;
   int raw_kind[kMaxRawStages], raw_fills[kMaxRawStages];
-  // The first position of a flagged token in unit u (of the CTA's), at u % 16: the
-  // look-up is at most two tiles ahead of the gather, that kStages ahead of the MMAs,
-  // and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1), which also bounds
-  // the scales' ring.
+  // The first position of a flagged token in unit u (of the CTA's), in its tiles so
+  // far, at u % 16: the look-up is at most two tiles ahead of the gather, that kStages
+  // ahead of the MMAs, and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1),
+  // which also bounds the scales' ring.
   int first_flagged[16];
 };
 enum RawKind { kRawNone, kRawCodes, kRawCareful, kRawEnd };   // none: zeros; careful: there may be NaN codes
@@ -501,18 +501,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (D == 128 && next_rec >= 0)
         bulk_prefetch_l2(p.kv_cache + static_cast<size_t>(next_rec) * Kv8Layout<D>::kBytes, L::kRaw);
       next = read_table();
-      // The first flagged token: the lowest bit of its block's flags.
+      if (now_number < 0) break;
+      // The unit's first flagged token so far: the lowest bit of its block's flags.
+      // It is stored before the tile's blocks are on their way, so whoever has seen
+      // this tile's products sees it, with query tile A already before the unit's end.
       const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
       if (__any_sync(0xffffffffu, bits != 0)) {
         const int at = bits != 0 ? (now_number * kPagesPerTile + lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
         flagged = min(flagged, __reduce_min_sync(0xffffffffu, at));
       }
+      if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
       if (now_last) {
-        if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
         flagged = 0x7fffffff;
         ++unit;
       }
-      if (now_number < 0) break;
       if (lane < kPagesPerTile) {
         // (No block, zeros: any scales.)
         reinterpret_cast<float4*>(smem + L::kOffScales)[n % kScaleTiles * 8 + lane] =
@@ -1191,7 +1193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float inv_l = 1.f / lsum;
       bool spoilt = false;
       if constexpr (KV8) {
-        // (The gather wrote this before the unit's last tile was full.)
+        // (The look-up stored this, as of this query tile's last K/V tile at least,
+        // before that tile's blocks were on their way; later ones are seen by no row.)
         spoilt = qpos >= reinterpret_cast<const volatile int*>(bar->first_flagged)[units & 15];
         if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
         if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
