@@ -170,6 +170,7 @@ struct FwdBarriers {
   uint32_t tmem_base;
   int abort;
   int raw_kind[kMaxRawStages], raw_fills[kMaxRawStages];
+  int q_loads[2];                     // copies of Q tile x asked for (its first thread's count)
   // The first position of a flagged token in unit u (of the CTA's), in its tiles so
   // far, at u % 16: the look-up is at most two tiles ahead of the gather, that kStages
   // ahead of the MMAs, and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1),
@@ -330,7 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_addr(&bar->mma_final), 1);
     if constexpr (KV8) {
-      for (int x = 0; x < 2; ++x) mbar_init(smem_addr(&bar->q_ready[x]), kBM);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_addr(&bar->q_ready[x]), kBM);
+        bar->q_loads[x] = 0;
+      }
       for (int x = 0; x < L::kRawStages; ++x) {
         mbar_init(smem_addr(&bar->raw_full[x]), 1);
         mbar_init(smem_addr(&bar->raw_empty[x]), 2);
@@ -927,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k = unit_at(band);
       if (quarter != 0 || lane != 0 || k >= p.num_units) return;
       const Unit u = unit_info(k);
+      ++bar->q_loads[x];
       mbar_arrive_expect_tx(q_full, L::kQTile);
       for (int c = 0; c < L::kChunks; ++c)
         tma_load_3d(q_tile + c * L::kQChunk, &tq, q_full, c * 64, u.qblk * kRowsPerCta + x * kBM, u.zq);
@@ -978,7 +983,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float back = 1.f;                              // 8-bit cache: the factor of this row of Q
     if constexpr (KV8) {
       if (!mbar_wait_warp(q_full, units & 1, wc)) {
-        if (lane == 0 && quarter == 0) mbar_wait(q_full, units & 1, wc, true);
         ok = false;
         break;
       }
@@ -1231,6 +1235,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     sx0 += n_kv;
     kv0 += u.nB;
     ++units;
+    }
+    if constexpr (KV8) {
+      // After a wait that ran out: the last copy of Q (this unit's, or already the
+      // next one's) must land before the CTA may exit.
+      if (!ok && quarter == 0 && lane == 0) {
+        const int loads = bar->q_loads[x];
+        if (loads > 0) mbar_wait(q_full, (loads - 1) & 1, wc, true);
+      }
     }
     tc_fence_before();
     named_barrier_sync(1, kThreads);
