@@ -779,7 +779,8 @@ def kv8_append_paged(q, k, v, kv_cache, block_table, seq_ids, positions, inv_fre
     [num_blocks,Hkv,kv8_record_bytes(d)] uint8 (updated in place), e4m3 codes
     with a scale (a power of two) per block of 16 tokens and head for the keys
     and one for the values.  Rows that fall into one block stand together, in
-    the order of their positions; a row for a block's first slot begins it anew.
+    ascending order of their positions (some may be left out); a row for a
+    block's first slot begins it anew.
     Returns q_out (or None without q)."""
     if stream is not None:
         return _on_stream(kv8_append_paged, stream, k, q, k, v, kv_cache, block_table, seq_ids, positions,

@@ -405,7 +405,8 @@ struct Kv8Append {
   // that lanes s = 0 .. 7 read neighbouring 16 bytes.
   alignas(16) float2 angles[kSlots][64];
   int token[kSlots], slot[kSlots], run[kSlots];          // of a row of the pass
-  int phys[kSlots], slot0[kSlots], length[kSlots];       // of a run
+  int phys[kSlots];                                      // of a run
+  uint32_t slots[kSlots];                                // a run's slots of its block, a bit each
   uint32_t most[2][4][kSlots];             // largest value of a run (bits): [key, value][head of the chunk][run]
   uint32_t bad[4][kSlots];                 // its rows with elements that are no numbers, as in the record's flags
   uint32_t scale[2][4][kSlots];
@@ -414,10 +415,11 @@ struct Kv8Append {
 
 // New keys and values into an 8-bit cache.  All tokens of a block share a scale
 // per head, so the unit of work is a run: consecutive rows of the batch whose
-// tokens are neighbours in one block (up to 16).  A CTA takes the runs that
-// begin in a window of rows, as many whole runs at a time as make 16 rows, and
-// the heads of its part in chunks: rows to registers, keys turned, the largest
-// value of each run and head to shared memory; then the scales; then the codes.
+// tokens lie in one block, in ascending order (up to 16; they may leave slots
+// out).  A CTA takes the runs that begin in a window of rows, as many whole runs at
+// a time as make 16 rows, and the heads of its part in chunks: rows to registers,
+// keys turned, the largest value of each run and head to shared memory; then the
+// scales; then the codes.
 // A block that a run enters at its first slot starts anew: its scale is what the
 // run needs, slots not yet written are zeros.  In any other the scale can only
 // grow, and where it does the codes that are there are brought to it.
@@ -464,7 +466,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
       }
     }
     const bool valid = seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < p.max_blocks * kSlots;
-    const bool more = valid && pos % kSlots != 0 && seq_before == seq && pos_before == pos - 1;
+    const bool more = valid && seq_before == seq && pos_before < pos && static_cast<unsigned>(pos_before ^ pos) < kSlots;
     const bool first = valid && !more && lane < p.kv_window;
     int phys = -1;
     if (first) {
@@ -490,8 +492,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         }
         if (warp == 0 && lane == at) {
           s8.phys[runs] = phys;
-          s8.slot0[runs] = pos % kSlots;
-          s8.length[runs] = n;
+          s8.slots[runs] = 0;
         }
         rows += n;
         ++runs;
@@ -503,6 +504,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         s8.run[my_row] = my_run;
       }
       __syncthreads();
+      if (tid < rows) atomicOr(&s8.slots[s8.run[tid]], 1u << s8.slot[tid]);
       // Items are rows of 16 of each head's keys, then of its values: a warp's are
       // neighbouring rows of one of them.  The first heads' rows come while the
       // angles are formed, the next ones' while these are written.
@@ -545,7 +547,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         uint8_t* tail_at = nullptr;
         if (keeper) {
           tail_at = p.kv_cache + (static_cast<size_t>(s8.phys[my]) * p.Hk + h0 + my_head) * Lt::kBytes + Lt::kOffTail;
-          if (s8.slot0[my] != 0) tail = *reinterpret_cast<const uint4*>(tail_at);
+          if (!(s8.slots[my] & 1u)) tail = *reinterpret_cast<const uint4*>(tail_at);
         }
         bool odd[kSteps];                        // some element of the lane's is no finite number
         // (Turned again for the codes: kept, the numbers would take 32 registers
@@ -600,14 +602,14 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
         }
         __syncthreads();
         if (keeper) {
-          const bool fresh = s8.slot0[my] == 0;
+          const bool fresh = (s8.slots[my] & 1u) != 0;
           const uint32_t had[2] = {tail.x, tail.y};
           uint32_t now[2], kept = 0;             // flags of slots that keep their codes
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             now[i] = kv8_scale_for(s8.most[i][my_head][my]);
             s8.most[i][my_head][my] = 0;
-            float turn = s8.length[my] < kSlots ? 0.f : 1.f;
+            float turn = s8.slots[my] != 0xffffu ? 0.f : 1.f;
             if (!fresh) {
               // (Anything but a scale: a block that no append has begun.)
               const float was = __uint_as_float(had[i]);
@@ -620,7 +622,7 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
             s8.scale[i][my_head][my] = now[i];
             s8.turn[i][my_head][my] = turn;
           }
-          const uint32_t slots = ((1u << s8.length[my]) - 1u) << s8.slot0[my];
+          const uint32_t slots = s8.slots[my];
           const uint32_t flags = (tail.z & kept & ~(slots * 0x10001u)) | s8.bad[my_head][my];
           s8.bad[my_head][my] = 0;
           *reinterpret_cast<uint4*>(tail_at) = make_uint4(now[0], now[1], flags, 0u);
@@ -662,10 +664,10 @@ __device__ __forceinline__ void append_kv8_units(const RopeParams& p, const Rope
           if (turn == 1.f) continue;
           uint8_t* codes = p.kv_cache + (static_cast<size_t>(s8.phys[run]) * p.Hk + h0 + h) * Lt::kBytes +
                            (value ? Lt::kOffV : 0);
-          const int from = s8.slot0[run], to = from + s8.length[run];
+          const uint32_t written = s8.slots[run];
           for (int piece = lane; piece < kSlots * kSlotLanes; piece += 32) {
             const int at = piece / kSlotLanes;
-            if (at >= from && at < to) continue;
+            if ((written >> at) & 1u) continue;
             uint4* dst = reinterpret_cast<uint4*>(codes) + piece;
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (turn != 0.f) {

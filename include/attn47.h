@@ -635,10 +635,11 @@ size_t kv8_record_bytes(int d);
  * keys and the values are quantised from fp32 (not through bf16).
  *
  * The tokens of a block share its scales, so the rows of a call that fall into
- * one block stand together, in the order of their positions (rows of other
- * blocks, sequences or padding do not stand between them); if they do not, what
- * that block then holds is unspecified.  A row for the first slot of a block
- * begins it anew: the slots of it that the call does not write become zeros.
+ * one block stand together, in ascending order of their positions, none of them
+ * twice (rows of other blocks, sequences or padding do not stand between them;
+ * positions may be left out); if they do not, what that block then holds is
+ * unspecified.  A row for the first slot of a block begins it anew: the slots of it
+ * that the call does not write become zeros.
  * In any other block the scales stay, or grow where a new value needs it, and
  * the codes of the other slots are then rounded to the larger scale (which
  * changes only those that become subnormal); in a block that was never begun
