@@ -989,6 +989,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
     f.max_blocks = max_blocks_per_seq;
     f.num_blocks = num_blocks;
     f.kv_cache = kv_cache;
+    f.q = q;
     f.rows = N;
     return launch_result(attn47::launch_fwd_sm103(f), what);
   }

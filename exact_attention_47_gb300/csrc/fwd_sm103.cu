@@ -87,6 +87,7 @@
 // held all the way from the copy to the MMA), copies issued by the gather warps
 // themselves (291), a fourth warpgroup with two warps to an operand (300: the softmax
 // has too few registers left).
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "fwd_sm103.h"
@@ -124,6 +125,7 @@ __host__ __device__ constexpr int sort_max_pairs(int source) { return source == 
 __host__ __device__ constexpr int raw_stages(int d) { return d == 128 ? 6 : 14; }
 constexpr int kMaxRawStages = 14;
 constexpr int kScaleTiles = 16;     // tiles whose scales are kept
+constexpr int kAgain = 64, kWideExps = 72;   // see FwdBarriers
 
 // SUMV (d = 64 with contiguous K/V): the row sums of P come from the tensor
 // core.  Every V stage gets a second 64-column chunk, written once, whose
@@ -144,7 +146,7 @@ struct FwdLayout {
   static constexpr int kOffK = kOffQ + kTiles * kQTile;
   static constexpr int kOffV = kOffK + kStages * kKV;
   static constexpr int kOffBar = kOffV + kStages * kVStage;
-  static constexpr int kOffCtx = kOffBar + 768;          // paged: ctx_b of each sequence
+  static constexpr int kOffCtx = kOffBar + 1024;         // paged: ctx_b of each sequence
   static constexpr int kOffOrder = kOffCtx + 4 * 256;    // paged: (b << 16 | qblk) of each cost rank
   // 8-bit cache: (K scale times scale log2 e, log2 of V's, 1 / V's) of the 8 blocks
   // of tile t at t % kScaleTiles; a ring of raw blocks.
@@ -171,14 +173,16 @@ struct FwdBarriers {
   int abort;
   int raw_kind[kMaxRawStages], raw_fills[kMaxRawStages];
   int q_loads[2];                     // copies of Q tile x asked for (its first thread's count)
+  unsigned again[8][kAgain / 32];     // bands of softmax warp w with rows for careful_rows (the last one: and those behind)
   // The first position of a flagged token in unit u (of the CTA's), in its tiles so
   // far, at u % 16: the look-up is at most two tiles ahead of the gather, that kStages
   // ahead of the MMAs, and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1),
   // which also bounds the scales' ring.
   int first_flagged[16];
+  int wide[16];                       // in the same way: whether its V scales are kWideExps powers of two apart
 };
 enum RawKind { kRawNone, kRawCodes, kRawCareful, kRawEnd };   // none: zeros; careful: there may be NaN codes
-static_assert(sizeof(FwdBarriers) <= 768, "room in the layout");
+static_assert(sizeof(FwdBarriers) <= 1024, "room in the layout");
 
 struct FwdParams {
   void* o;
@@ -200,6 +204,7 @@ struct FwdParams {
   const uint8_t* kv_cache;
   int rows;
   bool packed;
+  const __nv_bfloat16* q;   // [B, Hq, N, d]
 };
 
 // Cost ordering of the paged mode fits in shared memory up to these sizes
@@ -222,6 +227,103 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
 __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
   const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in the byte of a 0x7f or 0xff
   return w & ~(nan * 0xffu);
+}
+
+// 8-bit cache: rows that the tiles cannot hold, one to a lane, key by key in fp32, each
+// scale where its product is: the row's O and LSE, q at position qpos (-1: no such row).
+// The tiles' numerators P' carry the V scales, 2^e.  One that is under 2^-126 is lost, and
+// with it up to 2^(-126 - e) of l a key (moving m, up to 2^(-110 - e)), where l is at least
+// 2^(8 - e') by the largest P'.  With all e within kWideExps of each other that is 2^-46 of
+// l a key, beyond that with l of 2^-8 and more 2^-38 (e is at least -64); the other rows
+// (their largest P' has an e' over 16) come here.  About 1000 instructions a key
+// and 32 columns (4 sequences of 1000 tokens, 512 queries of 12 heads over 2, d = 128: 4.1
+// ms where the tiles take 40 us), out of line so that the tiles' loop stays as it is: sums
+// of l of its own in that loop cost the chunks 3 to 6 %.
+template <int D>
+__device__ __noinline__ void careful_rows(const uint8_t* kv_cache, const int* table, int num_blocks, int Hkv, int kvh,
+                                          float scale_log2, int qpos, const __nv_bfloat16* q, __nv_bfloat16* o,
+                                          float* lse) {
+  const int last = __reduce_max_sync(0xffffffffu, qpos);
+  uint32_t qw[D / 2];                              // fp16, as in the tiles
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 v = qpos < 0 ? make_uint4(0u, 0u, 0u, 0u) : reinterpret_cast<const uint4*>(q)[i];
+    qw[4 * i] = v.x;
+    qw[4 * i + 1] = v.y;
+    qw[4 * i + 2] = v.z;
+    qw[4 * i + 3] = v.w;
+    mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu),
+                  __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  }
+  const int fe = min(268 - static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7), 253);
+  const float up = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+  const float back = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 2; ++i)
+    qw[i] = pack_f16x2(__uint_as_float(qw[i] << 16) * up, __uint_as_float(qw[i] & 0xffff0000u) * up);
+  auto numbers = [](uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); };
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {             // 32 columns of O at a time
+    float m = -INFINITY, l = 0.f, acc[32];
+    bool spoilt = false;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) acc[c] = 0.f;
+#pragma unroll 1
+    for (int key = 0; key <= last; ++key) {
+      const int phys = __ldg(table + key / kPageRows), slot = key % kPageRows;
+      uint4 tail = make_uint4(0x3f800000u, 0x3f800000u, 0u, 0u);
+      const uint8_t* rec = nullptr;                // (a block outside the pool: keys and values of zero)
+      if (static_cast<unsigned>(phys) < static_cast<unsigned>(num_blocks)) {
+        rec = kv_cache + (static_cast<size_t>(phys) * Hkv + kvh) * Kv8Layout<D>::kBytes;
+        tail = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffTail));
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rec != nullptr) v = __ldg(reinterpret_cast<const uint4*>(rec + slot * D) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 k0 = numbers(e4m3x2_to_f16x2(w[c])), k1 = numbers(e4m3x2_hi_to_f16x2(w[c]));
+          const float2 q0 = numbers(qw[8 * i + 2 * c]), q1 = numbers(qw[8 * i + 2 * c + 1]);
+          s = fmaf(q0.x, k0.x, fmaf(q0.y, k0.y, fmaf(q1.x, k1.x, fmaf(q1.y, k1.y, s))));
+        }
+      }
+      s = s * back * scale_log2 * __uint_as_float(tail.x);     // (0 stays 0)
+      if (key > qpos) continue;
+      spoilt |= (((tail.z | (tail.z >> 16)) >> slot) & 1u) != 0;
+      const float to = fmaxf(m, s), turn = m == to ? 1.f : ex2(m - to);
+      const float w0 = s == to ? 1.f : ex2(s - to);
+      m = to;
+      l = fmaf(l, turn, w0);
+      const float wv = w0 * __uint_as_float(tail.y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rec != nullptr) v = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffV + slot * D + c0) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 v0 = numbers(e4m3x2_to_f16x2(w[c])), v1 = numbers(e4m3x2_hi_to_f16x2(w[c]));
+          float* a = acc + 16 * i + 4 * c;
+          a[0] = fmaf(a[0], turn, wv * v0.x);
+          a[1] = fmaf(a[1], turn, wv * v0.y);
+          a[2] = fmaf(a[2], turn, wv * v1.x);
+          a[3] = fmaf(a[3], turn, wv * v1.y);
+        }
+      }
+    }
+    if (qpos < 0) continue;
+    const float inv = spoilt ? __uint_as_float(0x7fc00000u) : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < 32; c += 8)
+      reinterpret_cast<uint4*>(o + c0 + c)[0] =
+          make_uint4(pack_bf16x2(acc[c] * inv, acc[c + 1] * inv), pack_bf16x2(acc[c + 2] * inv, acc[c + 3] * inv),
+                     pack_bf16x2(acc[c + 4] * inv, acc[c + 5] * inv), pack_bf16x2(acc[c + 6] * inv, acc[c + 7] * inv));
+    if (c0 == 0 && lse != nullptr) *lse = spoilt ? __uint_as_float(0x7fc00000u) : (m + __log2f(l)) * kLn2;
+  }
 }
 
 template <int D, bool CAUSAL, int SOURCE, bool SORTED>
@@ -335,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&bar->q_ready[x]), kBM);
         bar->q_loads[x] = 0;
       }
+      for (int x = 0; x < 8 * kAgain / 32; ++x) (&bar->again[0][0])[x] = 0;
       for (int x = 0; x < L::kRawStages; ++x) {
         mbar_init(smem_addr(&bar->raw_full[x]), 1);
         mbar_init(smem_addr(&bar->raw_empty[x]), 2);
@@ -484,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint4 tail = tail_of(now_rec);
     next = read_table();
     int unit = 0, flagged = 0x7fffffff, n = 0;
+    int least = 255, most = 0;                               // exponents of the unit's V scales so far
     bool ok = true;
     // Block number `at` into the ring.
     auto fill = [&](int at, int rec, int what) {
@@ -507,16 +611,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       next = read_table();
       if (now_number < 0) break;
       // The unit's first flagged token so far: the lowest bit of its block's flags.
-      // It is stored before the tile's blocks are on their way, so whoever has seen
-      // this tile's products sees it, with query tile A already before the unit's end.
+      // It and `wide` are stored before the tile's blocks are on their way, so whoever has
+      // seen this tile's products sees them, with query tile A already before the unit's end.
       const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
       if (__any_sync(0xffffffffu, bits != 0)) {
         const int at = bits != 0 ? (now_number * kPagesPerTile + lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
         flagged = min(flagged, __reduce_min_sync(0xffffffffu, at));
       }
-      if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
+      const int e = now_rec >= 0 ? static_cast<int>(tail.y >> 23) : -1;
+      most = max(most, __reduce_max_sync(0xffffffffu, e));
+      least = min(least, __reduce_min_sync(0xffffffffu, e < 0 ? 255 : e));
+      if (lane == 0) {
+        reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
+        reinterpret_cast<volatile int*>(bar->wide)[unit & 15] = most - least >= kWideExps;
+      }
       if (now_last) {
         flagged = 0x7fffffff;
+        least = 255;
+        most = 0;
         ++unit;
       }
       if (lane < kPagesPerTile) {
@@ -1202,6 +1314,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         spoilt = qpos >= reinterpret_cast<const volatile int*>(bar->first_flagged)[units & 15];
         if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
         if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
+        const bool again = l < 0x1p-8f && qpos >= 0 && qrow < p.N && !spoilt &&
+                           reinterpret_cast<const volatile int*>(bar->wide)[units & 15];
+        if (__any_sync(0xffffffffu, again) && lane == 0) {
+          const int at = min(band, kAgain - 1);
+          bar->again[warp][at / 32] |= 1u << (at % 32);
+        }
       }
       const bool in_range = qrow < p.N;
       __nv_bfloat16* orow =
@@ -1237,6 +1355,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++units;
     }
     if constexpr (KV8) {
+      __syncwarp();
+      for (int w = 0; w < kAgain / 32 && ok; ++w)
+        for (unsigned todo = bar->again[warp][w]; todo != 0; todo &= todo - 1) {
+          const int first = 32 * w + __ffs(todo) - 1;
+          for (int band = first; unit_at(band) < p.num_units && (band == first || first == kAgain - 1); ++band) {
+            const Unit u = unit_info(unit_at(band));
+            const int qrow = u.qblk * kRowsPerCta + x * kBM + row;
+            const size_t at = static_cast<size_t>(u.zq) * p.N + qrow;
+            const int qpos = qrow < p.N ? max(u.pos0 + qrow % p.rows, -1) : -1;
+            careful_rows<D>(p.kv_cache, p.block_table + static_cast<size_t>(u.b) * p.max_blocks, p.num_blocks, p.Hkv, u.kvh,
+                            p.scale_log2, qpos, p.q + at * D, static_cast<__nv_bfloat16*>(p.o) + at * D,
+                            p.lse != nullptr ? p.lse + at : nullptr);
+          }
+        }
       // After a wait that ran out: the last copy of Q (this unit's, or already the
       // next one's) must land before the CTA may exit.
       if (!ok && quarter == 0 && lane == 0) {
@@ -1280,6 +1412,7 @@ cudaError_t launch_t(const FwdLaunch& a) {
   p.kv_cache = static_cast<const uint8_t*>(a.kv_cache);
   p.rows = a.rows;
   p.packed = a.rows != a.N;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
   // Persistent: one CTA per SM (shared memory allows one), each walking units.
   const unsigned grid = static_cast<unsigned>(min(p.num_units, a.sms > 0 ? a.sms : 1));
   return launch_pdl(kern, dim3(grid), dim3(kThreads), L::kSmem, a.stream, *a.tq, *a.tk, *a.tv, p);

@@ -34,6 +34,7 @@ struct FwdLaunch {
   // ctx_lens holds the sequences' lengths, the `rows` new tokens included; either
   // Hq query heads of N = rows rows, or Hq = Hkv groups of N = group * rows rows.
   const void* kv_cache = nullptr;     // [num_blocks, Hkv, record] bytes
+  const void* q = nullptr;            // what tq covers
   int rows = 0;
 };
 

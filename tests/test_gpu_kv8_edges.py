@@ -7,7 +7,8 @@ import torch
 
 import exact_attention_47_gb300 as attn
 import oracle
-from kv8_bounds import compare_live
+from kv8_bounds import close_bound, compare_live
+from parity import to64
 from test_gpu_kv8_attention import DECODES, PREFILLS, case, decode, prefill, ways
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,68 @@ def test_flagged_tokens_where_the_query_tiles_end_apart(Hq, Hkv, N, d):
         o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
         compare_live(o, lse, ref, cache.numpy(), table.numpy(), lens, d, what="%d times" % times)
     assert attn.device_status() == 0
+
+
+def wide(i, kind):
+    """log2 of block i's V scale."""
+    return {"down": 64 if i < 9 else -64, "up": -64 if i < 9 else 64, "in turn": 64 if i % 2 else -64, "one": 64 if i == 9 else -64,
+            "first": 64 if i == 0 else -64, "zeros": -64 if i % 3 else 60, "near": 36 if i % 2 else -64, "three": (-64, 0, 64)[i % 3],
+            "small": -30 if i % 5 else -64}[kind]
+
+
+@pytest.mark.parametrize("kind", ["down", "up", "in turn", "one", "first", "zeros", "near", "three", "small"])
+@pytest.mark.parametrize("N,d", [(40, 128), (40, 64), (300, 64), (3, 128)])
+def test_value_scales_from_one_end_of_their_range_to_the_other(kind, N, d):
+    """Every V scale is accepted beside every other one: the weights of the tokens with
+    small values, which dominate the softmax sum where those with large ones have the
+    lower scores, are not lost.  ("zeros": blocks of no value at all have 2^-64.)"""
+    Hq, Hkv = 2, 1
+    lens = [420, 330]
+    q, cache, table, sl = case(lens, Hq, Hkv, d, seed=N + d, N=N, garbage=None)
+    for b in range(2):
+        for i in range(-(-lens[b] // 16)):
+            rec = cache[table[b, i].long(), 0]
+            tail = rec[32 * d: 32 * d + 8].view(torch.float32)
+            tail[0] *= 4.0                           # scores that differ by some ten log2 units
+            tail[1] = 2.0 ** wide(i, kind)
+            if kind == "zeros" and i % 3:
+                rec[16 * d: 32 * d] = 0
+    args = [x.to(DEV) for x in (q, cache, table, sl)]
+    q64, c = q.double().numpy(), cache.numpy()
+    o_ref, lse_ref = oracle.prefill_paged_kv8(q64, c, table.numpy(), lens, d ** -0.5, d)
+    # With keys four times as large as normalised ones the scores are off by under
+    # 2^-10, and so is the LSE.
+    lim = close_bound(q64, c, table.numpy(), lens, d ** -0.5, d, score=2.0 ** -10)
+    for times in ways(2, Hq, Hkv, N, d):
+        o, lse = prefill(args, times)
+        err = np.abs(to64(o) - o_ref)
+        lerr = np.abs(lse.double().cpu().numpy() - lse_ref).max()
+        assert lerr <= 2.0 ** -10, "%d times: lse off by %.3g" % (times, lerr)
+        assert np.all(err <= lim), "%d times: o at %.3g of its bound" % (times, (err / np.maximum(lim, 1e-300)).max())
+    assert attn.device_status() == 0
+
+
+def test_wide_value_scales_in_many_units():
+    """More units to a CTA than its list of rows to be computed again is long."""
+    d, Hq, Hkv, N = 64, 2, 2, 100
+    lens = [33, 48, 20, 41, 32]
+    q, cache, table, sl = case(lens, Hq, Hkv, d, seed=4, N=N, garbage=None)
+    for b in range(len(lens)):
+        for i in range(-(-lens[b] // 16)):
+            for h in range(Hkv):
+                tail = cache[table[b, i].long(), h, 32 * d: 32 * d + 8].view(torch.float32)
+                tail[0] *= 4.0
+                tail[1] = 2.0 ** wide(i, "in turn")
+    times = 70 * 152 // (len(lens) * Hkv) + 1
+    assert attn.attn_prefill_paged_kv8_workspace_size(times * len(lens), Hq, Hkv, N, d) == 0
+    q64, c = q.double().numpy(), cache.numpy()
+    o_ref, lse_ref = oracle.prefill_paged_kv8(q64, c, table.numpy(), lens, d ** -0.5, d)
+    lim = torch.from_numpy(close_bound(q64, c, table.numpy(), lens, d ** -0.5, d, score=2.0 ** -10)).to(DEV)
+    o, lse = attn.attn_prefill_paged_kv8(*(x.to(DEV).repeat(times, *[1] * (x.dim() - 1)) if x is not cache else x.to(DEV)
+                                           for x in (q, cache, table, sl)))
+    torch.cuda.synchronize()
+    err = (o.double().view(times, *o_ref.shape) - torch.from_numpy(o_ref).to(DEV)).abs()
+    lse, ref = lse.double().view(times, *lse_ref.shape), torch.from_numpy(lse_ref).to(DEV)
+    none = torch.isneginf(ref)
+    assert torch.all(torch.isneginf(lse) == none) and torch.all(err <= lim)
+    assert ((lse - ref).abs()[:, ~none] <= 2.0 ** -10).all() and attn.device_status() == 0
