@@ -261,8 +261,8 @@ struct RunState {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
       // (A block without visible tokens may come first: its numerators are then
-      // ex2(-inf + 1e30) = 0.)
-      stab[nt][0] = stab[nt][1] = -1e30f;
+      // ex2(-inf + 3e38) = 0.)
+      stab[nt][0] = stab[nt][1] = -3e38f;
       limit[nt][0] = limit[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
@@ -279,13 +279,16 @@ struct RunState {
         float mx = s[nt][h];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        const float top = stab[nt][h] + kHigh;   // the running maximum
+        const float top = __fadd_rd(stab[nt][h], kHigh);   // the running maximum
         // (To a multiple of 2^-10, so that adding whole numbers to a stabiliser,
-        // here and for the LSE, rounds nothing.)
-        const float to = __fsub_rn(__fadd_rn(mx > top + kTau ? mx : top, kGrid), kGrid) - kHigh;
+        // here and for the LSE, rounds nothing.  Beyond 2^13 every fp32 number is one;
+        // beyond 2^24 kHigh and kTau round themselves, so that a numerator is never more
+        // than 2^(kHigh + kTau) and the stabiliser never creeps up.)
+        const float most = mx > limit[nt][h] ? mx : top;
+        const float to = __fsub_ru(fabsf(most) < 8192.f ? __fsub_rn(__fadd_rn(most, kGrid), kGrid) : most, kHigh);
         f[h] = to == stab[nt][h] ? 1.f : ex2(stab[nt][h] - to);
         stab[nt][h] = to;
-        limit[nt][h] = to + kHigh + kTau;
+        limit[nt][h] = __fadd_rd(to, kHigh + kTau);
         l[nt][h] *= f[h];
       }
 #pragma unroll

@@ -235,7 +235,9 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 // with it up to 2^(-126 - e) of l a key (moving m, up to 2^(-110 - e)), where l is at least
 // 2^(8 - e') by the largest P'.  With all e within kWideExps of each other that is 2^-46 of
 // l a key, beyond that with l of 2^-8 and more 2^-38 (e is at least -64); the other rows
-// (their largest P' has an e' over 16) come here.  About 1000 instructions a key
+// (their largest P' has an e' over 16) come here.  So do rows with scores beyond 2^26 log2
+// units, where m is a multiple of 8 and more and P' may leave fp16, and those whose O shows
+// that it has done so.  About 1000 instructions a key
 // and 32 columns (4 sequences of 1000 tokens, 512 queries of 12 heads over 2, d = 128: 4.1
 // ms where the tiles take 40 us), out of line so that the tiles' loop stays as it is: sums
 // of l of its own in that loop cost the chunks 3 to 6 %.
@@ -1314,13 +1316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         spoilt = qpos >= reinterpret_cast<const volatile int*>(bar->first_flagged)[units & 15];
         if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
         if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
-        const bool again = l < 0x1p-8f && qpos >= 0 && qrow < p.N && !spoilt &&
-                           reinterpret_cast<const volatile int*>(bar->wide)[units & 15];
-        if (__any_sync(0xffffffffu, again) && lane == 0) {
-          const int at = min(band, kAgain - 1);
-          bar->again[warp][at / 32] |= 1u << (at % 32);
-        }
       }
+      bool again = KV8 && ((l < 0x1p-8f && reinterpret_cast<const volatile int*>(bar->wide)[units & 15]) || fabsf(m) >= 0x1p26f);
       const bool in_range = qrow < p.N;
       __nv_bfloat16* orow =
           reinterpret_cast<__nv_bfloat16*>(p.o) + (static_cast<size_t>(zq) * p.N + qrow) * D;
@@ -1329,6 +1326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         ATTN47_TMEM_LD32(tl + colO + c0, o);
         ATTN47_TMEM_LD_WAIT(o);
+        if constexpr (KV8) again |= !(fabsf(__uint_as_float(o[0])) <= 3.402823466e38f);
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c)
@@ -1343,6 +1341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (in_range && p.lse != nullptr)
         p.lse[static_cast<size_t>(zq) * p.N + qrow] =
             KV8 && spoilt ? __uint_as_float(0x7fc00000u) : (m + __log2f(l)) * kLn2;
+      if constexpr (KV8) {
+        // (A query that is not finite itself has back = 2^114, and NaN.)
+        again = again && qpos >= 0 && in_range && !spoilt && back < 0x1p114f;
+        if (__any_sync(0xffffffffu, again) && lane == 0) {
+          const int at = min(band, kAgain - 1);
+          bar->again[warp][at / 32] |= 1u << (at % 32);
+        }
+      }
       // O_X has been read out: the next unit's first P V may overwrite it.
       tc_fence_before();
       __syncwarp();

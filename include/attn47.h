@@ -735,8 +735,8 @@ size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int 
  * multiplied by its V scale first and rounded to 11 bits, or to 2^-32 of the row's
  * largest such product where that is coarser, and a block outside the pool counts
  * as keys and values of zero instead of being left out.  (Rows that attend to V
- * scales more than 2^72 apart, with the most weight on one over 2^16, are computed
- * key by key: 100 times as slow.)
+ * scales more than 2^72 apart, with the most weight on one over 2^16, and rows with
+ * scores beyond 2^26 are computed key by key: 100 times as slow.)
  */
 attn_status_t attn_prefill_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
                                      const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d,

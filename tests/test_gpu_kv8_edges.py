@@ -7,6 +7,7 @@ import torch
 
 import exact_attention_47_gb300 as attn
 import oracle
+import workloads
 from kv8_bounds import close_bound, compare_live
 from parity import to64
 from test_gpu_kv8_attention import DECODES, PREFILLS, case, decode, prefill, ways
@@ -126,3 +127,57 @@ def test_wide_value_scales_in_many_units():
     none = torch.isneginf(ref)
     assert torch.all(torch.isneginf(lse) == none) and torch.all(err <= lim)
     assert ((lse - ref).abs()[:, ~none] <= 2.0 ** -10).all() and attn.device_status() == 0
+
+
+def along(L, d, e, w, N, vscale):
+    """Keys of one sequence along a vector of signs, of sizes w (one head), queries 2^e
+    of it: all products and sums of a score are exact."""
+    table, _, _, nb = workloads.token_map([0], [L], 1)
+    cache = workloads.kv8_cache(nb, 1, attn.kv8_record_bytes(d), d, 2)
+    sign = torch.where(torch.rand(d, generator=torch.Generator().manual_seed(5)) < 0.5, -1.0, 1.0)
+    codes = (torch.tensor(w)[:, None] * sign).to(torch.float8_e4m3fn).view(torch.uint8)
+    for p in range(L):
+        rec = cache[table[0, p // 16].long(), 0]
+        rec[p % 16 * d: (p % 16 + 1) * d] = codes[p]
+        rec[32 * d: 32 * d + 8].view(torch.float32)[:] = torch.tensor([1.0, vscale(p // 16)])
+    q = (sign * 2.0 ** e).to(torch.bfloat16).expand(1, 2, N, d).contiguous()
+    return q, cache, table, torch.tensor([L], dtype=torch.int32)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("N", [1, 3, 64])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_every_size(d, N, sign):
+    """One key weighs more than all others by some 2^-5 of scores of 2^14 .. 2^94 log2
+    units, of either sign: o is its value.  (Numerators rounded to 11 bits and o to bf16;
+    a score of exact sums is off by its three products' roundings, and the LSE by two
+    more: 5 2^-24 of it and the sum's 2^-24.)"""
+    L = 200
+    size = [1.0 + (i * 7 % 5) / 8 for i in range(L)] if sign > 0 else [1.25 + (i * 7 % 5) / 8 for i in range(L)]
+    size[50], size[120] = (1.625, 1.75) if sign > 0 else (1.125, 1.0)
+    for e in (10, 14, 18, 20, 21, 22, 23, 24, 25, 27, 29, 31, 32, 33, 36, 45, 60, 90):
+        q, cache, table, sl = along(L, d, e, [sign * s for s in size], N, lambda i: 2.0 ** (i % 4 - 6))
+        o_ref, lse_ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), [L], d ** -0.5, d)
+        for times in ways(1, 2, 1, N, d):
+            o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
+            assert np.all(np.abs(to64(o) - o_ref) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(o_ref)), (e, times)
+            assert np.all(np.abs(lse.double().cpu().numpy() / lse_ref - 1) <= 6 * 2.0 ** -24), (e, times)
+    assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("N", [1, 3, 64])
+def test_the_same_large_score_twice(N):
+    """Two keys of the same score, the largest, beside V scales that differ: the mean of
+    their values."""
+    L, d = 200, 128
+    size = [1.0] * L
+    size[50] = size[120] = 1.75
+    for e in (24, 28, 34, 50):
+        q, cache, table, sl = along(L, d, e, size, N, lambda i: 2.0 ** (i % 4 - 6))
+        o_ref, lse_ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), [L], d ** -0.5, d)
+        v = np.abs(oracle.kv8_unpack(cache.numpy(), d)[1]).max()
+        for times in ways(1, 2, 1, N, d):
+            o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
+            assert np.all(np.abs(to64(o) - o_ref) <= 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * v), (e, times)
+            assert np.all(np.abs(lse.double().cpu().numpy() / lse_ref - 1) <= 6 * 2.0 ** -24), (e, times)
+    assert attn.device_status() == 0
