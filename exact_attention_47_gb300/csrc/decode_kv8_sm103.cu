@@ -367,7 +367,8 @@ __device__ __forceinline__ void take_blocks(const LaneData<D>& at, const uint32_
     any_flags |= tail[2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float f0 = q.back[nt][0] * scale_k, f1 = q.back[nt][1] * scale_k;
+      // (Finite, so that a score of 0 stays 0: queries of 2^78 beside keys of 2^64.)
+      const float f0 = fminf(q.back[nt][0] * scale_k, 3.402823466e38f), f1 = fminf(q.back[nt][1] * scale_k, 3.402823466e38f);
       s[n][nt][0] *= f0;
       s[n][nt][1] *= f1;
       s[n][nt][2] *= f0;

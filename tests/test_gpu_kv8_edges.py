@@ -181,3 +181,22 @@ def test_the_same_large_score_twice(N):
             assert np.all(np.abs(to64(o) - o_ref) <= 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * v), (e, times)
             assert np.all(np.abs(lse.double().cpu().numpy() / lse_ref - 1) <= 6 * 2.0 ** -24), (e, times)
     assert attn.device_status() == 0
+
+
+@pytest.mark.parametrize("N", [1, 3, 64])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_score_of_zero_beside_scores_beyond_fp32(d, N):
+    """A key of zeros in a block of the largest scale, under queries of 2^90: the others'
+    scores are minus infinity in fp32, and o is its value."""
+    L = 40
+    size = [-1.0] * L
+    size[20] = 0.0
+    q, cache, table, sl = along(L, d, 90, size, N, lambda i: 2.0 ** -6)
+    cache[:, :, 32 * d: 32 * d + 4].view(torch.float32)[:] = 2.0 ** 64
+    sees = np.arange(L - N, L) >= 20
+    v = oracle.kv8_unpack(cache.numpy(), d)[1][table[0, 1], 0, 4]
+    for times in ways(1, 2, 1, N, d):
+        o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
+        assert np.all(np.abs(to64(o)[:, :, sees] - v) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(v)), times
+        assert torch.all(lse.cpu()[:, :, torch.from_numpy(sees)] == 0.0), times
+    assert attn.device_status() == 0
