@@ -274,17 +274,13 @@ __device__ __noinline__ void careful_rows(const uint8_t* kv_cache, const int* ta
 #pragma unroll 1
     for (int key = 0; key <= last; ++key) {
       const int phys = __ldg(table + key / kPageRows), slot = key % kPageRows;
-      uint4 tail = make_uint4(0x3f800000u, 0x3f800000u, 0u, 0u);
-      const uint8_t* rec = nullptr;                // (a block outside the pool: keys and values of zero)
-      if (static_cast<unsigned>(phys) < static_cast<unsigned>(num_blocks)) {
-        rec = kv_cache + (static_cast<size_t>(phys) * Hkv + kvh) * Kv8Layout<D>::kBytes;
-        tail = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffTail));
-      }
+      if (static_cast<unsigned>(phys) >= static_cast<unsigned>(num_blocks)) continue;
+      const uint8_t* rec = kv_cache + (static_cast<size_t>(phys) * Hkv + kvh) * Kv8Layout<D>::kBytes;
+      const uint4 tail = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffTail));
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rec != nullptr) v = __ldg(reinterpret_cast<const uint4*>(rec + slot * D) + i);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(rec + slot * D) + i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -303,8 +299,7 @@ __device__ __noinline__ void careful_rows(const uint8_t* kv_cache, const int* ta
       const float wv = w0 * __uint_as_float(tail.y);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rec != nullptr) v = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffV + slot * D + c0) + i);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffV + slot * D + c0) + i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -318,7 +313,7 @@ __device__ __noinline__ void careful_rows(const uint8_t* kv_cache, const int* ta
       }
     }
     if (qpos < 0) continue;
-    const float inv = spoilt ? __uint_as_float(0x7fc00000u) : 1.f / l;
+    const float inv = spoilt ? __uint_as_float(0x7fc00000u) : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int c = 0; c < 32; c += 8)
       reinterpret_cast<uint4*>(o + c0 + c)[0] =
@@ -634,10 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++unit;
       }
       if (lane < kPagesPerTile) {
-        // (No block, zeros: any scales.)
+        // (No block: a V scale whose logarithm leaves nothing of its keys' numerators.)
         reinterpret_cast<float4*>(smem + L::kOffScales)[n % kScaleTiles * 8 + lane] =
             make_float4(now_rec >= 0 ? __uint_as_float(tail.x) * p.scale_log2 : 1.f,
-                        now_rec >= 0 ? static_cast<float>(static_cast<int>(tail.y >> 23) - 127) : 0.f,
+                        now_rec >= 0 ? static_cast<float>(static_cast<int>(tail.y >> 23) - 127) : -INFINITY,
                         now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, 0.f);
       }
       __syncwarp();                              // (lanes 0 and 1 release what all of them have stored)
@@ -1280,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == 0 || pass == 1) {                 // the tile's maximum is needed
           const float mt = KV8 ? row_max() - kHigh8 : row_max() * sl2;
           if (j == 0)
-            m = (mt == -INFINITY) ? 0.f : mt;
+            m = (mt == -INFINITY) ? (KV8 ? -1e30f : 0.f) : mt;   // (8-bit cache: keys may come in a later tile)
           else
             restabilise(mt);
         }

@@ -117,7 +117,7 @@ typedef enum attn_status {
 #define ATTN_DEV_BAD_BLOCK 0x2u  /* a block-table entry was outside [0, num_blocks); that block
                                     was skipped */
 #define ATTN_DEV_BAD_SEQLEN 0x4u /* a seq_lens entry was < 0 or > max_blocks_per_seq*block_size
-                                    (decode), or a ctx_lens entry was < 0 or
+                                    (decode, attn_prefill_paged_kv8), or a ctx_lens entry was < 0 or
                                     > max_blocks_per_seq*block_size - N (chunked prefill);
                                     it was clamped into range, outputs of that sequence invalid;
                                     or a token's cache position was outside its table (rope_append_*,
@@ -733,10 +733,9 @@ size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int 
  * head at a time, each time over the whole sequence; many (where the workspace
  * size is 0) through tiles of 128 rows by 128 keys.  In tiles a numerator is
  * multiplied by its V scale first and rounded to 11 bits, or to 2^-32 of the row's
- * largest such product where that is coarser, and a block outside the pool counts
- * as keys and values of zero instead of being left out.  (Rows that attend to V
- * scales more than 2^72 apart, with the most weight on one over 2^16, and rows with
- * scores beyond 2^26 are computed key by key: 100 times as slow.)
+ * largest such product where that is coarser.  (Rows that attend to V scales more
+ * than 2^72 apart, with the most weight on one over 2^16, and rows with scores
+ * beyond 2^26 are computed key by key: 100 times as slow.)
  */
 attn_status_t attn_prefill_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
                                      const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d,

@@ -200,3 +200,40 @@ def test_a_score_of_zero_beside_scores_beyond_fp32(d, N):
         assert np.all(np.abs(to64(o)[:, :, sees] - v) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(v)), times
         assert torch.all(lse.cpu()[:, :, torch.from_numpy(sees)] == 0.0), times
     assert attn.device_status() == 0
+
+
+def without(q, cache, table, lens, missing, d):
+    """The oracle's o and LSE where the blocks `missing` of each sequence are left out."""
+    k, v, _ = oracle.kv8_unpack(cache, d)
+    S, Hq, N, _ = q.shape
+    o, lse = np.zeros(q.shape), np.full(q.shape[:3], -np.inf)
+    for b in range(S):
+        j = np.array([p for p in range(lens[b]) if p // 16 not in missing[b]], dtype=int)
+        for h in range(Hq):
+            g = h // (Hq // cache.shape[1])
+            keys, vals = (x[np.asarray(table)[b, j // 16], g, j % 16] for x in (k, v))
+            for i in range(N):
+                see = j <= lens[b] - N + i
+                if see.any():
+                    x = d ** -0.5 * (keys[see] @ q[b, h, i])
+                    w = np.exp(x - x.max())
+                    o[b, h, i], lse[b, h, i] = w @ vals[see] / w.sum(), x.max() + np.log(w.sum())
+    return o, lse
+
+
+@pytest.mark.parametrize("Hq,Hkv,N,d", [(4, 2, 64, 64), (2, 1, 40, 128), (2, 2, 270, 64), (3, 3, 2, 128)])
+def test_blocks_outside_the_pool_are_left_out(Hq, Hkv, N, d):
+    """In either way through a batch: single blocks, the whole first tile of keys, all of
+    them, the last one."""
+    lens = [300, 300, 290, 100, 280, 333]
+    missing = [{1, 3, 17}, set(range(8)), set(range(19)), {0, 6}, {0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11}, set()]
+    q, cache, table, sl = case(lens, Hq, Hkv, d, seed=N, N=N)
+    bad = table.clone()
+    for b, gone in enumerate(missing):
+        for i in gone:
+            bad[b, i] = (-1, cache.shape[0], 2 ** 31 - 1)[i % 3]
+    ref = without(q.double().numpy(), cache.numpy(), table.numpy(), lens, missing, d)
+    for times in ways(len(lens), Hq, Hkv, N, d):
+        o, lse = prefill([x.to(DEV) for x in (q, cache, bad, sl)], times)
+        assert attn.device_status() == attn.ATTN_DEV_BAD_BLOCK
+        compare_live(o, lse, ref, cache.numpy(), table.numpy(), lens, d, what="%d times" % times)
