@@ -889,12 +889,12 @@ void fill_quantised_decode(Launch& a, const DeviceInfo& dev, const void* q, cons
   a.stream = static_cast<cudaStream_t>(stream);
 }
 
-// Tensor map over the codes of 8-bit records, as 128-byte lines in boxes of
-// `lines` lines, 128-byte swizzle.
-attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records, int d, int lines) {
+// Tensor map over the codes of 8-bit records, as 128-byte lines, a record's to a box,
+// 128-byte swizzle.
+attn_status_t encode_kv8(CUtensorMap* map, const void* base, cuuint64_t records, int d) {
   const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d / 4), records};
   const cuuint64_t strides[2] = {128, attn47::kv8_record_bytes_of(d)};
-  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(lines), 1};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(d / 4), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr);
   if (r != CUDA_SUCCESS) return fail(ATTN_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -964,7 +964,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
                                  static_cast<cuuint64_t>(num_seqs) * heads};
     alignas(64) CUtensorMap tq, blocks;
     attn_status_t enc = encode_bf16(&tq, q, 3, qdims, qbox);
-    if (enc == ATTN_OK) enc = encode_kv8(&blocks, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d, d / 4);
+    if (enc == ATTN_OK) enc = encode_kv8(&blocks, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d);
     if (enc != ATTN_OK) return enc;
     attn47::FwdLaunch f;
     f.tq = &tq;
@@ -998,7 +998,7 @@ attn_status_t attend_kv8(const char* what, bool decode, const void* q, const voi
                         scale, o, lse, workspace, stream);
   a.N = N;
   alignas(64) CUtensorMap records;
-  const attn_status_t enc = encode_kv8(&records, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d, d / 4);
+  const attn_status_t enc = encode_kv8(&records, kv_cache, static_cast<cuuint64_t>(num_blocks) * Hkv, d);
   if (enc != ATTN_OK) return enc;
   a.records = &records;
   return launch_result(attn47::launch_decode_kv8_sm103(a), what);

@@ -30,7 +30,7 @@ struct FwdLaunch {
   const int* ctx_lens = nullptr;      // [B] int32
   int max_blocks = 0, num_blocks = 0;
   // Paged mode over an 8-bit cache: tk covers the records' codes (bytes
-  // [num_blocks Hkv][d / 4 lines][128], boxes of d / 8 lines, 128-byte swizzle),
+  // [num_blocks Hkv][d / 4 lines][128], a record's to a box, 128-byte swizzle),
   // ctx_lens holds the sequences' lengths, the `rows` new tokens included; either
   // Hq query heads of N = rows rows, or Hq = Hkv groups of N = group * rows rows.
   const void* kv_cache = nullptr;     // [num_blocks, Hkv, record] bytes
