@@ -125,7 +125,8 @@ __host__ __device__ constexpr int sort_max_pairs(int source) { return source == 
 __host__ __device__ constexpr int raw_stages(int d) { return d == 128 ? 6 : 14; }
 constexpr int kMaxRawStages = 14;
 constexpr int kScaleTiles = 16;     // tiles whose scales are kept
-constexpr int kAgain = 64, kWideExps = 72;   // see FwdBarriers
+constexpr int kAgain = 64;          // see FwdBarriers
+constexpr int kWideExps = 72;       // see careful_rows
 
 // SUMV (d = 64 with contiguous K/V): the row sums of P come from the tensor
 // core.  Every V stage gets a second 64-column chunk, written once, whose
@@ -148,8 +149,9 @@ struct FwdLayout {
   static constexpr int kOffBar = kOffV + kStages * kVStage;
   static constexpr int kOffCtx = kOffBar + 1024;         // paged: ctx_b of each sequence
   static constexpr int kOffOrder = kOffCtx + 4 * 256;    // paged: (b << 16 | qblk) of each cost rank
-  // 8-bit cache: (K scale times scale log2 e, log2 of V's, 1 / V's) of the 8 blocks
-  // of tile t at t % kScaleTiles; a ring of raw blocks.
+  // 8-bit cache: (K scale times scale log2 e, log2 of V's, 1 / V's, whether the unit's V
+  // scales as of this tile are kWideExps powers of two apart) of the 8 blocks of tile t
+  // at t % kScaleTiles; a ring of raw blocks.
   static constexpr int kOffScales = kOffOrder + 4 * sort_max_pairs(SOURCE);
   static constexpr int kOffRaw = (kOffScales + kScaleTiles * 8 * 16 + 1023) / 1024 * 1024;
   static constexpr int kRawHalf = 16 * D;                     // a record's K or V codes
@@ -179,7 +181,6 @@ struct FwdBarriers {
   // ahead of the MMAs, and these a unit ahead of the epilogue (d = 64: 2 + 4 + 1 + 1),
   // which also bounds the scales' ring.
   int first_flagged[16];
-  int wide[16];                       // in the same way: whether its V scales are kWideExps powers of two apart
 };
 enum RawKind { kRawNone, kRawCodes, kRawCareful, kRawEnd };   // none: zeros; careful: there may be NaN codes
 static_assert(sizeof(FwdBarriers) <= 1024, "room in the layout");
@@ -608,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       next = read_table();
       if (now_number < 0) break;
       // The unit's first flagged token so far: the lowest bit of its block's flags.
-      // It and `wide` are stored before the tile's blocks are on their way, so whoever has
-      // seen this tile's products sees them, with query tile A already before the unit's end.
+      // It is stored before the tile's blocks are on their way, so whoever has seen
+      // this tile's products sees it, with query tile A already before the unit's end.
       const uint32_t bits = (tail.z | (tail.z >> 16)) & 0xffffu;
       if (__any_sync(0xffffffffu, bits != 0)) {
         const int at = bits != 0 ? (now_number * kPagesPerTile + lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
@@ -618,10 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = now_rec >= 0 ? static_cast<int>(tail.y >> 23) : -1;
       most = max(most, __reduce_max_sync(0xffffffffu, e));
       least = min(least, __reduce_min_sync(0xffffffffu, e < 0 ? 255 : e));
-      if (lane == 0) {
-        reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
-        reinterpret_cast<volatile int*>(bar->wide)[unit & 15] = most - least >= kWideExps;
-      }
+      if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
+      const bool wide = most - least >= kWideExps;
       if (now_last) {
         flagged = 0x7fffffff;
         least = 255;
@@ -633,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<float4*>(smem + L::kOffScales)[n % kScaleTiles * 8 + lane] =
             make_float4(now_rec >= 0 ? __uint_as_float(tail.x) * p.scale_log2 : 1.f,
                         now_rec >= 0 ? static_cast<float>(static_cast<int>(tail.y >> 23) - 127) : -INFINITY,
-                        now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, 0.f);
+                        now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, wide ? 1.f : 0.f);
       }
       __syncwarp();                              // (lanes 0 and 1 release what all of them have stored)
       const int kind = now_rec < 0 ? kRawNone : now_ends || bits != 0 ? kRawCareful : kRawCodes;
@@ -1312,7 +1311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
         if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
       }
-      bool again = KV8 && ((l < 0x1p-8f && reinterpret_cast<const volatile int*>(bar->wide)[units & 15]) || fabsf(m) >= 0x1p26f);
+      bool again = false;
+      if constexpr (KV8) {
+        // (As of the query tile's last K/V tile: whatever the look-up has met since.)
+        const float4* last = reinterpret_cast<const float4*>(smem + L::kOffScales) + (kv0 + n_kv - 1) % kScaleTiles * 8;
+        again = (l < 0x1p-8f && last->w != 0.f) || fabsf(m) >= 0x1p26f;
+      }
       const bool in_range = qrow < p.N;
       __nv_bfloat16* orow =
           reinterpret_cast<__nv_bfloat16*>(p.o) + (static_cast<size_t>(zq) * p.N + qrow) * D;
