@@ -616,7 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = bits != 0 ? (now_number * kPagesPerTile + lane) * kPageRows + __ffs(bits) - 1 : 0x7fffffff;
         flagged = min(flagged, __reduce_min_sync(0xffffffffu, at));
       }
-      const int e = now_rec >= 0 ? static_cast<int>(tail.y >> 23) : -1;
+      // (A block that nothing has been written to yet, all zeros, has values of zero by any
+      // scale: the least there is.)
+      const uint32_t scale_v = max(tail.y, static_cast<uint32_t>(127 + kKv8LeastExp) << 23);
+      const int e = now_rec >= 0 ? static_cast<int>(scale_v >> 23) : -1;
       most = max(most, __reduce_max_sync(0xffffffffu, e));
       least = min(least, __reduce_min_sync(0xffffffffu, e < 0 ? 255 : e));
       if (lane == 0) reinterpret_cast<volatile int*>(bar->first_flagged)[unit & 15] = flagged;
@@ -631,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (No block: a V scale whose logarithm leaves nothing of its keys' numerators.)
         reinterpret_cast<float4*>(smem + L::kOffScales)[n % kScaleTiles * 8 + lane] =
             make_float4(now_rec >= 0 ? __uint_as_float(tail.x) * p.scale_log2 : 1.f,
-                        now_rec >= 0 ? static_cast<float>(static_cast<int>(tail.y >> 23) - 127) : -INFINITY,
-                        now_rec >= 0 ? kv8_inverse(tail.y) : 1.f, wide ? 1.f : 0.f);
+                        now_rec >= 0 ? static_cast<float>(e - 127) : -INFINITY,
+                        now_rec >= 0 ? kv8_inverse(scale_v) : 1.f, wide ? 1.f : 0.f);
       }
       __syncwarp();                              // (lanes 0 and 1 release what all of them have stored)
       const int kind = now_rec < 0 ? kRawNone : now_ends || bits != 0 ? kRawCareful : kRawCodes;

@@ -237,3 +237,23 @@ def test_blocks_outside_the_pool_are_left_out(Hq, Hkv, N, d):
         o, lse = prefill([x.to(DEV) for x in (q, cache, bad, sl)], times)
         assert attn.device_status() == attn.ATTN_DEV_BAD_BLOCK
         compare_live(o, lse, ref, cache.numpy(), table.numpy(), lens, d, what="%d times" % times)
+
+
+@pytest.mark.parametrize("N", [3, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [0, 14, 24])
+def test_blocks_of_zeros_that_were_never_written(N, d, size):
+    """Keys and values of zero, whatever scale the zeros are: blocks of a pool as it is
+    allocated, in either way through a batch."""
+    Hq, Hkv = 2, 1
+    lens = [200, 150, 90]
+    q, cache, table, sl = case(lens, Hq, Hkv, d, seed=N, N=N, garbage=None)
+    cache[..., 32 * d + 4: 32 * d + 8] = (cache[..., 32 * d + 4: 32 * d + 8].contiguous().view(torch.float32)
+                                          * 2.0 ** size).view(torch.uint8)
+    for b, i in ((0, 0), (0, 5), (1, 2), (1, 3), (2, 5)):
+        cache[table[b, i].long()] = 0
+    ref = oracle.prefill_paged_kv8(q.double().numpy(), cache.numpy(), table.numpy(), lens, d ** -0.5, d)
+    for times in ways(3, Hq, Hkv, N, d):
+        o, lse = prefill([x.to(DEV) for x in (q, cache, table, sl)], times)
+        compare_live(o, lse, ref, cache.numpy(), table.numpy(), lens, d, what="%d times" % times)
+    assert attn.device_status() == 0
