@@ -10,19 +10,18 @@
 // stays exact); the numerators p are rounded to fp16's 11 bits, at 2^10 for the
 // largest so far, so that those 2^-34 below it still count.
 //
-// The MMAs are 16 tokens x 8 rows (S^T = K q^T) and 16 elements x 8 rows (O^T =
-// V^T P^T): the 16 slots of a block fill the MMA's rows, up to 8 query rows of a
-// KV head its columns; two column tiles make 16.  P^T changes operand layout with
-// movmatrix.  Which elements an MMA's columns of k are is free as long as both
-// operands agree, and so is which token an MMA row is, so a lane takes
-// neighbouring bytes: with r = lane / 4 and c = lane % 4, D/4 of two K rows
-// (tokens of MMA rows r and r + 8) and D/8 of four V rows (those of MMA rows 2 c,
-// 2 c + 1, 2 c + 8, 2 c + 9), whose bytes are paired by token with byte
-// permutations.
+// The MMAs are 16 tokens x 8 rows (S^T = K q^T) and 16 elements x 8 rows (O^T = V^T
+// P^T): the 16 slots of a block fill the MMA's rows, up to 8 query rows of a KV head
+// its columns; two column tiles make 16, three (d = 64) 24.  P^T changes operand
+// layout with movmatrix.  Which elements an MMA's columns of k are is free as long
+// as both operands agree, and so is which token an MMA row is, so a lane takes
+// neighbouring bytes: with r = lane / 4 and c = lane % 4, D/4 of two K rows (tokens
+// of MMA rows r and r + 8) and D/8 of four V rows (those of MMA rows 2 c, 2 c + 1, 2
+// c + 8, 2 c + 9), whose bytes are paired by token with byte permutations.
 //
 // The N queries of a sequence (draft tokens: its last N tokens) are rows like the
 // heads that share a KV head, but for the keys they see: row i sees keys up to
-// L - N + i.  More than 16 rows go in several groups, each its own pass.
+// L - N + i.  More than 16 rows (d = 64: 24) go in several groups, each its own pass.
 //
 // Work split: see decode_split.cuh.  A warp streams the records of its blocks
 // through a ring of its own in shared memory: the codes as one box of a tensor map

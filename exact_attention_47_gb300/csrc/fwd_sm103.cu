@@ -74,7 +74,8 @@
 // there, convert them and store them into the swizzled tile.  NaN codes are cleared
 // where there can be any (a sequence's last block, flagged blocks); the look-up keeps
 // the first position of a flagged token, and a row that sees that position gets NaN
-// in the epilogue.
+// in the epilogue.  Rows whose sizes these exponents cannot hold are computed again
+// behind the last unit (careful_rows).
 // With fewer than 256 new tokens the rows of all query heads that share a KV head
 // make one row of query blocks (row = head in the group times N + token), so that
 // a 256-row unit is not mostly empty.
