@@ -119,6 +119,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTau = 8.0f;        // lazy-rescale threshold, log2 units
 constexpr float kHigh8 = 8.0f;      // 8-bit cache: log2 of P' at the maximum
+constexpr float kNoKeys = -1e30f;   // 8-bit cache: m before the row's first key
 
 __host__ __device__ constexpr int sort_max_pairs(int source) { return source == kPagedKv8 ? 1024 : 2048; }
 // 8-bit cache: raw blocks (K and V codes) in flight, taken in pairs; as many as there
@@ -231,18 +232,19 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
   return w & ~(nan * 0xffu);
 }
 
-// 8-bit cache: rows that the tiles cannot hold, one to a lane, key by key in fp32, each
-// scale where its product is: the row's O and LSE, q at position qpos (-1: no such row).
-// The tiles' numerators P' carry the V scales, 2^e.  One that is under 2^-126 is lost, and
-// with it up to 2^(-126 - e) of l a key (moving m, up to 2^(-110 - e)), where l is at least
-// 2^(8 - e') by the largest P'.  With all e within kWideExps of each other that is 2^-46 of
-// l a key, beyond that with l of 2^-8 and more 2^-38 (e is at least -64); the other rows
-// (their largest P' has an e' over 16) come here.  So do rows with scores beyond 2^26 log2
-// units, where m is a multiple of 8 and more and P' may leave fp16, and those whose O shows
-// that it has done so.  About 1000 instructions a key
-// and 32 columns (4 sequences of 1000 tokens, 512 queries of 12 heads over 2, d = 128: 4.1
-// ms where the tiles take 40 us), out of line so that the tiles' loop stays as it is: sums
-// of l of its own in that loop cost the chunks 3 to 6 %.
+// 8-bit cache: rows that the tiles cannot hold, one to a lane, key by key in fp32,
+// each scale where its product is: the row's O and LSE, q at position qpos (-1: no
+// such row). The tiles' numerators P' carry the V scales, 2^e.  One that is under
+// 2^-126 is lost, and with it up to 2^(-126 - e) of l a key (moving m, up to 2^(-110 -
+// e)), where l is at least 2^(8 - e') by the largest P'.  With all e within kWideExps
+// of each other that is 2^-46 of l a key, beyond that with l of 2^-8 and more 2^-38 (e
+// is at least -64); the other rows (their largest P' has an e' over 16) come here.  So
+// do rows with scores beyond 2^26 log2 units, where m is a multiple of 8 and more and
+// P' may leave fp16, and those whose O shows that it has done so (from 2^40 on, where
+// rows not in use may be, they are NaN).  About 1000 instructions a key and 32 columns
+// (4 sequences of 1000 tokens, 512 queries of 12 heads over 2, d = 128: 3.9 ms where
+// the tiles take 40 us), out of line so that the tiles' loop stays as it is: sums of l
+// of its own in that loop cost the chunks 3 to 6 %.
 template <int D>
 __device__ __noinline__ void careful_rows(const uint8_t* kv_cache, const int* table, int num_blocks, int Hkv, int kvh,
                                           float scale_log2, int qpos, const __nv_bfloat16* q, __nv_bfloat16* o,
@@ -274,47 +276,56 @@ __device__ __noinline__ void careful_rows(const uint8_t* kv_cache, const int* ta
 #pragma unroll
     for (int c = 0; c < 32; ++c) acc[c] = 0.f;
 #pragma unroll 1
-    for (int key = 0; key <= last; ++key) {
-      const int phys = __ldg(table + key / kPageRows), slot = key % kPageRows;
+    for (int blk = 0; blk <= last / kPageRows; ++blk) {
+      const int phys = __ldg(table + blk);
       if (static_cast<unsigned>(phys) >= static_cast<unsigned>(num_blocks)) continue;
       const uint8_t* rec = kv_cache + (static_cast<size_t>(phys) * Hkv + kvh) * Kv8Layout<D>::kBytes;
       const uint4 tail = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffTail));
-      float s = 0.f;
+#pragma unroll 1
+      for (int slot = 0; slot < kPageRows && blk * kPageRows + slot <= last; ++slot) {
+        uint4 kw[D / 16], vw[2];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(rec + slot * D) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < D / 16; ++i) kw[i] = __ldg(reinterpret_cast<const uint4*>(rec + slot * D) + i);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 k0 = numbers(e4m3x2_to_f16x2(w[c])), k1 = numbers(e4m3x2_hi_to_f16x2(w[c]));
-          const float2 q0 = numbers(qw[8 * i + 2 * c]), q1 = numbers(qw[8 * i + 2 * c + 1]);
-          s = fmaf(q0.x, k0.x, fmaf(q0.y, k0.y, fmaf(q1.x, k1.x, fmaf(q1.y, k1.y, s))));
+        for (int i = 0; i < 2; ++i)
+          vw[i] = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffV + slot * D + c0) + i);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 k0 = numbers(e4m3x2_to_f16x2(w[c])), k1 = numbers(e4m3x2_hi_to_f16x2(w[c]));
+            const float2 q0 = numbers(qw[8 * i + 2 * c]), q1 = numbers(qw[8 * i + 2 * c + 1]);
+            s[c] = fmaf(q0.x, k0.x, fmaf(q0.y, k0.y, fmaf(q1.x, k1.x, fmaf(q1.y, k1.y, s[c]))));
+          }
         }
-      }
-      s = s * back * scale_log2 * __uint_as_float(tail.x);     // (0 stays 0)
-      if (key > qpos) continue;
-      spoilt |= (((tail.z | (tail.z >> 16)) >> slot) & 1u) != 0;
-      const float to = fmaxf(m, s), turn = m == to ? 1.f : ex2(m - to);
-      const float w0 = s == to ? 1.f : ex2(s - to);
-      m = to;
-      l = fmaf(l, turn, w0);
-      const float wv = w0 * __uint_as_float(tail.y);
+        // (0 stays 0.)
+        const float x = ((s[0] + s[1]) + (s[2] + s[3])) * back * scale_log2 * __uint_as_float(tail.x);
+        if (blk * kPageRows + slot > qpos) continue;
+        spoilt |= (((tail.z | (tail.z >> 16)) >> slot) & 1u) != 0;
+        const float to = fmaxf(m, x), turn = m == to ? 1.f : ex2(m - to);
+        const float w0 = x == to ? 1.f : ex2(x - to);
+        m = to;
+        l = fmaf(l, turn, w0);
+        const float wv = w0 * __uint_as_float(tail.y);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(rec + Kv8Layout<D>::kOffV + slot * D + c0) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 v0 = numbers(e4m3x2_to_f16x2(w[c])), v1 = numbers(e4m3x2_hi_to_f16x2(w[c]));
-          float* a = acc + 16 * i + 4 * c;
-          a[0] = fmaf(a[0], turn, wv * v0.x);
-          a[1] = fmaf(a[1], turn, wv * v0.y);
-          a[2] = fmaf(a[2], turn, wv * v1.x);
-          a[3] = fmaf(a[3], turn, wv * v1.y);
+          for (int c = 0; c < 4; ++c) {
+            const float2 v0 = numbers(e4m3x2_to_f16x2(w[c])), v1 = numbers(e4m3x2_hi_to_f16x2(w[c]));
+            float* a = acc + 16 * i + 4 * c;
+            a[0] = fmaf(a[0], turn, wv * v0.x);
+            a[1] = fmaf(a[1], turn, wv * v0.y);
+            a[2] = fmaf(a[2], turn, wv * v1.x);
+            a[3] = fmaf(a[3], turn, wv * v1.y);
+          }
         }
       }
     }
     if (qpos < 0) continue;
+    spoilt |= fabsf(m) >= 0x1p40f && l != 0.f;     // (as in the epilogue)
     const float inv = spoilt ? __uint_as_float(0x7fc00000u) : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int c = 0; c < 32; c += 8)
@@ -1278,7 +1289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == 0 || pass == 1) {                 // the tile's maximum is needed
           const float mt = KV8 ? row_max() - kHigh8 : row_max() * sl2;
           if (j == 0)
-            m = (mt == -INFINITY) ? (KV8 ? -1e30f : 0.f) : mt;   // (8-bit cache: keys may come in a later tile)
+            m = (mt == -INFINITY) ? (KV8 ? kNoKeys : 0.f) : mt;   // (8-bit cache: keys may come in a later tile)
           else
             restabilise(mt);
         }
@@ -1312,6 +1323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (The look-up stored this, as of this query tile's last K/V tile at least,
         // before that tile's blocks were on their way; later ones are seen by no row.)
         spoilt = qpos >= reinterpret_cast<const volatile int*>(bar->first_flagged)[units & 15];
+        // Scores that mean nothing any more: what lies in rows that are not in use, too.
+        spoilt |= fabsf(m) >= 0x1p40f && m != kNoKeys;
         if (lsum == 0.f) inv_l = 0.f;              // a row that sees nothing
         if (spoilt) inv_l = __uint_as_float(0x7fc00000u);
       }
@@ -1319,7 +1332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (KV8) {
         // (As of the query tile's last K/V tile: whatever the look-up has met since.)
         const float4* last = reinterpret_cast<const float4*>(smem + L::kOffScales) + (kv0 + n_kv - 1) % kScaleTiles * 8;
-        again = (l < 0x1p-8f && last->w != 0.f) || fabsf(m) >= 0x1p26f;
+        again = (l < 0x1p-8f && last->w != 0.f) || (fabsf(m) >= 0x1p26f && m != kNoKeys);
       }
       const bool in_range = qrow < p.N;
       __nv_bfloat16* orow =

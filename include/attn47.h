@@ -734,8 +734,9 @@ size_t attn_prefill_paged_kv8_workspace_size(int num_seqs, int Hq, int Hkv, int 
  * size is 0) through tiles of 128 rows by 128 keys.  In tiles a numerator is
  * multiplied by its V scale first and rounded to 11 bits, or to 2^-32 of the row's
  * largest such product where that is coarser.  (Rows that attend to V scales more
- * than 2^72 apart, with the most weight on one over 2^16, and rows with scores
- * beyond 2^26 are computed key by key: 100 times as slow.)
+ * than 2^72 apart, with the most weight on one over 2^16, and rows whose largest
+ * score, scale q . k log2 e, is of size 2^26 .. 2^40 are computed key by key, 100
+ * times as slow; from 2^40 on o and lse are NaN in tiles.)
  */
 attn_status_t attn_prefill_paged_kv8(const void* q, const void* kv_cache, const int32_t* block_table,
                                      const int32_t* seq_lens, int num_seqs, int Hq, int Hkv, int N, int d,
