@@ -35,7 +35,7 @@
 // over 2, d = 128 (346 MB) 64.3 us, 5.4 TB/s or 0.81 of a copy; 64 of 128 .. 4096, 12
 // heads over 2 (70 MB) 19.2 us, of which 4 are dependent reads before the first block
 // and 4 to 5 the merges at the end; 256 of 0 .. 2048, 64 heads over 4, d = 64 (139 MB)
-// 40.8 us: two column tiles, 340 instructions a block (ends included) issued in 48 % of
+// 40.8 us: two column tiles, 345 instructions a block (ends included) issued in 49 % of
 // the cycles by the three warps that a scheduler's registers hold; one sequence of 100 tokens 6.4
 // us, a chain of dependent steps.
 #include <atomic>
